@@ -1,5 +1,6 @@
 """Python binding of libfbd: exact attention (causal by default) forward, backward (GProj) and
-backward-over-backward on GB300.
+backward-over-backward on GB300; differential attention (forward, backward, one token over a
+cache) and multi-axis rotary positions.
 
 Argument marshalling only.  Every computation runs in the CUDA kernels of
 ``libfbd.so`` behind the C ABI declared in ``include/fbd.h``; PyTorch is used for
@@ -12,12 +13,14 @@ import ctypes
 import os
 
 from . import _lib
-from ._lib import (ATTN_BF16, ATTN_COL_PASS, ATTN_F32, ATTN_ROW_PASS, AttnDesc, FbdError, lib,  # noqa: F401
-                   status_name)
+from ._lib import (ATTN_BF16, ATTN_COL_PASS, ATTN_F32, ATTN_ROPE_HALF, ATTN_ROPE_MAX_TENSORS,  # noqa: F401
+                   ATTN_ROPE_NEIGHBOUR, ATTN_ROW_PASS, AttnDesc, FbdError, RopeDesc, RopeTensor, lib, status_name)
 
 __all__ = [
     "attn_fwd", "attn_bwd", "attn_bob", "attn_bwd_passes", "attn_bob_passes", "ATTN_ROW_PASS", "ATTN_COL_PASS", "attn_bwd_workspace_bytes", "attn_bob_workspace_bytes",
-    "attn_bob_static", "attn_bwd_projected_dS", "attn_segment_bounds", "attn_device_status", "attn_check_wait_timeout",
+    "attn_bob_static", "attn_bwd_projected_dS", "attn_segment_bounds",
+    "attn_diff_fwd", "attn_diff_bwd", "attn_diff_bwd_workspace_bytes", "attn_diff_decode",
+    "attn_diff_decode_workspace_bytes", "attn_rope", "attn_device_status", "attn_check_wait_timeout",
     "attn_status_string", "attn_version", "make_desc",
     "FbdError", "AttnDesc", "ATTN_F32", "ATTN_BF16", "lib",
 ]
@@ -198,6 +201,171 @@ def attn_segment_bounds(seg, seg_lo=None, seg_hi=None, stream=None):
     seg_hi = torch.empty_like(seg) if seg_hi is None else seg_hi
     _check(lib.attn_segment_bounds(int(B), int(N), _ptr(seg), _ptr(seg_lo), _ptr(seg_hi), _stream(stream)))
     return seg_lo, seg_hi
+
+
+class _on:
+    """The device and stream a call launches on: every tensor on one CUDA device, made current for
+    the call, and `stream` or that device's current stream.  Empty tensors launch nothing, so they
+    may be anywhere."""
+
+    def __init__(self, tensors, stream):
+        torch = _torch()
+        devices = {t.device for t in tensors if t is not None and t.numel() > 0}
+        if len(devices) > 1 or any(d.type != "cuda" for d in devices):
+            raise FbdError(1, f"tensors must be on one CUDA device (got {sorted(map(str, devices))})")
+        self.guard = torch.cuda.device(devices.pop()) if devices else None
+        self.stream = stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _want(name, t, shape, dtype):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise FbdError(1, f"{name} must be {dtype} {tuple(shape)} (got {t.dtype} {tuple(t.shape)})")
+
+
+def _diff_desc(Q, K, V, lam, scale, causal, window, bounds, queries=None) -> AttnDesc:
+    """Descriptor of a differential attention call and the checks of its tensors' shapes and types
+    (queries: 1 for a token over a cache, None where Q has the keys' length)."""
+    torch = _torch()
+    if Q.dim() != 4 or K.dim() != 4 or V.dim() != 4:
+        raise FbdError(1, "Q, K and V must be 4-dimensional")
+    B, maps, _, d = Q.shape
+    kmaps, N = K.shape[1], K.shape[2]
+    if maps % 2 or kmaps % 2:
+        raise FbdError(1, f"Q and K hold two maps per head, got {maps} and {kmaps} slices")
+    H, Hkv = maps // 2, kmaps // 2
+    if (Hkv == 0) != (H == 0) or (Hkv and H % Hkv):
+        raise FbdError(1, f"key/value heads ({Hkv}) must divide query heads ({H})")
+    _want("Q", Q, (B, maps, N if queries is None else queries, d), Q.dtype)
+    _want("K", K, (B, kmaps, N, d), Q.dtype)
+    _want("V", V, (B, Hkv, N, 2 * d), Q.dtype)
+    _want("lam", lam, (H,), torch.float32)
+    lo = hi = None
+    if bounds is not None:
+        for name, t in zip(("seg_lo", "seg_hi"), bounds):
+            _want(name, t, (B, N), torch.int32)
+        lo, hi = _ptr(bounds[0]), _ptr(bounds[1])
+    return AttnDesc(B, H, N, d, float(scale), int(causal), _dtype_code(Q), H // Hkv if Hkv else 1, int(window), lo, hi)
+
+
+def _out(name, t, shape, like, dtype=None):
+    dtype = like.dtype if dtype is None else dtype
+    if t is None:
+        return _torch().empty(shape, dtype=dtype, device=like.device)
+    _want(name, t, shape, dtype)
+    return t
+
+
+def attn_diff_fwd(Q, K, V, lam, O=None, O2=None, lse=None, scale: float = 0.0, stream=None, causal: bool = True,
+                  window: int = 0, bounds=None, for_backward: bool = True):
+    """O, O2, lse = differential attention (A_1 - lam_h A_2) V of Q [B, 2H, N, d], K [B, 2H/g, N, d] (the maps of a
+    head in neighbouring slices), V [B, H/g, N, 2d], lam [H] float32.  O2 = A_2 V and lse are what the backward
+    needs; for_backward=False leaves O2 out (returned as None)."""
+    torch = _torch()
+    desc = _diff_desc(Q, K, V, lam, scale, causal, window, bounds)
+    shape = (desc.B, desc.H, desc.N, 2 * desc.d)
+    O = _out("O", O, shape, Q)
+    O2 = _out("O2", O2, shape, Q) if for_backward or O2 is not None else None
+    lse = _out("lse", lse, Q.shape[:3], Q, torch.float32)
+    with _on([Q, K, V, lam, O, O2, lse, *(bounds or ())], stream) as st:
+        _check(lib.attn_diff_fwd(ctypes.byref(desc), _ptr(Q), _ptr(K), _ptr(V), _ptr(lam), _ptr(O), _ptr(O2), _ptr(lse),
+                                 st))
+    return O, O2, lse
+
+
+def attn_diff_bwd_workspace_bytes(desc: AttnDesc) -> int:
+    return int(lib.attn_diff_bwd_workspace_bytes(ctypes.byref(desc)))
+
+
+def attn_diff_bwd(Q, K, V, lam, O, O2, dO, lse, dQ=None, dK=None, dV=None, dlam=None, workspace=None,
+                  scale: float = 0.0, stream=None, causal: bool = True, window: int = 0, bounds=None):
+    """dQ, dK, dV, dlam = recompute backward of attn_diff_fwd (its mask and scale given again)."""
+    torch = _torch()
+    desc = _diff_desc(Q, K, V, lam, scale, causal, window, bounds)
+    shape = (desc.B, desc.H, desc.N, 2 * desc.d)
+    for name, t in (("O", O), ("O2", O2), ("dO", dO)):
+        _want(name, t, shape, Q.dtype)
+    _want("lse", lse, Q.shape[:3], torch.float32)
+    dQ, dK, dV = _out("dQ", dQ, Q.shape, Q), _out("dK", dK, K.shape, Q), _out("dV", dV, V.shape, Q)
+    dlam = _out("dlam", dlam, lam.shape, lam)
+    workspace = _workspace(attn_diff_bwd_workspace_bytes(desc), Q, workspace)
+    with _on([Q, K, V, lam, O, O2, dO, lse, dQ, dK, dV, dlam, workspace if Q.numel() else None, *(bounds or ())],
+             stream) as st:
+        _check(lib.attn_diff_bwd(ctypes.byref(desc), _ptr(Q), _ptr(K), _ptr(V), _ptr(lam), _ptr(O), _ptr(O2), _ptr(dO),
+                                 _ptr(lse), _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(dlam), _ptr(workspace),
+                                 ctypes.c_size_t(workspace.numel() * workspace.element_size()), st))
+    return dQ, dK, dV, dlam
+
+
+def attn_diff_decode_workspace_bytes(desc: AttnDesc) -> int:
+    return int(lib.attn_diff_decode_workspace_bytes(ctypes.byref(desc)))
+
+
+def attn_diff_decode(Q, K, V, lam, lens, O=None, workspace=None, scale: float = 0.0, stream=None, window: int = 0):
+    """O [B, H, 1, 2d] = differential attention of one token per sequence, Q [B, 2H, 1, d], over a cache K
+    [B, 2H/g, capacity, d], V [B, H/g, capacity, 2d] of which sequence b holds lens[b] keys (int32, on the device;
+    the new token's among them).  A sequence without a key gives zeros."""
+    torch = _torch()
+    desc = _diff_desc(Q, K, V, lam, scale, True, window, None, queries=1)
+    _want("lens", lens, (desc.B,), torch.int32)
+    O = _out("O", O, (desc.B, desc.H, 1, 2 * desc.d), Q)
+    workspace = _workspace(attn_diff_decode_workspace_bytes(desc), Q, workspace)
+    with _on([Q, K, V, lam, lens, O, workspace if Q.numel() else None], stream) as st:
+        _check(lib.attn_diff_decode(ctypes.byref(desc), _ptr(Q), _ptr(K), _ptr(V), _ptr(lam), _ptr(lens), _ptr(O),
+                                    _ptr(workspace), ctypes.c_size_t(workspace.numel() * workspace.element_size()), st))
+    return O
+
+
+def attn_rope(xs, pos, freq, axis, outs=None, paired: str = "half", inverse: bool = False, stream=None):
+    """Rotary positions with several axes: pair i of each token of the [B, heads, N, d] views `xs` (one tensor or up to
+    four, any strides with d contiguous) turns by freq[i] * pos[axis[i]]; pos [axes, B, N] or [axes, N] int32, freq
+    [d/2] float32, axis [d/2] int32 (-1: the pair is copied unturned).  paired: "half" (coordinates i, i + d/2) or
+    "neighbour" (2i, 2i + 1).  inverse=True turns back (the gradient).  Returns `outs` (contiguous [B, heads, N, d]
+    tensors when not given; views of any strides when given, x itself among them), one tensor for one."""
+    torch = _torch()
+    single = torch.is_tensor(xs)
+    xs = [xs] if single else list(xs)
+    if not 1 <= len(xs) <= ATTN_ROPE_MAX_TENSORS:
+        raise FbdError(1, f"1 to {ATTN_ROPE_MAX_TENSORS} tensors, got {len(xs)}")
+    if any(x.dim() != 4 for x in xs):
+        raise FbdError(1, "tensors must be [B, heads, N, d]")
+    if outs is None:
+        outs = [torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in xs]
+    else:
+        outs = [outs] if torch.is_tensor(outs) else list(outs)
+    if len(outs) != len(xs):
+        raise FbdError(1, f"{len(xs)} inputs and {len(outs)} outputs")
+    if paired not in ("half", "neighbour"):
+        raise FbdError(1, f"paired must be 'half' or 'neighbour' (got {paired!r})")
+    B, _, N, d = xs[0].shape
+    for x, y in zip(xs, outs):
+        _want("x", x, (B, x.shape[1], N, d), xs[0].dtype)
+        _want("out", y, x.shape, x.dtype)
+        if x.numel() and (x.stride(3) != 1 or y.stride(3) != 1):
+            raise FbdError(1, "the last dimension must be contiguous")
+    if pos.dim() not in (2, 3):
+        raise FbdError(1, "pos must be [axes, B, N] or [axes, N]")
+    axes = pos.shape[0]
+    _want("pos", pos, (axes, N) if pos.dim() == 2 else (axes, B, N), torch.int32)
+    _want("freq", freq, (d // 2,), torch.float32)
+    _want("axis", axis, (d // 2,), torch.int32)
+    desc = RopeDesc(B, N, d, axes, _dtype_code(xs[0]), ATTN_ROPE_HALF if paired == "half" else ATTN_ROPE_NEIGHBOUR,
+                    int(inverse), 0 if pos.dim() == 2 else N)
+    tensors = (RopeTensor * len(xs))()
+    for t, x, y in zip(tensors, xs, outs):
+        t.x, t.y, t.heads = x.data_ptr(), y.data_ptr(), x.shape[1]
+        t.x_stride[:], t.y_stride[:] = x.stride()[:3], y.stride()[:3]
+    with _on([*xs, *outs, pos, freq, axis] if any(x.numel() for x in xs) else [], stream) as st:
+        _check(lib.attn_rope(ctypes.byref(desc), tensors, len(xs), _ptr(pos), _ptr(freq), _ptr(axis), st))
+    return outs[0] if single else outs
 
 
 def attn_device_status(stream=None) -> int:

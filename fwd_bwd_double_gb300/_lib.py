@@ -10,6 +10,9 @@ ATTN_F32 = 0
 ATTN_BF16 = 1
 ATTN_ROW_PASS = 1
 ATTN_COL_PASS = 2
+ATTN_ROPE_MAX_TENSORS = 4
+ATTN_ROPE_HALF = 0
+ATTN_ROPE_NEIGHBOUR = 1
 
 STATUS_NAMES = {
     0: "ATTN_OK", 1: "ATTN_ERR_INVALID_ARG", 2: "ATTN_ERR_UNSUPPORTED", 3: "ATTN_ERR_ALIGNMENT",
@@ -34,6 +37,17 @@ class AttnDesc(ctypes.Structure):
                 ("seg_hi", ctypes.c_void_p)]
 
 
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("N", ctypes.c_int64), ("d", ctypes.c_int64), ("axes", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("paired", ctypes.c_int32), ("inverse", ctypes.c_int32),
+                ("pos_batch_stride", ctypes.c_int64)]
+
+
+class RopeTensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("heads", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64 * 3), ("y_stride", ctypes.c_int64 * 3)]
+
+
 _P = ctypes.c_void_p
 _D = ctypes.POINTER(AttnDesc)
 PROTOTYPES = {
@@ -48,6 +62,12 @@ PROTOTYPES = {
     "attn_bob_static": (ctypes.c_int, [_D] + [_P] * 13 + [_P]),
     "attn_bwd_projected_dS": (ctypes.c_int, [_D, _P, _P, _P, _P, _P, _P, _P, _P]),
     "attn_segment_bounds": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, _P, _P, _P, _P]),
+    "attn_diff_fwd": (ctypes.c_int, [_D] + [_P] * 8),
+    "attn_diff_bwd_workspace_bytes": (ctypes.c_size_t, [_D]),
+    "attn_diff_bwd": (ctypes.c_int, [_D] + [_P] * 13 + [ctypes.c_size_t, _P]),
+    "attn_diff_decode_workspace_bytes": (ctypes.c_size_t, [_D]),
+    "attn_diff_decode": (ctypes.c_int, [_D] + [_P] * 7 + [ctypes.c_size_t, _P]),
+    "attn_rope": (ctypes.c_int, [ctypes.POINTER(RopeDesc), ctypes.POINTER(RopeTensor), ctypes.c_int, _P, _P, _P, _P]),
     "attn_device_status": (ctypes.c_int, [_P]),
     "attn_check_wait_timeout": (ctypes.c_int, [_P]),
     "attn_status_string": (ctypes.c_char_p, [ctypes.c_int]),

@@ -11,26 +11,23 @@
 #include <initializer_list>
 #include <mutex>
 
+#include "checks.h"
 #include "fbd.h"
 #include "internal.h"
 
 namespace {
-
 thread_local char g_last_error[256] = "";
+}
 
-attn_status_t fail(attn_status_t s, const char* fmt, const char* what = "") {
+namespace fbd {
+
+attn_status_t fail(attn_status_t s, const char* fmt, const char* what) {
   std::snprintf(g_last_error, sizeof(g_last_error), fmt, what);
   return s;
 }
 
-struct Span {
-  const char* name;
-  uintptr_t lo, hi;  // [lo, hi)
-};
+static bool overlap(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
 
-bool overlap(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
-
-// Shape/type checks shared by every entry point.  Fills `p` on success.
 attn_status_t check_desc(const attn_desc_t* desc, fbd::Problem& p) {
   if (desc == nullptr) return fail(ATTN_ERR_INVALID_ARG, "desc is NULL%s");
   if (desc->B < 0 || desc->H < 0 || desc->N < 0 || desc->d <= 0)
@@ -79,9 +76,8 @@ attn_status_t check_desc(const attn_desc_t* desc, fbd::Problem& p) {
 size_t elem_size(const fbd::Problem& p) { return p.dtype == ATTN_F32 ? 4 : 2; }
 
 // Bytes of one [B, H / group, N, d] key/value-side tensor.
-size_t kv_bytes(const fbd::Problem& p) { return static_cast<size_t>(p.BHkv * p.N * p.d) * elem_size(p); }
+static size_t kv_bytes(const fbd::Problem& p) { return static_cast<size_t>(p.BHkv * p.N * p.d) * elem_size(p); }
 
-// Non-NULL, 16-byte aligned, pairwise non-overlapping outputs vs everything.
 attn_status_t check_ptrs(const Span* in, int nin, const Span* out, int nout) {
   for (int k = 0; k < nin + nout; ++k) {
     const Span& s = k < nin ? in[k] : out[k - nin];
@@ -102,6 +98,18 @@ Span span(const char* name, const void* ptr, size_t bytes) {
   return Span{name, lo, lo + bytes};
 }
 
+attn_status_t launch_status(cudaError_t e) {
+  if (e == cudaSuccess) return ATTN_OK;
+  (void)cudaGetLastError();  // clear the sticky-free launch error
+  return fail(ATTN_ERR_LAUNCH, "CUDA: %s", cudaGetErrorString(e));
+}
+
+}  // namespace fbd
+
+namespace {
+
+using namespace fbd;
+
 // The inputs of an entry point, with the document bounds appended when they are given.
 struct Inputs {
   Span s[13];
@@ -115,12 +123,6 @@ struct Inputs {
     }
   }
 };
-
-attn_status_t launch_status(cudaError_t e) {
-  if (e == cudaSuccess) return ATTN_OK;
-  (void)cudaGetLastError();  // clear the sticky-free launch error
-  return fail(ATTN_ERR_LAUNCH, "CUDA: %s", cudaGetErrorString(e));
-}
 
 bool tc_path(const fbd::Problem& p, int op) { return p.dtype == ATTN_BF16 && fbd::tc_supports(op, p.d); }
 // float32 inputs on the tensor cores (three tf32 products per product), every supported d.

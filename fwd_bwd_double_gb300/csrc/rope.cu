@@ -1,0 +1,131 @@
+// Rotary positions with several axes (time, height, width, ...): coordinate pair i of a
+// token turns by the angle freq[i] * pos[axis[i]], (u, v) -> (u cos - v sin, u sin + v cos);
+// `inverse` turns back, which is the gradient (the map is orthogonal).
+//
+// Bound by reading and writing each element once (16 bytes per thread and half).  Angles
+// are exact before they are rounded: freq / 2 pi as a 64-bit fraction of a turn times the
+// integer position, modulo 2^64, is the fraction of a turn left over, so a position in
+// the millions loses nothing (an fp32 product freq * pos would lose its low bits there).
+// A thread holds the sines of its pairs and applies them to several heads.
+#include <cuda_bf16.h>
+
+#include "ptx.cuh"
+#include "rope.h"
+#include "tc_common.cuh"
+
+namespace fbd {
+namespace {
+
+constexpr int kT = 256;
+constexpr int kMaxPairs = 128;
+
+// 16 bytes as floats.
+__device__ __forceinline__ void ldv(const float* p, float (&x)[4]) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+}
+__device__ __forceinline__ void ldv(const __nv_bfloat16* p, float (&x)[8]) {
+  const uint4 v = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int u = 0; u < 4; ++u) x[2 * u] = tc::bf16_lo(w[u]), x[2 * u + 1] = tc::bf16_hi(w[u]);
+}
+__device__ __forceinline__ void stv(float* p, const float (&x)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void stv(__nv_bfloat16* p, const float (&x)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(ptx::pack_bf16(x[0], x[1]), ptx::pack_bf16(x[2], x[3]),
+                                            ptx::pack_bf16(x[4], x[5]), ptx::pack_bf16(x[6], x[7]));
+}
+
+template <typename T, bool HALF>
+__global__ void __launch_bounds__(kT)
+    rope_kernel(const RopeArgs a, const int* __restrict__ pos, const float* __restrict__ freq,
+                const int* __restrict__ axis) {
+  constexpr int W = 16 / sizeof(T);  // pairs per thread
+  __shared__ unsigned long long sT[kMaxPairs];
+  __shared__ int sAx[kMaxPairs];
+  const int pairs = a.d / 2, per = pairs / W;  // threads per token
+  for (int i = threadIdx.x; i < pairs; i += kT) {
+    double t = static_cast<double>(freq[i]) * 0.15915494309189533577;  // turns per step (1 / 2 pi)
+    t -= floor(t);
+    sT[i] = __double2ull_rz(t * 18446744073709551616.0);
+    const int ax = axis[i];
+    sAx[i] = ax < a.axes ? ax : -1;
+  }
+  __syncthreads();
+  const int64_t gid = static_cast<int64_t>(blockIdx.x) * kT + threadIdx.x;
+  const int64_t token = gid / per;
+  const int part = static_cast<int>(gid - token * per);
+  if (token >= a.B * a.N) return;
+  const int64_t b = token / a.N, n = token - b * a.N;
+  float cs[W], sn[W];
+#pragma unroll
+  for (int u = 0; u < W; ++u) {
+    const int i = part * W + u, ax = sAx[i];
+    cs[u] = 1.f, sn[u] = 0.f;
+    if (ax >= 0) {
+      const long long p = pos[ax * a.pos_axis + b * a.pos_batch + n];
+      const unsigned long long turn = static_cast<unsigned long long>(p) * sT[i];  // mod 2^64: whole turns drop out
+      sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f, &sn[u], &cs[u]);
+      if (a.inverse) sn[u] = -sn[u];
+    }
+  }
+  const int hb = blockIdx.y * a.per_thread;
+  const int he = min(hb + a.per_thread, a.heads);
+  const int c0 = HALF ? part * W : 2 * part * W, c1 = HALF ? c0 + pairs : c0 + W;
+  for (int h = hb; h < he; ++h) {
+    int t = 0, hh = h;  // head h of all tensors: head hh of tensor t
+    while (hh >= a.t[t].heads) hh -= a.t[t].heads, ++t;
+    const RopeTensor& z = a.t[t];
+    const T* x = static_cast<const T*>(z.x) + b * z.xs[0] + hh * z.xs[1] + n * z.xs[2];
+    T* y = static_cast<T*>(z.y) + b * z.ys[0] + hh * z.ys[1] + n * z.ys[2];
+    float p[W], q[W];
+    ldv(x + c0, p);
+    ldv(x + c1, q);
+    if constexpr (HALF) {
+#pragma unroll
+      for (int u = 0; u < W; ++u) {
+        const float s = p[u], r = q[u];
+        p[u] = s * cs[u] - r * sn[u];
+        q[u] = s * sn[u] + r * cs[u];
+      }
+    } else {  // neighbouring pairs: p holds the thread's first W / 2 pairs, q the rest
+#pragma unroll
+      for (int u = 0; u < W / 2; ++u) {
+        float s = p[2 * u], r = p[2 * u + 1];
+        p[2 * u] = s * cs[u] - r * sn[u];
+        p[2 * u + 1] = s * sn[u] + r * cs[u];
+        s = q[2 * u], r = q[2 * u + 1];
+        q[2 * u] = s * cs[W / 2 + u] - r * sn[W / 2 + u];
+        q[2 * u + 1] = s * sn[W / 2 + u] + r * cs[W / 2 + u];
+      }
+    }
+    stv(y + c0, p);
+    stv(y + c1, q);
+  }
+}
+
+template <typename T>
+cudaError_t run(RopeArgs a, bool half, const int* pos, const float* freq, const int* axis, cudaStream_t st) {
+  const int64_t threads = a.B * a.N * (a.d / 2 / (16 / static_cast<int>(sizeof(T))));
+  // Heads per thread: as many as leave two full waves of threads on 152 SMs.
+  const int64_t hp = a.heads * threads / (2 * 152 * 2048);
+  a.per_thread = static_cast<int>(hp < 1 ? 1 : hp > a.heads ? a.heads : hp);
+  const dim3 grid(static_cast<unsigned>((threads + kT - 1) / kT),
+                  static_cast<unsigned>((a.heads + a.per_thread - 1) / a.per_thread));
+  if (half)
+    rope_kernel<T, true><<<grid, kT, 0, st>>>(a, pos, freq, axis);
+  else
+    rope_kernel<T, false><<<grid, kT, 0, st>>>(a, pos, freq, axis);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t rope(const RopeArgs& a, int dtype, bool half, const int* pos, const float* freq, const int* axis,
+                 cudaStream_t st) {
+  return dtype == ATTN_BF16 ? run<__nv_bfloat16>(a, half, pos, freq, axis, st) : run<float>(a, half, pos, freq, axis, st);
+}
+
+}  // namespace fbd

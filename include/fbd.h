@@ -315,6 +315,91 @@ attn_status_t attn_bwd_projected_dS(const attn_desc_t* desc, const void* Q, cons
                                     const void* V, const void* O, const void* dO,
                                     const float* lse, float* dS_out, void* stream);
 
+/* ---------------------------------------------------------------------------------
+ * Differential attention.  A differential head holds two softmax maps over one value
+ * head of twice their width; the second map, weighted by a learned number per head, is
+ * taken off the first:
+ *   A_m = softmax(s Q_m K_m^T + mask), m = 1, 2;    O = (A_1 - lam_h A_2) V.
+ * The source pages have no counterpart.  desc->H counts differential heads and desc->d is
+ * the width of one map; desc->group query heads share a key/value head.  Layout:
+ *   Q [B,2H,N,d], K [B,2H/g,N,d]: the two maps of head h are the neighbouring slices 2h
+ *   and 2h + 1 (so Q and K are what 2H heads of attn_fwd would be); V [B,H/g,N,2d];
+ *   O, O2, dO [B,H,N,2d]; lse [B,2H,N] float32; lam, dlam [H] float32.
+ * Masks (causal, full, window, document bounds), types, scale, alignment, streams and
+ * errors are those of attn_fwd, with these differences: d in {32, 64} (else
+ * ATTN_ERR_UNSUPPORTED), and lam, dlam and lens need only their element's alignment. */
+
+/* Forward.
+ *   In:  Q, K, V, lam.
+ *   Out: O; lse of both maps; O2 = A_2 V, which the backward needs (NULL: not written). */
+attn_status_t attn_diff_fwd(const attn_desc_t* desc, const void* Q, const void* K, const void* V, const float* lam,
+                            void* O, void* O2, float* lse, void* stream);
+
+/* Workspace for attn_diff_bwd (its layout is internal). */
+size_t attn_diff_bwd_workspace_bytes(const attn_desc_t* desc);
+
+/* Recompute backward.  With dP = dO V^T, D_2 = dO.O2, D_1 = dO.O + lam D_2, w = (1, -lam):
+ *   dS_m = w_m P_m (dP - D_m);  dQ_m = s dS_m K_m;  dK_m = s dS_m^T Q_m;
+ *   dV = (P_1 - lam P_2)^T dO;  dlam_h = -sum over b, i, j of (P_2)_ij dP_ij.
+ * The gradients of a shared key/value head are sums over its query heads.  A row that sees
+ * one key has dS = 0 exactly.  O, O2, lse: the forward's outputs for the same inputs.
+ *   dlam is summed in a fixed order; it is written also when B*N == 0 (zeros).
+ *   workspace: >= attn_diff_bwd_workspace_bytes(desc) bytes, 16-byte aligned, contents
+ *   ignored on entry.  Calls that may run at the same time need one each. */
+attn_status_t attn_diff_bwd(const attn_desc_t* desc, const void* Q, const void* K, const void* V, const float* lam,
+                            const void* O, const void* O2, const void* dO, const float* lse, void* dQ, void* dK,
+                            void* dV, float* dlam, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace for attn_diff_decode (may be 0: then workspace may be NULL). */
+size_t attn_diff_decode_workspace_bytes(const attn_desc_t* desc);
+
+/* One new token per sequence over a cache: desc->N is the cache's capacity.
+ *   Q [B,2H,1,d]; K [B,2H/g,N,d] and V [B,H/g,N,2d]: the cache; lens [B] int32 (device):
+ *   the keys each sequence holds, the new token's among them.  The token sees the keys
+ *   0 <= j < lens[b], with desc->window = W > 0 the last W of them.  Cache rows it does not
+ *   see are never used, whatever they hold.  lens outside 0 .. N is taken as the nearest
+ *   bound; a sequence with no key gives O = 0.
+ *   O [B,H,1,2d].  causal must be 1 and the document bounds NULL (ATTN_ERR_UNSUPPORTED).
+ *   workspace: >= attn_diff_decode_workspace_bytes(desc) bytes, 16-byte aligned, contents
+ *   ignored on entry.  Calls that may run at the same time need one each. */
+attn_status_t attn_diff_decode(const attn_desc_t* desc, const void* Q, const void* K, const void* V, const float* lam,
+                               const int32_t* lens, void* O, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Rotary positions with several axes (time, height, width, ... of text, images and video),
+ * for the queries and keys of any attention call here.  The source pages have no
+ * counterpart.  Coordinate pair i < d/2 of a token turns by freq[i] * pos[axis[i]]:
+ *   (u, v) -> (u cos - v sin, u sin + v cos);
+ * inverse = 1 turns back, which is the gradient of the turn.
+ *   pos [axes, B, N] int32 (pos_batch_stride = 0: [axes, N], shared by the batch);
+ *   freq [d/2] float32 (finite), radians per step; axis [d/2] int32: the axis each pair
+ *   turns with, outside 0 .. axes - 1: the pair is copied unturned.
+ * Angles are exact before rounding for every int32 position.
+ * Up to ATTN_ROPE_MAX_TENSORS tensors with the same tokens in one launch, each a
+ * [B, heads, N, d] view with strides of its own (d contiguous), so that a projection's
+ * [B,N,heads,d] output is turned and laid out as [B,H,N,d] in one pass, or back.  y may be
+ * exactly x (same address and strides); otherwise no y may share an element with any x or
+ * other y.  That is checked for a contiguous x and its contiguous y (ATTN_ERR_INVALID_ARG). */
+#define ATTN_ROPE_MAX_TENSORS 4
+#define ATTN_ROPE_HALF 0      /* pair i: coordinates i and i + d/2 */
+#define ATTN_ROPE_NEIGHBOUR 1 /* pair i: coordinates 2i and 2i + 1 */
+typedef struct {
+  int64_t B, N, d;   /* d in {32, 64, 96, 128, 256} */
+  int32_t axes;      /* position axes, 1 .. 64 */
+  int32_t dtype;     /* attn_dtype_t of every x and y */
+  int32_t paired;    /* ATTN_ROPE_HALF or ATTN_ROPE_NEIGHBOUR */
+  int32_t inverse;   /* 0 or 1 */
+  int64_t pos_batch_stride; /* N for [axes, B, N], 0 for [axes, N] */
+} attn_rope_desc_t;
+typedef struct {
+  const void* x;
+  void* y;
+  int64_t heads;
+  int64_t x_stride[3], y_stride[3]; /* of (batch, head, position) in elements; multiples of 16 bytes, >= 0;
+                                       y's, in order of size, each past the extent of the smaller ones */
+} attn_rope_tensor_t;
+attn_status_t attn_rope(const attn_rope_desc_t* desc, const attn_rope_tensor_t* tensors, int count,
+                        const int32_t* pos, const float* freq, const int32_t* axis, void* stream);
+
 /* Synchronises `stream` and reports (then clears) the device-side status word:
  * ATTN_ERR_TIMEOUT if any kernel's bounded wait gave up since the last call,
  * ATTN_ERR_LAUNCH if the stream holds a CUDA error, else ATTN_OK. */
