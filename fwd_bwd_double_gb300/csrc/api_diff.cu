@@ -79,7 +79,9 @@ attn_status_t attn_diff_fwd(const attn_desc_t* desc, const void* Q, const void* 
   if (O2 != nullptr) out[nout++] = span("O2", O2, z.o);
   if ((s = check_ptrs(in.s, in.n, out, nout)) != ATTN_OK) return s;
   if ((s = check_apart(span("lam", lam, p.H * sizeof(float)), out, nout)) != ATTN_OK) return s;
-  return launch_status(simt_diff_fwd(p, Q, K, V, lam, O, O2, lse, static_cast<cudaStream_t>(stream)));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return launch_status(p.dtype == ATTN_BF16 ? tc_diff_fwd(p, Q, K, V, lam, O, O2, lse, st)
+                                            : simt_diff_fwd(p, Q, K, V, lam, O, O2, lse, st));
 }
 
 size_t attn_diff_bwd_workspace_bytes(const attn_desc_t* desc) {

@@ -16,6 +16,11 @@ namespace fbd {
 // The widths with kernels.
 inline bool diff_supports(int64_t d) { return d == 32 || d == 64; }
 
+// bf16 tensor-core kernels (tc_diff_fwd.cu).
+cudaError_t tc_diff_fwd(const Problem& p, const void* Q, const void* K, const void* V, const float* lam, void* O,
+                        void* O2, float* lse, cudaStream_t st);
+uint32_t tc_diff_fwd_take_error();
+
 // CUDA-core kernels (simt_diff.cu).
 cudaError_t simt_diff_fwd(const Problem& p, const void* Q, const void* K, const void* V, const float* lam, void* O,
                           void* O2, float* lse, cudaStream_t st);

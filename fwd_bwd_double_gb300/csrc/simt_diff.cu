@@ -463,9 +463,6 @@ size_t simt_diff_bwd_bytes(int64_t BH, int64_t N) {
 
 cudaError_t simt_diff_fwd(const Problem& p, const void* Q, const void* K, const void* V, const float* lam, void* O,
                           void* O2, float* lse, cudaStream_t st) {
-  if (p.dtype == ATTN_BF16)
-    return p.d == 32 ? fwd<32, __nv_bfloat16>(p, Q, K, V, lam, O, O2, lse, st)
-                     : fwd<64, __nv_bfloat16>(p, Q, K, V, lam, O, O2, lse, st);
   return p.d == 32 ? fwd<32, float>(p, Q, K, V, lam, O, O2, lse, st)
                    : fwd<64, float>(p, Q, K, V, lam, O, O2, lse, st);
 }

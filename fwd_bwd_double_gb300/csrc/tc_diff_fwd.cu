@@ -1,0 +1,328 @@
+// Differential attention forward, bf16, on the tensor cores.
+//
+//   A_m = softmax(s Q_m K_m^T + mask), m = 1, 2;   O = (A_1 - lam A_2) V,  O_2 = A_2 V.
+// One CTA owns 128 query rows of a head and streams blocks of 128 keys (K_1, K_2 and V, so
+// that V is read once for both maps).  Per block and map
+//   S_m = Q_m K_m^T          A and B from shared memory, accumulator in TMEM
+//   P_m = 2^(S_m c - M_m c)  online softmax, one query row per thread, bf16 over S_m's columns
+//   O_m += P_m V             A = P_m from TMEM, B = V (MN-major)
+// The two maps take turns: while four warps exponentiate S_1, the tensor cores run P_2 V and
+// the next S_2, and the other way round (six products of 128 x 128 x 64 a block).  TMEM is
+// full: S_1, S_2 (128 columns each, P_m over the first half of S_m) and O_1, O_2 (2d each).
+// The MMA warp issues S_m of block j + 1 behind P_m V of block j; products of one thread
+// run in order, so S_m overwrites P_m only once it has been read.
+//
+// The reference maximum M_m moves only when a row's maximum passes it by more than 2^8 in
+// the probabilities (P_m <= 2^8, l and O_m in fp32): most blocks then rescale nothing.
+// P is rounded to bf16 for its product; the sums l are of the unrounded fp32 values.
+#include <cuda_bf16.h>
+
+#include "diff.h"
+#include "ptx.cuh"
+#include "tc_common.cuh"
+
+namespace fbd {
+namespace {
+
+__device__ unsigned int g_err = 0;
+
+constexpr int BM = 128, BN = 128;
+constexpr int NS = 3;
+constexpr int kThreads = 320;  // warps 0-3: map 1, 4-7: map 2, 8: TMA, 9: MMA
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 8.f;  // log2 of the largest P
+
+template <int D>
+struct Lay {
+  static constexpr int DV = 2 * D;
+  static constexpr int kQ = BM * 128;         // a map's tile: 64 columns (d = 32: the rest zero-filled)
+  static constexpr int kV = BN * DV * 2;
+  static constexpr int kStage = 2 * kQ + kV;  // K_1, K_2, V
+  static constexpr int oStage = 2 * kQ;
+  static constexpr int oInv = oStage + NS * kStage;  // 1 / l_2 of every row
+  static constexpr int oBar = oInv + BM * 4;
+  static constexpr int bytes = oBar + 160;
+  static constexpr uint32_t cS = 0, cO = 2 * BN;  // S_m at cS + m BN, O_m at cO + m DV
+};
+static_assert(Lay<64>::bytes <= 232448, "shared memory");
+
+// WIN: a banded causal mask is in force (window and/or document bounds).
+template <int D, bool WIN>
+__global__ void __launch_bounds__(kThreads, 1)
+    fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+               const __grid_constant__ CUtensorMap tmV, const float* __restrict__ lam, __nv_bfloat16* __restrict__ O,
+               __nv_bfloat16* __restrict__ O2, float* __restrict__ lse, int N, int H, int nrb, int BH, float scale,
+               float c, int causal, Band bd, int G) {
+  using L = Lay<D>;
+  constexpr int DV = L::DV;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::oBar);
+  uint64_t* q_full = bars;
+  uint64_t* k_full = bars + 1;            // [NS]
+  uint64_t* v_full = k_full + NS;         // [NS]
+  uint64_t* empty = v_full + NS;          // [NS] both maps' P V of the stage done
+  uint64_t* s_full = empty + NS;          // [2] S_m in TMEM (and the previous P_m V done)
+  uint64_t* p_ready = s_full + 2;         // [2] P_m in TMEM, O_m rescaled
+  uint64_t* o_full = p_ready + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* sInv = reinterpret_cast<float*>(sm + L::oInv);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const tc::Order ord = tc::grid_order(BH, nrb);
+  const int bh = ord.bh, kvh = bh / G;
+  const int rb = nrb - 1 - ord.k;  // heaviest row blocks first
+  const int j0 = (WIN && causal) ? bd.row_lo(bh, rb * BM) / BN : 0;
+  const int lo_last = (WIN && causal) ? bd.row_lo(bh, min(rb * BM + BM - 1, N - 1)) : 0;
+  const int nkv = (causal ? rb + 1 : nrb) - j0;
+
+  if (threadIdx.x == 0) {
+    ptx::mbar_init(q_full, 1);
+    for (int s = 0; s < NS; ++s) {
+      ptx::mbar_init(&k_full[s], 1);
+      ptx::mbar_init(&v_full[s], 1);
+      ptx::mbar_init(&empty[s], 1);
+    }
+    for (int m = 0; m < 2; ++m) {
+      ptx::mbar_init(&s_full[m], 1);
+      ptx::mbar_init(&p_ready[m], 128);
+    }
+    ptx::mbar_init(o_full, 1);
+    *abort_flag = (ptx::smem_u32(sm) & 1023u) ? 1 : 0;  // the swizzled tiles need 1024-byte alignment
+    if (*abort_flag) atomicOr(&g_err, FBD_ERR_TIMEOUT);
+    ptx::fence_mbar_init();
+  }
+  if (warp == 9) {
+    ptx::tmem_alloc(tmem_slot, 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const ptx::BoundedWait wait{abort_flag, &g_err};
+  const bool ok = *abort_flag == 0;
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0 && ok) {
+      ptx::prefetch_tmap(&tmQ);
+      ptx::prefetch_tmap(&tmK);
+      ptx::prefetch_tmap(&tmV);
+      ptx::mbar_expect_tx(q_full, 2 * L::kQ);
+      for (int m = 0; m < 2; ++m) ptx::tma_load_3d(sm + m * L::kQ, &tmQ, q_full, 0, rb * BM, 2 * bh + m);
+      for (int j = 0; j < nkv; ++j) {
+        const int s = j % NS;
+        uint8_t* st = sm + L::oStage + s * L::kStage;
+        if (j >= NS) wait(&empty[s], ((j / NS) - 1) & 1);
+        ptx::mbar_expect_tx(&k_full[s], 2 * L::kQ);
+        for (int m = 0; m < 2; ++m) ptx::tma_load_3d(st + m * L::kQ, &tmK, &k_full[s], 0, (j0 + j) * BN, 2 * kvh + m);
+        ptx::mbar_expect_tx(&v_full[s], L::kV);
+        for (int u = 0; u < DV / 64; ++u)
+          ptx::tma_load_3d(st + 2 * L::kQ + u * BN * 128, &tmV, &v_full[s], u * 64, (j0 + j) * BN, kvh);
+      }
+      // the last stages must have been consumed before the CTA exits
+      for (int j = (nkv > NS ? nkv - NS : 0); j < nkv; ++j) wait(&empty[j % NS], (j / NS) & 1);
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------- MMA issuer
+    if (ok) {
+      constexpr uint32_t idS = ptx::idesc_bf16(BM, BN, 0, 0);
+      constexpr uint32_t idO = ptx::idesc_bf16(BM, DV, 0, 1);
+      const uint64_t dQ = tc::kmajor_desc(ptx::smem_u32(sm), BM, 0);
+      const uint64_t dK = tc::kmajor_desc(ptx::smem_u32(sm + L::oStage), BN, 0);
+      const uint64_t dV = tc::mnmajor_desc(ptx::smem_u32(sm + L::oStage + 2 * L::kQ), BN, 0);
+      auto issue_s = [&](int m, int j) {
+        const uint32_t so = static_cast<uint32_t>((j % NS) * L::kStage + m * L::kQ);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          ptx::mma_ss_e(tmem + L::cS + m * BN, tc::desc_add(dQ, m * L::kQ + tc::kmajor_off(BM, k)),
+                        tc::desc_add(dK, so + tc::kmajor_off(BN, k)), idS, k > 0 ? 1u : 0u);
+        ptx::mma_commit_e(&s_full[m]);
+      };
+      wait(q_full, 0);
+      wait(&k_full[0], 0);
+      ptx::tc_fence_after();
+      issue_s(0, 0);
+      issue_s(1, 0);
+      for (int j = 0; j < nkv; ++j) {
+        const int s = j % NS;
+        const uint32_t so = static_cast<uint32_t>(s * L::kStage);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          wait(&p_ready[m], j & 1);
+          if (m == 0) wait(&v_full[s], (j / NS) & 1);
+          ptx::tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < BN / 16; ++k)
+            ptx::mma_ts_e(tmem + L::cO + m * DV, tmem + L::cS + m * BN + k * 8, tc::desc_add(dV, so + k * 2048), idO,
+                          (j > 0 || k > 0) ? 1u : 0u);
+          if (m == 1) ptx::mma_commit_e(&empty[s]);
+          if (j + 1 < nkv) {
+            if (m == 0) {
+              wait(&k_full[(j + 1) % NS], ((j + 1) / NS) & 1);
+              ptx::tc_fence_after();
+            }
+            issue_s(m, j + 1);
+          }
+        }
+      }
+      ptx::mma_commit_e(o_full);
+    }
+  } else {
+    // --------------------------- softmax of map m: thread r owns query row r
+    const int m = warp >> 2;
+    const int r = threadIdx.x & 127;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + L::cS + m * BN + lane_off, tO = tmem + L::cO + lane_off;
+    const int64_t row = static_cast<int64_t>(rb) * BM + r;
+    const int lo_row = (WIN && causal) ? bd.row_lo(bh, row) : 0;
+    const float slack = kSlack / c;
+    const uint64_t c2 = tc::pk2f(c, c);
+    float mref = -INFINITY, l = 0.f;
+    for (int j = 0; j < nkv; ++j) {
+      const int kb = j0 + j;
+      const bool diag = causal ? kb == rb : (j == nkv - 1 && (N % BN) != 0);
+      const bool low = WIN && causal && kb * BN < lo_last;
+      const int klim = causal ? (WIN ? rb * BM + r - kb * BN : r) : N - 1 - kb * BN;  // last visible key
+      const int klo = (WIN && causal) ? lo_row - kb * BN : 0;                         // first one
+      wait(&s_full[m], j & 1);
+      ptx::tc_fence_after();
+      uint32_t v[4][32];
+#pragma unroll
+      for (int ch = 0; ch < 4; ++ch) ptx::tmem_ld32(tS + ch * 32, v[ch]);
+      ptx::tmem_wait_ld();
+      if (diag || low) {
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch)
+#pragma unroll
+          for (int t = 0; t < 32; ++t)
+            if (ch * 32 + t > klim || ch * 32 + t < klo) v[ch][t] = __float_as_uint(-INFINITY);
+      }
+      float mx[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) mx[u] = -INFINITY;
+#pragma unroll
+      for (int ch = 0; ch < 4; ++ch)
+#pragma unroll
+        for (int t = 0; t < 32; t += 16)
+#pragma unroll
+          for (int u = 0; u < 8; ++u) mx[u] = fmaxf(mx[u], fmaxf(tc::f(v[ch][t + u]), tc::f(v[ch][t + 8 + u])));
+#pragma unroll
+      for (int u = 1; u < 8; ++u) mx[0] = fmaxf(mx[0], mx[u]);
+      const bool moved = mx[0] > mref + slack;  // always at the first visible key (mref = -inf)
+      const float mnew = moved ? mx[0] : mref;
+      const float alpha = moved ? ptx::ex2((mref - mnew) * c) : 1.f;
+      if (j > 0 && __any_sync(0xffffffffu, moved)) {
+        const uint64_t a2 = tc::pk2f(alpha, alpha);
+#pragma unroll 1
+        for (int c0 = 0; c0 < DV; c0 += 16) {  // 16 columns at a time: the scores hold 128 registers
+          uint32_t o[16];
+          ptx::tmem_ld16(tO + m * DV + c0, o);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int t = 0; t < 16; t += 2) {
+            const float2 x = tc::unpk2(tc::mul2(tc::pk2(o[t], o[t + 1]), a2));
+            o[t] = __float_as_uint(x.x);
+            o[t + 1] = __float_as_uint(x.y);
+          }
+          ptx::tmem_st16(tO + m * DV + c0, o);
+        }
+      }
+      l *= alpha;
+      mref = mnew;
+      // a row that has seen no key yet subtracts 0, not -inf: every term is 2^-inf = 0
+      const float nm = mref == -INFINITY ? 0.f : -mref * c;
+      const uint64_t nm2 = tc::pk2f(nm, nm);
+      uint64_t rs[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int ch = 0; ch < 4; ++ch) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int t = 0; t < 32; t += 2) {
+          const float2 arg = tc::unpk2(tc::fma2(tc::pk2(v[ch][t], v[ch][t + 1]), c2, nm2));
+          const float p0 = ptx::ex2(arg.x), p1 = ptx::ex2(arg.y);
+          rs[(t >> 1) & 3] = tc::add2(rs[(t >> 1) & 3], tc::pk2f(p0, p1));
+          pk[t >> 1] = ptx::pack_bf16(p0, p1);
+        }
+        ptx::tmem_st16(tS + ch * 16, pk);
+      }
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(&p_ready[m]);
+      const float2 x = tc::unpk2(tc::add2(tc::add2(rs[0], rs[1]), tc::add2(rs[2], rs[3])));
+      l += x.x + x.y;
+    }
+    // ------------------------------------------------------------------ epilogue
+    const float inv = 1.f / l;
+    if (m == 1) sInv[r] = inv;
+    if (row < N) lse[(2 * static_cast<int64_t>(bh) + m) * N + row] = mref * scale + logf(l);
+    wait(o_full, 0);
+    tc::named_sync(1, 256);
+    ptx::tc_fence_after();
+    __nv_bfloat16* out = m == 0 ? O : O2;
+    if (out != nullptr) {
+      const float w = m == 0 ? -lam[bh % H] * sInv[r] : inv;  // of O_2's columns
+#pragma unroll
+      for (int ch = 0; ch < DV / 32; ++ch) {
+        uint32_t a[32], b[32];
+        ptx::tmem_ld32(tO + DV + ch * 32, b);
+        if (m == 0) ptx::tmem_ld32(tO + ch * 32, a);
+        ptx::tmem_wait_ld();
+        if (row < N) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int t = 0; t < 32; t += 2) {
+            float x0 = tc::f(b[t]) * w, x1 = tc::f(b[t + 1]) * w;
+            if (m == 0) x0 = fmaf(tc::f(a[t]), inv, x0), x1 = fmaf(tc::f(a[t + 1]), inv, x1);
+            pk[t >> 1] = ptx::pack_bf16(x0, x1);
+          }
+          uint4* dst = reinterpret_cast<uint4*>(out + (static_cast<int64_t>(bh) * N + row) * DV + ch * 32);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) dst[u] = make_uint4(pk[u * 4], pk[u * 4 + 1], pk[u * 4 + 2], pk[u * 4 + 3]);
+        }
+      }
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t launch(const Problem& p, const void* Q, const void* K, const void* V, const float* lam, void* O, void* O2,
+                   float* lse, cudaStream_t st) {
+  alignas(64) CUtensorMap mq, mk, mv;
+  if (!make_tmap_bf16(&mq, Q, p.N, D, 2 * p.BH, BM) || !make_tmap_bf16(&mk, K, p.N, D, 2 * p.BHkv, BN) ||
+      !make_tmap_bf16(&mv, V, p.N, 2 * D, p.BHkv, BN))
+    return cudaErrorInvalidValue;
+  const int nrb = static_cast<int>((p.N + BM - 1) / BM);
+  auto kern = banded(p) ? fwd_kernel<D, true> : fwd_kernel<D, false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::bytes);
+  if (e != cudaSuccess) return e;
+  kern<<<static_cast<unsigned>(nrb * p.BH), kThreads, Lay<D>::bytes, st>>>(
+      mq, mk, mv, lam, static_cast<__nv_bfloat16*>(O), static_cast<__nv_bfloat16*>(O2), lse, static_cast<int>(p.N),
+      static_cast<int>(p.H), nrb, static_cast<int>(p.BH), p.scale, p.scale * kLog2e, p.causal,
+      make_band(p, eff_window_tc(p), false), p.group);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t tc_diff_fwd(const Problem& p, const void* Q, const void* K, const void* V, const float* lam, void* O,
+                        void* O2, float* lse, cudaStream_t st) {
+  return p.d == 32 ? launch<32>(p, Q, K, V, lam, O, O2, lse, st) : launch<64>(p, Q, K, V, lam, O, O2, lse, st);
+}
+
+uint32_t tc_diff_fwd_take_error() {
+  uint32_t v = 0, z = 0;
+  if (cudaMemcpyFromSymbol(&v, g_err, sizeof(v)) != cudaSuccess) return 0;
+  if (v) cudaMemcpyToSymbol(g_err, &z, sizeof(z));
+  return v;
+}
+
+}  // namespace fbd
