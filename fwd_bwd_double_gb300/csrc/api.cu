@@ -316,7 +316,8 @@ attn_status_t attn_device_status(void* stream) {
   if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "CUDA: %s", cudaGetErrorString(e));
   const uint32_t flags = fbd::tc_fwd_take_error() | fbd::tc_bwd_take_error() | fbd::tc_bwd_wide_take_error() | fbd::tc_bwd_fused_take_error() |
                          fbd::tc_bob_take_error() | fbd::tc_bob128_take_error() | fbd::tc32_take_error() |
-                         fbd::selftest_take_error() | fbd::tc_diff_fwd_take_error();
+                         fbd::selftest_take_error() | fbd::tc_diff_fwd_take_error() |
+                         fbd::tc_diff_bwd_take_error();
   if (flags != 0) return fail(ATTN_ERR_TIMEOUT, "a device-side bounded wait gave up%s");
   return ATTN_OK;
 }

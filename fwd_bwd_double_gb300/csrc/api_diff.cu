@@ -86,7 +86,8 @@ attn_status_t attn_diff_fwd(const attn_desc_t* desc, const void* Q, const void* 
 
 size_t attn_diff_bwd_workspace_bytes(const attn_desc_t* desc) {
   if (desc == nullptr || desc->B < 0 || desc->H < 0 || desc->N < 0) return 0;
-  return simt_diff_bwd_bytes(desc->B * desc->H, desc->N);
+  return desc->dtype == ATTN_BF16 ? tc_diff_bwd_bytes(desc->B * desc->H, desc->N)
+                                  : simt_diff_bwd_bytes(desc->B * desc->H, desc->N);
 }
 
 attn_status_t attn_diff_bwd(const attn_desc_t* desc, const void* Q, const void* K, const void* V, const float* lam,
@@ -113,7 +114,9 @@ attn_status_t attn_diff_bwd(const attn_desc_t* desc, const void* Q, const void* 
   if ((s = check_apart(la, out, 4)) != ATTN_OK || (s = check_apart(dl, out, 4)) != ATTN_OK ||
       (s = check_apart(dl, in.s, in.n)) != ATTN_OK || (s = check_apart(dl, &la, 1)) != ATTN_OK)
     return s;
-  return launch_status(simt_diff_bwd(p, Q, K, V, lam, O, O2, dO, lse, dQ, dK, dV, dlam, workspace, st));
+  return launch_status(p.dtype == ATTN_BF16
+                           ? tc_diff_bwd(p, Q, K, V, lam, O, O2, dO, lse, dQ, dK, dV, dlam, workspace, st)
+                           : simt_diff_bwd(p, Q, K, V, lam, O, O2, dO, lse, dQ, dK, dV, dlam, workspace, st));
 }
 
 size_t attn_diff_decode_workspace_bytes(const attn_desc_t* desc) {

@@ -16,12 +16,17 @@ namespace fbd {
 // The widths with kernels.
 inline bool diff_supports(int64_t d) { return d == 32 || d == 64; }
 
-// bf16 tensor-core kernels (tc_diff_fwd.cu).
+// bf16 tensor-core kernels (tc_diff_fwd.cu, tc_diff_bwd.cu).
 cudaError_t tc_diff_fwd(const Problem& p, const void* Q, const void* K, const void* V, const float* lam, void* O,
                         void* O2, float* lse, cudaStream_t st);
 uint32_t tc_diff_fwd_take_error();
+cudaError_t tc_diff_bwd(const Problem& p, const void* Q, const void* K, const void* V, const float* lam, const void* O,
+                        const void* O2, const void* dO, const float* lse, void* dQ, void* dK, void* dV, float* dlam,
+                        void* ws, cudaStream_t st);
+size_t tc_diff_bwd_bytes(int64_t BH, int64_t N);
+uint32_t tc_diff_bwd_take_error();
 
-// CUDA-core kernels (simt_diff.cu).
+// CUDA-core kernels for float32 (simt_diff.cu).
 cudaError_t simt_diff_fwd(const Problem& p, const void* Q, const void* K, const void* V, const float* lam, void* O,
                           void* O2, float* lse, cudaStream_t st);
 cudaError_t simt_diff_bwd(const Problem& p, const void* Q, const void* K, const void* V, const float* lam,

@@ -1,4 +1,4 @@
-// Differential attention forward and backward on CUDA cores in fp32.
+// Differential attention forward and backward on CUDA cores in fp32 (float32 inputs).
 //
 //   A_m = softmax(s Q_m K_m^T + mask), O = (A_1 - lam A_2) V,
 // one block of 64 query rows per CTA, both maps' running maxima and sums kept per row
@@ -14,8 +14,6 @@
 // Each of the 256 threads owns 4 held rows: 4 x 2 elements of a score tile, and
 // 4 x (width / 16) columns of an accumulator, so that a k-step of four does 32 to 64
 // multiply-adds on 6 to 8 16-byte shared-memory reads.
-#include <cuda_bf16.h>
-
 #include "diff.h"
 #include "ptx.cuh"
 #include "tc_common.cuh"
@@ -38,13 +36,9 @@ __device__ __forceinline__ void load4(const float* p, float (&x)[4]) {
   const float4 v = *reinterpret_cast<const float4*>(p);
   x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
 }
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&x)[4]) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
-  x[0] = tc::bf16_lo(v.x), x[1] = tc::bf16_hi(v.x), x[2] = tc::bf16_lo(v.y), x[3] = tc::bf16_hi(v.y);
-}
 // Rows [r0, r0 + R) of a [N, D] slice into shared memory as floats; rows past N are zero.
-template <int D, int R, typename T>
-__device__ __forceinline__ void load_tile(float* dst, const T* src, int64_t r0, int64_t N) {
+template <int D, int R>
+__device__ __forceinline__ void load_tile(float* dst, const float* src, int64_t r0, int64_t N) {
   constexpr int C = D / 4;
   for (int u = threadIdx.x; u < R * C; u += kT) {
     const int r = u / C, c = (u % C) * 4;
@@ -103,12 +97,6 @@ __device__ __forceinline__ void accumulate(const float* T, const float* B, int t
   }
 }
 template <int W>
-__device__ __forceinline__ void store_row(__nv_bfloat16* dst, const float (&x)[W], float f) {
-#pragma unroll
-  for (int c = 0; c < W; c += 2)
-    *reinterpret_cast<uint32_t*>(dst + c) = ptx::pack_bf16(x[c] * f, x[c + 1] * f);
-}
-template <int W>
 __device__ __forceinline__ void store_row(float* dst, const float (&x)[W], float f) {
   if constexpr (W == 2) {
     *reinterpret_cast<float2*>(dst) = make_float2(x[0] * f, x[1] * f);
@@ -124,10 +112,10 @@ constexpr size_t fwd_smem() {
   return sizeof(float) * (2 * BQ * Pitch<D>::v + 2 * BK * Pitch<D>::v + BK * Pitch<2 * D>::v + 2 * BQ * PP);
 }
 
-template <int D, typename T>
+template <int D>
 __global__ void __launch_bounds__(kT, 2)
-    fwd_kernel(const T* __restrict__ Q, const T* __restrict__ K, const T* __restrict__ V,
-               const float* __restrict__ lam, T* __restrict__ O, T* __restrict__ O2, float* __restrict__ lse,
+    fwd_kernel(const float* __restrict__ Q, const float* __restrict__ K, const float* __restrict__ V,
+               const float* __restrict__ lam, float* __restrict__ O, float* __restrict__ O2, float* __restrict__ lse,
                int64_t N, int64_t H, int nqb, int BH, int G, float scale, int causal, Band bd) {
   constexpr int DV = 2 * D, WV = DV / 16;
   extern __shared__ __align__(16) float sh[];
@@ -222,9 +210,9 @@ __global__ void __launch_bounds__(kT, 2)
 
 // Row statistics of the backward: (L_1, L_2, D_1, D_2), D_2 = dO.O_2, D_1 = dO.O + lam D_2;
 // D = +inf marks a row with one visible key (its dS is 0).  16 threads per row.
-template <int DV, typename T>
+template <int DV>
 __global__ void __launch_bounds__(256)
-    prep_kernel(const T* __restrict__ O, const T* __restrict__ O2, const T* __restrict__ dO,
+    prep_kernel(const float* __restrict__ O, const float* __restrict__ O2, const float* __restrict__ dO,
                 const float* __restrict__ lse, const float* __restrict__ lam, float4* __restrict__ stats, int64_t N,
                 int64_t H, int64_t BH, int causal, Band bd) {
   const int64_t gid = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
@@ -264,11 +252,11 @@ constexpr size_t bwd_smem() {
 // COL = false: holds queries (Q_m, dO), streams keys (K_m, V), writes dQ_m and the block's
 // share of dlam.  COL = true: holds keys, streams the queries of the G query heads that
 // share them, writes dK_m, dV.
-template <int D, bool COL, typename T>
+template <int D, bool COL>
 __global__ void __launch_bounds__(kT, 1)
-    bwd_kernel(const T* __restrict__ Q, const T* __restrict__ K, const T* __restrict__ V, const T* __restrict__ dO,
-               const float* __restrict__ lam, const float4* __restrict__ stats, T* __restrict__ out1,
-               T* __restrict__ outV, float* __restrict__ partial, int64_t N, int64_t H, int nblk, int slices, int G,
+    bwd_kernel(const float* __restrict__ Q, const float* __restrict__ K, const float* __restrict__ V, const float* __restrict__ dO,
+               const float* __restrict__ lam, const float4* __restrict__ stats, float* __restrict__ out1,
+               float* __restrict__ outV, float* __restrict__ partial, int64_t N, int64_t H, int nblk, int slices, int G,
                float scale, int causal, Band bd) {
   constexpr int DV = 2 * D, W = D / 16, WV = DV / 16, PD = Pitch<D>::v;
   extern __shared__ __align__(16) float sh[];
@@ -287,8 +275,8 @@ __global__ void __launch_bounds__(kT, 1)
   const int64_t kvh = COL ? sl : sl / G;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const float c = scale * kLog2e;
-  const T* heldM = COL ? K : Q;
-  const T* heldV = COL ? V : dO;
+  const float* heldM = COL ? K : Q;
+  const float* heldV = COL ? V : dO;
 #pragma unroll
   for (int m = 0; m < 2; ++m) load_tile<D, BQ>(sA + m * BQ * PD, heldM + (2 * sl + m) * N * D, a0, N);
   load_tile<DV, BQ>(sAV, heldV + sl * N * DV, a0, N);
@@ -324,8 +312,8 @@ __global__ void __launch_bounds__(kT, 1)
   for (int g = 0; g < (COL ? G : 1); ++g) {
     const int64_t qs = COL ? kvh * G + g : sl;  // query slice
     const float lm = lam[qs % H];
-    const T* strM = COL ? Q + 2 * qs * N * D : K + 2 * kvh * N * D;
-    const T* strV = COL ? dO + qs * N * DV : V + kvh * N * DV;
+    const float* strM = COL ? Q + 2 * qs * N * D : K + 2 * kvh * N * D;
+    const float* strV = COL ? dO + qs * N * DV : V + kvh * N * DV;
     for (int64_t k0 = b0; k0 < b1; k0 += BK) {
       __syncthreads();
 #pragma unroll
@@ -410,41 +398,41 @@ cudaError_t set_smem(F kern, size_t bytes) {
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
 }
 
-template <int D, typename T>
+template <int D>
 cudaError_t fwd(const Problem& p, const void* Q, const void* K, const void* V, const float* lam, void* O, void* O2,
                 float* lse, cudaStream_t st) {
   const int nqb = static_cast<int>((p.N + BQ - 1) / BQ);
-  cudaError_t e = set_smem(fwd_kernel<D, T>, fwd_smem<D>());
+  cudaError_t e = set_smem(fwd_kernel<D>, fwd_smem<D>());
   if (e != cudaSuccess) return e;
-  fwd_kernel<D, T><<<static_cast<unsigned>(nqb * p.BH), kT, fwd_smem<D>(), st>>>(
-      static_cast<const T*>(Q), static_cast<const T*>(K), static_cast<const T*>(V), lam, static_cast<T*>(O),
-      static_cast<T*>(O2), lse, p.N, p.H, nqb, static_cast<int>(p.BH), p.group, p.scale, p.causal,
+  fwd_kernel<D><<<static_cast<unsigned>(nqb * p.BH), kT, fwd_smem<D>(), st>>>(
+      static_cast<const float*>(Q), static_cast<const float*>(K), static_cast<const float*>(V), lam, static_cast<float*>(O),
+      static_cast<float*>(O2), lse, p.N, p.H, nqb, static_cast<int>(p.BH), p.group, p.scale, p.causal,
       make_band(p, eff_window(p), false));
   return cudaGetLastError();
 }
 
-template <int D, typename T>
+template <int D>
 cudaError_t bwd(const Problem& p, const void* Q_, const void* K_, const void* V_, const float* lam, const void* O,
                 const void* O2, const void* dO_, const float* lse, void* dQ, void* dK, void* dV, float* dlam,
                 float4* stats, cudaStream_t st) {
-  const T *Q = static_cast<const T*>(Q_), *K = static_cast<const T*>(K_), *V = static_cast<const T*>(V_);
-  const T* dO = static_cast<const T*>(dO_);
+  const float *Q = static_cast<const float*>(Q_), *K = static_cast<const float*>(K_), *V = static_cast<const float*>(V_);
+  const float* dO = static_cast<const float*>(dO_);
   const int nblk = static_cast<int>((p.N + BQ - 1) / BQ);
   float* partial = reinterpret_cast<float*>(stats + p.BH * p.N);
   const int64_t threads = p.BH * p.N * 16;
-  prep_kernel<2 * D, T><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, st>>>(
-      static_cast<const T*>(O), static_cast<const T*>(O2), dO, lse, lam, stats, p.N, p.H, p.BH, p.causal,
+  prep_kernel<2 * D><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, st>>>(
+      static_cast<const float*>(O), static_cast<const float*>(O2), dO, lse, lam, stats, p.N, p.H, p.BH, p.causal,
       make_band(p, eff_window(p), false));
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if ((e = set_smem(bwd_kernel<D, false, T>, bwd_smem<D>())) != cudaSuccess) return e;
-  if ((e = set_smem(bwd_kernel<D, true, T>, bwd_smem<D>())) != cudaSuccess) return e;
-  bwd_kernel<D, false, T><<<static_cast<unsigned>(nblk * p.BH), kT, bwd_smem<D>(), st>>>(
-      Q, K, V, dO, lam, stats, static_cast<T*>(dQ), nullptr, partial, p.N, p.H, nblk, static_cast<int>(p.BH), p.group,
+  if ((e = set_smem(bwd_kernel<D, false>, bwd_smem<D>())) != cudaSuccess) return e;
+  if ((e = set_smem(bwd_kernel<D, true>, bwd_smem<D>())) != cudaSuccess) return e;
+  bwd_kernel<D, false><<<static_cast<unsigned>(nblk * p.BH), kT, bwd_smem<D>(), st>>>(
+      Q, K, V, dO, lam, stats, static_cast<float*>(dQ), nullptr, partial, p.N, p.H, nblk, static_cast<int>(p.BH), p.group,
       p.scale, p.causal, make_band(p, eff_window(p), false));
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  bwd_kernel<D, true, T><<<static_cast<unsigned>(nblk * p.BHkv), kT, bwd_smem<D>(), st>>>(
-      Q, K, V, dO, lam, stats, static_cast<T*>(dK), static_cast<T*>(dV), nullptr, p.N, p.H, nblk,
+  bwd_kernel<D, true><<<static_cast<unsigned>(nblk * p.BHkv), kT, bwd_smem<D>(), st>>>(
+      Q, K, V, dO, lam, stats, static_cast<float*>(dK), static_cast<float*>(dV), nullptr, p.N, p.H, nblk,
       static_cast<int>(p.BHkv), p.group, p.scale, p.causal, make_band(p, eff_window(p), true));
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return diff_reduce_dlam(partial, dlam, p.B, p.H, nblk, st);
@@ -463,19 +451,16 @@ size_t simt_diff_bwd_bytes(int64_t BH, int64_t N) {
 
 cudaError_t simt_diff_fwd(const Problem& p, const void* Q, const void* K, const void* V, const float* lam, void* O,
                           void* O2, float* lse, cudaStream_t st) {
-  return p.d == 32 ? fwd<32, float>(p, Q, K, V, lam, O, O2, lse, st)
-                   : fwd<64, float>(p, Q, K, V, lam, O, O2, lse, st);
+  return p.d == 32 ? fwd<32>(p, Q, K, V, lam, O, O2, lse, st)
+                   : fwd<64>(p, Q, K, V, lam, O, O2, lse, st);
 }
 
 cudaError_t simt_diff_bwd(const Problem& p, const void* Q, const void* K, const void* V, const float* lam,
                           const void* O, const void* O2, const void* dO, const float* lse, void* dQ, void* dK,
                           void* dV, float* dlam, void* ws, cudaStream_t st) {
   float4* s = static_cast<float4*>(ws);
-  if (p.dtype == ATTN_BF16)
-    return p.d == 32 ? bwd<32, __nv_bfloat16>(p, Q, K, V, lam, O, O2, dO, lse, dQ, dK, dV, dlam, s, st)
-                     : bwd<64, __nv_bfloat16>(p, Q, K, V, lam, O, O2, dO, lse, dQ, dK, dV, dlam, s, st);
-  return p.d == 32 ? bwd<32, float>(p, Q, K, V, lam, O, O2, dO, lse, dQ, dK, dV, dlam, s, st)
-                   : bwd<64, float>(p, Q, K, V, lam, O, O2, dO, lse, dQ, dK, dV, dlam, s, st);
+  return p.d == 32 ? bwd<32>(p, Q, K, V, lam, O, O2, dO, lse, dQ, dK, dV, dlam, s, st)
+                   : bwd<64>(p, Q, K, V, lam, O, O2, dO, lse, dQ, dK, dV, dlam, s, st);
 }
 
 }  // namespace fbd
