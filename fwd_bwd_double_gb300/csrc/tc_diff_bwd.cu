@@ -535,7 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the diagonal block, a block past the first key's last query, past N, or with keys past N
       const bool masked = (causal && i == kb) || (WIN && causal && i * BW + BW - 1 > hi_first) ||
                           i * BW + c0 + kC > N || (!causal && kb * BW + BW > N);
-      auto probs = [&](int m, uint32_t (&v)[2][16]) {
+      auto probs = [&](auto mk, int m, uint32_t (&v)[2][16]) {
+        constexpr bool masked = decltype(mk)::value;
         wait(&s_full[m], t & 1);
         ptx::tc_fence_after();
 #pragma unroll
@@ -554,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int e = 4 * k + 2 * u;
               const float2 a = tc::unpk2(tc::fma2(tc::pk2(v[x][e], v[x][e + 1]), c2, nL));
               float p0 = ptx::ex2(a.x), p1 = ptx::ex2(a.y);
-              if (masked) {
+              if constexpr (masked) {
                 const int q0 = qbase + 8 * k, kk = kbase + 16 * x + 8 * u;
                 if ((causal ? (q0 < kk || (WIN && q0 > khi[x][u])) : kk >= N) || q0 >= N) p0 = 0.f;
                 if ((causal ? (q0 + 1 < kk || (WIN && q0 + 1 > khi[x][u])) : kk >= N) || q0 + 1 >= N) p1 = 0.f;
@@ -564,51 +565,58 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
       };
-      uint32_t p1[2][16], p2[2][16];
-      probs(0, p1);
-      probs(1, p2);
-      wait(dp_full, t & 1);
-      ptx::tc_fence_after();
-      if (t > 0) wait(out_done, (t - 1) & 1);  // dS_2's tile has been read
+      auto block = [&](auto mk) {
+        constexpr bool masked = decltype(mk)::value;
+        uint32_t p1[2][16], p2[2][16];
+        probs(mk, 0, p1);
+        probs(mk, 1, p2);
+        wait(dp_full, t & 1);
+        ptx::tc_fence_after();
+        if (t > 0) wait(out_done, (t - 1) & 1);  // dS_2's tile has been read
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const uint32_t la = lo + (static_cast<uint32_t>(16 * x) << 16);
-        uint32_t g[16], pw[8], d1[8], d2[8];
-        ptx::tmem_ld16x256_x4(tmem + cX + c0 + la, g);
-        ptx::tmem_wait_ld();
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t la = lo + (static_cast<uint32_t>(16 * x) << 16);
+          uint32_t g[16], pw[8], d1[8], d2[8];
+          ptx::tmem_ld16x256_x4(tmem + cX + c0 + la, g);
+          ptx::tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint64_t nD1 = pair(st.z, k), nD2 = pair(st.w, k);
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t nD1 = pair(st.z, k), nD2 = pair(st.w, k);
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int e = 4 * k + 2 * u;
-            const uint64_t dp = tc::pk2(g[e], g[e + 1]);
-            const uint64_t P1 = tc::pk2(p1[x][e], p1[x][e + 1]);
-            const uint64_t P2 = tc::mul2(tc::pk2(p2[x][e], p2[x][e + 1]), w2);
-            const float2 w = tc::unpk2(tc::add2(P1, P2));
-            float2 a = tc::unpk2(tc::mul2(P1, tc::add2(dp, nD1)));
-            float2 b = tc::unpk2(tc::mul2(P2, tc::add2(dp, nD2)));
-            if (masked) {  // rows with one visible key
-              const float2 d = tc::unpk2(nD1);
-              if (d.x == -INFINITY) a.x = b.x = 0.f;
-              if (d.y == -INFINITY) a.y = b.y = 0.f;
+            for (int u = 0; u < 2; ++u) {
+              const int e = 4 * k + 2 * u;
+              const uint64_t dp = tc::pk2(g[e], g[e + 1]);
+              const uint64_t P1 = tc::pk2(p1[x][e], p1[x][e + 1]);
+              const uint64_t P2 = tc::mul2(tc::pk2(p2[x][e], p2[x][e + 1]), w2);
+              const float2 w = tc::unpk2(tc::add2(P1, P2));
+              float2 a = tc::unpk2(tc::mul2(P1, tc::add2(dp, nD1)));
+              float2 b = tc::unpk2(tc::mul2(P2, tc::add2(dp, nD2)));
+              if constexpr (masked) {  // rows with one visible key
+                const float2 d = tc::unpk2(nD1);
+                if (d.x == -INFINITY) a.x = b.x = 0.f;
+                if (d.y == -INFINITY) a.y = b.y = 0.f;
+              }
+              pw[2 * k + u] = ptx::pack_bf16(w.x, w.y);
+              d1[2 * k + u] = ptx::pack_bf16(a.x, a.y);
+              d2[2 * k + u] = ptx::pack_bf16(b.x, b.y);
             }
-            pw[2 * k + u] = ptx::pack_bf16(w.x, w.y);
-            d1[2 * k + u] = ptx::pack_bf16(a.x, a.y);
-            d2[2 * k + u] = ptx::pack_bf16(b.x, b.y);
           }
-        }
-        ptx::tmem_st16x128_x4(tmem + cX + c0 + la, pw);
-        ptx::tmem_st16x128_x4(tmem + cX + c0 + 16 + la, d1);
-        // dS_2 (key rows, 128-byte lines of queries): the values are the fragments of 8x8
-        // matrices, so one stmatrix writes the four chunks of 8 queries of a (x, u)
-        const int qcol = c0 + 8 * (lane >> 3);
-        const uint32_t cb = ptx::smem_u32(sm + L::oT) + static_cast<uint32_t>((qcol >> 6) * kSlab);
+          ptx::tmem_st16x128_x4(tmem + cX + c0 + la, pw);
+          ptx::tmem_st16x128_x4(tmem + cX + c0 + 16 + la, d1);
+          // dS_2 (key rows, 128-byte lines of queries): the values are the fragments of 8x8
+          // matrices, so one stmatrix writes the four chunks of 8 queries of a (x, u)
+          const int qcol = c0 + 8 * (lane >> 3);
+          const uint32_t cb = ptx::smem_u32(sm + L::oT) + static_cast<uint32_t>((qcol >> 6) * kSlab);
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-          ptx::stmatrix_x4(cb + sw128(qd * 32 + 16 * x + 8 * u + (lane & 7), (qcol & 63) >> 3), d2[u], d2[2 + u],
-                           d2[4 + u], d2[6 + u]);
-      }
+          for (int u = 0; u < 2; ++u)
+            ptx::stmatrix_x4(cb + sw128(qd * 32 + 16 * x + 8 * u + (lane & 7), (qcol & 63) >> 3), d2[u], d2[2 + u],
+                             d2[4 + u], d2[6 + u]);
+        }
+      };
+      if (masked)
+        block(std::true_type{});
+      else
+        block(std::false_type{});
       ptx::fence_proxy_async_smem();
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
