@@ -37,15 +37,23 @@ __device__ unsigned int g_err = 0;
 constexpr int BW = 128;          // held and streamed rows
 constexpr int NS = 2;            // stages of streamed blocks
 constexpr int kCW = 16;          // compute warps
-constexpr int kCompute = kCW * 32;
-constexpr int kThreads = kCompute + 64;
 constexpr int kC = 32;           // tile columns per compute warp
+// Column pass: 640 threads launched with 96 registers; the compute warps take 104 (each
+// thread's two maps of P alone are 64), the fifth warpgroup's warps keep 64:
+// 512 * 104 + 128 * 64 = 640 * 96.
+constexpr int kColThreads = kCW * 32 + 128;
+constexpr int kColRegs = 104, kColRegsOther = 64;
+constexpr int kPlanes = 5;       // row statistics: -L_1 log2 e, -L_2 log2 e, -D_1, lam D_2, -D_2
 constexpr int kSlab = BW * 128;  // 64 bf16 columns of 128 rows: 16 KB
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Byte offset of (row, 16-byte chunk) in a 128-byte-swizzled tile of 128-byte lines.
 __device__ __forceinline__ uint32_t sw128(int row, int chunk) {
   return static_cast<uint32_t>(row * 128 + ((chunk ^ (row & 7)) << 4));
+}
+
+__device__ __forceinline__ void st_shared4(uint32_t a, const uint32_t* v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
 }
 
 // Shared memory of both passes: the held block (two maps' 64-column tiles, d = 32 zero-filled
@@ -56,7 +64,8 @@ struct Lay {
   static constexpr int kBlock = 2 * kSlab + kV;
   static constexpr int oT = kBlock;
   static constexpr int oStage = oT + (COL ? 2 * kSlab : 0);
-  static constexpr int oBar = oStage + NS * kBlock;
+  static constexpr int oStat = oStage + NS * kBlock;  // column pass: the streamed queries' statistics
+  static constexpr int oBar = oStat + (COL ? 4 * BW * 4 : 0);
   static constexpr int bytes = oBar + 256;
 };
 static_assert(Lay<128, true>::bytes <= 232448, "shared memory");
@@ -70,10 +79,10 @@ __device__ __forceinline__ void init_abort(uint8_t* sm, volatile int* abort_flag
 // TMEM columns: S (S_1, then S_2), dP, dS_1, dS_2 (bf16 pairs), dQ_1, dQ_2.
 // WIN: a banded causal mask is in force (window and/or document bounds).
 template <int DV, bool WIN>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__((kCW + 2) * 32, 1)
     row_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
                const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-               const float* __restrict__ lam, const float4* __restrict__ stats, __nv_bfloat16* __restrict__ dQ,
+               const float* __restrict__ lam, const float* __restrict__ stats, __nv_bfloat16* __restrict__ dQ,
                float* __restrict__ partial, int N, int H, int nrb, int BH, float scale, float c, int causal, Band bd,
                int G) {
   using L = Lay<DV, false>;
@@ -113,12 +122,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int m = 0; m < 2; ++m) {
       ptx::mbar_init(&s_full[m], 1);
-      ptx::mbar_init(&s_cons[m], kCompute);
-      ptx::mbar_init(&ds_ready[m], kCompute);
+      ptx::mbar_init(&s_cons[m], kCW * 32);
+      ptx::mbar_init(&ds_ready[m], kCW * 32);
       ptx::mbar_init(&dq_done[m], 1);
     }
     ptx::mbar_init(dp_full, 1);
-    ptx::mbar_init(dp_cons, kCompute);
+    ptx::mbar_init(dp_cons, kCW * 32);
     init_abort(sm, abort_flag);
     ptx::fence_mbar_init();
   }
@@ -222,43 +231,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------- compute: a query row, 32 keys of a block
-    const int qd = warp & 3, cg = warp >> 2;
+    const int qd = warp & 3, cg = warp >> 2, c0 = cg * kC;
     const uint32_t lo = static_cast<uint32_t>(qd * 32) << 16;
-    const int r = qd * 32 + lane;
-    const int row = rb * BW + r;
+    const int row = rb * BW + qd * 32 + lane;
     const int lo_row = (WIN && causal) ? bd.row_lo(bh, row) : 0;
-    // (-L_1 log2 e, -L_2 log2 e, -D_1, -D_2); D = +inf: the row sees one key, its dS is 0
-    const float4 st = row < N ? stats[static_cast<int64_t>(bh) * N + row] : make_float4(0.f, 0.f, 0.f, 0.f);
-    const bool one = st.z == -INFINITY;
-    const float wl = -lam[bh % H];
-    const uint64_t c2 = tc::pk2f(c, c), w2 = tc::pk2f(wl, wl);
+    const float* st = stats + (static_cast<int64_t>(bh) * nrb + rb) * (kPlanes * BW) + qd * 32 + lane;
+    const bool one = st[2 * BW] == -INFINITY;  // the row sees one key: its dS is 0
+    const uint64_t c2 = tc::pk2f(c, c);
+    const uint64_t nL[2] = {tc::pk2f(st[0], st[0]), tc::pk2f(st[BW], st[BW])};
+    const uint64_t nD[2] = {tc::pk2f(st[2 * BW], st[2 * BW]), tc::pk2f(st[4 * BW], st[4 * BW])};
     uint64_t dl2 = 0;
     for (int t = 0; t < nt; ++t) {
       const int kb = j0 + t;
       const bool diag = causal ? kb == rb : (t == nt - 1 && (N % BW) != 0);
       const bool low = WIN && causal && kb * BW < lo_last;
-      const int klim = (causal ? row : N - 1) - kb * BW - cg * kC;  // last visible key, from this warp's first
-      const int klo = (WIN && causal) ? lo_row - kb * BW - cg * kC : 0;
+      const int klim = (causal ? row : N - 1) - kb * BW - c0;  // last visible key, from this warp's first
+      const int klo = (WIN && causal) ? lo_row - kb * BW - c0 : 0;
       uint32_t dp[32];
-      auto map = [&](auto mm) {
-        constexpr int m = decltype(mm)::value;
-        const uint64_t nL = m == 0 ? tc::pk2f(st.x, st.x) : tc::pk2f(st.y, st.y);
-        const uint64_t nD = m == 0 ? tc::pk2f(st.z, st.z) : tc::pk2f(st.w, st.w);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
         uint32_t v[32], pk[16];
         wait(&s_full[m], t & 1);
         ptx::tc_fence_after();
-        ptx::tmem_ld32(tmem + cS + cg * kC + lo, v);
+        ptx::tmem_ld32(tmem + cS + c0 + lo, v);
         ptx::tmem_wait_ld();
         ptx::tc_fence_before();
         ptx::mbar_arrive(&s_cons[m]);
         if (m == 0) {
           wait(dp_full, t & 1);
           ptx::tc_fence_after();
-          ptx::tmem_ld32(tmem + cdP + cg * kC + lo, dp);
+          ptx::tmem_ld32(tmem + cdP + c0 + lo, dp);
         }
 #pragma unroll
         for (int u = 0; u < 32; u += 2) {
-          const float2 a = tc::unpk2(tc::fma2(tc::pk2(v[u], v[u + 1]), c2, nL));
+          const float2 a = tc::unpk2(tc::fma2(tc::pk2(v[u], v[u + 1]), c2, nL[m]));
           v[u] = __float_as_uint(ptx::ex2(a.x));
           v[u + 1] = __float_as_uint(ptx::ex2(a.y));
         }
@@ -274,13 +280,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int u = 0; u < 32; u += 2) {
-          uint64_t P = tc::pk2(v[u], v[u + 1]);
-          const uint64_t g = tc::pk2(dp[u], dp[u + 1]);
-          if (m == 1) {
-            dl2 = tc::fma2(P, g, dl2);
-            P = tc::mul2(P, w2);
-          }
-          const float2 d = tc::unpk2(tc::mul2(P, tc::add2(g, nD)));
+          const uint64_t P = tc::pk2(v[u], v[u + 1]), g = tc::pk2(dp[u], dp[u + 1]);
+          if (m == 1) dl2 = tc::fma2(P, g, dl2);
+          const float2 d = tc::unpk2(tc::mul2(P, tc::add2(g, nD[m])));
           pk[u >> 1] = ptx::pack_bf16(d.x, d.y);
         }
         if ((diag || low) && one) {
@@ -295,9 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         ptx::mbar_arrive(&ds_ready[m]);
-      };
-      map(std::integral_constant<int, 0>{});
-      map(std::integral_constant<int, 1>{});
+      }
     }
     {  // this warp's share of dlam's sum
       const float2 x = tc::unpk2(dl2);
@@ -306,6 +306,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = 1; u < 32; u <<= 1) v += __shfl_xor_sync(0xffffffffu, v, u);
       if (lane == 0) partial[(static_cast<int64_t>(bh) * nrb + rb) * kCW + warp] = v;
     }
+    // dQ_m = s w_m (P_m (dP - D_m)) K_m: the weight -lam of map 2 enters here
+    const float f[2] = {scale, -scale * lam[bh % H]};
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       wait(&dq_done[m], (nt - 1) & 1);
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (row < N && cg * 16 < D) {
         uint32_t o[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) o[u] = ptx::pack_bf16(scale * tc::f(a[2 * u]), scale * tc::f(a[2 * u + 1]));
+        for (int u = 0; u < 8; ++u) o[u] = ptx::pack_bf16(f[m] * tc::f(a[2 * u]), f[m] * tc::f(a[2 * u + 1]));
         uint4* p = reinterpret_cast<uint4*>(dQ + ((2 * static_cast<int64_t>(bh) + m) * N + row) * D + cg * 16);
         p[0] = make_uint4(o[0], o[1], o[2], o[3]);
         p[1] = make_uint4(o[4], o[5], o[6], o[7]);
@@ -334,17 +336,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // --------------------------------------------------------------- column pass
 // TMEM columns: S^T (S_1, then S_2), dP^T, dK_1, dK_2, dV.  W^T and dS_1^T (bf16 pairs) are
-// written over dP^T by the warp that read it: 16 columns each of the warp's 32.  dS_2^T goes
+// written over dP^T by the warp that read it: of 16 queries' columns, W^T takes the first 8.  dS_2^T goes
 // through shared memory, so that S_1 of the next block can be formed while this one's are read.
 // Order of the products: S_1(t+1) while the compute warps finish block t; dV(t), dK_1(t),
 // S_2(t+1), dP(t+1), dK_2(t) once they have, so the chain from one block's operands to the
 // next's is dV, dK_1, S_2, dP and the last steps of the CUDA cores.  (dP(t+1) overwrites the
 // operands of dV(t), dK_1(t): products of one thread run in order.)
 template <int DV, bool WIN>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kColThreads, 1)
     col_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
-               const float* __restrict__ lam, const float4* __restrict__ stats, __nv_bfloat16* __restrict__ dK,
+               const float* __restrict__ lam, const float* __restrict__ stats, __nv_bfloat16* __restrict__ dK,
                __nv_bfloat16* __restrict__ dV, int N, int H, int nb, int BHkv, float scale, float c, int causal,
                Band bd, int G) {
   using L = Lay<DV, true>;
@@ -384,10 +386,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int m = 0; m < 2; ++m) {
       ptx::mbar_init(&s_full[m], 1);
-      ptx::mbar_init(&s_cons[m], kCompute);
+      ptx::mbar_init(&s_cons[m], kCW * 32);
     }
     ptx::mbar_init(dp_full, 1);
-    ptx::mbar_init(ready, kCompute);
+    ptx::mbar_init(ready, kCW * 32);
     ptx::mbar_init(out_done, 1);
     init_abort(sm, abort_flag);
     ptx::fence_mbar_init();
@@ -403,6 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const ptx::BoundedWait wait{abort_flag, &g_err};
   const bool ok = *abort_flag == 0;
 
+  if (warp >= kCW) ptx::setmaxnreg_dec<kColRegsOther>();
   if (warp == kCW) {
     // ------------------------------------------------------------ TMA loads
     if (lane == 0 && ok) {
@@ -433,10 +436,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t idV = ptx::idesc_bf16(BW, DV, 0, 1);
       constexpr uint32_t idK = ptx::idesc_bf16(BW, 64, 0, 1);
       const uint32_t sH = ptx::smem_u32(sm), sS = ptx::smem_u32(sm + L::oStage);
-      const uint64_t dHk = tc::kmajor_desc(sH, BW, 0);   // held block, rows = M
-      const uint64_t dSk = tc::kmajor_desc(sS, BW, 0);   // streamed block, rows = N
-      const uint64_t dSm = tc::mnmajor_desc(sS, BW, 0);  // streamed block, rows = K
-      const uint64_t dTk = tc::kmajor_desc(ptx::smem_u32(sm + L::oT), BW, 0);  // dS_2^T
+      uint64_t dHk = tc::kmajor_desc(sH, BW, 0);   // held block, rows = M
+      uint64_t dSk = tc::kmajor_desc(sS, BW, 0);   // streamed block, rows = N
+      uint64_t dSm = tc::mnmajor_desc(sS, BW, 0);  // streamed block, rows = K
+      uint64_t dTk = tc::kmajor_desc(ptx::smem_u32(sm + L::oT), BW, 0);  // dS_2^T
       auto S = [&](int m, int t) {
         const uint32_t so = static_cast<uint32_t>((t % NS) * L::kBlock + m * kSlab);
 #pragma unroll
@@ -465,6 +468,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = 0; t < nt; ++t) {
         const int s1 = (t + 1) % NS, ph1 = ((t + 1) / NS) & 1;
         const uint32_t so = static_cast<uint32_t>((t % NS) * L::kBlock);
+        // The steps' descriptors are formed in the loop, one add each: hoisted out of it they
+        // would take more registers than this warp keeps.
+        asm volatile("" : "+l"(dHk), "+l"(dSk), "+l"(dSm), "+l"(dTk));
         if (t + 1 < nt) {
           wait(&s_cons[1], t & 1);
           wait(&a_full[s1], ph1);
@@ -475,11 +481,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_after();
 #pragma unroll
         for (int k = 0; k < BW / 16; ++k)
-          ptx::mma_ts_e(tmem + cdV, tmem + cX + (k >> 1) * kC + (k & 1) * 8,
+          ptx::mma_ts_e(tmem + cdV, tmem + cX + k * 16,
                         tc::desc_add(dSm, so + 2 * kSlab + 2048 * k), idV, (t > 0 || k > 0) ? 1u : 0u);
 #pragma unroll
         for (int k = 0; k < BW / 16; ++k)
-          ptx::mma_ts_e(tmem + cdK, tmem + cX + (k >> 1) * kC + 16 + (k & 1) * 8, tc::desc_add(dSm, so + 2048 * k), idK,
+          ptx::mma_ts_e(tmem + cdK, tmem + cX + k * 16 + 8, tc::desc_add(dSm, so + 2048 * k), idK,
                         (t > 0 || k > 0) ? 1u : 0u);
         ptx::mma_commit_e(&a_empty[t % NS]);
         if (t + 1 < nt) {
@@ -497,130 +503,120 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mma_commit_e(out_done);
       }
     }
-  } else {
-    // ------------------------------------------------------------ compute
+  } else if (warp < kCW) {
+    ptx::setmaxnreg_inc<kColRegs>();
+    // ----------------------------------- compute: a key row, 32 queries of a block
     const int qd = warp & 3, cg = warp >> 2;
     const uint32_t lo = static_cast<uint32_t>(qd * 32) << 16;
-    const int key = kb * BW + qd * 32 + lane;  // key row (TMEM lane) of the outputs
+    const int r = qd * 32 + lane, key = kb * BW + r;
     const int c0 = cg * kC;
-    // Tiles through the 16-lane shapes: a thread sees 8 queries of the warp's 32 (pairs
-    // 2(t%4) + 8k, k < 4) for 4 keys (rows t/4 + 8u of each 16-lane half h).
-    const int g4 = lane >> 2, q4 = lane & 3;
     const uint64_t c2 = tc::pk2f(c, c);
-    int khi[2][2] = {{0, 0}, {0, 0}};  // last query each of the four keys is seen by
-    if constexpr (WIN) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) khi[h][u] = bd.key_hi(kvh, kb * BW + qd * 32 + g4 + 16 * h + 8 * u);
-    }
-    // The statistics of the warp's 32 queries, one per lane, loaded a block ahead; a thread
-    // takes those of its own 8 by shuffles.
-    auto load_stats = [&](int t) {
-      const int h = t / ntile, q = (i0 + t - h * ntile) * BW + c0 + lane;
-      return q < N ? stats[(static_cast<int64_t>(kvh) * G + h) * N + q] : make_float4(0.f, 0.f, 0.f, 0.f);
-    };
-    auto pair = [&](float x, int k) {
-      return tc::pk2f(__shfl_sync(0xffffffffu, x, 8 * k + 2 * q4), __shfl_sync(0xffffffffu, x, 8 * k + 2 * q4 + 1));
-    };
-    float4 next = load_stats(0);
-    for (int t = 0; t < nt; ++t) {
-      const int h = t / ntile, i = i0 + t - h * ntile;
-      const float wl = -lam[(kvh * G + h) % H];
+    const int khi = (WIN && causal) ? bd.key_hi(kvh, key) : 0;  // the key's last query
+    const uint32_t sT = ptx::smem_u32(sm + L::oT) + static_cast<uint32_t>((c0 >> 6) * kSlab);
+    float* sSt = reinterpret_cast<float*>(sm + L::oStat);
+    // plane qd of the query block's statistics, this lane's query
+    const float* st = stats + (static_cast<int64_t>(kvh) * G * nb + i0) * (kPlanes * BW) + qd * BW + c0 + lane;
+    float next = *st;
+    int t = 0;
+    for (int h = 0; h < G; ++h) {
+      const int64_t bh = static_cast<int64_t>(kvh) * G + h;
+      const float wl = -lam[bh % H];
       const uint64_t w2 = tc::pk2f(wl, wl);
-      const float4 st = next;
-      if (t + 1 < nt) next = load_stats(t + 1);
-      const int qbase = i * BW + c0 + 2 * q4;    // query of column (k = 0, col 0)
-      const int kbase = kb * BW + qd * 32 + g4;  // key of (h = 0, row 0)
-      // the diagonal block, a block past the first key's last query, past N, or with keys past N
-      const bool masked = (causal && i == kb) || (WIN && causal && i * BW + BW - 1 > hi_first) ||
-                          i * BW + c0 + kC > N || (!causal && kb * BW + BW > N);
-      auto probs = [&](auto mk, int m, uint32_t (&v)[2][16]) {
-        constexpr bool masked = decltype(mk)::value;
-        wait(&s_full[m], t & 1);
-        ptx::tc_fence_after();
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-          ptx::tmem_ld16x256_x4(tmem + cS + c0 + lo + (static_cast<uint32_t>(16 * x) << 16), v[x]);
-        ptx::tmem_wait_ld();
-        ptx::tc_fence_before();
-        ptx::mbar_arrive(&s_cons[m]);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint64_t nL = pair(m == 0 ? st.x : st.y, k);
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int e = 4 * k + 2 * u;
-              const float2 a = tc::unpk2(tc::fma2(tc::pk2(v[x][e], v[x][e + 1]), c2, nL));
-              float p0 = ptx::ex2(a.x), p1 = ptx::ex2(a.y);
-              if constexpr (masked) {
-                const int q0 = qbase + 8 * k, kk = kbase + 16 * x + 8 * u;
-                if ((causal ? (q0 < kk || (WIN && q0 > khi[x][u])) : kk >= N) || q0 >= N) p0 = 0.f;
-                if ((causal ? (q0 + 1 < kk || (WIN && q0 + 1 > khi[x][u])) : kk >= N) || q0 + 1 >= N) p1 = 0.f;
-              }
-              v[x][e] = __float_as_uint(p0);
-              v[x][e + 1] = __float_as_uint(p1);
-            }
+      for (int i = i0; i < i0 + ntile; ++i, ++t) {
+        // The block's statistics go to shared memory, where every lane reads the same ones: each
+        // of the four warps of a column group writes one plane, loaded a block ahead.
+        if (t > 0) tc::named_sync(1 + cg, 128);  // the previous block's have been read
+        sSt[qd * BW + c0 + lane] = next;
+        tc::named_sync(1 + cg, 128);
+        if (t + 1 < nt) {  // the next block, or the next head's first
+          st += (i + 1 < i0 + ntile ? 1 : nb - ntile + 1) * (kPlanes * BW);
+          next = *st;
         }
-      };
-      auto block = [&](auto mk) {
-        constexpr bool masked = decltype(mk)::value;
-        uint32_t p1[2][16], p2[2][16];
-        probs(mk, 0, p1);
-        probs(mk, 1, p2);
-        wait(dp_full, t & 1);
-        ptx::tc_fence_after();
-        if (t > 0) wait(out_done, (t - 1) & 1);  // dS_2's tile has been read
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t la = lo + (static_cast<uint32_t>(16 * x) << 16);
-          uint32_t g[16], pw[8], d1[8], d2[8];
-          ptx::tmem_ld16x256_x4(tmem + cX + c0 + la, g);
+        // the diagonal block, a block past the first key's last query, past N, or with keys past N
+        const bool masked = (causal && i == kb) || (WIN && causal && i * BW + BW - 1 > hi_first) ||
+                            i * BW + c0 + kC > N || (!causal && kb * BW + BW > N);
+        auto probs = [&](auto mk, int m, uint32_t (&v)[32]) {
+          wait(&s_full[m], t & 1);
+          ptx::tc_fence_after();
+          ptx::tmem_ld32(tmem + cS + c0 + lo, v);
           ptx::tmem_wait_ld();
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(&s_cons[m]);
+          // queries u of the block's 32 the key is seen by: from .. to
+          const int from = causal ? key - i * BW - c0 : (key < N ? 0 : kC);
+          const int to = min((WIN && causal ? khi : N - 1), N - 1) - i * BW - c0;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint64_t nD1 = pair(st.z, k), nD2 = pair(st.w, k);
+          for (int u = 0; u < kC; u += 4) {
+            const float4 L = *reinterpret_cast<const float4*>(sSt + m * BW + c0 + u);
+            const float2 a = tc::unpk2(tc::fma2(tc::pk2(v[u], v[u + 1]), c2, tc::pk2f(L.x, L.y)));
+            const float2 b = tc::unpk2(tc::fma2(tc::pk2(v[u + 2], v[u + 3]), c2, tc::pk2f(L.z, L.w)));
+            float p[4] = {ptx::ex2(a.x), ptx::ex2(a.y), ptx::ex2(b.x), ptx::ex2(b.y)};
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int e = 4 * k + 2 * u;
-              const uint64_t dp = tc::pk2(g[e], g[e + 1]);
-              const uint64_t P1 = tc::pk2(p1[x][e], p1[x][e + 1]);
-              const uint64_t P2 = tc::mul2(tc::pk2(p2[x][e], p2[x][e + 1]), w2);
-              const float2 w = tc::unpk2(tc::add2(P1, P2));
-              float2 a = tc::unpk2(tc::mul2(P1, tc::add2(dp, nD1)));
-              float2 b = tc::unpk2(tc::mul2(P2, tc::add2(dp, nD2)));
-              if constexpr (masked) {  // rows with one visible key
-                const float2 d = tc::unpk2(nD1);
-                if (d.x == -INFINITY) a.x = b.x = 0.f;
-                if (d.y == -INFINITY) a.y = b.y = 0.f;
-              }
-              pw[2 * k + u] = ptx::pack_bf16(w.x, w.y);
-              d1[2 * k + u] = ptx::pack_bf16(a.x, a.y);
-              d2[2 * k + u] = ptx::pack_bf16(b.x, b.y);
+            for (int x = 0; x < 4; ++x) {
+              if constexpr (decltype(mk)::value)
+                if (u + x < from || u + x > to) p[x] = 0.f;
+              v[u + x] = __float_as_uint(p[x]);
             }
           }
-          ptx::tmem_st16x128_x4(tmem + cX + c0 + la, pw);
-          ptx::tmem_st16x128_x4(tmem + cX + c0 + 16 + la, d1);
-          // dS_2 (key rows, 128-byte lines of queries): the values are the fragments of 8x8
-          // matrices, so one stmatrix writes the four chunks of 8 queries of a (x, u)
-          const int qcol = c0 + 8 * (lane >> 3);
-          const uint32_t cb = ptx::smem_u32(sm + L::oT) + static_cast<uint32_t>((qcol >> 6) * kSlab);
+        };
+        auto block = [&](auto mk) {
+          uint32_t p1[32], p2[32];
+          probs(mk, 0, p1);
+          probs(mk, 1, p2);
+          wait(dp_full, t & 1);
+          ptx::tc_fence_after();
+          if (t > 0) wait(out_done, (t - 1) & 1);  // dS_2's tile has been read
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
-            ptx::stmatrix_x4(cb + sw128(qd * 32 + 16 * x + 8 * u + (lane & 7), (qcol & 63) >> 3), d2[u], d2[2 + u],
-                             d2[4 + u], d2[6 + u]);
-        }
-      };
-      if (masked)
-        block(std::true_type{});
-      else
-        block(std::false_type{});
-      ptx::fence_proxy_async_smem();
-      ptx::tmem_wait_st();
-      ptx::tc_fence_before();
-      ptx::mbar_arrive(ready);
+          for (int x = 0; x < 2; ++x) {  // 16 queries at a time: the maps' P hold 64 registers
+            uint32_t pw[8], d1[8], d2[8];
+#pragma unroll
+            for (int z = 0; z < 16; z += 8) {
+              uint32_t g[8];
+              ptx::tmem_ld8(tmem + cX + c0 + 16 * x + z + lo, g);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int u = 0; u < 8; u += 4) {
+                const int q = 16 * x + z + u;
+                const float4 D1 = *reinterpret_cast<const float4*>(sSt + 2 * BW + c0 + q);
+                const float4 D2 = *reinterpret_cast<const float4*>(sSt + 3 * BW + c0 + q);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  const int e = q + 2 * y, o = (z + u + 2 * y) >> 1;
+                  const uint64_t dp = tc::pk2(g[u + 2 * y], g[u + 2 * y + 1]);
+                  const uint64_t n1 = y == 0 ? tc::pk2f(D1.x, D1.y) : tc::pk2f(D1.z, D1.w);
+                  const uint64_t n2 = y == 0 ? tc::pk2f(D2.x, D2.y) : tc::pk2f(D2.z, D2.w);
+                  const uint64_t P1 = tc::pk2(p1[e], p1[e + 1]), P2 = tc::pk2(p2[e], p2[e + 1]);
+                  float2 a = tc::unpk2(tc::mul2(P1, tc::add2(dp, n1)));      // P_1 (dP - D_1)
+                  float2 b = tc::unpk2(tc::mul2(P2, tc::fma2(dp, w2, n2)));  // -lam P_2 (dP - D_2)
+                  const float2 w = tc::unpk2(tc::fma2(P2, w2, P1));
+                  if constexpr (decltype(mk)::value) {  // rows with one visible key
+                    const float2 d = tc::unpk2(n1);
+                    if (d.x == -INFINITY) a.x = b.x = 0.f;
+                    if (d.y == -INFINITY) a.y = b.y = 0.f;
+                  }
+                  pw[o] = ptx::pack_bf16(w.x, w.y);
+                  d1[o] = ptx::pack_bf16(a.x, a.y);
+                  d2[o] = ptx::pack_bf16(b.x, b.y);
+                }
+              }
+            }
+            // W over the 8 columns' worth of dP just read, dS_1 over the next 8
+            ptx::tmem_st8(tmem + cX + c0 + 16 * x + lo, pw);
+            ptx::tmem_st8(tmem + cX + c0 + 16 * x + 8 + lo, d1);
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+              st_shared4(sT + sw128(r, ((c0 & 63) >> 3) + 2 * x + y), &d2[4 * y]);
+          }
+        };
+        if (masked)
+          block(std::true_type{});
+        else
+          block(std::false_type{});
+        ptx::fence_proxy_async_smem();
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(ready);
+      }
     }
     wait(out_done, (nt - 1) & 1);
     ptx::tc_fence_after();
@@ -662,20 +658,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The row statistics (-L_1 log2 e, -L_2 log2 e, -D_1, -D_2) both passes read.  16 threads per row.
+// The row statistics both passes read, kPlanes rows of 128 per block of queries (zeros past N):
+// -L_1 log2 e, -L_2 log2 e, -D_1, lam D_2, -D_2.  16 threads per row.
 template <int DV>
 __global__ void __launch_bounds__(256)
     prep_kernel(const __nv_bfloat16* __restrict__ O, const __nv_bfloat16* __restrict__ O2,
                 const __nv_bfloat16* __restrict__ dO, const float* __restrict__ lse, const float* __restrict__ lam,
-                float4* __restrict__ stats, int64_t N, int64_t H, int64_t BH, int causal, Band bd) {
+                float* __restrict__ stats, int64_t N, int64_t Np, int64_t H, int64_t BH, int causal, Band bd) {
   constexpr int W = DV / 16;  // columns per thread
   const int64_t gid = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   const int64_t rowg = gid >> 4;
   const int part = static_cast<int>(gid & 15);
-  const bool live = rowg < BH * N;  // every lane stays for the shuffles below
+  const bool valid = rowg < BH * Np;  // every lane stays for the shuffles below
+  const int64_t bh = valid ? rowg / Np : 0, row = valid ? rowg - bh * Np : 0;
+  const bool live = valid && row < N;
   float d = 0.f, d2 = 0.f;
   if (live) {
-    const int64_t off = rowg * DV + part * W;
+    const int64_t off = (bh * N + row) * DV + part * W;
 #pragma unroll
     for (int u = 0; u < W; u += 4) {
       const uint2 g = *reinterpret_cast<const uint2*>(dO + off + u), o = *reinterpret_cast<const uint2*>(O + off + u),
@@ -694,11 +693,17 @@ __global__ void __launch_bounds__(256)
     d += __shfl_xor_sync(0xffffffffu, d, x);
     d2 += __shfl_xor_sync(0xffffffffu, d2, x);
   }
-  if (live && part == 0) {
-    const int64_t bh = rowg / N, row = rowg - bh * N;
-    const bool one = diff_one_key(bd, causal, bh, row);
-    stats[rowg] = make_float4(-lse[2 * bh * N + row] * kLog2e, -lse[(2 * bh + 1) * N + row] * kLog2e,
-                              -diff_mark_D(fmaf(lam[bh % H], d2, d), one), -diff_mark_D(d2, one));
+  if (valid && part < kPlanes) {
+    float v = 0.f;
+    if (live) {
+      const float lm = lam[bh % H];
+      const bool one = diff_one_key(bd, causal, bh, row);
+      v = part < 2 ? -lse[(2 * bh + part) * N + row] * kLog2e
+          : part == 2 ? -diff_mark_D(fmaf(lm, d2, d), one)
+          : part == 3 ? lm * d2
+                      : -diff_mark_D(d2, one);
+    }
+    stats[((bh * Np + row) / BW * kPlanes + part) * BW + row % BW] = v;
   }
 }
 
@@ -710,16 +715,17 @@ cudaError_t run(const Problem& p, const void* Q, const void* K, const void* V, c
                 cudaStream_t st) {
   constexpr int D = DV / 2;
   const int64_t N = p.N, BH = p.BH;
-  float4* stats = static_cast<float4*>(ws);                       // [BH][N]
-  float* partial = reinterpret_cast<float*>(stats + BH * N);      // [BH][blocks][kCW]
+  const int64_t Np = blocks(N) * BW;
+  float* stats = static_cast<float*>(ws);          // [BH][blocks][kPlanes][BW]
+  float* partial = stats + BH * kPlanes * Np;      // [BH][blocks][kCW]
   alignas(64) CUtensorMap k, v, q, g;
   if (!make_tmap_bf16(&q, Q, N, D, 2 * BH, BW) || !make_tmap_bf16(&g, dO, N, DV, BH, BW) ||
       !make_tmap_bf16(&k, K, N, D, 2 * p.BHkv, BW) || !make_tmap_bf16(&v, V, N, DV, p.BHkv, BW))
     return cudaErrorInvalidValue;
-  const int64_t threads = BH * N * 16;
+  const int64_t threads = BH * Np * 16;
   prep_kernel<DV><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, st>>>(
       static_cast<const __nv_bfloat16*>(O), static_cast<const __nv_bfloat16*>(O2),
-      static_cast<const __nv_bfloat16*>(dO), lse, lam, stats, N, p.H, BH, p.causal, make_band(p, eff_window(p), false));
+      static_cast<const __nv_bfloat16*>(dO), lse, lam, stats, N, Np, p.H, BH, p.causal, make_band(p, eff_window(p), false));
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int nb = static_cast<int>(blocks(N)), H = static_cast<int>(p.H), n = static_cast<int>(N);
@@ -729,11 +735,11 @@ cudaError_t run(const Problem& p, const void* Q, const void* K, const void* V, c
   constexpr int rs = Lay<DV, false>::bytes, cs = Lay<DV, true>::bytes;
   if ((e = cudaFuncSetAttribute(row, cudaFuncAttributeMaxDynamicSharedMemorySize, rs)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(col, cudaFuncAttributeMaxDynamicSharedMemorySize, cs)) != cudaSuccess) return e;
-  row<<<static_cast<unsigned>(nb * BH), kThreads, rs, st>>>(
+  row<<<static_cast<unsigned>(nb * BH), (kCW + 2) * 32, rs, st>>>(
       q, g, k, v, lam, stats, static_cast<__nv_bfloat16*>(dQ), partial, n, H, nb, static_cast<int>(BH), p.scale, c,
       p.causal, make_band(p, eff_window_tc(p), false), p.group);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  col<<<static_cast<unsigned>(nb * p.BHkv), kThreads, cs, st>>>(
+  col<<<static_cast<unsigned>(nb * p.BHkv), kColThreads, cs, st>>>(
       k, v, q, g, lam, stats, static_cast<__nv_bfloat16*>(dK), static_cast<__nv_bfloat16*>(dV), n, H, nb,
       static_cast<int>(p.BHkv), p.scale, c, p.causal, make_band(p, eff_window_tc(p), true), p.group);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -743,7 +749,7 @@ cudaError_t run(const Problem& p, const void* Q, const void* K, const void* V, c
 }  // namespace
 
 size_t tc_diff_bwd_bytes(int64_t BH, int64_t N) {
-  return static_cast<size_t>(BH) * (N * sizeof(float4) + blocks(N) * kCW * sizeof(float));
+  return static_cast<size_t>(BH) * blocks(N) * (kPlanes * BW + kCW) * sizeof(float);
 }
 
 cudaError_t tc_diff_bwd(const Problem& p, const void* Q, const void* K, const void* V, const float* lam, const void* O,
