@@ -382,7 +382,8 @@ __global__ void __launch_bounds__(256)
     dlam_kernel(const float* __restrict__ partial, float* __restrict__ dlam, int64_t B, int64_t H, int64_t nblk) {
   const int64_t h = blockIdx.x;
   float t = 0.f;
-  for (int64_t u = threadIdx.x; u < B * nblk; u += 256) t += partial[((u / nblk) * H + h) * nblk + u % nblk];
+  for (int64_t b = 0; b < B; ++b)
+    for (int64_t k = threadIdx.x; k < nblk; k += 256) t += partial[(b * H + h) * nblk + k];
   __shared__ float red[256];
   red[threadIdx.x] = t;
   __syncthreads();

@@ -20,7 +20,8 @@
 // exponents' arguments and dlam's sums are fp32.
 //
 // Warps 0-15 compute (warp w: TMEM lanes 32(w%4).., tile columns 32(w/4)..), warp 16 issues
-// the TMA loads, warp 17 allocates TMEM and issues the products (elect.sync from the warp).
+// the TMA loads, warp 17 allocates TMEM and issues the products (elect.sync from the warp); in
+// the column pass warp 18 brings the streamed rows' statistics.
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -103,6 +104,7 @@ __global__ void __launch_bounds__((kCW + 2) * 32, 1)
   uint64_t* dq_done = ds_ready + 2;   // [2] dS_m K_m done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dq_done + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* sRed = reinterpret_cast<float*>(sm + L::oBar + 160);  // [kCW]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const tc::Order ord = tc::grid_order(BH, nrb);
@@ -304,7 +306,7 @@ __global__ void __launch_bounds__((kCW + 2) * 32, 1)
       float v = x.x + x.y;
 #pragma unroll
       for (int u = 1; u < 32; u <<= 1) v += __shfl_xor_sync(0xffffffffu, v, u);
-      if (lane == 0) partial[(static_cast<int64_t>(bh) * nrb + rb) * kCW + warp] = v;
+      if (lane == 0) sRed[warp] = v;
     }
     // dQ_m = s w_m (P_m (dP - D_m)) K_m: the weight -lam of map 2 enters here
     const float f[2] = {scale, -scale * lam[bh % H]};
@@ -331,6 +333,11 @@ __global__ void __launch_bounds__((kCW + 2) * 32, 1)
   if (warp == kCW + 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0) {
+    float v = 0.f;
+    for (int u = 0; u < kCW; ++u) v += sRed[u];
+    partial[static_cast<int64_t>(bh) * nrb + rb] = v;
   }
 }
 
@@ -364,7 +371,8 @@ __global__ void __launch_bounds__(kColThreads, 1)
   uint64_t* dp_full = s_cons + 2;    // dP^T in TMEM (and the previous block's dV, dK_1 done)
   uint64_t* ready = dp_full + 1;     // W^T, dS_1^T in TMEM, dS_2^T in shared memory
   uint64_t* out_done = ready + 1;    // all products of the block done
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(out_done + 1);
+  uint64_t* st_full = out_done + 1;  // the block's statistics in shared memory
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(st_full + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -391,6 +399,7 @@ __global__ void __launch_bounds__(kColThreads, 1)
     ptx::mbar_init(dp_full, 1);
     ptx::mbar_init(ready, kCW * 32);
     ptx::mbar_init(out_done, 1);
+    ptx::mbar_init(st_full, 32);
     init_abort(sm, abort_flag);
     ptx::fence_mbar_init();
   }
@@ -503,6 +512,26 @@ __global__ void __launch_bounds__(kColThreads, 1)
         ptx::mma_commit_e(out_done);
       }
     }
+  } else if (warp == kCW + 2) {
+    // -------------------- the streamed queries' statistics (four planes) into shared memory:
+    // loaded a block ahead, written once the compute warps are done with the previous block
+    float4* dst = reinterpret_cast<float4*>(sm + L::oStat);
+    auto src = [&](int t) {
+      const int h = t / ntile, i = i0 + t - h * ntile;
+      return reinterpret_cast<const float4*>(stats + ((static_cast<int64_t>(kvh) * G + h) * nb + i) * (kPlanes * BW));
+    };
+    float4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = src(0)[32 * u + lane];
+    for (int t = 0; t < nt; ++t) {
+      if (t > 0) wait(ready, (t - 1) & 1);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) dst[32 * u + lane] = v[u];
+      ptx::mbar_arrive(st_full);
+      const float4* next = src(min(t + 1, nt - 1));
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = next[32 * u + lane];
+    }
   } else if (warp < kCW) {
     ptx::setmaxnreg_inc<kColRegs>();
     // ----------------------------------- compute: a key row, 32 queries of a block
@@ -513,25 +542,14 @@ __global__ void __launch_bounds__(kColThreads, 1)
     const uint64_t c2 = tc::pk2f(c, c);
     const int khi = (WIN && causal) ? bd.key_hi(kvh, key) : 0;  // the key's last query
     const uint32_t sT = ptx::smem_u32(sm + L::oT) + static_cast<uint32_t>((c0 >> 6) * kSlab);
-    float* sSt = reinterpret_cast<float*>(sm + L::oStat);
-    // plane qd of the query block's statistics, this lane's query
-    const float* st = stats + (static_cast<int64_t>(kvh) * G * nb + i0) * (kPlanes * BW) + qd * BW + c0 + lane;
-    float next = *st;
+    const float* sSt = reinterpret_cast<const float*>(sm + L::oStat) + c0;
     int t = 0;
     for (int h = 0; h < G; ++h) {
       const int64_t bh = static_cast<int64_t>(kvh) * G + h;
       const float wl = -lam[bh % H];
       const uint64_t w2 = tc::pk2f(wl, wl);
       for (int i = i0; i < i0 + ntile; ++i, ++t) {
-        // The block's statistics go to shared memory, where every lane reads the same ones: each
-        // of the four warps of a column group writes one plane, loaded a block ahead.
-        if (t > 0) tc::named_sync(1 + cg, 128);  // the previous block's have been read
-        sSt[qd * BW + c0 + lane] = next;
-        tc::named_sync(1 + cg, 128);
-        if (t + 1 < nt) {  // the next block, or the next head's first
-          st += (i + 1 < i0 + ntile ? 1 : nb - ntile + 1) * (kPlanes * BW);
-          next = *st;
-        }
+        wait(st_full, t & 1);
         // the diagonal block, a block past the first key's last query, past N, or with keys past N
         const bool masked = (causal && i == kb) || (WIN && causal && i * BW + BW - 1 > hi_first) ||
                             i * BW + c0 + kC > N || (!causal && kb * BW + BW > N);
@@ -547,7 +565,7 @@ __global__ void __launch_bounds__(kColThreads, 1)
           const int to = min((WIN && causal ? khi : N - 1), N - 1) - i * BW - c0;
 #pragma unroll
           for (int u = 0; u < kC; u += 4) {
-            const float4 L = *reinterpret_cast<const float4*>(sSt + m * BW + c0 + u);
+            const float4 L = *reinterpret_cast<const float4*>(sSt + m * BW + u);
             const float2 a = tc::unpk2(tc::fma2(tc::pk2(v[u], v[u + 1]), c2, tc::pk2f(L.x, L.y)));
             const float2 b = tc::unpk2(tc::fma2(tc::pk2(v[u + 2], v[u + 3]), c2, tc::pk2f(L.z, L.w)));
             float p[4] = {ptx::ex2(a.x), ptx::ex2(a.y), ptx::ex2(b.x), ptx::ex2(b.y)};
@@ -577,8 +595,8 @@ __global__ void __launch_bounds__(kColThreads, 1)
 #pragma unroll
               for (int u = 0; u < 8; u += 4) {
                 const int q = 16 * x + z + u;
-                const float4 D1 = *reinterpret_cast<const float4*>(sSt + 2 * BW + c0 + q);
-                const float4 D2 = *reinterpret_cast<const float4*>(sSt + 3 * BW + c0 + q);
+                const float4 D1 = *reinterpret_cast<const float4*>(sSt + 2 * BW + q);
+                const float4 D2 = *reinterpret_cast<const float4*>(sSt + 3 * BW + q);
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                   const int e = q + 2 * y, o = (z + u + 2 * y) >> 1;
@@ -658,6 +676,17 @@ __global__ void __launch_bounds__(kColThreads, 1)
   }
 }
 
+template <int N>
+__device__ __forceinline__ void load_words(const __nv_bfloat16* p, uint32_t (&x)[N]) {
+  if constexpr (N == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    x[0] = v.x, x[1] = v.y;
+  }
+}
+
 // The row statistics both passes read, kPlanes rows of 128 per block of queries (zeros past N):
 // -L_1 log2 e, -L_2 log2 e, -D_1, lam D_2, -D_2.  16 threads per row.
 template <int DV>
@@ -675,17 +704,15 @@ __global__ void __launch_bounds__(256)
   float d = 0.f, d2 = 0.f;
   if (live) {
     const int64_t off = (bh * N + row) * DV + part * W;
+    uint32_t g[W / 2], o[W / 2], o2[W / 2];
+    load_words<W / 2>(dO + off, g);
+    load_words<W / 2>(O + off, o);
+    load_words<W / 2>(O2 + off, o2);
 #pragma unroll
-    for (int u = 0; u < W; u += 4) {
-      const uint2 g = *reinterpret_cast<const uint2*>(dO + off + u), o = *reinterpret_cast<const uint2*>(O + off + u),
-                  p = *reinterpret_cast<const uint2*>(O2 + off + u);
-      const uint32_t gw[2] = {g.x, g.y}, ow[2] = {o.x, o.y}, pw[2] = {p.x, p.y};
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float x = tc::bf16_lo(gw[e]), y = tc::bf16_hi(gw[e]);
-        d = fmaf(x, tc::bf16_lo(ow[e]), fmaf(y, tc::bf16_hi(ow[e]), d));
-        d2 = fmaf(x, tc::bf16_lo(pw[e]), fmaf(y, tc::bf16_hi(pw[e]), d2));
-      }
+    for (int e = 0; e < W / 2; ++e) {
+      const float x = tc::bf16_lo(g[e]), y = tc::bf16_hi(g[e]);
+      d = fmaf(x, tc::bf16_lo(o[e]), fmaf(y, tc::bf16_hi(o[e]), d));
+      d2 = fmaf(x, tc::bf16_lo(o2[e]), fmaf(y, tc::bf16_hi(o2[e]), d2));
     }
   }
 #pragma unroll
@@ -717,7 +744,7 @@ cudaError_t run(const Problem& p, const void* Q, const void* K, const void* V, c
   const int64_t N = p.N, BH = p.BH;
   const int64_t Np = blocks(N) * BW;
   float* stats = static_cast<float*>(ws);          // [BH][blocks][kPlanes][BW]
-  float* partial = stats + BH * kPlanes * Np;      // [BH][blocks][kCW]
+  float* partial = stats + BH * kPlanes * Np;      // [BH][blocks]
   alignas(64) CUtensorMap k, v, q, g;
   if (!make_tmap_bf16(&q, Q, N, D, 2 * BH, BW) || !make_tmap_bf16(&g, dO, N, DV, BH, BW) ||
       !make_tmap_bf16(&k, K, N, D, 2 * p.BHkv, BW) || !make_tmap_bf16(&v, V, N, DV, p.BHkv, BW))
@@ -743,13 +770,13 @@ cudaError_t run(const Problem& p, const void* Q, const void* K, const void* V, c
       k, v, q, g, lam, stats, static_cast<__nv_bfloat16*>(dK), static_cast<__nv_bfloat16*>(dV), n, H, nb,
       static_cast<int>(p.BHkv), p.scale, c, p.causal, make_band(p, eff_window_tc(p), true), p.group);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return diff_reduce_dlam(partial, dlam, p.B, p.H, static_cast<int64_t>(nb) * kCW, st);
+  return diff_reduce_dlam(partial, dlam, p.B, p.H, nb, st);
 }
 
 }  // namespace
 
 size_t tc_diff_bwd_bytes(int64_t BH, int64_t N) {
-  return static_cast<size_t>(BH) * blocks(N) * (kPlanes * BW + kCW) * sizeof(float);
+  return static_cast<size_t>(BH) * blocks(N) * (kPlanes * BW + 1) * sizeof(float);
 }
 
 cudaError_t tc_diff_bwd(const Problem& p, const void* Q, const void* K, const void* V, const float* lam, const void* O,
