@@ -203,65 +203,61 @@ def attn_segment_bounds(seg, seg_lo=None, seg_hi=None, stream=None):
     return seg_lo, seg_hi
 
 
-class _on:
-    """The device and stream a call launches on: every tensor on one CUDA device, made current for
-    the call, and `stream` or that device's current stream.  Empty tensors launch nothing, so they
-    may be anywhere."""
+def _launch(fn, tensors, stream, *args):
+    """fn(*args, stream) on the device the tensors are on: one CUDA device, made current for the call, and `stream`
+    or that device's current stream.  Empty tensors launch nothing, so they may be anywhere."""
+    cuda = _torch().cuda
+    devices = {t.get_device() for t in tensors if t is not None and t.numel()}
+    if len(devices) > 1 or -1 in devices:
+        raise FbdError(1, f"tensors must be on one CUDA device (got {sorted({str(t.device) for t in tensors if t is not None})})")
+    if not devices:
+        _check(fn(*args, None))
+        return
+    device = devices.pop()
+    if stream is None:
+        stream = cuda.current_stream(device).cuda_stream
+    else:
+        stream = int(getattr(stream, "cuda_stream", stream))
+    if device == cuda.current_device():
+        _check(fn(*args, stream))
+    else:
+        with cuda.device(device):
+            _check(fn(*args, stream))
 
-    def __init__(self, tensors, stream):
-        torch = _torch()
-        devices = {t.device for t in tensors if t is not None and t.numel() > 0}
-        if len(devices) > 1 or any(d.type != "cuda" for d in devices):
-            raise FbdError(1, f"tensors must be on one CUDA device (got {sorted(map(str, devices))})")
-        self.guard = torch.cuda.device(devices.pop()) if devices else None
-        self.stream = stream
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return _stream(self.stream)
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _at(name, t):
+    """Address of a contiguous tensor."""
+    if not t.is_contiguous():
+        raise FbdError(1, f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _want(name, t, shape, dtype):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    """The address of t, contiguous and of that shape and type."""
+    if t.shape != shape or t.dtype != dtype:
         raise FbdError(1, f"{name} must be {dtype} {tuple(shape)} (got {t.dtype} {tuple(t.shape)})")
+    return _at(name, t)
 
 
-def _diff_desc(Q, K, V, lam, scale, causal, window, bounds, queries=None) -> AttnDesc:
-    """Descriptor of a differential attention call and the checks of its tensors' shapes and types
-    (queries: 1 for a token over a cache, None where Q has the keys' length)."""
-    torch = _torch()
+def _diff_desc(Q, K, V, lam, scale, causal, window, bounds, queries=None):
+    """Descriptor of a differential attention call (queries: 1 for a token over a cache, None where Q has the keys'
+    length) and the addresses of Q, K, V and lam, their shapes and types checked."""
     if Q.dim() != 4 or K.dim() != 4 or V.dim() != 4:
         raise FbdError(1, "Q, K and V must be 4-dimensional")
+    dtype = Q.dtype
     B, maps, _, d = Q.shape
-    kmaps, N = K.shape[1], K.shape[2]
+    _, kmaps, N, _ = K.shape
     if maps % 2 or kmaps % 2:
         raise FbdError(1, f"Q and K hold two maps per head, got {maps} and {kmaps} slices")
     H, Hkv = maps // 2, kmaps // 2
     if (Hkv == 0) != (H == 0) or (Hkv and H % Hkv):
         raise FbdError(1, f"key/value heads ({Hkv}) must divide query heads ({H})")
-    _want("Q", Q, (B, maps, N if queries is None else queries, d), Q.dtype)
-    _want("K", K, (B, kmaps, N, d), Q.dtype)
-    _want("V", V, (B, Hkv, N, 2 * d), Q.dtype)
-    _want("lam", lam, (H,), torch.float32)
+    ptrs = (_want("Q", Q, (B, maps, N if queries is None else queries, d), dtype), _want("K", K, (B, kmaps, N, d), dtype),
+            _want("V", V, (B, Hkv, N, 2 * d), dtype), _want("lam", lam, (H,), _torch().float32))
     lo = hi = None
     if bounds is not None:
-        for name, t in zip(("seg_lo", "seg_hi"), bounds):
-            _want(name, t, (B, N), torch.int32)
-        lo, hi = _ptr(bounds[0]), _ptr(bounds[1])
-    return AttnDesc(B, H, N, d, float(scale), int(causal), _dtype_code(Q), H // Hkv if Hkv else 1, int(window), lo, hi)
-
-
-def _out(name, t, shape, like, dtype=None):
-    dtype = like.dtype if dtype is None else dtype
-    if t is None:
-        return _torch().empty(shape, dtype=dtype, device=like.device)
-    _want(name, t, shape, dtype)
-    return t
+        lo, hi = (_want(name, t, (B, N), _torch().int32) for name, t in zip(("seg_lo", "seg_hi"), bounds))
+    return AttnDesc(B, H, N, d, scale, causal, _dtype_code(Q), H // Hkv if Hkv else 1, window, lo, hi), ptrs
 
 
 def attn_diff_fwd(Q, K, V, lam, O=None, O2=None, lse=None, scale: float = 0.0, stream=None, causal: bool = True,
@@ -270,14 +266,17 @@ def attn_diff_fwd(Q, K, V, lam, O=None, O2=None, lse=None, scale: float = 0.0, s
     head in neighbouring slices), V [B, H/g, N, 2d], lam [H] float32.  O2 = A_2 V and lse are what the backward
     needs; for_backward=False leaves O2 out (returned as None)."""
     torch = _torch()
-    desc = _diff_desc(Q, K, V, lam, scale, causal, window, bounds)
+    desc, ptrs = _diff_desc(Q, K, V, lam, scale, causal, window, bounds)
     shape = (desc.B, desc.H, desc.N, 2 * desc.d)
-    O = _out("O", O, shape, Q)
-    O2 = _out("O2", O2, shape, Q) if for_backward or O2 is not None else None
-    lse = _out("lse", lse, Q.shape[:3], Q, torch.float32)
-    with _on([Q, K, V, lam, O, O2, lse, *(bounds or ())], stream) as st:
-        _check(lib.attn_diff_fwd(ctypes.byref(desc), _ptr(Q), _ptr(K), _ptr(V), _ptr(lam), _ptr(O), _ptr(O2), _ptr(lse),
-                                 st))
+    if O is None:
+        O = torch.empty(shape, dtype=Q.dtype, device=Q.device)
+    if O2 is None and for_backward:
+        O2 = torch.empty_like(O)
+    if lse is None:
+        lse = torch.empty(Q.shape[:3], dtype=torch.float32, device=Q.device)
+    outs = (_want("O", O, shape, Q.dtype), None if O2 is None else _want("O2", O2, shape, Q.dtype),
+            _want("lse", lse, Q.shape[:3], torch.float32))
+    _launch(lib.attn_diff_fwd, (Q, K, V, lam, O, O2, lse, *(bounds or ())), stream, ctypes.byref(desc), *ptrs, *outs)
     return O, O2, lse
 
 
@@ -289,19 +288,20 @@ def attn_diff_bwd(Q, K, V, lam, O, O2, dO, lse, dQ=None, dK=None, dV=None, dlam=
                   scale: float = 0.0, stream=None, causal: bool = True, window: int = 0, bounds=None):
     """dQ, dK, dV, dlam = recompute backward of attn_diff_fwd (its mask and scale given again)."""
     torch = _torch()
-    desc = _diff_desc(Q, K, V, lam, scale, causal, window, bounds)
-    shape = (desc.B, desc.H, desc.N, 2 * desc.d)
-    for name, t in (("O", O), ("O2", O2), ("dO", dO)):
-        _want(name, t, shape, Q.dtype)
-    _want("lse", lse, Q.shape[:3], torch.float32)
-    dQ, dK, dV = _out("dQ", dQ, Q.shape, Q), _out("dK", dK, K.shape, Q), _out("dV", dV, V.shape, Q)
-    dlam = _out("dlam", dlam, lam.shape, lam)
-    workspace = _workspace(attn_diff_bwd_workspace_bytes(desc), Q, workspace)
-    with _on([Q, K, V, lam, O, O2, dO, lse, dQ, dK, dV, dlam, workspace if Q.numel() else None, *(bounds or ())],
-             stream) as st:
-        _check(lib.attn_diff_bwd(ctypes.byref(desc), _ptr(Q), _ptr(K), _ptr(V), _ptr(lam), _ptr(O), _ptr(O2), _ptr(dO),
-                                 _ptr(lse), _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(dlam), _ptr(workspace),
-                                 ctypes.c_size_t(workspace.numel() * workspace.element_size()), st))
+    desc, ptrs = _diff_desc(Q, K, V, lam, scale, causal, window, bounds)
+    shape, dtype = (desc.B, desc.H, desc.N, 2 * desc.d), Q.dtype
+    ins = (_want("O", O, shape, dtype), _want("O2", O2, shape, dtype), _want("dO", dO, shape, dtype),
+           _want("lse", lse, Q.shape[:3], torch.float32))
+    dQ = torch.empty_like(Q) if dQ is None else dQ
+    dK = torch.empty_like(K) if dK is None else dK
+    dV = torch.empty_like(V) if dV is None else dV
+    dlam = torch.empty_like(lam) if dlam is None else dlam
+    outs = (_want("dQ", dQ, Q.shape, dtype), _want("dK", dK, K.shape, dtype), _want("dV", dV, V.shape, dtype),
+            _want("dlam", dlam, lam.shape, torch.float32))
+    workspace = _workspace(lib.attn_diff_bwd_workspace_bytes(ctypes.byref(desc)), Q, workspace)
+    _launch(lib.attn_diff_bwd, (Q, K, V, lam, O, O2, dO, lse, dQ, dK, dV, dlam, workspace if Q.numel() else None,
+                                *(bounds or ())), stream, ctypes.byref(desc), *ptrs, *ins, *outs,
+            _at("workspace", workspace), workspace.nbytes)
     return dQ, dK, dV, dlam
 
 
@@ -314,13 +314,15 @@ def attn_diff_decode(Q, K, V, lam, lens, O=None, workspace=None, scale: float = 
     [B, 2H/g, capacity, d], V [B, H/g, capacity, 2d] of which sequence b holds lens[b] keys (int32, on the device;
     the new token's among them).  A sequence without a key gives zeros."""
     torch = _torch()
-    desc = _diff_desc(Q, K, V, lam, scale, True, window, None, queries=1)
-    _want("lens", lens, (desc.B,), torch.int32)
-    O = _out("O", O, (desc.B, desc.H, 1, 2 * desc.d), Q)
-    workspace = _workspace(attn_diff_decode_workspace_bytes(desc), Q, workspace)
-    with _on([Q, K, V, lam, lens, O, workspace if Q.numel() else None], stream) as st:
-        _check(lib.attn_diff_decode(ctypes.byref(desc), _ptr(Q), _ptr(K), _ptr(V), _ptr(lam), _ptr(lens), _ptr(O),
-                                    _ptr(workspace), ctypes.c_size_t(workspace.numel() * workspace.element_size()), st))
+    desc, ptrs = _diff_desc(Q, K, V, lam, scale, True, window, None, queries=1)
+    shape = (desc.B, desc.H, 1, 2 * desc.d)
+    lens_at = _want("lens", lens, (desc.B,), torch.int32)
+    if O is None:
+        O = torch.empty(shape, dtype=Q.dtype, device=Q.device)
+    O_at = _want("O", O, shape, Q.dtype)
+    workspace = _workspace(lib.attn_diff_decode_workspace_bytes(ctypes.byref(desc)), Q, workspace)
+    _launch(lib.attn_diff_decode, (Q, K, V, lam, lens, O, workspace if Q.numel() else None), stream,
+            ctypes.byref(desc), *ptrs, lens_at, O_at, _at("workspace", workspace), workspace.nbytes)
     return O
 
 
@@ -346,25 +348,26 @@ def attn_rope(xs, pos, freq, axis, outs=None, paired: str = "half", inverse: boo
     if paired not in ("half", "neighbour"):
         raise FbdError(1, f"paired must be 'half' or 'neighbour' (got {paired!r})")
     B, _, N, d = xs[0].shape
-    for x, y in zip(xs, outs):
-        _want("x", x, (B, x.shape[1], N, d), xs[0].dtype)
-        _want("out", y, x.shape, x.dtype)
-        if x.numel() and (x.stride(3) != 1 or y.stride(3) != 1):
-            raise FbdError(1, "the last dimension must be contiguous")
-    if pos.dim() not in (2, 3):
-        raise FbdError(1, "pos must be [axes, B, N] or [axes, N]")
-    axes = pos.shape[0]
-    _want("pos", pos, (axes, N) if pos.dim() == 2 else (axes, B, N), torch.int32)
-    _want("freq", freq, (d // 2,), torch.float32)
-    _want("axis", axis, (d // 2,), torch.int32)
-    desc = RopeDesc(B, N, d, axes, _dtype_code(xs[0]), ATTN_ROPE_HALF if paired == "half" else ATTN_ROPE_NEIGHBOUR,
-                    int(inverse), 0 if pos.dim() == 2 else N)
+    dtype = xs[0].dtype
     tensors = (RopeTensor * len(xs))()
     for t, x, y in zip(tensors, xs, outs):
-        t.x, t.y, t.heads = x.data_ptr(), y.data_ptr(), x.shape[1]
-        t.x_stride[:], t.y_stride[:] = x.stride()[:3], y.stride()[:3]
-    with _on([*xs, *outs, pos, freq, axis] if any(x.numel() for x in xs) else [], stream) as st:
-        _check(lib.attn_rope(ctypes.byref(desc), tensors, len(xs), _ptr(pos), _ptr(freq), _ptr(axis), st))
+        heads = x.shape[1]
+        if x.shape != (B, heads, N, d) or y.shape != x.shape or x.dtype != dtype or y.dtype != dtype:
+            raise FbdError(1, f"tensors must be {dtype} [{B}, heads, {N}, {d}], an output like its input (got "
+                              f"{x.dtype} {tuple(x.shape)} and {y.dtype} {tuple(y.shape)})")
+        xs_, ys_ = x.stride(), y.stride()
+        if heads and B and N and (xs_[3] != 1 or ys_[3] != 1):
+            raise FbdError(1, "the last dimension must be contiguous")
+        t.x, t.y, t.heads, t.x_stride[:], t.y_stride[:] = x.data_ptr(), y.data_ptr(), heads, xs_[:3], ys_[:3]
+    if pos.dim() not in (2, 3):
+        raise FbdError(1, "pos must be [axes, B, N] or [axes, N]")
+    axes, shared = pos.shape[0], pos.dim() == 2
+    tables = (_want("pos", pos, (axes, N) if shared else (axes, B, N), torch.int32),
+              _want("freq", freq, (d // 2,), torch.float32), _want("axis", axis, (d // 2,), torch.int32))
+    desc = RopeDesc(B, N, d, axes, _dtype_code(xs[0]), ATTN_ROPE_HALF if paired == "half" else ATTN_ROPE_NEIGHBOUR,
+                    bool(inverse), 0 if shared else N)
+    _launch(lib.attn_rope, (*xs, *outs, pos, freq, axis) if any(x.numel() for x in xs) else (), stream,
+            ctypes.byref(desc), tensors, len(xs), *tables)
     return outs[0] if single else outs
 
 
