@@ -2,10 +2,18 @@
 //
 //   o_m = sum_j softmax_j(s q_m.k_mj) v_j over the keys lo <= j < len of the sequence,
 //   O = o_1 - lam o_2;  a sequence with no key gives 0.
-// Bound by reading the cache once: the g query heads that share a key/value head are
+// Bound by reading the cache once: up to eight query heads that share a key/value head are
 // handled together, both maps against the same V rows.  The keys of a sequence are split
 // over `nsplit` CTAs, each leaving (max, sum, unnormalised o) per row and map, which a
 // second launch joins; with one split the result is written at once.
+//
+// bf16 on warp-level matrix products (m16n8k16): rows 0-7 of a tile are the heads' first maps,
+// rows 8-15 their second ones, so one product P V serves both maps, and S is Q_1 K_1^T with
+// rows 8-15 zero plus Q_2 K_2^T with rows 0-7 zero.  (tcgen05 has 128 rows to fill.)  Each of
+// four warps takes 16 of a tile's 64 keys with a softmax of its own; the four are joined at
+// the end.  Three 32 KB stages of 16-byte asynchronous copies, two CTAs an SM: 192 KB in
+// flight on each SM.  P is rounded to bf16 for its product; sums, maxima and o are fp32.
+// float32 on the CUDA cores, a key per lane.
 #include <cuda_bf16.h>
 
 #include "diff.h"
@@ -15,7 +23,9 @@
 namespace fbd {
 namespace {
 
-constexpr int BK = 32;    // keys per tile: one per lane
+constexpr int BK = 32;    // float32: keys per tile, one per lane
+constexpr int MK = 64;    // bf16: keys per tile, 16 per warp
+constexpr int NS = 3;     // bf16: stages
 constexpr int RMAX = 8;   // query heads handled together
 constexpr int kT = 128;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -27,20 +37,16 @@ Plan make_plan(const Problem& p) {
   Plan q;
   q.rows = p.group < RMAX ? p.group : RMAX;
   q.chunks = (p.group + q.rows - 1) / q.rows;
-  // about four CTAs for each of the 152 SMs, a split no shorter than eight tiles
+  // about four CTAs for each of the 152 SMs, a split no shorter than 128 keys
   const int64_t base = p.BHkv * q.chunks;
   const int64_t want = base > 0 ? (4 * 152 + base - 1) / base : 1;
-  const int64_t most = (p.N + 8 * BK - 1) / (8 * BK);
+  const int64_t most = (p.N + 127) / 128;
   const int64_t n = want < most ? want : most;
   q.nsplit = static_cast<int>(n < 1 ? 1 : n > 256 ? 256 : n);
   return q;
 }
 
 __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
-  return make_float4(tc::bf16_lo(v.x), tc::bf16_hi(v.x), tc::bf16_lo(v.y), tc::bf16_hi(v.y));
-}
 __device__ __forceinline__ void st1(float* p, float x) { *p = x; }
 __device__ __forceinline__ void st1(__nv_bfloat16* p, float x) { *p = __float2bfloat16(x); }
 
@@ -51,11 +57,231 @@ __device__ __forceinline__ void key_range(const int* lens, int b, int64_t cap, i
   n = len - lo;
 }
 
+// ------------------------------------------------------------------------- bf16
+// 16 bytes global -> shared, or 16 bytes of zeros (nothing is read) where !in.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void ldm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldm4t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Byte offset of a 16-byte chunk in a tile of RB-byte rows, swizzled so that the same chunk of
+// eight consecutive rows lies in eight different 16-byte columns.
+template <int RB>
+__device__ __forceinline__ uint32_t at(int row, int chunk) {
+  return static_cast<uint32_t>(row * RB + ((chunk ^ (RB >= 128 ? row & 7 : (row >> 1) & 3)) << 4));
+}
+
+template <int D>
+struct Stage {
+  static constexpr int kK = MK * D * 2, kV = MK * D * 4, bytes = 2 * kK + kV;
+};
+
 // ws: per (b, h, map, split) 2d + 2 floats: o, max (scaled, in powers of two), sum.
-template <int D, typename T>
+template <int D>
+__global__ void __launch_bounds__(kT, 2)
+    mma_kernel(const __nv_bfloat16* __restrict__ Q, const __nv_bfloat16* __restrict__ K,
+               const __nv_bfloat16* __restrict__ V, const float* __restrict__ lam, const int* __restrict__ lens,
+               __nv_bfloat16* __restrict__ O, float* __restrict__ ws, int64_t cap, int H, int G, int rows, int nsplit,
+               int64_t win, float c) {
+  using St = Stage<D>;
+  constexpr int DV = 2 * D, NT = DV / 8;  // 8-column tiles of o
+  extern __shared__ __align__(128) uint8_t sh[];
+  const uint32_t s0 = ptx::smem_u32(sh);
+  const int split = blockIdx.x % nsplit, Hkv = H / G, chunks = (G + rows - 1) / rows;
+  const int unit = blockIdx.x / nsplit;  // (b, key/value head, chunk of its query heads)
+  const int r0 = unit % chunks * rows, n = unit / chunks % Hkv, b = unit / chunks / Hkv;
+  const int R = min(rows, G - r0);
+  const int64_t kvh = static_cast<int64_t>(b) * Hkv + n;
+  const int64_t h0 = static_cast<int64_t>(b) * H + n * G + r0;  // first query head
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q4 = lane & 3;
+  int64_t lo, cnt;
+  key_range(lens, b, cap, win, lo, cnt);
+  const int64_t per = ((cnt + nsplit - 1) / nsplit + MK - 1) / MK * MK;
+  const int64_t kb = lo + split * per, ke = min(lo + cnt, kb + per);
+  const int nt = ke > kb ? static_cast<int>((ke - kb + MK - 1) / MK) : 0;
+  const __nv_bfloat16* K0 = K + 2 * kvh * cap * D;  // map 1; map 2 is cap * D further on
+  const __nv_bfloat16* V0 = V + kvh * cap * DV;
+  auto load = [&](int t) {
+    const uint32_t st = s0 + static_cast<uint32_t>((t % NS) * St::bytes);
+    const int64_t k0 = kb + static_cast<int64_t>(t) * MK;
+    // keys past the end are not read: zeros there (a cache row not yet written may hold anything)
+#pragma unroll
+    for (int u = 0; u < 2 * MK * D / 8 / kT; ++u) {
+      const int x = u * kT + threadIdx.x, m = x / (MK * D / 8), y = x % (MK * D / 8), r = y / (D / 8), ch = y % (D / 8);
+      const bool in = k0 + r < ke;
+      copy16(st + m * St::kK + at<D * 2>(r, ch), K0 + (m * cap + (in ? k0 + r : kb)) * D + ch * 8, in);
+    }
+#pragma unroll
+    for (int u = 0; u < MK * DV / 8 / kT; ++u) {
+      const int x = u * kT + threadIdx.x, r = x / (DV / 8), ch = x % (DV / 8);
+      const bool in = k0 + r < ke;
+      copy16(st + 2 * St::kK + at<DV * 2>(r, ch), V0 + (in ? k0 + r : kb) * DV + ch * 8, in);
+    }
+  };
+#pragma unroll
+  for (int t = 0; t < NS - 1; ++t) {
+    if (t < nt) load(t);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  // The heads' queries as the A operand: row g their first maps, row g + 8 their second.
+  uint32_t qa[2][D / 16][2];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        qa[m][k][x] =
+            g < R ? *reinterpret_cast<const uint32_t*>(Q + (2 * (h0 + g) + m) * D + k * 16 + x * 8 + q4 * 2) : 0u;
+  float mx[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // of map 1, map 2 (l: this thread's keys)
+  float o[NT][4];
+#pragma unroll
+  for (int u = 0; u < NT; ++u) o[u][0] = o[u][1] = o[u][2] = o[u][3] = 0.f;
+  for (int t = 0; t < nt; ++t) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(NS - 2) : "memory");
+    __syncthreads();
+    if (t + NS - 1 < nt) load(t + NS - 1);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    const uint32_t st = s0 + static_cast<uint32_t>((t % NS) * St::bytes);
+    float s[2][4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      s[u][0] = s[u][1] = s[u][2] = s[u][3] = 0.f;
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+          uint32_t f[4];
+          ldm4(st + m * St::kK + at<D * 2>(warp * 16 + u * 8 + (lane & 7), k * 4 + (lane >> 3)), f);
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            mma(s[u], m == 0 ? qa[0][2 * k + x][0] : 0u, m == 1 ? qa[1][2 * k + x][0] : 0u,
+                m == 0 ? qa[0][2 * k + x][1] : 0u, m == 1 ? qa[1][2 * k + x][1] : 0u, f[2 * x], f[2 * x + 1]);
+        }
+    }
+    if (t == nt - 1) {
+      const int64_t k0 = kb + static_cast<int64_t>(t) * MK + warp * 16 + q4 * 2;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (k0 + u * 8 + (x & 1) >= ke) s[u][x] = -INFINITY;
+    }
+    float a[2], nm[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      float v = fmaxf(fmaxf(s[0][2 * m], s[0][2 * m + 1]), fmaxf(s[1][2 * m], s[1][2 * m + 1])) * c;
+      v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+      v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+      v = fmaxf(mx[m], v);
+      const float sub = v == -INFINITY ? 0.f : v;  // no key of this warp's yet
+      a[m] = ptx::ex2(mx[m] - sub);
+      nm[m] = -sub;
+      l[m] *= a[m];
+      mx[m] = v;
+    }
+    if (__any_sync(0xffffffffu, a[0] != 1.f || a[1] != 1.f)) {
+#pragma unroll
+      for (int u = 0; u < NT; ++u) o[u][0] *= a[0], o[u][1] *= a[0], o[u][2] *= a[1], o[u][3] *= a[1];
+    }
+    uint32_t p[2][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const float x = ptx::ex2(fmaf(s[u][2 * m], c, nm[m])), y = ptx::ex2(fmaf(s[u][2 * m + 1], c, nm[m]));
+        l[m] += x + y;
+        p[u][m] = ptx::pack_bf16(x, y);
+      }
+#pragma unroll
+    for (int u = 0; u < NT; u += 2) {
+      uint32_t f[4];
+      ldm4t(st + 2 * St::kK + at<DV * 2>(warp * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), u + (lane >> 4)), f);
+      mma(o[u], p[0][0], p[0][1], p[1][0], p[1][1], f[0], f[1]);
+      mma(o[u + 1], p[0][0], p[0][1], p[1][0], p[1][1], f[2], f[3]);
+    }
+  }
+  // The warps' parts joined through shared memory: row 8 m + head of each, o and (max, sum).
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+  float* so = reinterpret_cast<float*>(sh);            // [4][16][DV]
+  float* sm = so + 4 * 16 * DV;                        // [4][16] max, [4][16] sum
+  static_assert((4 * 16 * DV + 128) * 4 <= NS * St::bytes, "the join fits");
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    float v = l[m];
+    v += __shfl_xor_sync(0xffffffffu, v, 1);
+    v += __shfl_xor_sync(0xffffffffu, v, 2);
+    if (q4 == 0) sm[warp * 16 + 8 * m + g] = mx[m], sm[64 + warp * 16 + 8 * m + g] = v;
+#pragma unroll
+    for (int u = 0; u < NT; ++u)
+      *reinterpret_cast<float2*>(so + (warp * 16 + 8 * m + g) * DV + u * 8 + q4 * 2) =
+          make_float2(o[u][2 * m], o[u][2 * m + 1]);
+  }
+  __syncthreads();
+  constexpr int C = DV / 4;  // threads per row, four columns each
+  for (int r = threadIdx.x / C; r < R; r += kT / C) {
+    const int col = threadIdx.x % C * 4;
+    float res[4], ll = 0.f, mm = -INFINITY;
+    float4 first;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const int row = 8 * m + r;
+      mm = fmaxf(fmaxf(sm[row], sm[16 + row]), fmaxf(sm[32 + row], sm[48 + row]));
+      const float sub = mm == -INFINITY ? 0.f : mm;
+      ll = 0.f;
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float f = ptx::ex2(sm[w * 16 + row] - sub);
+        const float4 v = *reinterpret_cast<const float4*>(so + (w * 16 + row) * DV + col);
+        ll = fmaf(f, sm[64 + w * 16 + row], ll);
+        x[0] = fmaf(f, v.x, x[0]), x[1] = fmaf(f, v.y, x[1]), x[2] = fmaf(f, v.z, x[2]), x[3] = fmaf(f, v.w, x[3]);
+      }
+      if (nsplit > 1) {
+        float* w = ws + (((h0 + r) * 2 + m) * nsplit + split) * (DV + 2);
+#pragma unroll
+        for (int y = 0; y < 4; y += 2) *reinterpret_cast<float2*>(w + col + y) = make_float2(x[y], x[y + 1]);
+        if (col == 0) w[DV] = mm, w[DV + 1] = ll;
+      } else {
+        const float inv = ll > 0.f ? 1.f / ll : 0.f;
+        if (m == 0) {
+          first = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+        } else {
+          const float f = lam[n * G + r0 + r] * inv;
+          res[0] = first.x - f * x[0], res[1] = first.y - f * x[1];
+          res[2] = first.z - f * x[2], res[3] = first.w - f * x[3];
+          *reinterpret_cast<uint2*>(O + (h0 + r) * DV + col) =
+              make_uint2(ptx::pack_bf16(res[0], res[1]), ptx::pack_bf16(res[2], res[3]));
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------- float32
+template <int D>
 __global__ void __launch_bounds__(kT)
-    decode_kernel(const T* __restrict__ Q, const T* __restrict__ K, const T* __restrict__ V,
-                  const float* __restrict__ lam, const int* __restrict__ lens, T* __restrict__ O,
+    decode_kernel(const float* __restrict__ Q, const float* __restrict__ K, const float* __restrict__ V,
+                  const float* __restrict__ lam, const int* __restrict__ lens, float* __restrict__ O,
                   float* __restrict__ ws, int64_t cap, int H, int G, int rows, int nsplit, int64_t win, float c) {
   constexpr int DV = 2 * D, PD = D + 4, PV = DV;
   constexpr int VC = DV / 64;  // a thread's columns: (t & 63) + 64 v of map t >> 6
@@ -180,7 +406,7 @@ __global__ void __launch_bounds__(kT)
         const float lm = lam[n * G + r0 + r];
 #pragma unroll
         for (int v = 0; v < VC; ++v)
-          st1(O + (h0 + r) * DV + pc + 64 * v, acc[r][v] - lm * x2[r * DV + pc + 64 * v]);
+          *(O + (h0 + r) * DV + pc + 64 * v) = acc[r][v] - lm * x2[r * DV + pc + 64 * v];
       }
   }
 }
@@ -209,17 +435,32 @@ __global__ void __launch_bounds__(DV)
   st1(O + bh * DV + threadIdx.x, o[0] - lam[bh % H] * o[1]);
 }
 
-template <int D, typename T>
+template <int D>
 cudaError_t run(const Problem& p, const void* Q, const void* K, const void* V, const float* lam, const int* lens,
                 void* O, float* ws, cudaStream_t st) {
   const Plan q = make_plan(p);
-  decode_kernel<D, T><<<static_cast<unsigned>(p.BHkv * q.chunks * q.nsplit), kT, 0, st>>>(
-      static_cast<const T*>(Q), static_cast<const T*>(K), static_cast<const T*>(V), lam, lens, static_cast<T*>(O), ws,
-      p.N, static_cast<int>(p.H), p.group, q.rows, q.nsplit, p.window, p.scale * kLog2e);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || q.nsplit == 1) return e;
-  join_kernel<2 * D, T><<<static_cast<unsigned>(p.BH), 2 * D, 0, st>>>(ws, lam, static_cast<T*>(O),
-                                                                      static_cast<int>(p.H), q.nsplit);
+  const unsigned grid = static_cast<unsigned>(p.BHkv * q.chunks * q.nsplit);
+  const int H = static_cast<int>(p.H);
+  const float c = p.scale * kLog2e;
+  cudaError_t e;
+  if (p.dtype == ATTN_BF16) {
+    using T = __nv_bfloat16;
+    constexpr int smem = NS * Stage<D>::bytes;
+    e = cudaFuncSetAttribute(mma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    mma_kernel<D><<<grid, kT, smem, st>>>(static_cast<const T*>(Q), static_cast<const T*>(K), static_cast<const T*>(V),
+                                          lam, lens, static_cast<T*>(O), ws, p.N, H, p.group, q.rows, q.nsplit,
+                                          p.window, c);
+    if ((e = cudaGetLastError()) != cudaSuccess || q.nsplit == 1) return e;
+    join_kernel<2 * D><<<static_cast<unsigned>(p.BH), 2 * D, 0, st>>>(ws, lam, static_cast<T*>(O), H, q.nsplit);
+  } else {
+    using T = float;
+    decode_kernel<D><<<grid, kT, 0, st>>>(static_cast<const T*>(Q), static_cast<const T*>(K), static_cast<const T*>(V),
+                                          lam, lens, static_cast<T*>(O), ws, p.N, H, p.group, q.rows, q.nsplit,
+                                          p.window, c);
+    if ((e = cudaGetLastError()) != cudaSuccess || q.nsplit == 1) return e;
+    join_kernel<2 * D><<<static_cast<unsigned>(p.BH), 2 * D, 0, st>>>(ws, lam, static_cast<T*>(O), H, q.nsplit);
+  }
   return cudaGetLastError();
 }
 
@@ -232,12 +473,8 @@ size_t diff_decode_bytes(const Problem& p) {
 
 cudaError_t diff_decode(const Problem& p, const void* Q, const void* K, const void* V, const float* lam,
                         const int* lens, void* O, void* ws, cudaStream_t st) {
-  float* w = static_cast<float*>(ws);
-  if (p.dtype == ATTN_BF16)
-    return p.d == 32 ? run<32, __nv_bfloat16>(p, Q, K, V, lam, lens, O, w, st)
-                     : run<64, __nv_bfloat16>(p, Q, K, V, lam, lens, O, w, st);
-  return p.d == 32 ? run<32, float>(p, Q, K, V, lam, lens, O, w, st)
-                   : run<64, float>(p, Q, K, V, lam, lens, O, w, st);
+  return p.d == 32 ? run<32>(p, Q, K, V, lam, lens, O, static_cast<float*>(ws), st)
+                   : run<64>(p, Q, K, V, lam, lens, O, static_cast<float*>(ws), st);
 }
 
 }  // namespace fbd
