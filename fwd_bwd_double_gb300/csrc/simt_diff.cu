@@ -1,19 +1,22 @@
 // Differential attention forward and backward on CUDA cores in fp32 (float32 inputs).
 //
 //   A_m = softmax(s Q_m K_m^T + mask), O = (A_1 - lam A_2) V,
-// one block of 64 query rows per CTA, both maps' running maxima and sums kept per row
+// one block of 32 query rows per CTA, both maps' running maxima and sums kept per row
 // while 32-key tiles stream through shared memory; V's tile serves both maps.  The
 // backward recomputes P from the stored log-sum-exps in two passes over the same tiles:
 // with dP = dO V^T, D_2 = dO.O_2, D_1 = dO.O + lam D_2 and w = (1, -lam)
 //   dS_m = w_m P_m (dP - D_m),  dQ_m = s dS_m K_m,  dK_m = s dS_m^T Q_m,
 //   dV = (P_1 - lam P_2)^T dO,  dlam = -sum P_2 dP.
-// One kernel does both passes: it holds 64 rows of one side (queries, or keys) and
+// One kernel does both passes: it holds 32 rows of one side (queries, or keys) and
 // streams 32 rows of the other, and forms the score tiles [held x streamed]; every
 // output is written once and summed in a fixed order.
 //
-// Each of the 256 threads owns 4 held rows: 4 x 2 elements of a score tile, and
+// Each of the 128 threads owns 4 held rows: 4 x 2 elements of a score tile, and
 // 4 x (width / 16) columns of an accumulator, so that a k-step of four does 32 to 64
-// multiply-adds on 6 to 8 16-byte shared-memory reads.
+// multiply-adds on 6 to 8 16-byte shared-memory reads.  The streamed tiles come by
+// asynchronous copies into two buffers, the next one while this one is used; two (backward) or
+// three CTAs share an SM.  (Blocks of 64 rows without the second buffer: 667 against 372 us
+// for the backward of B1 H6 N1000 d64.)
 #include "diff.h"
 #include "ptx.cuh"
 #include "tc_common.cuh"
@@ -21,9 +24,9 @@
 namespace fbd {
 namespace {
 
-constexpr int BQ = 64;   // held rows
+constexpr int BQ = 32;   // held rows
 constexpr int BK = 32;   // streamed rows
-constexpr int kT = 256;  // threads: 16 (ty: 4 held rows each) x 16 (tx)
+constexpr int kT = 128;  // threads: 8 (ty: 4 held rows each) x 16 (tx)
 constexpr int PP = BK + 4;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -47,6 +50,22 @@ __device__ __forceinline__ void load_tile(float* dst, const float* src, int64_t 
     *reinterpret_cast<float4*>(dst + r * Pitch<D>::v + c) = make_float4(x[0], x[1], x[2], x[3]);
   }
 }
+// The same by asynchronous copies (zeros past N: nothing is read there).
+template <int D, int R>
+__device__ __forceinline__ void copy_tile(float* dst, const float* src, int64_t r0, int64_t N) {
+  constexpr int C = D / 4;
+  const uint32_t d = ptx::smem_u32(dst);
+#pragma unroll
+  for (int v = 0; v < R * C / kT; ++v) {
+    const int u = v * kT + threadIdx.x, r = u / C, c = (u % C) * 4;
+    const bool in = r0 + r < N;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d + (r * Pitch<D>::v + c) * 4),
+                 "l"(src + (in ? r0 + r : 0) * D + c), "r"(in ? 16 : 0)
+                 : "memory");
+  }
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ float dot4(float4 a, float4 b, float s) {
   return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, s))));
 }
@@ -109,7 +128,7 @@ __device__ __forceinline__ void store_row(float* dst, const float (&x)[W], float
 
 template <int D>
 constexpr size_t fwd_smem() {
-  return sizeof(float) * (2 * BQ * Pitch<D>::v + 2 * BK * Pitch<D>::v + BK * Pitch<2 * D>::v + 2 * BQ * PP);
+  return sizeof(float) * (2 * BQ * Pitch<D>::v + 2 * (2 * BK * Pitch<D>::v + BK * Pitch<2 * D>::v) + 2 * BQ * PP);
 }
 
 template <int D>
@@ -120,9 +139,9 @@ __global__ void __launch_bounds__(kT, 2)
   constexpr int DV = 2 * D, WV = DV / 16;
   extern __shared__ __align__(16) float sh[];
   float* sQ = sh;                                // [2][BQ]
-  float* sK = sQ + 2 * BQ * Pitch<D>::v;         // [2][BK]
-  float* sV = sK + 2 * BK * Pitch<D>::v;         // [BK]
-  float* sP = sV + BK * Pitch<DV>::v;            // [2][BQ]
+  constexpr int kTile = 2 * BK * Pitch<D>::v + BK * Pitch<DV>::v;  // K_1, K_2, V
+  float* sB = sQ + 2 * BQ * Pitch<D>::v;         // two tiles
+  float* sP = sB + 2 * kTile;                    // [2][BQ]
   const tc::Order ord = tc::grid_order(BH, nqb);
   const int64_t bh = ord.bh, kvh = bh / G;
   const int64_t q0 = static_cast<int64_t>(nqb - 1 - ord.k) * BQ;  // heaviest blocks first
@@ -145,12 +164,19 @@ __global__ void __launch_bounds__(kT, 2)
 #pragma unroll
       for (int u = 0; u < WV; ++u) acc[m][r][u] = 0.f;
     }
-  for (int64_t k0 = kbeg; k0 < kend; k0 += BK) {
-    __syncthreads();
+  auto load = [&](int64_t k0, float* dst) {
 #pragma unroll
-    for (int m = 0; m < 2; ++m) load_tile<D, BK>(sK + m * BK * Pitch<D>::v, K + (2 * kvh + m) * N * D, k0, N);
-    load_tile<DV, BK>(sV, V + kvh * N * DV, k0, N);
-    __syncthreads();
+    for (int m = 0; m < 2; ++m) copy_tile<D, BK>(dst + m * BK * Pitch<D>::v, K + (2 * kvh + m) * N * D, k0, N);
+    copy_tile<DV, BK>(dst + 2 * BK * Pitch<D>::v, V + kvh * N * DV, k0, N);
+    copies_commit();
+  };
+  load(kbeg, sB);
+  int buf = 0;
+  for (int64_t k0 = kbeg; k0 < kend; k0 += BK, buf ^= 1) {
+    copies_wait();
+    __syncthreads();  // this tile is there, the other buffer's has been read
+    if (k0 + BK < kend) load(k0 + BK, sB + (buf ^ 1) * kTile);
+    const float *sK = sB + buf * kTile, *sV = sK + 2 * BK * Pitch<D>::v;
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       float s[4][2];
@@ -246,14 +272,14 @@ __global__ void __launch_bounds__(256)
 
 template <int D>
 constexpr size_t bwd_smem() {
-  return sizeof(float) * ((2 * BQ + 2 * BK) * Pitch<D>::v + (BQ + BK) * Pitch<2 * D>::v + 3 * BQ * PP + 4 * BK + 8);
+  return sizeof(float) * ((2 * BQ + 4 * BK) * Pitch<D>::v + (BQ + 2 * BK) * Pitch<2 * D>::v + 2 * BQ * PP + 8 * BK + 8);
 }
 
 // COL = false: holds queries (Q_m, dO), streams keys (K_m, V), writes dQ_m and the block's
 // share of dlam.  COL = true: holds keys, streams the queries of the G query heads that
 // share them, writes dK_m, dV.
 template <int D, bool COL>
-__global__ void __launch_bounds__(kT, 1)
+__global__ void __launch_bounds__(kT, 2)
     bwd_kernel(const float* __restrict__ Q, const float* __restrict__ K, const float* __restrict__ V, const float* __restrict__ dO,
                const float* __restrict__ lam, const float4* __restrict__ stats, float* __restrict__ out1,
                float* __restrict__ outV, float* __restrict__ partial, int64_t N, int64_t H, int nblk, int slices, int G,
@@ -262,12 +288,11 @@ __global__ void __launch_bounds__(kT, 1)
   extern __shared__ __align__(16) float sh[];
   float* sA = sh;                      // [2][BQ] held Q_m or K_m
   float* sAV = sA + 2 * BQ * PD;       // [BQ]    held dO or V
-  float* sB = sAV + BQ * Pitch<DV>::v; // [2][BK] streamed K_m or Q_m
-  float* sBV = sB + 2 * BK * PD;       // [BK]    streamed V or dO
-  float* sT = sBV + BK * Pitch<DV>::v; // [2][BQ] dS_m
-  float* sW = sT + 2 * BQ * PP;        // [BQ]    P_1 - lam P_2 (COL)
-  float4* sSt = reinterpret_cast<float4*>(sW + BQ * PP);  // [BK] streamed rows' statistics (COL)
-  float* sRed = reinterpret_cast<float*>(sSt + BK);       // [8]
+  constexpr int kTile = 2 * BK * PD + BK * Pitch<DV>::v;  // K_m or Q_m, and V or dO
+  float* sS = sAV + BQ * Pitch<DV>::v; // two streamed tiles
+  float* sT = sS + 2 * kTile;          // [2][BQ] dS_m; then in the first P_1 - lam P_2 (COL)
+  float4* sSt0 = reinterpret_cast<float4*>(sT + 2 * BQ * PP);  // [2][BK] streamed rows' statistics (COL)
+  float* sRed = reinterpret_cast<float*>(sSt0 + 2 * BK);       // [4]
   const tc::Order ord = tc::grid_order(slices, nblk);
   const int64_t sl = ord.bh;                                      // query slice, or key/value slice
   const int64_t blk = COL || !causal ? ord.k : nblk - 1 - ord.k;  // heaviest first
@@ -309,19 +334,36 @@ __global__ void __launch_bounds__(kT, 1)
     }
   }
   float dl = 0.f;
+  auto load = [&](int g, int64_t k0, int buf) {
+    const int64_t qs = COL ? kvh * G + g : sl;
+    const float* strM = COL ? Q + 2 * qs * N * D : K + 2 * kvh * N * D;
+    const float* strV = COL ? dO + qs * N * DV : V + kvh * N * DV;
+    float* dst = sS + buf * kTile;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) copy_tile<D, BK>(dst + m * BK * PD, strM + m * N * D, k0, N);
+    copy_tile<DV, BK>(dst + 2 * BK * PD, strV, k0, N);
+    if (COL && threadIdx.x < BK) {
+      const bool in = k0 + threadIdx.x < N;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_u32(sSt0 + buf * BK + threadIdx.x)),
+                   "l"(stats + qs * N + (in ? k0 + threadIdx.x : 0)), "r"(in ? 16 : 0)
+                   : "memory");
+    }
+    copies_commit();
+  };
+  load(0, b0, 0);
+  int buf = 0;
   for (int g = 0; g < (COL ? G : 1); ++g) {
     const int64_t qs = COL ? kvh * G + g : sl;  // query slice
     const float lm = lam[qs % H];
-    const float* strM = COL ? Q + 2 * qs * N * D : K + 2 * kvh * N * D;
-    const float* strV = COL ? dO + qs * N * DV : V + kvh * N * DV;
-    for (int64_t k0 = b0; k0 < b1; k0 += BK) {
-      __syncthreads();
-#pragma unroll
-      for (int m = 0; m < 2; ++m) load_tile<D, BK>(sB + m * BK * PD, strM + m * N * D, k0, N);
-      load_tile<DV, BK>(sBV, strV, k0, N);
-      if (COL && threadIdx.x < BK)
-        sSt[threadIdx.x] = k0 + threadIdx.x < N ? stats[qs * N + k0 + threadIdx.x] : make_float4(0.f, 0.f, 0.f, 0.f);
-      __syncthreads();
+    for (int64_t k0 = b0; k0 < b1; k0 += BK, buf ^= 1) {
+      copies_wait();
+      __syncthreads();  // this tile is there, the other buffer's has been read
+      if (k0 + BK < b1)
+        load(g, k0 + BK, buf ^ 1);
+      else if (COL && g + 1 < G)
+        load(g + 1, b0, buf ^ 1);
+      const float *sB = sS + buf * kTile, *sBV = sB + 2 * BK * PD;
+      const float4* sSt = sSt0 + buf * BK;
       float dp[4][2], w[4][2];
       scores<DV>(sAV, sBV, ty, tx, dp);
 #pragma unroll
@@ -346,7 +388,6 @@ __global__ void __launch_bounds__(kT, 1)
             sT[m * BQ * PP + (4 * ty + r) * PP + tx + 16 * u] = ds;
             if (COL) {
               w[r][u] = m == 0 ? p : fmaf(wm, p, w[r][u]);
-              if (m == 1) sW[(4 * ty + r) * PP + tx + 16 * u] = w[r][u];
             }
           }
         }
@@ -354,7 +395,15 @@ __global__ void __launch_bounds__(kT, 1)
       __syncwarp();
 #pragma unroll
       for (int m = 0; m < 2; ++m) accumulate<D>(sT + m * BQ * PP, sB + m * BK * PD, ty, tx, acc[m]);
-      if constexpr (COL) accumulate<DV>(sW, sBV, ty, tx, accV);
+      if constexpr (COL) {
+        __syncwarp();  // a row of sT is written and read by the 16 threads of one ty, in one warp
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) sT[(4 * ty + r) * PP + tx + 16 * u] = w[r][u];
+        __syncwarp();
+        accumulate<DV>(sT, sBV, ty, tx, accV);
+      }
     }
   }
 #pragma unroll
