@@ -249,6 +249,10 @@ __global__ void __launch_bounds__((kCW + 2) * 32, 1)
       const bool low = WIN && causal && kb * BW < lo_last;
       const int klim = (causal ? row : N - 1) - kb * BW - c0;  // last visible key, from this warp's first
       const int klo = (WIN && causal) ? lo_row - kb * BW - c0 : 0;
+      // bounds grow with the row: the warp's first row has the first last key, its last row the
+      // last first one
+      const bool masked = (diag || low) && (kC - 1 > __shfl_sync(0xffffffffu, klim, 0) ||
+                                            0 < __shfl_sync(0xffffffffu, klo, 31));
       uint32_t dp[32];
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
@@ -275,7 +279,7 @@ __global__ void __launch_bounds__((kCW + 2) * 32, 1)
           ptx::tc_fence_before();
           ptx::mbar_arrive(dp_cons);
         }
-        if (diag || low) {
+        if (masked) {
 #pragma unroll
           for (int u = 0; u < 32; ++u)
             if (u > klim || u < klo) v[u] = 0u;
@@ -287,7 +291,7 @@ __global__ void __launch_bounds__((kCW + 2) * 32, 1)
           const float2 d = tc::unpk2(tc::mul2(P, tc::add2(g, nD[m])));
           pk[u >> 1] = ptx::pack_bf16(d.x, d.y);
         }
-        if ((diag || low) && one) {
+        if (masked && one) {
 #pragma unroll
           for (int u = 0; u < 16; ++u) pk[u] = 0u;
         }
@@ -381,7 +385,6 @@ __global__ void __launch_bounds__(kColThreads, 1)
   const int kb = ord.k;            // first key blocks have the most query blocks: first
   const int i0 = causal ? kb : 0;  // first query block that sees this key block
   const int ntile = ((WIN && causal) ? bd.key_hi(kvh, min(kb * BW + BW - 1, N - 1)) / BW + 1 : nb) - i0;
-  const int hi_first = (WIN && causal) ? bd.key_hi(kvh, kb * BW) : 0;  // the first key's last query
   const int nt = G * ntile;        // tile t = (h, i - i0)
 
   if (threadIdx.x == 0) {
@@ -541,6 +544,7 @@ __global__ void __launch_bounds__(kColThreads, 1)
     const int c0 = cg * kC;
     const uint64_t c2 = tc::pk2f(c, c);
     const int khi = (WIN && causal) ? bd.key_hi(kvh, key) : 0;  // the key's last query
+    const int khi_first = __shfl_sync(0xffffffffu, khi, 0);     // (they grow with the key)
     const uint32_t sT = ptx::smem_u32(sm + L::oT) + static_cast<uint32_t>((c0 >> 6) * kSlab);
     const float* sSt = reinterpret_cast<const float*>(sm + L::oStat) + c0;
     int t = 0;
@@ -550,9 +554,10 @@ __global__ void __launch_bounds__(kColThreads, 1)
       const uint64_t w2 = tc::pk2f(wl, wl);
       for (int i = i0; i < i0 + ntile; ++i, ++t) {
         wait(st_full, t & 1);
-        // the diagonal block, a block past the first key's last query, past N, or with keys past N
-        const bool masked = (causal && i == kb) || (WIN && causal && i * BW + BW - 1 > hi_first) ||
-                            i * BW + c0 + kC > N || (!causal && kb * BW + BW > N);
+        // Some of the warp's 32 keys x 32 queries are not visible: queries before the last key,
+        // past the first key's last query, past N, or keys past N.
+        const int q0 = i * BW + c0, k0 = kb * BW + qd * 32;
+        const bool masked = (causal ? q0 < k0 + 31 || (WIN && q0 + kC - 1 > khi_first) : k0 + 32 > N) || q0 + kC > N;
         auto probs = [&](auto mk, int m, uint32_t (&v)[32]) {
           wait(&s_full[m], t & 1);
           ptx::tc_fence_after();

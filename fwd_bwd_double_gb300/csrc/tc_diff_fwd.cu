@@ -28,7 +28,11 @@ __device__ unsigned int g_err = 0;
 
 constexpr int BM = 128, BN = 128;
 constexpr int NS = 3;
-constexpr int kThreads = 320;  // warps 0-3: map 1, 4-7: map 2, 8: TMA, 9: MMA
+// Warps 0-3: map 1, 4-7: map 2, 8: TMA, 9: MMA.  384 threads launched with 168 registers; the
+// softmax warps (a row of 128 scores each thread) take 208, the third warpgroup's keep 80:
+// 256 * 208 + 128 * 80 <= 384 * 168.
+constexpr int kThreads = 384;
+constexpr int kRegs = 208, kRegsOther = 80;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;  // log2 of the largest P
 
@@ -103,6 +107,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const ptx::BoundedWait wait{abort_flag, &g_err};
   const bool ok = *abort_flag == 0;
 
+  if (warp >= 8) ptx::setmaxnreg_dec<kRegsOther>();
   if (warp == 8) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0 && ok) {
@@ -169,7 +174,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ptx::mma_commit_e(o_full);
     }
-  } else {
+  } else if (warp < 8) {
+    ptx::setmaxnreg_inc<kRegs>();
     // --------------------------- softmax of map m: thread r owns query row r
     const int m = warp >> 2;
     const int r = threadIdx.x & 127;
@@ -193,11 +199,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int ch = 0; ch < 4; ++ch) ptx::tmem_ld32(tS + ch * 32, v[ch]);
       ptx::tmem_wait_ld();
       if (diag || low) {
+        // bounds grow with the row: the warp's first row has the first last key, its last row
+        // the last first one, and 32 keys between the two need no masking
+        const int klim0 = __shfl_sync(0xffffffffu, klim, 0), klo31 = __shfl_sync(0xffffffffu, klo, 31);
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch)
+          if (ch * 32 + 31 > klim0 || ch * 32 < klo31) {
 #pragma unroll
-          for (int t = 0; t < 32; ++t)
-            if (ch * 32 + t > klim || ch * 32 + t < klo) v[ch][t] = __float_as_uint(-INFINITY);
+            for (int t = 0; t < 32; ++t)
+              if (ch * 32 + t > klim || ch * 32 + t < klo) v[ch][t] = __float_as_uint(-INFINITY);
+          }
       }
       float mx[8];
 #pragma unroll
