@@ -26,6 +26,12 @@ __device__ __forceinline__ uint64_t mnmajor_desc(uint32_t base, int rows, int k)
   return ptx::sdesc_sw128(base + k * 16 * 128, rows * 128, 1024);
 }
 
+// Byte offset of (row, 16-byte chunk) in a 128-byte-swizzled tile of 128-byte lines (the layout
+// a TMA box with 128-byte swizzle reads and writes; tile 1024-byte aligned).
+__device__ __forceinline__ uint32_t sw128(int row, int chunk) {
+  return static_cast<uint32_t>(row * 128 + ((chunk ^ (row & 7)) << 4));
+}
+
 // A descriptor moved by `bytes` within shared memory: the start address sits in
 // bits 0-13 of the low word in 16-byte units, and every operand of these kernels
 // lies in the first 256 KB, so the move never carries out of the low word.  The

@@ -48,11 +48,6 @@ constexpr int kPlanes = 5;       // row statistics: -L_1 log2 e, -L_2 log2 e, -D
 constexpr int kSlab = BW * 128;  // 64 bf16 columns of 128 rows: 16 KB
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Byte offset of (row, 16-byte chunk) in a 128-byte-swizzled tile of 128-byte lines.
-__device__ __forceinline__ uint32_t sw128(int row, int chunk) {
-  return static_cast<uint32_t>(row * 128 + ((chunk ^ (row & 7)) << 4));
-}
-
 __device__ __forceinline__ void st_shared4(uint32_t a, const uint32_t* v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
 }
@@ -71,6 +66,16 @@ struct Lay {
 };
 static_assert(Lay<128, true>::bytes <= 232448, "shared memory");
 
+// 16 columns (from c0) of a thread's row r as bf16 into its 64-column tiles, scaled.
+__device__ __forceinline__ void stage16(uint8_t* tiles, int r, int c0, const uint32_t (&a)[16], float f) {
+  uint32_t o[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) o[u] = ptx::pack_bf16(f * tc::f(a[2 * u]), f * tc::f(a[2 * u + 1]));
+  uint8_t* t = tiles + (c0 >> 6) * kSlab;
+  *reinterpret_cast<uint4*>(t + tc::sw128(r, (c0 & 63) >> 3)) = make_uint4(o[0], o[1], o[2], o[3]);
+  *reinterpret_cast<uint4*>(t + tc::sw128(r, ((c0 & 63) >> 3) + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
 __device__ __forceinline__ void init_abort(uint8_t* sm, volatile int* abort_flag) {
   *abort_flag = (ptx::smem_u32(sm) & 1023u) ? 1 : 0;  // the swizzled tiles need 1024-byte alignment
   if (*abort_flag) atomicOr(&g_err, FBD_ERR_TIMEOUT);
@@ -83,8 +88,8 @@ template <int DV, bool WIN>
 __global__ void __launch_bounds__((kCW + 2) * 32, 1)
     row_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
                const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-               const float* __restrict__ lam, const float* __restrict__ stats, __nv_bfloat16* __restrict__ dQ,
-               float* __restrict__ partial, int N, int H, int nrb, int BH, float scale, float c, int causal, Band bd,
+               const __grid_constant__ CUtensorMap tmdQ, const float* __restrict__ lam,
+               const float* __restrict__ stats, float* __restrict__ partial, int N, int H, int nrb, int BH, float scale, float c, int causal, Band bd,
                int G) {
   using L = Lay<DV, false>;
   constexpr int D = DV / 2;
@@ -321,14 +326,15 @@ __global__ void __launch_bounds__((kCW + 2) * 32, 1)
       uint32_t a[16];
       ptx::tmem_ld16(tmem + cdQ + m * 64 + cg * 16 + lo, a);
       ptx::tmem_wait_ld();
-      if (row < N && cg * 16 < D) {
-        uint32_t o[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) o[u] = ptx::pack_bf16(f[m] * tc::f(a[2 * u]), f[m] * tc::f(a[2 * u + 1]));
-        uint4* p = reinterpret_cast<uint4*>(dQ + ((2 * static_cast<int64_t>(bh) + m) * N + row) * D + cg * 16);
-        p[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        p[1] = make_uint4(o[4], o[5], o[6], o[7]);
-      }
+      stage16(sm + L::oStage + m * kSlab, qd * 32 + lane, cg * 16, a, f[m]);
+    }
+    // (the stages are free: every block has been read)
+    ptx::fence_proxy_async_smem();
+    tc::named_sync(1, kCW * 32);
+    if (threadIdx.x == 0) {
+      for (int m = 0; m < 2; ++m) ptx::tma_store_3d(&tmdQ, sm + L::oStage + m * kSlab, 0, rb * BW, 2 * bh + m);
+      ptx::bulk_commit_group();
+      ptx::bulk_wait_group_read0();
     }
   }
 
@@ -357,8 +363,8 @@ template <int DV, bool WIN>
 __global__ void __launch_bounds__(kColThreads, 1)
     col_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
-               const float* __restrict__ lam, const float* __restrict__ stats, __nv_bfloat16* __restrict__ dK,
-               __nv_bfloat16* __restrict__ dV, int N, int H, int nb, int BHkv, float scale, float c, int causal,
+               const __grid_constant__ CUtensorMap tmdK, const __grid_constant__ CUtensorMap tmdV,
+               const float* __restrict__ lam, const float* __restrict__ stats, int N, int H, int nb, int BHkv, float scale, float c, int causal,
                Band bd, int G) {
   using L = Lay<DV, true>;
   constexpr int D = DV / 2;
@@ -628,7 +634,7 @@ __global__ void __launch_bounds__(kColThreads, 1)
             ptx::tmem_st8(tmem + cX + c0 + 16 * x + 8 + lo, d1);
 #pragma unroll
             for (int y = 0; y < 2; ++y)
-              st_shared4(sT + sw128(r, ((c0 & 63) >> 3) + 2 * x + y), &d2[4 * y]);
+              st_shared4(sT + tc::sw128(r, ((c0 & 63) >> 3) + 2 * x + y), &d2[4 * y]);
           }
         };
         if (masked)
@@ -648,28 +654,25 @@ __global__ void __launch_bounds__(kColThreads, 1)
       uint32_t a[16];
       ptx::tmem_ld16(tmem + cdK + m * 64 + cg * 16 + lo, a);
       ptx::tmem_wait_ld();
-      if (key < N && cg * 16 < D) {
-        uint32_t o[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) o[u] = ptx::pack_bf16(scale * tc::f(a[2 * u]), scale * tc::f(a[2 * u + 1]));
-        uint4* p = reinterpret_cast<uint4*>(dK + ((2 * static_cast<int64_t>(kvh) + m) * N + key) * D + cg * 16);
-        p[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        p[1] = make_uint4(o[4], o[5], o[6], o[7]);
-      }
+      stage16(sm + L::oStage + m * kSlab, r, cg * 16, a, scale);
     }
     constexpr int VG = DV / 4;  // dV columns per thread
 #pragma unroll
     for (int u = 0; u < VG / 16; ++u) {
-      uint32_t a[16], o[8];
+      uint32_t a[16];
       ptx::tmem_ld16(tmem + cdV + cg * VG + u * 16 + lo, a);
       ptx::tmem_wait_ld();
-#pragma unroll
-      for (int x = 0; x < 8; ++x) o[x] = ptx::pack_bf16(tc::f(a[2 * x]), tc::f(a[2 * x + 1]));
-      if (key < N) {
-        uint4* p = reinterpret_cast<uint4*>(dV + (static_cast<int64_t>(kvh) * N + key) * DV + cg * VG + u * 16);
-        p[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        p[1] = make_uint4(o[4], o[5], o[6], o[7]);
-      }
+      stage16(sm + L::oStage + 2 * kSlab, r, cg * VG + u * 16, a, 1.f);
+    }
+    // (the stages are free: every block has been read)
+    ptx::fence_proxy_async_smem();
+    tc::named_sync(1, kCW * 32);
+    if (threadIdx.x == 0) {
+      for (int m = 0; m < 2; ++m) ptx::tma_store_3d(&tmdK, sm + L::oStage + m * kSlab, 0, kb * BW, 2 * kvh + m);
+      for (int u = 0; u < DV / 64; ++u)
+        ptx::tma_store_3d(&tmdV, sm + L::oStage + (2 + u) * kSlab, u * 64, kb * BW, kvh);
+      ptx::bulk_commit_group();
+      ptx::bulk_wait_group_read0();
     }
   }
 
@@ -750,9 +753,11 @@ cudaError_t run(const Problem& p, const void* Q, const void* K, const void* V, c
   const int64_t Np = blocks(N) * BW;
   float* stats = static_cast<float*>(ws);          // [BH][blocks][kPlanes][BW]
   float* partial = stats + BH * kPlanes * Np;      // [BH][blocks]
-  alignas(64) CUtensorMap k, v, q, g;
+  alignas(64) CUtensorMap k, v, q, g, mdq, mdk, mdv;
   if (!make_tmap_bf16(&q, Q, N, D, 2 * BH, BW) || !make_tmap_bf16(&g, dO, N, DV, BH, BW) ||
-      !make_tmap_bf16(&k, K, N, D, 2 * p.BHkv, BW) || !make_tmap_bf16(&v, V, N, DV, p.BHkv, BW))
+      !make_tmap_bf16(&k, K, N, D, 2 * p.BHkv, BW) || !make_tmap_bf16(&v, V, N, DV, p.BHkv, BW) ||
+      !make_tmap_bf16(&mdq, dQ, N, D, 2 * BH, BW) || !make_tmap_bf16(&mdk, dK, N, D, 2 * p.BHkv, BW) ||
+      !make_tmap_bf16(&mdv, dV, N, DV, p.BHkv, BW))
     return cudaErrorInvalidValue;
   const int64_t threads = BH * Np * 16;
   prep_kernel<DV><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, st>>>(
@@ -768,11 +773,11 @@ cudaError_t run(const Problem& p, const void* Q, const void* K, const void* V, c
   if ((e = cudaFuncSetAttribute(row, cudaFuncAttributeMaxDynamicSharedMemorySize, rs)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(col, cudaFuncAttributeMaxDynamicSharedMemorySize, cs)) != cudaSuccess) return e;
   row<<<static_cast<unsigned>(nb * BH), (kCW + 2) * 32, rs, st>>>(
-      q, g, k, v, lam, stats, static_cast<__nv_bfloat16*>(dQ), partial, n, H, nb, static_cast<int>(BH), p.scale, c,
+      q, g, k, v, mdq, lam, stats, partial, n, H, nb, static_cast<int>(BH), p.scale, c,
       p.causal, make_band(p, eff_window_tc(p), false), p.group);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   col<<<static_cast<unsigned>(nb * p.BHkv), kColThreads, cs, st>>>(
-      k, v, q, g, lam, stats, static_cast<__nv_bfloat16*>(dK), static_cast<__nv_bfloat16*>(dV), n, H, nb,
+      k, v, q, g, mdk, mdv, lam, stats, n, H, nb,
       static_cast<int>(p.BHkv), p.scale, c, p.causal, make_band(p, eff_window_tc(p), true), p.group);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return diff_reduce_dlam(partial, dlam, p.B, p.H, nb, st);
