@@ -42,7 +42,7 @@ constexpr int kC = 32;           // tile columns per compute warp
 // Column pass: 640 threads launched with 96 registers; the compute warps take 104 (each
 // thread's two maps of P alone are 64), the fifth warpgroup's warps keep 64:
 // 512 * 104 + 128 * 64 = 640 * 96.
-constexpr int kColThreads = kCW * 32 + 128;
+constexpr int kThreads = kCW * 32 + 128;
 constexpr int kColRegs = 104, kColRegsOther = 64;
 constexpr int kPlanes = 5;       // row statistics: -L_1 log2 e, -L_2 log2 e, -D_1, lam D_2, -D_2
 constexpr int kSlab = BW * 128;  // 64 bf16 columns of 128 rows: 16 KB
@@ -81,16 +81,23 @@ __device__ __forceinline__ void init_abort(uint8_t* sm, volatile int* abort_flag
   if (*abort_flag) atomicOr(&g_err, FBD_ERR_TIMEOUT);
 }
 
+struct Args {
+  const float* lam;
+  const float* stats;
+  float* partial;
+  int N, H, nb, BHkv;
+  float scale, c;
+  int causal;
+  Band bd;  // over key/value slices (the row pass asks by its key/value slice too)
+  int G;
+};
+
 // ------------------------------------------------------------------ row pass
 // TMEM columns: S (S_1, then S_2), dP, dS_1, dS_2 (bf16 pairs), dQ_1, dQ_2.
 // WIN: a banded causal mask is in force (window and/or document bounds).
 template <int DV, bool WIN>
-__global__ void __launch_bounds__((kCW + 2) * 32, 1)
-    row_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
-               const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-               const __grid_constant__ CUtensorMap tmdQ, const float* __restrict__ lam,
-               const float* __restrict__ stats, float* __restrict__ partial, int N, int H, int nrb, int BH, float scale, float c, int causal, Band bd,
-               int G) {
+__device__ __forceinline__ void row_pass(const Args& p, int block, const CUtensorMap& tmQ, const CUtensorMap& tmdO,
+                                         const CUtensorMap& tmK, const CUtensorMap& tmV, const CUtensorMap& tmdQ) {
   using L = Lay<DV, false>;
   constexpr int D = DV / 2;
   constexpr uint32_t cS = 0, cdP = 128, cdS = 256, cdQ = 384;
@@ -112,14 +119,33 @@ __global__ void __launch_bounds__((kCW + 2) * 32, 1)
   float* sRed = reinterpret_cast<float*>(sm + L::oBar + 160);  // [kCW]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const tc::Order ord = tc::grid_order(BH, nrb);
+  const float *lam = p.lam, *stats = p.stats;
+  float* partial = p.partial;
+  const int N = p.N, H = p.H, nrb = p.nb, causal = p.causal, G = p.G, BH = p.BHkv * p.G;
+  const float scale = p.scale, c = p.c;
+  const Band& bd = p.bd;
+  const tc::Order ord = tc::grid_order_at(block, BH, nrb);
   const int bh = ord.bh, kvh = bh / G;
   const int rb = nrb - 1 - ord.k;  // heaviest row blocks first
-  const int j0 = (WIN && causal) ? bd.row_lo(bh, rb * BW) / BW : 0;
-  const int lo_last = (WIN && causal) ? bd.row_lo(bh, min(rb * BW + BW - 1, N - 1)) : 0;
+  const int j0 = (WIN && causal) ? bd.row_lo(kvh, rb * BW) / BW : 0;
+  const int lo_last = (WIN && causal) ? bd.row_lo(kvh, min(rb * BW + BW - 1, N - 1)) : 0;
   const int nt = (causal ? rb + 1 : nrb) - j0;
 
-  if (threadIdx.x == 0) {
+  auto load_v = [&](int t) {
+    const int s = t % NS;
+    ptx::mbar_expect_tx(&v_full[s], L::kV);
+    for (int u = 0; u < DV / 64; ++u)
+      ptx::tma_load_3d(sm + L::oStage + s * L::kBlock + (2 + u) * kSlab, &tmV, &v_full[s], u * 64, (j0 + t) * BW, kvh);
+  };
+  auto load_k = [&](int t) {
+    const int s = t % NS;
+    ptx::mbar_expect_tx(&k_full[s], 2 * kSlab);
+    for (int m = 0; m < 2; ++m)
+      ptx::tma_load_3d(sm + L::oStage + s * L::kBlock + m * kSlab, &tmK, &k_full[s], 0, (j0 + t) * BW, 2 * kvh + m);
+  };
+  // The TMA thread sets the barriers up and starts the first loads before the others are let in
+  // (the TMEM allocation alone takes about a thousand cycles).
+  if (threadIdx.x == kCW * 32) {
     ptx::mbar_init(held_full, 1);
     for (int s = 0; s < NS; ++s) {
       ptx::mbar_init(&k_full[s], 1);
@@ -137,6 +163,16 @@ __global__ void __launch_bounds__((kCW + 2) * 32, 1)
     ptx::mbar_init(dp_cons, kCW * 32);
     init_abort(sm, abort_flag);
     ptx::fence_mbar_init();
+    if (!*abort_flag) {
+      ptx::mbar_expect_tx(held_full, L::kBlock);
+      for (int m = 0; m < 2; ++m) ptx::tma_load_3d(sm + m * kSlab, &tmQ, held_full, 0, rb * BW, 2 * bh + m);
+      for (int u = 0; u < DV / 64; ++u)
+        ptx::tma_load_3d(sm + (2 + u) * kSlab, &tmdO, held_full, u * 64, rb * BW, bh);
+      for (int t = 0; t < nt && t < NS; ++t) {
+        load_k(t);
+        load_v(t);
+      }
+    }
   }
   if (warp == kCW + 1) {
     ptx::tmem_alloc(tmem_slot, 512);
@@ -152,23 +188,12 @@ __global__ void __launch_bounds__((kCW + 2) * 32, 1)
   if (warp == kCW) {
     // ------------------------------------------------------------ TMA loads
     if (lane == 0 && ok) {
-      ptx::prefetch_tmap(&tmK);
-      ptx::prefetch_tmap(&tmV);
-      ptx::mbar_expect_tx(held_full, L::kBlock);
-      for (int m = 0; m < 2; ++m) ptx::tma_load_3d(sm + m * kSlab, &tmQ, held_full, 0, rb * BW, 2 * bh + m);
-      for (int u = 0; u < DV / 64; ++u)
-        ptx::tma_load_3d(sm + (2 + u) * kSlab, &tmdO, held_full, u * 64, rb * BW, bh);
-      for (int t = 0; t < nt; ++t) {
+      for (int t = NS; t < nt; ++t) {
         const int s = t % NS, ph = ((t / NS) - 1) & 1;
-        uint8_t* st = sm + L::oStage + s * L::kBlock;
-        if (t >= NS) wait(&v_empty[s], ph);
-        ptx::mbar_expect_tx(&v_full[s], L::kV);
-        for (int u = 0; u < DV / 64; ++u)
-          ptx::tma_load_3d(st + (2 + u) * kSlab, &tmV, &v_full[s], u * 64, (j0 + t) * BW, kvh);
-        if (t >= NS) wait(&k_empty[s], ph);
-        ptx::mbar_expect_tx(&k_full[s], 2 * kSlab);
-        for (int m = 0; m < 2; ++m)
-          ptx::tma_load_3d(st + m * kSlab, &tmK, &k_full[s], 0, (j0 + t) * BW, 2 * kvh + m);
+        wait(&v_empty[s], ph);
+        load_v(t);
+        wait(&k_empty[s], ph);
+        load_k(t);
       }
     }
   } else if (warp == kCW + 1) {
@@ -236,13 +261,14 @@ __global__ void __launch_bounds__((kCW + 2) * 32, 1)
         ptx::mma_commit_e(&k_empty[t % NS]);
       }
     }
-  } else {
+  } else if (warp < kCW) {
     // ------------------------------------- compute: a query row, 32 keys of a block
     const int qd = warp & 3, cg = warp >> 2, c0 = cg * kC;
     const uint32_t lo = static_cast<uint32_t>(qd * 32) << 16;
     const int row = rb * BW + qd * 32 + lane;
-    const int lo_row = (WIN && causal) ? bd.row_lo(bh, row) : 0;
+    const int lo_row = (WIN && causal) ? bd.row_lo(kvh, row) : 0;
     const float* st = stats + (static_cast<int64_t>(bh) * nrb + rb) * (kPlanes * BW) + qd * 32 + lane;
+    const float lm = lam[bh % H];
     const bool one = st[2 * BW] == -INFINITY;  // the row sees one key: its dS is 0
     const uint64_t c2 = tc::pk2f(c, c);
     const uint64_t nL[2] = {tc::pk2f(st[0], st[0]), tc::pk2f(st[BW], st[BW])};
@@ -318,7 +344,7 @@ __global__ void __launch_bounds__((kCW + 2) * 32, 1)
       if (lane == 0) sRed[warp] = v;
     }
     // dQ_m = s w_m (P_m (dP - D_m)) K_m: the weight -lam of map 2 enters here
-    const float f[2] = {scale, -scale * lam[bh % H]};
+    const float f[2] = {scale, -scale * lm};
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       wait(&dq_done[m], (nt - 1) & 1);
@@ -360,12 +386,9 @@ __global__ void __launch_bounds__((kCW + 2) * 32, 1)
 // next's is dV, dK_1, S_2, dP and the last steps of the CUDA cores.  (dP(t+1) overwrites the
 // operands of dV(t), dK_1(t): products of one thread run in order.)
 template <int DV, bool WIN>
-__global__ void __launch_bounds__(kColThreads, 1)
-    col_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-               const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
-               const __grid_constant__ CUtensorMap tmdK, const __grid_constant__ CUtensorMap tmdV,
-               const float* __restrict__ lam, const float* __restrict__ stats, int N, int H, int nb, int BHkv, float scale, float c, int causal,
-               Band bd, int G) {
+__device__ __forceinline__ void col_pass(const Args& p, int block, const CUtensorMap& tmQ, const CUtensorMap& tmdO,
+                                         const CUtensorMap& tmK, const CUtensorMap& tmV, const CUtensorMap& tmdK,
+                                         const CUtensorMap& tmdV) {
   using L = Lay<DV, true>;
   constexpr int D = DV / 2;
   constexpr uint32_t cS = 0, cX = 128, cdK = 256, cdV = 384;
@@ -386,14 +409,32 @@ __global__ void __launch_bounds__(kColThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const tc::Order ord = tc::grid_order(BHkv, nb);
+  const float *lam = p.lam, *stats = p.stats;
+  const int N = p.N, H = p.H, nb = p.nb, causal = p.causal, G = p.G, BHkv = p.BHkv;
+  const float scale = p.scale, c = p.c;
+  const Band& bd = p.bd;
+  const tc::Order ord = tc::grid_order_at(block, BHkv, nb);
   const int kvh = ord.bh;          // key/value slice; its query heads are kvh * G + h, h < G
   const int kb = ord.k;            // first key blocks have the most query blocks: first
   const int i0 = causal ? kb : 0;  // first query block that sees this key block
   const int ntile = ((WIN && causal) ? bd.key_hi(kvh, min(kb * BW + BW - 1, N - 1)) / BW + 1 : nb) - i0;
   const int nt = G * ntile;        // tile t = (h, i - i0)
 
-  if (threadIdx.x == 0) {
+  auto load_a = [&](int t) {  // Q_1, dO
+    const int s = t % NS, h = t / ntile, i = i0 + t - h * ntile;
+    uint8_t* st = sm + L::oStage + s * L::kBlock;
+    ptx::mbar_expect_tx(&a_full[s], kSlab + L::kV);
+    ptx::tma_load_3d(st, &tmQ, &a_full[s], 0, i * BW, 2 * (kvh * G + h));
+    for (int u = 0; u < DV / 64; ++u)
+      ptx::tma_load_3d(st + (2 + u) * kSlab, &tmdO, &a_full[s], u * 64, i * BW, kvh * G + h);
+  };
+  auto load_b = [&](int t) {  // Q_2
+    const int s = t % NS, h = t / ntile, i = i0 + t - h * ntile;
+    ptx::mbar_expect_tx(&b_full[s], kSlab);
+    ptx::tma_load_3d(sm + L::oStage + s * L::kBlock + kSlab, &tmQ, &b_full[s], 0, i * BW, 2 * (kvh * G + h) + 1);
+  };
+  // As in the row pass: the first loads before the others are let in.
+  if (threadIdx.x == kCW * 32) {
     ptx::mbar_init(held_full, 1);
     for (int s = 0; s < NS; ++s) {
       ptx::mbar_init(&a_full[s], 1);
@@ -411,6 +452,16 @@ __global__ void __launch_bounds__(kColThreads, 1)
     ptx::mbar_init(st_full, 32);
     init_abort(sm, abort_flag);
     ptx::fence_mbar_init();
+    if (!*abort_flag) {
+      ptx::mbar_expect_tx(held_full, L::kBlock);
+      for (int m = 0; m < 2; ++m) ptx::tma_load_3d(sm + m * kSlab, &tmK, held_full, 0, kb * BW, 2 * kvh + m);
+      for (int u = 0; u < DV / 64; ++u)
+        ptx::tma_load_3d(sm + (2 + u) * kSlab, &tmV, held_full, u * 64, kb * BW, kvh);
+      for (int t = 0; t < nt && t < NS; ++t) {
+        load_a(t);
+        load_b(t);
+      }
+    }
   }
   if (warp == kCW + 1) {
     ptx::tmem_alloc(tmem_slot, 512);
@@ -427,24 +478,12 @@ __global__ void __launch_bounds__(kColThreads, 1)
   if (warp == kCW) {
     // ------------------------------------------------------------ TMA loads
     if (lane == 0 && ok) {
-      ptx::prefetch_tmap(&tmQ);
-      ptx::prefetch_tmap(&tmdO);
-      ptx::mbar_expect_tx(held_full, L::kBlock);
-      for (int m = 0; m < 2; ++m) ptx::tma_load_3d(sm + m * kSlab, &tmK, held_full, 0, kb * BW, 2 * kvh + m);
-      for (int u = 0; u < DV / 64; ++u)
-        ptx::tma_load_3d(sm + (2 + u) * kSlab, &tmV, held_full, u * 64, kb * BW, kvh);
-      for (int t = 0; t < nt; ++t) {
+      for (int t = NS; t < nt; ++t) {
         const int s = t % NS, ph = ((t / NS) - 1) & 1;
-        const int h = t / ntile, bh = kvh * G + h, i = i0 + t - h * ntile;
-        uint8_t* st = sm + L::oStage + s * L::kBlock;
-        if (t >= NS) wait(&a_empty[s], ph);
-        ptx::mbar_expect_tx(&a_full[s], kSlab + L::kV);
-        ptx::tma_load_3d(st, &tmQ, &a_full[s], 0, i * BW, 2 * bh);
-        for (int u = 0; u < DV / 64; ++u)
-          ptx::tma_load_3d(st + (2 + u) * kSlab, &tmdO, &a_full[s], u * 64, i * BW, bh);
-        if (t >= NS) wait(&b_empty[s], ph);
-        ptx::mbar_expect_tx(&b_full[s], kSlab);
-        ptx::tma_load_3d(st + kSlab, &tmQ, &b_full[s], 0, i * BW, 2 * bh + 1);
+        wait(&a_empty[s], ph);
+        load_a(t);
+        wait(&b_empty[s], ph);
+        load_b(t);
       }
     }
   } else if (warp == kCW + 1) {
@@ -684,6 +723,22 @@ __global__ void __launch_bounds__(kColThreads, 1)
   }
 }
 
+// Both passes in one launch: they read the same statistics and nothing of one another's, so the
+// row pass's blocks fill the SMs that the column pass's last ones leave, and the other way round
+// for short sequences.  The column pass's blocks, the longer ones, come first.
+template <int DV, bool WIN>
+__global__ void __launch_bounds__(kThreads, 1)
+    bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
+               const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+               const __grid_constant__ CUtensorMap tmdQ, const __grid_constant__ CUtensorMap tmdK,
+               const __grid_constant__ CUtensorMap tmdV, const __grid_constant__ Args p) {
+  const int ncol = p.nb * p.BHkv, x = static_cast<int>(blockIdx.x);
+  if (x < ncol)
+    col_pass<DV, WIN>(p, x, tmQ, tmdO, tmK, tmV, tmdK, tmdV);
+  else
+    row_pass<DV, WIN>(p, x - ncol, tmQ, tmdO, tmK, tmV, tmdQ);
+}
+
 template <int N>
 __device__ __forceinline__ void load_words(const __nv_bfloat16* p, uint32_t (&x)[N]) {
   if constexpr (N == 4) {
@@ -765,20 +820,14 @@ cudaError_t run(const Problem& p, const void* Q, const void* K, const void* V, c
       static_cast<const __nv_bfloat16*>(dO), lse, lam, stats, N, Np, p.H, BH, p.causal, make_band(p, eff_window(p), false));
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int nb = static_cast<int>(blocks(N)), H = static_cast<int>(p.H), n = static_cast<int>(N);
-  const float c = p.scale * kLog2e;
-  auto row = banded(p) ? row_kernel<DV, true> : row_kernel<DV, false>;
-  auto col = banded(p) ? col_kernel<DV, true> : col_kernel<DV, false>;
-  constexpr int rs = Lay<DV, false>::bytes, cs = Lay<DV, true>::bytes;
-  if ((e = cudaFuncSetAttribute(row, cudaFuncAttributeMaxDynamicSharedMemorySize, rs)) != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(col, cudaFuncAttributeMaxDynamicSharedMemorySize, cs)) != cudaSuccess) return e;
-  row<<<static_cast<unsigned>(nb * BH), (kCW + 2) * 32, rs, st>>>(
-      q, g, k, v, mdq, lam, stats, partial, n, H, nb, static_cast<int>(BH), p.scale, c,
-      p.causal, make_band(p, eff_window_tc(p), false), p.group);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  col<<<static_cast<unsigned>(nb * p.BHkv), kColThreads, cs, st>>>(
-      k, v, q, g, mdk, mdv, lam, stats, n, H, nb,
-      static_cast<int>(p.BHkv), p.scale, c, p.causal, make_band(p, eff_window_tc(p), true), p.group);
+  const int nb = static_cast<int>(blocks(N));
+  const Args args{lam,      stats,  partial, static_cast<int>(N), static_cast<int>(p.H), nb, static_cast<int>(p.BHkv),
+                  p.scale,  p.scale * kLog2e, p.causal, make_band(p, eff_window_tc(p), true), p.group};
+  auto kern = banded(p) ? bwd_kernel<DV, true> : bwd_kernel<DV, false>;
+  constexpr int smem = Lay<DV, true>::bytes;
+  static_assert(smem >= Lay<DV, false>::bytes, "one launch, one size");
+  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+  kern<<<static_cast<unsigned>(nb * (BH + p.BHkv)), kThreads, smem, st>>>(q, g, k, v, mdq, mdk, mdv, args);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return diff_reduce_dlam(partial, dlam, p.B, p.H, nb, st);
 }

@@ -81,7 +81,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lo_last = (WIN && causal) ? bd.row_lo(bh, min(rb * BM + BM - 1, N - 1)) : 0;
   const int nkv = (causal ? rb + 1 : nrb) - j0;
 
-  if (threadIdx.x == 0) {
+  auto load = [&](int j) {
+    const int s = j % NS;
+    uint8_t* st = sm + L::oStage + s * L::kStage;
+    ptx::mbar_expect_tx(&k_full[s], 2 * L::kQ);
+    for (int m = 0; m < 2; ++m) ptx::tma_load_3d(st + m * L::kQ, &tmK, &k_full[s], 0, (j0 + j) * BN, 2 * kvh + m);
+    ptx::mbar_expect_tx(&v_full[s], L::kV);
+    for (int u = 0; u < DV / 64; ++u)
+      ptx::tma_load_3d(st + 2 * L::kQ + u * BN * 128, &tmV, &v_full[s], u * 64, (j0 + j) * BN, kvh);
+  };
+  // The TMA thread sets the barriers up and starts the first loads before the others are let in
+  // (the TMEM allocation alone takes about a thousand cycles).
+  if (threadIdx.x == 8 * 32) {
     ptx::mbar_init(q_full, 1);
     for (int s = 0; s < NS; ++s) {
       ptx::mbar_init(&k_full[s], 1);
@@ -96,6 +107,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = (ptx::smem_u32(sm) & 1023u) ? 1 : 0;  // the swizzled tiles need 1024-byte alignment
     if (*abort_flag) atomicOr(&g_err, FBD_ERR_TIMEOUT);
     ptx::fence_mbar_init();
+    if (!*abort_flag) {
+      ptx::mbar_expect_tx(q_full, 2 * L::kQ);
+      for (int m = 0; m < 2; ++m) ptx::tma_load_3d(sm + m * L::kQ, &tmQ, q_full, 0, rb * BM, 2 * bh + m);
+      for (int j = 0; j < nkv && j < NS; ++j) load(j);
+    }
   }
   if (warp == 9) {
     ptx::tmem_alloc(tmem_slot, 512);
@@ -112,20 +128,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 8) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0 && ok) {
-      ptx::prefetch_tmap(&tmQ);
-      ptx::prefetch_tmap(&tmK);
-      ptx::prefetch_tmap(&tmV);
-      ptx::mbar_expect_tx(q_full, 2 * L::kQ);
-      for (int m = 0; m < 2; ++m) ptx::tma_load_3d(sm + m * L::kQ, &tmQ, q_full, 0, rb * BM, 2 * bh + m);
-      for (int j = 0; j < nkv; ++j) {
-        const int s = j % NS;
-        uint8_t* st = sm + L::oStage + s * L::kStage;
-        if (j >= NS) wait(&empty[s], ((j / NS) - 1) & 1);
-        ptx::mbar_expect_tx(&k_full[s], 2 * L::kQ);
-        for (int m = 0; m < 2; ++m) ptx::tma_load_3d(st + m * L::kQ, &tmK, &k_full[s], 0, (j0 + j) * BN, 2 * kvh + m);
-        ptx::mbar_expect_tx(&v_full[s], L::kV);
-        for (int u = 0; u < DV / 64; ++u)
-          ptx::tma_load_3d(st + 2 * L::kQ + u * BN * 128, &tmV, &v_full[s], u * 64, (j0 + j) * BN, kvh);
+      for (int j = NS; j < nkv; ++j) {
+        wait(&empty[j % NS], ((j / NS) - 1) & 1);
+        load(j);
       }
       // the last stages must have been consumed before the CTA exits
       for (int j = (nkv > NS ? nkv - NS : 0); j < nkv; ++j) wait(&empty[j % NS], (j / NS) & 1);
@@ -184,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + L::cS + m * BN + lane_off, tO = tmem + L::cO + lane_off;
     const int64_t row = static_cast<int64_t>(rb) * BM + r;
     const int lo_row = (WIN && causal) ? bd.row_lo(bh, row) : 0;
-    const float slack = kSlack / c;
+    const float slack = kSlack / c, lm = lam[bh % H];
     const uint64_t c2 = tc::pk2f(c, c);
     float mref = -INFINITY, l = 0.f;
     for (int j = 0; j < nkv; ++j) {
@@ -273,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::named_sync(1, 256);
     ptx::tc_fence_after();
     if (m == 0 || with_O2) {
-      const float w = m == 0 ? -lam[bh % H] * sInv[r] : inv;  // of O_2's columns
+      const float w = m == 0 ? -lm * sInv[r] : inv;  // of O_2's columns
       // Through the stages (every block has been read) as 64-column tiles, and out by TMA: a row
       // per thread straight to memory, 16 bytes at a time, took 5.6 thousand cycles of each CTA.
       uint8_t* out = sm + L::oStage + m * BM * DV * 2;
