@@ -13,7 +13,7 @@
 // four warps takes 16 of a tile's 64 keys with a softmax of its own; the four are joined at
 // the end.  Three 32 KB stages of 16-byte asynchronous copies, two CTAs an SM: 192 KB in
 // flight on each SM.  P is rounded to bf16 for its product; sums, maxima and o are fp32.
-// float32 on the CUDA cores, a key per lane.
+// float32 on the CUDA cores, a key per lane, two stages.
 #include <cuda_bf16.h>
 
 #include "diff.h"
@@ -27,6 +27,7 @@ constexpr int BK = 32;    // float32: keys per tile, one per lane
 constexpr int MK = 64;    // bf16: keys per tile, 16 per warp
 constexpr int NS = 3;     // bf16: stages
 constexpr int RMAX = 8;   // query heads handled together
+constexpr int kMaxSplits = 256;
 constexpr int kT = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -37,12 +38,12 @@ Plan make_plan(const Problem& p) {
   Plan q;
   q.rows = p.group < RMAX ? p.group : RMAX;
   q.chunks = (p.group + q.rows - 1) / q.rows;
-  // about four CTAs for each of the 152 SMs, a split no shorter than 128 keys
+  // about three CTAs for each of the 152 SMs (two fit at a time), a split no shorter than 128 keys
   const int64_t base = p.BHkv * q.chunks;
-  const int64_t want = base > 0 ? (4 * 152 + base - 1) / base : 1;
+  const int64_t want = base > 0 ? (3 * 152 + base - 1) / base : 1;
   const int64_t most = (p.N + 127) / 128;
   const int64_t n = want < most ? want : most;
-  q.nsplit = static_cast<int>(n < 1 ? 1 : n > 256 ? 256 : n);
+  q.nsplit = static_cast<int>(n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n);
   return q;
 }
 
@@ -94,12 +95,13 @@ struct Stage {
   static constexpr int kK = MK * D * 2, kV = MK * D * 4, bytes = 2 * kK + kV;
 };
 
-// ws: per (b, h, map, split) 2d + 2 floats: o, max (scaled, in powers of two), sum.
+// ws: o of every (b, h, map, split), 2d floats each, then their (max (scaled, in powers of two),
+// sum) at `tail`.
 template <int D>
 __global__ void __launch_bounds__(kT, 2)
     mma_kernel(const __nv_bfloat16* __restrict__ Q, const __nv_bfloat16* __restrict__ K,
                const __nv_bfloat16* __restrict__ V, const float* __restrict__ lam, const int* __restrict__ lens,
-               __nv_bfloat16* __restrict__ O, float* __restrict__ ws, int64_t cap, int H, int G, int rows, int nsplit,
+               __nv_bfloat16* __restrict__ O, float* __restrict__ ws, float2* __restrict__ tail, int64_t cap, int H, int G, int rows, int nsplit,
                int64_t win, float c) {
   using St = Stage<D>;
   constexpr int DV = 2 * D, NT = DV / 8;  // 8-column tiles of o
@@ -257,10 +259,9 @@ __global__ void __launch_bounds__(kT, 2)
         x[0] = fmaf(f, v.x, x[0]), x[1] = fmaf(f, v.y, x[1]), x[2] = fmaf(f, v.z, x[2]), x[3] = fmaf(f, v.w, x[3]);
       }
       if (nsplit > 1) {
-        float* w = ws + (((h0 + r) * 2 + m) * nsplit + split) * (DV + 2);
-#pragma unroll
-        for (int y = 0; y < 4; y += 2) *reinterpret_cast<float2*>(w + col + y) = make_float2(x[y], x[y + 1]);
-        if (col == 0) w[DV] = mm, w[DV + 1] = ll;
+        const int64_t w = ((h0 + r) * 2 + m) * nsplit + split;
+        *reinterpret_cast<float4*>(ws + w * DV + col) = make_float4(x[0], x[1], x[2], x[3]);
+        if (col == 0) tail[w] = make_float2(mm, ll);
       } else {
         const float inv = ll > 0.f ? 1.f / ll : 0.f;
         if (m == 0) {
@@ -282,11 +283,13 @@ template <int D>
 __global__ void __launch_bounds__(kT)
     decode_kernel(const float* __restrict__ Q, const float* __restrict__ K, const float* __restrict__ V,
                   const float* __restrict__ lam, const int* __restrict__ lens, float* __restrict__ O,
-                  float* __restrict__ ws, int64_t cap, int H, int G, int rows, int nsplit, int64_t win, float c) {
+                  float* __restrict__ ws, float2* __restrict__ tail, int64_t cap, int H, int G, int rows, int nsplit, int64_t win, float c) {
   constexpr int DV = 2 * D, PD = D + 4, PV = DV;
   constexpr int VC = DV / 64;  // a thread's columns: (t & 63) + 64 v of map t >> 6
-  __shared__ __align__(16) float sQ[2 * RMAX * D], sK[2 * BK * PD], sV[BK * PV], sP[2 * RMAX * BK];
-  __shared__ float sA[2 * RMAX], sM[2 * RMAX], sL[2 * RMAX];
+  constexpr int kTile = 2 * BK * PD + BK * PV;  // K_1, K_2, V
+  extern __shared__ __align__(128) uint8_t sh[];
+  float* sB = reinterpret_cast<float*>(sh);  // two tiles
+  float *sQ = sB + 2 * kTile, *sP = sQ + 2 * RMAX * D, *sA = sP + 2 * RMAX * BK, *sM = sA + 2 * RMAX, *sL = sM + 2 * RMAX;
   const int split = blockIdx.x % nsplit, Hkv = H / G, chunks = (G + rows - 1) / rows;
   const int unit = blockIdx.x / nsplit;  // (b, key/value head, chunk of its query heads)
   const int r0 = unit % chunks * rows, n = unit / chunks % Hkv, b = unit / chunks / Hkv;
@@ -310,20 +313,31 @@ __global__ void __launch_bounds__(kT)
 #pragma unroll
     for (int v = 0; v < VC; ++v) acc[r][v] = 0.f;
   const int pm = threadIdx.x >> 6, pc = threadIdx.x & 63;
-  for (int64_t k0 = kb; k0 < ke; k0 += BK) {
-    __syncthreads();
-    // keys past the end are never read: zeros there (a cache row not yet written may hold anything)
-    for (int u = threadIdx.x; u < 2 * BK * D / 4; u += kT) {
+  auto load = [&](int64_t k0, int buf) {
+    // keys past the end are not read: zeros there (a cache row not yet written may hold anything)
+    const uint32_t dst = ptx::smem_u32(sB + buf * kTile);
+#pragma unroll
+    for (int v = 0; v < 2 * BK * D / 4 / kT; ++v) {
+      const int u = v * kT + threadIdx.x;
       const int m = u / (BK * D / 4), w = u % (BK * D / 4), r = w / (D / 4), cc = w % (D / 4) * 4;
-      const float4 x = k0 + r < ke ? ld4(K + ((2 * kvh + m) * cap + k0 + r) * D + cc) : make_float4(0, 0, 0, 0);
-      *reinterpret_cast<float4*>(sK + (m * BK + r) * PD + cc) = x;
+      const bool in = k0 + r < ke;
+      copy16(dst + ((m * BK + r) * PD + cc) * 4, K + ((2 * kvh + m) * cap + (in ? k0 + r : kb)) * D + cc, in);
     }
-    for (int u = threadIdx.x; u < BK * DV / 4; u += kT) {
-      const int r = u / (DV / 4), cc = u % (DV / 4) * 4;
-      const float4 x = k0 + r < ke ? ld4(V + (kvh * cap + k0 + r) * DV + cc) : make_float4(0, 0, 0, 0);
-      *reinterpret_cast<float4*>(sV + r * PV + cc) = x;
+#pragma unroll
+    for (int v = 0; v < BK * DV / 4 / kT; ++v) {
+      const int u = v * kT + threadIdx.x, r = u / (DV / 4), cc = u % (DV / 4) * 4;
+      const bool in = k0 + r < ke;
+      copy16(dst + (2 * BK * PD + r * PV + cc) * 4, V + (kvh * cap + (in ? k0 + r : kb)) * DV + cc, in);
     }
-    __syncthreads();
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (kb < ke) load(kb, 0);
+  int buf = 0;
+  for (int64_t k0 = kb; k0 < ke; k0 += BK, buf ^= 1) {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // this tile is there, the other buffer's has been read
+    if (k0 + BK < ke) load(k0 + BK, buf ^ 1);
+    const float *sK = sB + buf * kTile, *sV = sK + 2 * BK * PD;
     // warp w: map w & 1, rows w >> 1, + 2, ...; lane = key
     for (int r = warp >> 1; r < R; r += 2) {
       const int row = 2 * r + (warp & 1);
@@ -378,16 +392,16 @@ __global__ void __launch_bounds__(kT)
 #pragma unroll
     for (int r = 0; r < RMAX; ++r)
       if (r < R) {
-        float* w = ws + (((h0 + r) * 2 + pm) * nsplit + split) * (DV + 2);
+        const int64_t w = ((h0 + r) * 2 + pm) * nsplit + split;
 #pragma unroll
-        for (int v = 0; v < VC; ++v) w[pc + 64 * v] = acc[r][v];
-        if (pc == 0) w[DV] = sM[2 * r + pm], w[DV + 1] = sL[2 * r + pm];
+        for (int v = 0; v < VC; ++v) ws[w * DV + pc + 64 * v] = acc[r][v];
+        if (pc == 0) tail[w] = make_float2(sM[2 * r + pm], sL[2 * r + pm]);
       }
     return;
   }
   // one split: map 2's rows through shared memory (the tiles are done), then the difference
-  float* x2 = sK;  // [R][DV]
-  static_assert(RMAX * DV <= 2 * BK * PD, "exchange fits");
+  float* x2 = sB;  // [R][DV]
+  static_assert(RMAX * DV <= kTile, "exchange fits");
 #pragma unroll
   for (int r = 0; r < RMAX; ++r)
     if (r < R) {
@@ -411,28 +425,53 @@ __global__ void __launch_bounds__(kT)
   }
 }
 
-// One block per (b, h), one thread per column: the splits of both maps joined.
+// One block per (b, h): the splits of both maps joined.  The splits' weights are formed once, in
+// shared memory; then groups of threads, each four columns wide, sum every kGroups-th split with
+// four loads in flight, and the groups are added in order.
 template <int DV, typename T>
-__global__ void __launch_bounds__(DV)
-    join_kernel(const float* __restrict__ ws, const float* __restrict__ lam, T* __restrict__ O, int H, int nsplit) {
+__global__ void __launch_bounds__(256)
+    join_kernel(const float* __restrict__ ws, const float2* __restrict__ tail, const float* __restrict__ lam,
+                T* __restrict__ O, int H, int nsplit) {
+  constexpr int C = DV / 4, kGroups = 256 / C;
+  __shared__ float w[2][kMaxSplits];
+  __shared__ __align__(16) float part[kGroups][DV];
   const int64_t bh = blockIdx.x;
-  float o[2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp < 2) {  // map `warp`: w = 2^(max_s - max) / sum, minus lam of that for the second
+    const float2* t = tail + (bh * 2 + warp) * nsplit;
+    float mx = -INFINITY, l = 0.f;
+    for (int s = lane; s < nsplit; s += 32) mx = fmaxf(mx, t[s].x);
 #pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    const float* w = ws + (bh * 2 + m) * nsplit * (DV + 2);
-    float mx = -INFINITY;
-    for (int s = 0; s < nsplit; ++s) mx = fmaxf(mx, w[s * (DV + 2) + DV]);
-    float l = 0.f, a = 0.f;
-    if (mx != -INFINITY)
-      for (int s = 0; s < nsplit; ++s) {
-        const float* x = w + s * (DV + 2);
-        const float f = ptx::ex2(x[DV] - mx);
-        l = fmaf(f, x[DV + 1], l);
-        a = fmaf(f, x[threadIdx.x], a);
-      }
-    o[m] = l > 0.f ? a / l : 0.f;
+    for (int x = 1; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+    const float sub = mx == -INFINITY ? 0.f : mx;  // no key at all
+    for (int s = lane; s < nsplit; s += 32) {
+      const float f = ptx::ex2(t[s].x - sub);
+      w[warp][s] = f;
+      l = fmaf(f, t[s].y, l);
+    }
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+    const float f = l > 0.f ? (warp == 0 ? 1.f : -lam[bh % H]) / l : 0.f;
+    for (int s = lane; s < nsplit; s += 32) w[warp][s] *= f;
   }
-  st1(O + bh * DV + threadIdx.x, o[0] - lam[bh % H] * o[1]);
+  __syncthreads();
+  const int g = threadIdx.x / C, col = threadIdx.x % C * 4;
+  const float* x = ws + bh * 2 * nsplit * DV + col;
+  float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = g; s < 2 * nsplit; s += kGroups) {  // map 1's splits, then map 2's
+    const float4 v = *reinterpret_cast<const float4*>(x + static_cast<int64_t>(s) * DV);
+    const float f = s < nsplit ? w[0][s] : w[1][s - nsplit];
+    a[0] = fmaf(f, v.x, a[0]), a[1] = fmaf(f, v.y, a[1]), a[2] = fmaf(f, v.z, a[2]), a[3] = fmaf(f, v.w, a[3]);
+  }
+  *reinterpret_cast<float4*>(&part[g][col]) = make_float4(a[0], a[1], a[2], a[3]);
+  __syncthreads();
+  for (int c = threadIdx.x; c < DV; c += 256) {
+    float o = 0.f;
+#pragma unroll
+    for (int u = 0; u < kGroups; ++u) o += part[u][c];
+    st1(O + bh * DV + c, o);
+  }
 }
 
 template <int D>
@@ -442,6 +481,7 @@ cudaError_t run(const Problem& p, const void* Q, const void* K, const void* V, c
   const unsigned grid = static_cast<unsigned>(p.BHkv * q.chunks * q.nsplit);
   const int H = static_cast<int>(p.H);
   const float c = p.scale * kLog2e;
+  float2* tail = reinterpret_cast<float2*>(ws + p.BH * 2 * q.nsplit * 2 * D);
   cudaError_t e;
   if (p.dtype == ATTN_BF16) {
     using T = __nv_bfloat16;
@@ -449,17 +489,20 @@ cudaError_t run(const Problem& p, const void* Q, const void* K, const void* V, c
     e = cudaFuncSetAttribute(mma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     mma_kernel<D><<<grid, kT, smem, st>>>(static_cast<const T*>(Q), static_cast<const T*>(K), static_cast<const T*>(V),
-                                          lam, lens, static_cast<T*>(O), ws, p.N, H, p.group, q.rows, q.nsplit,
+                                          lam, lens, static_cast<T*>(O), ws, tail, p.N, H, p.group, q.rows, q.nsplit,
                                           p.window, c);
     if ((e = cudaGetLastError()) != cudaSuccess || q.nsplit == 1) return e;
-    join_kernel<2 * D><<<static_cast<unsigned>(p.BH), 2 * D, 0, st>>>(ws, lam, static_cast<T*>(O), H, q.nsplit);
+    join_kernel<2 * D><<<static_cast<unsigned>(p.BH), 256, 0, st>>>(ws, tail, lam, static_cast<T*>(O), H, q.nsplit);
   } else {
     using T = float;
-    decode_kernel<D><<<grid, kT, 0, st>>>(static_cast<const T*>(Q), static_cast<const T*>(K), static_cast<const T*>(V),
-                                          lam, lens, static_cast<T*>(O), ws, p.N, H, p.group, q.rows, q.nsplit,
+    constexpr int smem = 4 * (2 * (2 * BK * (D + 4) + BK * 2 * D) + 2 * RMAX * (D + BK + 3));
+    e = cudaFuncSetAttribute(decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    decode_kernel<D><<<grid, kT, smem, st>>>(static_cast<const T*>(Q), static_cast<const T*>(K), static_cast<const T*>(V),
+                                          lam, lens, static_cast<T*>(O), ws, tail, p.N, H, p.group, q.rows, q.nsplit,
                                           p.window, c);
     if ((e = cudaGetLastError()) != cudaSuccess || q.nsplit == 1) return e;
-    join_kernel<2 * D><<<static_cast<unsigned>(p.BH), 2 * D, 0, st>>>(ws, lam, static_cast<T*>(O), H, q.nsplit);
+    join_kernel<2 * D><<<static_cast<unsigned>(p.BH), 256, 0, st>>>(ws, tail, lam, static_cast<T*>(O), H, q.nsplit);
   }
   return cudaGetLastError();
 }
