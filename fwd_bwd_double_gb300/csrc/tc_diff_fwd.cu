@@ -10,7 +10,8 @@
 // the next S_2, and the other way round (six products of 128 x 128 x 64 a block).  TMEM is
 // full: S_1, S_2 (128 columns each, P_m over the first half of S_m) and O_1, O_2 (2d each).
 // The MMA warp issues S_m of block j + 1 behind P_m V of block j; products of one thread
-// run in order, so S_m overwrites P_m only once it has been read.
+// run in order, so S_m overwrites P_m only once it has been read.  P_m V starts on the first
+// 64 keys' P while the rest is exponentiated.
 //
 // The reference maximum M_m moves only when a row's maximum passes it by more than 2^8 in
 // the probabilities (P_m <= 2^8, l and O_m in fp32): most blocks then rescale nothing.
@@ -45,7 +46,7 @@ struct Lay {
   static constexpr int oStage = 2 * kQ;
   static constexpr int oInv = oStage + NS * kStage;  // 1 / l_2 of every row
   static constexpr int oBar = oInv + BM * 4;
-  static constexpr int bytes = oBar + 160;
+  static constexpr int bytes = oBar + 192;
   static constexpr uint32_t cS = 0, cO = 2 * BN;  // S_m at cS + m BN, O_m at cO + m DV
 };
 static_assert(Lay<64>::bytes <= 232448, "shared memory");
@@ -67,7 +68,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* v_full = k_full + NS;         // [NS]
   uint64_t* empty = v_full + NS;          // [NS] both maps' P V of the stage done
   uint64_t* s_full = empty + NS;          // [2] S_m in TMEM (and the previous P_m V done)
-  uint64_t* p_ready = s_full + 2;         // [2] P_m in TMEM, O_m rescaled
+  uint64_t* p_half = s_full + 2;          // [2] P_m of the first 64 keys in TMEM, O_m rescaled
+  uint64_t* p_ready = p_half + 2;         // [2] of all keys
   uint64_t* o_full = p_ready + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -101,6 +103,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int m = 0; m < 2; ++m) {
       ptx::mbar_init(&s_full[m], 1);
+      ptx::mbar_init(&p_half[m], 128);
       ptx::mbar_init(&p_ready[m], 128);
     }
     ptx::mbar_init(o_full, 1);
@@ -161,13 +164,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t so = static_cast<uint32_t>(s * L::kStage);
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-          wait(&p_ready[m], j & 1);
+          wait(&p_half[m], j & 1);
           if (m == 0) wait(&v_full[s], (j / NS) & 1);
           ptx::tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < BN / 16; ++k)
+          for (int k = 0; k < BN / 16; ++k) {
+            if (k == BN / 32) {
+              wait(&p_ready[m], j & 1);
+              ptx::tc_fence_after();
+            }
             ptx::mma_ts_e(tmem + L::cO + m * DV, tmem + L::cS + m * BN + k * 8, tc::desc_add(dV, so + k * 2048), idO,
                           (j > 0 || k > 0) ? 1u : 0u);
+          }
           if (m == 1) ptx::mma_commit_e(&empty[s]);
           if (j + 1 < nkv) {
             if (m == 0) {
@@ -263,10 +271,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           pk[t >> 1] = ptx::pack_bf16(p0, p1);
         }
         ptx::tmem_st16(tS + ch * 16, pk);
+        if (ch & 1) {
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(ch == 1 ? &p_half[m] : &p_ready[m]);
+        }
       }
-      ptx::tmem_wait_st();
-      ptx::tc_fence_before();
-      ptx::mbar_arrive(&p_ready[m]);
       const float2 x = tc::unpk2(tc::add2(tc::add2(rs[0], rs[1]), tc::add2(rs[2], rs[3])));
       l += x.x + x.y;
     }
