@@ -18,7 +18,9 @@ attn_status_t check_diff(const attn_desc_t* desc, Problem& p) {
   attn_status_t s = check_desc(desc, p);
   if (s != ATTN_OK) return s;
   if (!diff_supports(p.d)) return fail(ATTN_ERR_UNSUPPORTED, "differential attention: d must be 32 or 64%s");
-  if (p.BH >= (int64_t(1) << 30)) return fail(ATTN_ERR_INVALID_ARG, "B*H must be < 2^30%s");
+  // 2H maps in a tensor-map extent; the backward's preparation takes eight blocks per 128 rows of a head
+  if (p.BH >= (int64_t(1) << 30) || p.BH * ((p.N + 127) / 128) >= (int64_t(1) << 28))
+    return fail(ATTN_ERR_INVALID_ARG, "B*H must be < 2^30 and B*H*ceil(N/128) < 2^28%s");
   return ATTN_OK;
 }
 

@@ -366,13 +366,13 @@ __global__ void __launch_bounds__(kT)
       }
     }
     __syncthreads();
+    // The tile's sums, then added to the running ones: a chain of additions as long as the
+    // context would lose bits with its square root.
+    float part[RMAX][VC];
 #pragma unroll
-    for (int r = 0; r < RMAX; ++r) {
-      if (r >= R) break;
-      const float a = sA[2 * r + pm];
+    for (int r = 0; r < RMAX; ++r)
 #pragma unroll
-      for (int v = 0; v < VC; ++v) acc[r][v] *= a;
-    }
+      for (int v = 0; v < VC; ++v) part[r][v] = 0.f;
 #pragma unroll 4
     for (int k = 0; k < BK; ++k) {
       float x[VC];
@@ -383,8 +383,15 @@ __global__ void __launch_bounds__(kT)
         if (r >= R) break;
         const float p = sP[(2 * r + pm) * BK + k];
 #pragma unroll
-        for (int v = 0; v < VC; ++v) acc[r][v] = fmaf(p, x[v], acc[r][v]);
+        for (int v = 0; v < VC; ++v) part[r][v] = fmaf(p, x[v], part[r][v]);
       }
+    }
+#pragma unroll
+    for (int r = 0; r < RMAX; ++r) {
+      if (r >= R) break;
+      const float a = sA[2 * r + pm];
+#pragma unroll
+      for (int v = 0; v < VC; ++v) acc[r][v] = fmaf(acc[r][v], a, part[r][v]);
     }
   }
   __syncthreads();

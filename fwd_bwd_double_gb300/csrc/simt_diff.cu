@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kT, 2)
         load(g + 1, b0, buf ^ 1);
       const float *sB = sS + buf * kTile, *sBV = sB + 2 * BK * PD;
       const float4* sSt = sSt0 + buf * BK;
-      float dp[4][2], w[4][2];
+      float dp[4][2], w[4][2], sum = 0.f;  // sum: of P_2 dP in this tile (short chains of additions)
       scores<DV>(sAV, sBV, ty, tx, dp);
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kT, 2)
             if (causal) see = see && (COL ? (a <= b && b <= lim[r]) : (b <= a && b >= lim[r]));
             const float p = see ? ptx::ex2(fmaf(s[r][u], c, -L * kLog2e)) : 0.f;
             const float ds = (see && Dm != INFINITY) ? wm * p * (dp[r][u] - Dm) : 0.f;
-            if (m == 1 && !COL) dl = fmaf(p, see ? dp[r][u] : 0.f, dl);
+            if (m == 1 && !COL) sum = fmaf(p, see ? dp[r][u] : 0.f, sum);
             sT[m * BQ * PP + (4 * ty + r) * PP + tx + 16 * u] = ds;
             if (COL) {
               w[r][u] = m == 0 ? p : fmaf(wm, p, w[r][u]);
@@ -392,6 +392,7 @@ __global__ void __launch_bounds__(kT, 2)
           }
         }
       }
+      dl += sum;
       __syncwarp();
 #pragma unroll
       for (int m = 0; m < 2; ++m) accumulate<D>(sT + m * BQ * PP, sB + m * BK * PD, ty, tx, acc[m]);

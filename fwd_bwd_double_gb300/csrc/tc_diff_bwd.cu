@@ -288,6 +288,7 @@ __device__ __forceinline__ void row_pass(const Args& p, int block, const CUtenso
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         uint32_t v[32], pk[16];
+        uint64_t sum = 0;  // of P_2 dP in this block: short chains of additions (dlam is fp32)
         wait(&s_full[m], t & 1);
         ptx::tc_fence_after();
         ptx::tmem_ld32(tmem + cS + c0 + lo, v);
@@ -318,10 +319,11 @@ __device__ __forceinline__ void row_pass(const Args& p, int block, const CUtenso
 #pragma unroll
         for (int u = 0; u < 32; u += 2) {
           const uint64_t P = tc::pk2(v[u], v[u + 1]), g = tc::pk2(dp[u], dp[u + 1]);
-          if (m == 1) dl2 = tc::fma2(P, g, dl2);
+          if (m == 1) sum = tc::fma2(P, g, sum);
           const float2 d = tc::unpk2(tc::mul2(P, tc::add2(g, nD[m])));
           pk[u >> 1] = ptx::pack_bf16(d.x, d.y);
         }
+        if (m == 1) dl2 = tc::add2(dl2, sum);
         if (masked && one) {
 #pragma unroll
           for (int u = 0; u < 16; ++u) pk[u] = 0u;

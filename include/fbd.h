@@ -327,7 +327,12 @@ attn_status_t attn_bwd_projected_dS(const attn_desc_t* desc, const void* Q, cons
  *   O, O2, dO [B,H,N,2d]; lse [B,2H,N] float32; lam, dlam [H] float32.
  * Masks (causal, full, window, document bounds), types, scale, alignment, streams and
  * errors are those of attn_fwd, with these differences: d in {32, 64} (else
- * ATTN_ERR_UNSUPPORTED), and lam, dlam and lens need only their element's alignment. */
+ * ATTN_ERR_UNSUPPORTED), B*H < 2^30 and B*H*ceil(N/128) < 2^28 (else ATTN_ERR_INVALID_ARG),
+ * and lam, dlam and lens need only their element's alignment.
+ * Kernels: bf16 attn_diff_fwd and attn_diff_bwd on the tcgen05/TMA tensor-core kernels (P, and
+ * dS in the backward, rounded to bf16 for their products, all sums fp32); bf16 attn_diff_decode
+ * on warp-level matrix products; float32 in fp32 on the CUDA cores.  Every output is the same
+ * bits on every call. */
 
 /* Forward.
  *   In:  Q, K, V, lam.

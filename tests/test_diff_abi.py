@@ -43,7 +43,8 @@ def decode(dsc, p=None, ws=None):
     (dict(d=96), UNSUP), (dict(d=128), UNSUP), (dict(d=16), UNSUP), (dict(dtype=5), UNSUP), (dict(causal=2), UNSUP),
     (dict(B=-1), INVALID), (dict(H=3, group=2), INVALID), (dict(window=-1), INVALID), (dict(scale=-1.0), INVALID),
     (dict(scale=float("nan")), INVALID), (dict(causal=0, window=4), UNSUP), (dict(N=1 << 31), INVALID),
-    (dict(lo=FAKE), INVALID), (dict(B=1 << 15, H=1 << 15, N=1), INVALID),
+    (dict(lo=FAKE), INVALID), (dict(B=1 << 15, H=1 << 15, N=1), INVALID), (dict(B=1 << 14, H=1 << 14, N=1), INVALID),
+    (dict(B=1 << 10, H=1 << 10, N=(1 << 15) + 1), INVALID),
 ])
 def test_refuses_bad_descriptors(kw, code):
     d = desc(**kw)

@@ -252,6 +252,42 @@ def test_empty_gradient_of_lambda_is_zero():
     assert dQ.numel() == 0 and (dlam == 0).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_offsets_past_2_31_elements(dtype):
+    """16 heads of a 2^20-token window: Q and V alone have 2^31 elements.  The last head is what it is
+    alone, bit for bit."""
+    import fwd_bwd_double_gb300 as fbd
+    torch = _t()
+    N, d, W = 1 << 20, 64, 40
+    H = 16 if dtype == "bf16" else 17
+    if torch.cuda.mem_get_info()[0] < 160 << 30:
+        pytest.skip("needs 160 GB of device memory")
+    gen = torch.Generator(device="cuda").manual_seed(0)
+
+    def big(heads, width):  # the last head's values random, the others' zero
+        x = torch.zeros(1, heads, N, width, dtype=dt(dtype), device="cuda")
+        x[:, -(heads // H):] = torch.randn(1, heads // H, N, width, generator=gen, device="cuda").to(dt(dtype))
+        return x
+
+    Q, K, V, dO = big(2 * H, d), big(2 * H, d), big(H, 2 * d), big(H, 2 * d)
+    lam = torch.full((H,), 0.5, device="cuda")
+    a = run((Q, K, V, lam, dO), window=W)
+    last = tuple(t[:, -(t.shape[1] // H):].contiguous() for t in (Q, K, V)) + (lam[-1:], dO[:, -1:].contiguous())
+    b = run(last, window=W)
+    for k in b:
+        got = a[k][-1:] if k == "dlam" else a[k][:, -(a[k].shape[1] // H):]
+        assert torch.equal(got, b[k]), k
+    if dtype == "bf16":  # and over a cache of that size
+        lens = torch.tensor([N], dtype=torch.int32, device="cuda")
+        o = fbd.attn_diff_decode(Q[:, :, -1:].contiguous(), K, V, lam, lens)
+        want, tol = decode_reference(last[0][:, :, -1:], last[1], last[2], last[3], lens, 1)
+        assert ((o[:, -1:].double() - want).abs() <= tol).all()
+        pos = torch.arange(N, device="cuda", dtype=torch.int32)[None]
+        freq, axis = torch.rand(d // 2, device="cuda"), torch.zeros(d // 2, dtype=torch.int32, device="cuda")
+        r = fbd.attn_rope(Q, pos, freq, axis)
+        assert torch.equal(r[:, -2:], fbd.attn_rope(last[0], pos, freq, axis))
+
+
 # ------------------------------------------------------------------ one token over a cache
 def decode_reference(Q, K, V, lam, lens, g, window=0):
     torch = _t()
