@@ -49,6 +49,23 @@ __device__ __forceinline__ bool diff_one_key(const Band& bd, int causal, int64_t
 // fixed order by one block per head.
 cudaError_t diff_reduce_dlam(const float* partial, float* dlam, int64_t B, int64_t H, int64_t nblk, cudaStream_t st);
 
+// A launch that may be set up while the kernel before it in the stream ends: it may read what
+// that kernel wrote only behind ptx::grid_dependency_wait().
+template <typename... P, typename... A>
+inline cudaError_t launch_behind(void (*kern)(P...), int64_t grid, int block, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(block));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 // One token over a cache (diff_decode.cu).  p.N is the cache's capacity.
 size_t diff_decode_bytes(const Problem& p);
 cudaError_t diff_decode(const Problem& p, const void* Q, const void* K, const void* V, const float* lam,

@@ -437,13 +437,14 @@ __global__ void __launch_bounds__(kT)
 // four loads in flight, and the groups are added in order.
 template <int DV, typename T>
 __global__ void __launch_bounds__(256)
-    join_kernel(const float* __restrict__ ws, const float2* __restrict__ tail, const float* __restrict__ lam,
+    join_kernel(const float* ws, const float2* tail, const float* __restrict__ lam,
                 T* __restrict__ O, int H, int nsplit) {
   constexpr int C = DV / 4, kGroups = 256 / C;
   __shared__ float w[2][kMaxSplits];
   __shared__ __align__(16) float part[kGroups][DV];
   const int64_t bh = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  ptx::grid_dependency_wait();  // the splits' parts
   if (warp < 2) {  // map `warp`: w = 2^(max_s - max) / sum, minus lam of that for the second
     const float2* t = tail + (bh * 2 + warp) * nsplit;
     float mx = -INFINITY, l = 0.f;
@@ -499,7 +500,7 @@ cudaError_t run(const Problem& p, const void* Q, const void* K, const void* V, c
                                           lam, lens, static_cast<T*>(O), ws, tail, p.N, H, p.group, q.rows, q.nsplit,
                                           p.window, c);
     if ((e = cudaGetLastError()) != cudaSuccess || q.nsplit == 1) return e;
-    join_kernel<2 * D><<<static_cast<unsigned>(p.BH), 256, 0, st>>>(ws, tail, lam, static_cast<T*>(O), H, q.nsplit);
+    return launch_behind(join_kernel<2 * D, T>, p.BH, 256, 0, st, ws, tail, lam, static_cast<T*>(O), H, q.nsplit);
   } else {
     using T = float;
     constexpr int smem = 4 * (2 * (2 * BK * (D + 4) + BK * 2 * D) + 2 * RMAX * (D + BK + 3));
@@ -509,9 +510,8 @@ cudaError_t run(const Problem& p, const void* Q, const void* K, const void* V, c
                                           lam, lens, static_cast<T*>(O), ws, tail, p.N, H, p.group, q.rows, q.nsplit,
                                           p.window, c);
     if ((e = cudaGetLastError()) != cudaSuccess || q.nsplit == 1) return e;
-    join_kernel<2 * D><<<static_cast<unsigned>(p.BH), 256, 0, st>>>(ws, tail, lam, static_cast<T*>(O), H, q.nsplit);
+    return launch_behind(join_kernel<2 * D, T>, p.BH, 256, 0, st, ws, tail, lam, static_cast<T*>(O), H, q.nsplit);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace

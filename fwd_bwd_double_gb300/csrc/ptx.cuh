@@ -144,6 +144,10 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// Wait until the kernels before this one in the stream, which it may have been launched ahead
+// of, have completed and their writes are visible (no effect in an ordinary launch).
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Registers per thread of the calling warpgroup, lowered or raised (all four warps execute
 // it).  A raise waits until the block's own launch-time registers (threads x registers at
 // launch) cover it, so the shares of all warpgroups must sum to no more than that.

@@ -279,11 +279,12 @@ constexpr size_t bwd_smem() {
 // share of dlam.  COL = true: holds keys, streams the queries of the G query heads that
 // share them, writes dK_m, dV.
 template <int D, bool COL>
-__global__ void __launch_bounds__(kT, 2)
-    bwd_kernel(const float* __restrict__ Q, const float* __restrict__ K, const float* __restrict__ V, const float* __restrict__ dO,
-               const float* __restrict__ lam, const float4* __restrict__ stats, float* __restrict__ out1,
-               float* __restrict__ outV, float* __restrict__ partial, int64_t N, int64_t H, int nblk, int slices, int G,
-               float scale, int causal, Band bd) {
+__device__ __forceinline__ void bwd_pass(const float* __restrict__ Q, const float* __restrict__ K,
+                                         const float* __restrict__ V, const float* __restrict__ dO,
+                                         const float* __restrict__ lam, const float4* stats, float* __restrict__ out1,
+                                         float* __restrict__ outV, float* __restrict__ partial, int64_t N, int64_t H,
+                                         int nblk, int slices, int G, float scale, int causal, const Band& bd,
+                                         int block) {
   constexpr int DV = 2 * D, W = D / 16, WV = DV / 16, PD = Pitch<D>::v;
   extern __shared__ __align__(16) float sh[];
   float* sA = sh;                      // [2][BQ] held Q_m or K_m
@@ -293,7 +294,7 @@ __global__ void __launch_bounds__(kT, 2)
   float* sT = sS + 2 * kTile;          // [2][BQ] dS_m; then in the first P_1 - lam P_2 (COL)
   float4* sSt0 = reinterpret_cast<float4*>(sT + 2 * BQ * PP);  // [2][BK] streamed rows' statistics (COL)
   float* sRed = reinterpret_cast<float*>(sSt0 + 2 * BK);       // [4]
-  const tc::Order ord = tc::grid_order(slices, nblk);
+  const tc::Order ord = tc::grid_order_at(block, slices, nblk);
   const int64_t sl = ord.bh;                                      // query slice, or key/value slice
   const int64_t blk = COL || !causal ? ord.k : nblk - 1 - ord.k;  // heaviest first
   const int64_t a0 = blk * BQ;
@@ -311,16 +312,16 @@ __global__ void __launch_bounds__(kT, 2)
   if (causal) {
     if (COL) {
       b0 = a0 / BK * BK;
-      b1 = static_cast<int64_t>(bd.key_hi(sl, a0 + BQ - 1)) + 1;
+      b1 = static_cast<int64_t>(bd.key_hi(kvh, a0 + BQ - 1)) + 1;
     } else {
-      b0 = bd.row_lo(sl, a0) / BK * BK;
+      b0 = bd.row_lo(kvh, a0) / BK * BK;
       b1 = a0 + BQ < N ? a0 + BQ : N;
     }
   }
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     const int64_t a = a0 + 4 * ty + r;
-    lim[r] = !causal ? 0 : (COL ? bd.key_hi(sl, a) : bd.row_lo(sl, a));
+    lim[r] = !causal ? 0 : (COL ? bd.key_hi(kvh, a) : bd.row_lo(kvh, a));
     hst[r] = (!COL && a < N) ? stats[sl * N + a] : make_float4(0.f, 0.f, 0.f, 0.f);
   }
   float acc[2][4][W], accV[COL ? 4 : 1][WV];
@@ -428,8 +429,25 @@ __global__ void __launch_bounds__(kT, 2)
   }
 }
 
+// Both passes in one launch: they read nothing of one another's, and a short sequence's blocks of
+// one pass do not fill the SMs.  The column pass's blocks, the longer ones, come first.
+template <int D>
+__global__ void __launch_bounds__(kT, 2)
+    bwd_kernel(const float* __restrict__ Q, const float* __restrict__ K, const float* __restrict__ V,
+               const float* __restrict__ dO, const float* __restrict__ lam, const float4* stats,
+               float* __restrict__ dQ, float* __restrict__ dK, float* __restrict__ dV, float* __restrict__ partial,
+               int64_t N, int64_t H, int nblk, int BHkv, int G, float scale, int causal, Band bd) {
+  const int ncol = nblk * BHkv, x = static_cast<int>(blockIdx.x);
+  if (x < ncol)
+    bwd_pass<D, true>(Q, K, V, dO, lam, stats, dK, dV, nullptr, N, H, nblk, BHkv, G, scale, causal, bd, x);
+  else
+    bwd_pass<D, false>(Q, K, V, dO, lam, stats, dQ, nullptr, partial, N, H, nblk, BHkv * G, G, scale, causal, bd,
+                       x - ncol);
+}
+
 __global__ void __launch_bounds__(256)
-    dlam_kernel(const float* __restrict__ partial, float* __restrict__ dlam, int64_t B, int64_t H, int64_t nblk) {
+    dlam_kernel(const float* partial, float* __restrict__ dlam, int64_t B, int64_t H, int64_t nblk) {
+  ptx::grid_dependency_wait();  // the blocks' sums
   const int64_t h = blockIdx.x;
   float t = 0.f;
   for (int64_t b = 0; b < B; ++b)
@@ -476,15 +494,10 @@ cudaError_t bwd(const Problem& p, const void* Q_, const void* K_, const void* V_
       make_band(p, eff_window(p), false));
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if ((e = set_smem(bwd_kernel<D, false>, bwd_smem<D>())) != cudaSuccess) return e;
-  if ((e = set_smem(bwd_kernel<D, true>, bwd_smem<D>())) != cudaSuccess) return e;
-  bwd_kernel<D, false><<<static_cast<unsigned>(nblk * p.BH), kT, bwd_smem<D>(), st>>>(
-      Q, K, V, dO, lam, stats, static_cast<float*>(dQ), nullptr, partial, p.N, p.H, nblk, static_cast<int>(p.BH), p.group,
-      p.scale, p.causal, make_band(p, eff_window(p), false));
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  bwd_kernel<D, true><<<static_cast<unsigned>(nblk * p.BHkv), kT, bwd_smem<D>(), st>>>(
-      Q, K, V, dO, lam, stats, static_cast<float*>(dK), static_cast<float*>(dV), nullptr, p.N, p.H, nblk,
-      static_cast<int>(p.BHkv), p.group, p.scale, p.causal, make_band(p, eff_window(p), true));
+  if ((e = set_smem(bwd_kernel<D>, bwd_smem<D>())) != cudaSuccess) return e;
+  bwd_kernel<D><<<static_cast<unsigned>(nblk * (p.BH + p.BHkv)), kT, bwd_smem<D>(), st>>>(
+      Q, K, V, dO, lam, stats, static_cast<float*>(dQ), static_cast<float*>(dK), static_cast<float*>(dV), partial, p.N,
+      p.H, nblk, static_cast<int>(p.BHkv), p.group, p.scale, p.causal, make_band(p, eff_window(p), true));
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return diff_reduce_dlam(partial, dlam, p.B, p.H, nblk, st);
 }
@@ -492,8 +505,7 @@ cudaError_t bwd(const Problem& p, const void* Q_, const void* K_, const void* V_
 }  // namespace
 
 cudaError_t diff_reduce_dlam(const float* partial, float* dlam, int64_t B, int64_t H, int64_t nblk, cudaStream_t st) {
-  dlam_kernel<<<static_cast<unsigned>(H), 256, 0, st>>>(partial, dlam, B, H, nblk);
-  return cudaGetLastError();
+  return launch_behind(dlam_kernel, H, 256, 0, st, partial, dlam, B, H, nblk);
 }
 
 size_t simt_diff_bwd_bytes(int64_t BH, int64_t N) {

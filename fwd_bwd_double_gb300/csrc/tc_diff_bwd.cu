@@ -269,6 +269,7 @@ __device__ __forceinline__ void row_pass(const Args& p, int block, const CUtenso
     const int lo_row = (WIN && causal) ? bd.row_lo(kvh, row) : 0;
     const float* st = stats + (static_cast<int64_t>(bh) * nrb + rb) * (kPlanes * BW) + qd * 32 + lane;
     const float lm = lam[bh % H];
+    ptx::grid_dependency_wait();  // the statistics are the preparation's
     const bool one = st[2 * BW] == -INFINITY;  // the row sees one key: its dS is 0
     const uint64_t c2 = tc::pk2f(c, c);
     const uint64_t nL[2] = {tc::pk2f(st[0], st[0]), tc::pk2f(st[BW], st[BW])};
@@ -571,6 +572,7 @@ __device__ __forceinline__ void col_pass(const Args& p, int block, const CUtenso
       return reinterpret_cast<const float4*>(stats + ((static_cast<int64_t>(kvh) * G + h) * nb + i) * (kPlanes * BW));
     };
     float4 v[4];
+    ptx::grid_dependency_wait();  // the statistics are the preparation's
 #pragma unroll
     for (int u = 0; u < 4; ++u) v[u] = src(0)[32 * u + lane];
     for (int t = 0; t < nt; ++t) {
@@ -753,19 +755,16 @@ __device__ __forceinline__ void load_words(const __nv_bfloat16* p, uint32_t (&x)
 }
 
 // The row statistics both passes read, kPlanes rows of 128 per block of queries (zeros past N):
-// -L_1 log2 e, -L_2 log2 e, -D_1, lam D_2, -D_2.  16 threads per row.
+// -L_1 log2 e, -L_2 log2 e, -D_1, lam D_2, -D_2.  16 threads per row, 16 rows of a head per block.
 template <int DV>
 __global__ void __launch_bounds__(256)
     prep_kernel(const __nv_bfloat16* __restrict__ O, const __nv_bfloat16* __restrict__ O2,
                 const __nv_bfloat16* __restrict__ dO, const float* __restrict__ lse, const float* __restrict__ lam,
-                float* __restrict__ stats, int64_t N, int64_t Np, int64_t H, int64_t BH, int causal, Band bd) {
+                float* __restrict__ stats, int64_t N, unsigned per_head, unsigned H, int causal, Band bd) {
   constexpr int W = DV / 16;  // columns per thread
-  const int64_t gid = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const int64_t rowg = gid >> 4;
-  const int part = static_cast<int>(gid & 15);
-  const bool valid = rowg < BH * Np;  // every lane stays for the shuffles below
-  const int64_t bh = valid ? rowg / Np : 0, row = valid ? rowg - bh * Np : 0;
-  const bool live = valid && row < N;
+  const unsigned bh = blockIdx.x / per_head, blk = blockIdx.x - bh * per_head;
+  const int row = static_cast<int>(blk * 16 + (threadIdx.x >> 4)), part = static_cast<int>(threadIdx.x & 15);
+  const bool live = row < N;
   float d = 0.f, d2 = 0.f;
   if (live) {
     const int64_t off = (bh * N + row) * DV + part * W;
@@ -785,17 +784,17 @@ __global__ void __launch_bounds__(256)
     d += __shfl_xor_sync(0xffffffffu, d, x);
     d2 += __shfl_xor_sync(0xffffffffu, d2, x);
   }
-  if (valid && part < kPlanes) {
+  if (part < kPlanes) {
     float v = 0.f;
     if (live) {
       const float lm = lam[bh % H];
       const bool one = diff_one_key(bd, causal, bh, row);
-      v = part < 2 ? -lse[(2 * bh + part) * N + row] * kLog2e
+      v = part < 2 ? -lse[(2 * static_cast<int64_t>(bh) + part) * N + row] * kLog2e
           : part == 2 ? -diff_mark_D(fmaf(lm, d2, d), one)
           : part == 3 ? lm * d2
                       : -diff_mark_D(d2, one);
     }
-    stats[((bh * Np + row) / BW * kPlanes + part) * BW + row % BW] = v;
+    stats[(static_cast<int64_t>(bh) * (per_head / 8) + row / BW) * (kPlanes * BW) + part * BW + row % BW] = v;
   }
 }
 
@@ -816,10 +815,11 @@ cudaError_t run(const Problem& p, const void* Q, const void* K, const void* V, c
       !make_tmap_bf16(&mdq, dQ, N, D, 2 * BH, BW) || !make_tmap_bf16(&mdk, dK, N, D, 2 * p.BHkv, BW) ||
       !make_tmap_bf16(&mdv, dV, N, DV, p.BHkv, BW))
     return cudaErrorInvalidValue;
-  const int64_t threads = BH * Np * 16;
-  prep_kernel<DV><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, st>>>(
+  const int64_t per_head = Np / 16;
+  prep_kernel<DV><<<static_cast<unsigned>(BH * per_head), 256, 0, st>>>(
       static_cast<const __nv_bfloat16*>(O), static_cast<const __nv_bfloat16*>(O2),
-      static_cast<const __nv_bfloat16*>(dO), lse, lam, stats, N, Np, p.H, BH, p.causal, make_band(p, eff_window(p), false));
+      static_cast<const __nv_bfloat16*>(dO), lse, lam, stats, N, static_cast<unsigned>(per_head),
+      static_cast<unsigned>(p.H), p.causal, make_band(p, eff_window(p), false));
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int nb = static_cast<int>(blocks(N));
@@ -829,8 +829,8 @@ cudaError_t run(const Problem& p, const void* Q, const void* K, const void* V, c
   constexpr int smem = Lay<DV, true>::bytes;
   static_assert(smem >= Lay<DV, false>::bytes, "one launch, one size");
   if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(nb * (BH + p.BHkv)), kThreads, smem, st>>>(q, g, k, v, mdq, mdk, mdv, args);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_behind(kern, nb * (BH + p.BHkv), kThreads, smem, st, q, g, k, v, mdq, mdk, mdv, args);
+  if (e != cudaSuccess) return e;
   return diff_reduce_dlam(partial, dlam, p.B, p.H, nb, st);
 }
 
