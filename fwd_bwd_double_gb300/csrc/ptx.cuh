@@ -148,6 +148,31 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 // of, have completed and their writes are visible (no effect in an ordinary launch).
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Cluster launch control: ask for a block of this grid that has not started yet.  The answer (16
+// bytes, 16-byte aligned shared memory) completes 16 bytes of `bar`; after an answer without a
+// block no further one may be asked for.
+__device__ __forceinline__ void clc_request(void* answer, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          smem_u32(answer)),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+// The x index of the block in the answer, which is this CTA's to run now, or -1.
+__device__ __forceinline__ int clc_block(const void* answer) {
+  int x;
+  asm volatile(
+      "{\n\t.reg .b128 a;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 a, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "mov.s32 %0, -1;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, a;\n\t}"
+      : "=r"(x)
+      : "r"(smem_u32(answer))
+      : "memory");
+  return x;
+}
+
 // Registers per thread of the calling warpgroup, lowered or raised (all four warps execute
 // it).  A raise waits until the block's own launch-time registers (threads x registers at
 // launch) cover it, so the shares of all warpgroups must sum to no more than that.

@@ -9,6 +9,11 @@
 // The two maps take turns: while four warps exponentiate S_1, the tensor cores run P_2 V and
 // the next S_2, and the other way round (six products of 128 x 128 x 64 a block).  TMEM is
 // full: S_1, S_2 (128 columns each, P_m over the first half of S_m) and O_1, O_2 (2d each).
+// A CTA takes row blocks one after another, heaviest first, each next one by cluster launch
+// control: its loads and first products run under this one's epilogue, and the uneven blocks
+// spread over the SMs as separate CTAs would (a CTA per row block: 143 against 130 us at B4 H6
+// N4096, 98 against 88 us for a window of 1024 in 8000; row blocks dealt out in a fixed order:
+// 241 against 166 us at B1 H2 N16384).
 // The MMA warp issues S_m of block j + 1 behind P_m V of block j; products of one thread
 // run in order, so S_m overwrites P_m only once it has been read.  P_m V starts on the first
 // 64 keys' P while the rest is exponentiated.
@@ -28,7 +33,7 @@ namespace {
 __device__ unsigned int g_err = 0;
 
 constexpr int BM = 128, BN = 128;
-constexpr int NS = 3;
+constexpr int NS = 2;
 // Warps 0-3: map 1, 4-7: map 2, 8: TMA, 9: MMA.  384 threads launched with 168 registers; the
 // softmax warps (a row of 128 scores each thread) take 208, the third warpgroup's keep 80:
 // 256 * 208 + 128 * 80 <= 384 * 168.
@@ -44,9 +49,11 @@ struct Lay {
   static constexpr int kV = BN * DV * 2;
   static constexpr int kStage = 2 * kQ + kV;  // K_1, K_2, V
   static constexpr int oStage = 2 * kQ;
-  static constexpr int oInv = oStage + NS * kStage;  // 1 / l_2 of every row
+  static constexpr int oOut = oStage + NS * kStage;  // O, O_2 on their way out
+  static constexpr int oInv = oOut + 2 * BM * DV * 2;  // 1 / l_2 of every row
   static constexpr int oBar = oInv + BM * 4;
-  static constexpr int bytes = oBar + 192;
+  static constexpr int oClc = oBar + 192;
+  static constexpr int bytes = oClc + 16;
   static constexpr uint32_t cS = 0, cO = 2 * BN;  // S_m at cS + m BN, O_m at cO + m DV
 };
 static_assert(Lay<64>::bytes <= 232448, "shared memory");
@@ -71,26 +78,52 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* p_half = s_full + 2;          // [2] P_m of the first 64 keys in TMEM, O_m rescaled
   uint64_t* p_ready = p_half + 2;         // [2] of all keys
   uint64_t* o_full = p_ready + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + 1);
+  uint64_t* o_empty = o_full + 1;         // O_1, O_2 read by the epilogue
+  uint64_t* q_empty = o_empty + 1;        // the row block's last S_1, S_2 done
+  uint64_t* x_full = q_empty + 1;         // the next row block is known
+  uint64_t* x_empty = x_full + 1;         // ... and every role has taken it
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(x_empty + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* sInv = reinterpret_cast<float*>(sm + L::oInv);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const tc::Order ord = tc::grid_order(BH, nrb);
-  const int bh = ord.bh, kvh = bh / G;
-  const int rb = nrb - 1 - ord.k;  // heaviest row blocks first
-  const int j0 = (WIN && causal) ? bd.row_lo(bh, rb * BM) / BN : 0;
-  const int lo_last = (WIN && causal) ? bd.row_lo(bh, min(rb * BM + BM - 1, N - 1)) : 0;
-  const int nkv = (causal ? rb + 1 : nrb) - j0;
+  // A row block: its slices, and the key blocks j0 + j, j < nkv, it sees.
+  struct Item {
+    int bh, kvh, rb, j0, nkv;
+  };
+  auto item_at = [&](int x) {
+    const tc::Order ord = tc::grid_order_at(x, BH, nrb);
+    Item it;
+    it.bh = ord.bh, it.kvh = ord.bh / G;
+    it.rb = nrb - 1 - ord.k;  // heaviest row blocks first
+    it.j0 = (WIN && causal) ? bd.row_lo(it.bh, it.rb * BM) / BN : 0;
+    it.nkv = (causal ? it.rb + 1 : nrb) - it.j0;
+    return it;
+  };
+  // The row block after the n-th (-1: none), for a whole warp or for one thread of it.
+  auto next_item = [&](int n, const auto& w, bool whole_warp) {
+    bool known = w(x_full, n & 1);
+    if (whole_warp) known = __all_sync(0xffffffffu, known);
+    if (!known) return -1;  // a wait has given up: the CTA ends
+    const int x = ptx::clc_block(sm + L::oClc);
+    ptx::fence_proxy_async_smem();
+    if (whole_warp) __syncwarp();
+    if (!whole_warp || lane == 0) ptx::mbar_arrive(x_empty);
+    return x;
+  };
 
-  auto load = [&](int j) {
-    const int s = j % NS;
+  auto load_q = [&](const Item& it) {
+    ptx::mbar_expect_tx(q_full, 2 * L::kQ);
+    for (int m = 0; m < 2; ++m) ptx::tma_load_3d(sm + m * L::kQ, &tmQ, q_full, 0, it.rb * BM, 2 * it.bh + m);
+  };
+  auto load = [&](const Item& it, int j, int T) {  // key block j; T: blocks so far, the ring's position
+    const int s = T % NS;
     uint8_t* st = sm + L::oStage + s * L::kStage;
     ptx::mbar_expect_tx(&k_full[s], 2 * L::kQ);
-    for (int m = 0; m < 2; ++m) ptx::tma_load_3d(st + m * L::kQ, &tmK, &k_full[s], 0, (j0 + j) * BN, 2 * kvh + m);
+    for (int m = 0; m < 2; ++m) ptx::tma_load_3d(st + m * L::kQ, &tmK, &k_full[s], 0, (it.j0 + j) * BN, 2 * it.kvh + m);
     ptx::mbar_expect_tx(&v_full[s], L::kV);
     for (int u = 0; u < DV / 64; ++u)
-      ptx::tma_load_3d(st + 2 * L::kQ + u * BN * 128, &tmV, &v_full[s], u * 64, (j0 + j) * BN, kvh);
+      ptx::tma_load_3d(st + 2 * L::kQ + u * BN * 128, &tmV, &v_full[s], u * 64, (it.j0 + j) * BN, it.kvh);
   };
   // The TMA thread sets the barriers up and starts the first loads before the others are let in
   // (the TMEM allocation alone takes about a thousand cycles).
@@ -107,13 +140,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&p_ready[m], 128);
     }
     ptx::mbar_init(o_full, 1);
+    ptx::mbar_init(o_empty, 256);
+    ptx::mbar_init(q_empty, 1);
+    ptx::mbar_init(x_full, 1);
+    ptx::mbar_init(x_empty, 10);  // the TMA thread, the MMA warp, eight softmax warps
     *abort_flag = (ptx::smem_u32(sm) & 1023u) ? 1 : 0;  // the swizzled tiles need 1024-byte alignment
     if (*abort_flag) atomicOr(&g_err, FBD_ERR_TIMEOUT);
     ptx::fence_mbar_init();
     if (!*abort_flag) {
-      ptx::mbar_expect_tx(q_full, 2 * L::kQ);
-      for (int m = 0; m < 2; ++m) ptx::tma_load_3d(sm + m * L::kQ, &tmQ, q_full, 0, rb * BM, 2 * bh + m);
-      for (int j = 0; j < nkv && j < NS; ++j) load(j);
+      const Item it = item_at(static_cast<int>(blockIdx.x));
+      load_q(it);
+      for (int j = 0; j < it.nkv && j < NS; ++j) load(it, j, j);
     }
   }
   if (warp == 9) {
@@ -131,12 +168,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 8) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0 && ok) {
-      for (int j = NS; j < nkv; ++j) {
-        wait(&empty[j % NS], ((j / NS) - 1) & 1);
-        load(j);
+      int T = 0;
+      for (int x = static_cast<int>(blockIdx.x), n = 0; x >= 0; x = next_item(n, wait, false), ++n) {
+        const Item it = item_at(x);
+        if (n > 0) {
+          wait(q_empty, (n - 1) & 1);
+          load_q(it);
+        }
+        for (int j = 0; j < it.nkv; ++j, ++T) {
+          if (n == 0 && j < NS) continue;  // (issued above)
+          if (T >= NS) wait(&empty[T % NS], ((T / NS) - 1) & 1);
+          load(it, j, T);
+        }
+        // Ask for the next row block now, a few key blocks before this one ends: asked for sooner,
+        // it would wait here while other SMs run out.
+        if (n > 0) wait(x_empty, (n - 1) & 1);
+        ptx::mbar_expect_tx(x_full, 16);
+        ptx::clc_request(sm + L::oClc, x_full);
       }
-      // the last stages must have been consumed before the CTA exits
-      for (int j = (nkv > NS ? nkv - NS : 0); j < nkv; ++j) wait(&empty[j % NS], (j / NS) & 1);
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------- MMA issuer
@@ -146,47 +195,54 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dQ = tc::kmajor_desc(ptx::smem_u32(sm), BM, 0);
       const uint64_t dK = tc::kmajor_desc(ptx::smem_u32(sm + L::oStage), BN, 0);
       const uint64_t dV = tc::mnmajor_desc(ptx::smem_u32(sm + L::oStage + 2 * L::kQ), BN, 0);
-      auto issue_s = [&](int m, int j) {
-        const uint32_t so = static_cast<uint32_t>((j % NS) * L::kStage + m * L::kQ);
+      auto issue_s = [&](int m, int T) {
+        const uint32_t so = static_cast<uint32_t>((T % NS) * L::kStage + m * L::kQ);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
           ptx::mma_ss_e(tmem + L::cS + m * BN, tc::desc_add(dQ, m * L::kQ + tc::kmajor_off(BM, k)),
                         tc::desc_add(dK, so + tc::kmajor_off(BN, k)), idS, k > 0 ? 1u : 0u);
         ptx::mma_commit_e(&s_full[m]);
       };
-      wait(q_full, 0);
-      wait(&k_full[0], 0);
-      ptx::tc_fence_after();
-      issue_s(0, 0);
-      issue_s(1, 0);
-      for (int j = 0; j < nkv; ++j) {
-        const int s = j % NS;
-        const uint32_t so = static_cast<uint32_t>(s * L::kStage);
+      int T = 0;
+      for (int x = static_cast<int>(blockIdx.x), n = 0; x >= 0; x = next_item(n, wait, true), ++n) {
+        const int nkv = item_at(x).nkv;
+        wait(q_full, n & 1);
+        wait(&k_full[T % NS], (T / NS) & 1);
+        ptx::tc_fence_after();
+        issue_s(0, T);
+        issue_s(1, T);
+        if (nkv == 1) ptx::mma_commit_e(q_empty);
+        for (int j = 0; j < nkv; ++j, ++T) {
+          const int s = T % NS;
+          const uint32_t so = static_cast<uint32_t>(s * L::kStage);
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          wait(&p_half[m], j & 1);
-          if (m == 0) wait(&v_full[s], (j / NS) & 1);
-          ptx::tc_fence_after();
+          for (int m = 0; m < 2; ++m) {
+            wait(&p_half[m], T & 1);
+            if (m == 0) wait(&v_full[s], (T / NS) & 1);
+            if (m == 0 && j == 0 && n > 0) wait(o_empty, (n - 1) & 1);
+            ptx::tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < BN / 16; ++k) {
-            if (k == BN / 32) {
-              wait(&p_ready[m], j & 1);
-              ptx::tc_fence_after();
+            for (int k = 0; k < BN / 16; ++k) {
+              if (k == BN / 32) {
+                wait(&p_ready[m], T & 1);
+                ptx::tc_fence_after();
+              }
+              ptx::mma_ts_e(tmem + L::cO + m * DV, tmem + L::cS + m * BN + k * 8, tc::desc_add(dV, so + k * 2048), idO,
+                            (j > 0 || k > 0) ? 1u : 0u);
             }
-            ptx::mma_ts_e(tmem + L::cO + m * DV, tmem + L::cS + m * BN + k * 8, tc::desc_add(dV, so + k * 2048), idO,
-                          (j > 0 || k > 0) ? 1u : 0u);
-          }
-          if (m == 1) ptx::mma_commit_e(&empty[s]);
-          if (j + 1 < nkv) {
-            if (m == 0) {
-              wait(&k_full[(j + 1) % NS], ((j + 1) / NS) & 1);
-              ptx::tc_fence_after();
+            if (m == 1) ptx::mma_commit_e(&empty[s]);
+            if (j + 1 < nkv) {
+              if (m == 0) {
+                wait(&k_full[(T + 1) % NS], ((T + 1) / NS) & 1);
+                ptx::tc_fence_after();
+              }
+              issue_s(m, T + 1);
+              if (m == 1 && j + 2 == nkv) ptx::mma_commit_e(q_empty);
             }
-            issue_s(m, j + 1);
           }
         }
+        ptx::mma_commit_e(o_full);
       }
-      ptx::mma_commit_e(o_full);
     }
   } else if (warp < 8) {
     ptx::setmaxnreg_inc<kRegs>();
@@ -195,130 +251,145 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = threadIdx.x & 127;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + L::cS + m * BN + lane_off, tO = tmem + L::cO + lane_off;
-    const int64_t row = static_cast<int64_t>(rb) * BM + r;
-    const int lo_row = (WIN && causal) ? bd.row_lo(bh, row) : 0;
-    const float slack = kSlack / c, lm = lam[bh % H];
+    const float slack = kSlack / c;
     const uint64_t c2 = tc::pk2f(c, c);
-    float mref = -INFINITY, l = 0.f;
-    for (int j = 0; j < nkv; ++j) {
-      const int kb = j0 + j;
-      const bool diag = causal ? kb == rb : (j == nkv - 1 && (N % BN) != 0);
-      const bool low = WIN && causal && kb * BN < lo_last;
-      const int klim = causal ? (WIN ? rb * BM + r - kb * BN : r) : N - 1 - kb * BN;  // last visible key
-      const int klo = (WIN && causal) ? lo_row - kb * BN : 0;                         // first one
-      wait(&s_full[m], j & 1);
-      ptx::tc_fence_after();
-      uint32_t v[4][32];
+    int T = 0;
+    for (int x = static_cast<int>(blockIdx.x), n = 0; x >= 0; x = next_item(n, wait, true), ++n) {
+      const Item it = item_at(x);
+      const int bh = it.bh, rb = it.rb, j0 = it.j0, nkv = it.nkv;
+      const float lm = lam[bh % H];
+      const int64_t row = static_cast<int64_t>(rb) * BM + r;
+      const int lo_row = (WIN && causal) ? bd.row_lo(bh, row) : 0;
+      const int lo_last = (WIN && causal) ? bd.row_lo(bh, min(rb * BM + BM - 1, N - 1)) : 0;
+      float mref = -INFINITY, l = 0.f;
+      for (int j = 0; j < nkv; ++j, ++T) {
+        const int kb = j0 + j;
+        const bool diag = causal ? kb == rb : (j == nkv - 1 && (N % BN) != 0);
+        const bool low = WIN && causal && kb * BN < lo_last;
+        const int klim = causal ? (WIN ? rb * BM + r - kb * BN : r) : N - 1 - kb * BN;  // last visible key
+        const int klo = (WIN && causal) ? lo_row - kb * BN : 0;                         // first one
+        wait(&s_full[m], T & 1);
+        ptx::tc_fence_after();
+        uint32_t v[4][32];
 #pragma unroll
-      for (int ch = 0; ch < 4; ++ch) ptx::tmem_ld32(tS + ch * 32, v[ch]);
-      ptx::tmem_wait_ld();
-      if (diag || low) {
-        // bounds grow with the row: the warp's first row has the first last key, its last row
-        // the last first one, and 32 keys between the two need no masking
-        const int klim0 = __shfl_sync(0xffffffffu, klim, 0), klo31 = __shfl_sync(0xffffffffu, klo, 31);
+        for (int ch = 0; ch < 4; ++ch) ptx::tmem_ld32(tS + ch * 32, v[ch]);
+        ptx::tmem_wait_ld();
+        if (diag || low) {
+          // bounds grow with the row: the warp's first row has the first last key, its last row
+          // the last first one, and 32 keys between the two need no masking
+          const int klim0 = __shfl_sync(0xffffffffu, klim, 0), klo31 = __shfl_sync(0xffffffffu, klo, 31);
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch)
+            if (ch * 32 + 31 > klim0 || ch * 32 < klo31) {
+#pragma unroll
+              for (int t = 0; t < 32; ++t)
+                if (ch * 32 + t > klim || ch * 32 + t < klo) v[ch][t] = __float_as_uint(-INFINITY);
+            }
+        }
+        float mx[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) mx[u] = -INFINITY;
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch)
-          if (ch * 32 + 31 > klim0 || ch * 32 < klo31) {
 #pragma unroll
-            for (int t = 0; t < 32; ++t)
-              if (ch * 32 + t > klim || ch * 32 + t < klo) v[ch][t] = __float_as_uint(-INFINITY);
-          }
-      }
-      float mx[8];
+          for (int t = 0; t < 32; t += 16)
 #pragma unroll
-      for (int u = 0; u < 8; ++u) mx[u] = -INFINITY;
+            for (int u = 0; u < 8; ++u) mx[u] = fmaxf(mx[u], fmaxf(tc::f(v[ch][t + u]), tc::f(v[ch][t + 8 + u])));
 #pragma unroll
-      for (int ch = 0; ch < 4; ++ch)
-#pragma unroll
-        for (int t = 0; t < 32; t += 16)
-#pragma unroll
-          for (int u = 0; u < 8; ++u) mx[u] = fmaxf(mx[u], fmaxf(tc::f(v[ch][t + u]), tc::f(v[ch][t + 8 + u])));
-#pragma unroll
-      for (int u = 1; u < 8; ++u) mx[0] = fmaxf(mx[0], mx[u]);
-      const bool moved = mx[0] > mref + slack;  // always at the first visible key (mref = -inf)
-      const float mnew = moved ? mx[0] : mref;
-      const float alpha = moved ? ptx::ex2((mref - mnew) * c) : 1.f;
-      if (j > 0 && __any_sync(0xffffffffu, moved)) {
-        const uint64_t a2 = tc::pk2f(alpha, alpha);
+        for (int u = 1; u < 8; ++u) mx[0] = fmaxf(mx[0], mx[u]);
+        const bool moved = mx[0] > mref + slack;  // always at the first visible key (mref = -inf)
+        const float mnew = moved ? mx[0] : mref;
+        const float alpha = moved ? ptx::ex2((mref - mnew) * c) : 1.f;
+        if (j > 0 && __any_sync(0xffffffffu, moved)) {
+          const uint64_t a2 = tc::pk2f(alpha, alpha);
 #pragma unroll 1
-        for (int c0 = 0; c0 < DV; c0 += 16) {  // 16 columns at a time: the scores hold 128 registers
-          uint32_t o[16];
-          ptx::tmem_ld16(tO + m * DV + c0, o);
-          ptx::tmem_wait_ld();
+          for (int c0 = 0; c0 < DV; c0 += 16) {  // 16 columns at a time: the scores hold 128 registers
+            uint32_t o[16];
+            ptx::tmem_ld16(tO + m * DV + c0, o);
+            ptx::tmem_wait_ld();
 #pragma unroll
-          for (int t = 0; t < 16; t += 2) {
-            const float2 x = tc::unpk2(tc::mul2(tc::pk2(o[t], o[t + 1]), a2));
-            o[t] = __float_as_uint(x.x);
-            o[t + 1] = __float_as_uint(x.y);
+            for (int t = 0; t < 16; t += 2) {
+              const float2 x = tc::unpk2(tc::mul2(tc::pk2(o[t], o[t + 1]), a2));
+              o[t] = __float_as_uint(x.x);
+              o[t + 1] = __float_as_uint(x.y);
+            }
+            ptx::tmem_st16(tO + m * DV + c0, o);
           }
-          ptx::tmem_st16(tO + m * DV + c0, o);
         }
-      }
-      l *= alpha;
-      mref = mnew;
-      // a row that has seen no key yet subtracts 0, not -inf: every term is 2^-inf = 0
-      const float nm = mref == -INFINITY ? 0.f : -mref * c;
-      const uint64_t nm2 = tc::pk2f(nm, nm);
-      uint64_t rs[4] = {0, 0, 0, 0};
+        l *= alpha;
+        mref = mnew;
+        // a row that has seen no key yet subtracts 0, not -inf: every term is 2^-inf = 0
+        const float nm = mref == -INFINITY ? 0.f : -mref * c;
+        const uint64_t nm2 = tc::pk2f(nm, nm);
+        uint64_t rs[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int ch = 0; ch < 4; ++ch) {
-        uint32_t pk[16];
+        for (int ch = 0; ch < 4; ++ch) {
+          uint32_t pk[16];
 #pragma unroll
-        for (int t = 0; t < 32; t += 2) {
-          const float2 arg = tc::unpk2(tc::fma2(tc::pk2(v[ch][t], v[ch][t + 1]), c2, nm2));
-          const float p0 = ptx::ex2(arg.x), p1 = ptx::ex2(arg.y);
-          rs[(t >> 1) & 3] = tc::add2(rs[(t >> 1) & 3], tc::pk2f(p0, p1));
-          pk[t >> 1] = ptx::pack_bf16(p0, p1);
+          for (int t = 0; t < 32; t += 2) {
+            const float2 arg = tc::unpk2(tc::fma2(tc::pk2(v[ch][t], v[ch][t + 1]), c2, nm2));
+            const float p0 = ptx::ex2(arg.x), p1 = ptx::ex2(arg.y);
+            rs[(t >> 1) & 3] = tc::add2(rs[(t >> 1) & 3], tc::pk2f(p0, p1));
+            pk[t >> 1] = ptx::pack_bf16(p0, p1);
+          }
+          ptx::tmem_st16(tS + ch * 16, pk);
+          if (ch & 1) {
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(ch == 1 ? &p_half[m] : &p_ready[m]);
+          }
         }
-        ptx::tmem_st16(tS + ch * 16, pk);
-        if (ch & 1) {
-          ptx::tmem_wait_st();
-          ptx::tc_fence_before();
-          ptx::mbar_arrive(ch == 1 ? &p_half[m] : &p_ready[m]);
-        }
+        const float2 x = tc::unpk2(tc::add2(tc::add2(rs[0], rs[1]), tc::add2(rs[2], rs[3])));
+        l += x.x + x.y;
       }
-      const float2 x = tc::unpk2(tc::add2(tc::add2(rs[0], rs[1]), tc::add2(rs[2], rs[3])));
-      l += x.x + x.y;
+      // ------------------------------------------------------------------ epilogue
+      const float inv = 1.f / l;
+      if (row < N) lse[(2 * static_cast<int64_t>(bh) + m) * N + row] = mref * scale + logf(l);
+      wait(o_full, n & 1);
+      if (m == 1) sInv[r] = inv;  // (map 1 is done with the last row block's: it has taken part in this one)
+      tc::named_sync(1, 256);
+      ptx::tc_fence_after();
+      if (m == 0 || with_O2) {
+        const float w = m == 0 ? -lm * sInv[r] : inv;  // of O_2's columns
+        // Through shared memory as 64-column tiles, and out by TMA: a row per thread straight to
+        // memory, 16 bytes at a time, took 5.6 thousand cycles of each row block.
+        uint8_t* out = sm + L::oOut + m * BM * DV * 2;
+        if (r == 0) ptx::bulk_wait_group_read0();  // the last row block's has left
+        tc::named_sync(2 + m, 128);
+#pragma unroll
+        for (int ch = 0; ch < DV / 32; ++ch) {
+          uint32_t a[32], b[32];
+          ptx::tmem_ld32(tO + DV + ch * 32, b);
+          if (m == 0) ptx::tmem_ld32(tO + ch * 32, a);
+          ptx::tmem_wait_ld();
+          if (ch == DV / 32 - 1) {
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(o_empty);
+          }
+          uint32_t pk[16];
+#pragma unroll
+          for (int t = 0; t < 32; t += 2) {
+            float x0 = tc::f(b[t]) * w, x1 = tc::f(b[t + 1]) * w;
+            if (m == 0) x0 = fmaf(tc::f(a[t]), inv, x0), x1 = fmaf(tc::f(a[t + 1]), inv, x1);
+            pk[t >> 1] = ptx::pack_bf16(x0, x1);
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            *reinterpret_cast<uint4*>(out + (ch >> 1) * BM * 128 + tc::sw128(r, (ch & 1) * 4 + u)) =
+                make_uint4(pk[u * 4], pk[u * 4 + 1], pk[u * 4 + 2], pk[u * 4 + 3]);
+        }
+        ptx::fence_proxy_async_smem();
+        tc::named_sync(2 + m, 128);
+        if (r == 0) {
+          for (int u = 0; u < DV / 64; ++u)
+            ptx::tma_store_3d(m == 0 ? &tmO : &tmO2, out + u * BM * 128, u * 64, rb * BM, bh);
+          ptx::bulk_commit_group();
+        }
+      } else {
+        ptx::mbar_arrive(o_empty);
+      }
     }
-    // ------------------------------------------------------------------ epilogue
-    const float inv = 1.f / l;
-    if (m == 1) sInv[r] = inv;
-    if (row < N) lse[(2 * static_cast<int64_t>(bh) + m) * N + row] = mref * scale + logf(l);
-    wait(o_full, 0);
-    tc::named_sync(1, 256);
-    ptx::tc_fence_after();
-    if (m == 0 || with_O2) {
-      const float w = m == 0 ? -lm * sInv[r] : inv;  // of O_2's columns
-      // Through the stages (every block has been read) as 64-column tiles, and out by TMA: a row
-      // per thread straight to memory, 16 bytes at a time, took 5.6 thousand cycles of each CTA.
-      uint8_t* out = sm + L::oStage + m * BM * DV * 2;
-#pragma unroll
-      for (int ch = 0; ch < DV / 32; ++ch) {
-        uint32_t a[32], b[32];
-        ptx::tmem_ld32(tO + DV + ch * 32, b);
-        if (m == 0) ptx::tmem_ld32(tO + ch * 32, a);
-        ptx::tmem_wait_ld();
-        uint32_t pk[16];
-#pragma unroll
-        for (int t = 0; t < 32; t += 2) {
-          float x0 = tc::f(b[t]) * w, x1 = tc::f(b[t + 1]) * w;
-          if (m == 0) x0 = fmaf(tc::f(a[t]), inv, x0), x1 = fmaf(tc::f(a[t + 1]), inv, x1);
-          pk[t >> 1] = ptx::pack_bf16(x0, x1);
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          *reinterpret_cast<uint4*>(out + (ch >> 1) * BM * 128 + tc::sw128(r, (ch & 1) * 4 + u)) =
-              make_uint4(pk[u * 4], pk[u * 4 + 1], pk[u * 4 + 2], pk[u * 4 + 3]);
-      }
-      ptx::fence_proxy_async_smem();
-      tc::named_sync(2 + m, 128);
-      if (r == 0) {
-        for (int u = 0; u < DV / 64; ++u)
-          ptx::tma_store_3d(m == 0 ? &tmO : &tmO2, out + u * BM * 128, u * 64, rb * BM, bh);
-        ptx::bulk_commit_group();
-        ptx::bulk_wait_group_read0();
-      }
-    }
+    if (r == 0) ptx::bulk_wait_group_read0();
   }
 
   ptx::tc_fence_before();
