@@ -19,7 +19,10 @@
 // 64 keys' P while the rest is exponentiated.
 //
 // The reference maximum M_m moves only when a row's maximum passes it by more than 2^8 in
-// the probabilities (P_m <= 2^8, l and O_m in fp32): most blocks then rescale nothing.
+// the probabilities (P_m <= 2^8, l and O_m in fp32): most blocks then rescale nothing.  Moving it
+// with every maximum took 569 against 452 us at B4 H6 N8192; what it buys, a largest P of exactly
+// 1, is a little accuracy where attention is nearly one-hot (keys with a shared mean of norm 40:
+// O within 1.8e-3 against 2.1e-3 of 64-bit values, dQ 1.9e-2 against 2.1e-2).
 // P is rounded to bf16 for its product; the sums l are of the unrounded fp32 values.
 #include <cuda_bf16.h>
 
