@@ -10,6 +10,7 @@ if it is missing: there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 from . import _lib
@@ -203,9 +204,28 @@ def attn_segment_bounds(seg, seg_lo=None, seg_hi=None, stream=None):
     return seg_lo, seg_hi
 
 
-def _launch(fn, tensors, stream, *args):
-    """fn(*args, stream) on the device the tensors are on: one CUDA device, made current for the call, and `stream`
-    or that device's current stream.  Empty tensors launch nothing, so they may be anywhere."""
+def _on_stream(call):
+    """A call given a stream runs under it as torch's current stream, so that what it allocates, the workspace above
+    all, belongs to that stream and is not handed out again while the kernels there still use it."""
+
+    @functools.wraps(call)
+    def wrapped(*args, stream=None, **kwargs):
+        if stream is None:
+            return call(*args, **kwargs)
+        cuda = _torch().cuda
+        if not isinstance(stream, cuda.Stream):  # a handle: a stream of the tensors' device
+            t = args[0] if args else next(iter(kwargs.values()))
+            t = t if _torch().is_tensor(t) else t[0]
+            stream = cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=t.device)
+        with cuda.stream(stream):
+            return call(*args, **kwargs)
+
+    return wrapped
+
+
+def _launch(fn, tensors, *args):
+    """fn(*args, stream) on the device the tensors are on: one CUDA device, made current for the call, and its current
+    stream.  Empty tensors launch nothing, so they may be anywhere."""
     cuda = _torch().cuda
     devices = {t.get_device() for t in tensors if t is not None and t.numel()}
     if len(devices) > 1 or -1 in devices:
@@ -214,10 +234,7 @@ def _launch(fn, tensors, stream, *args):
         _check(fn(*args, None))
         return
     device = devices.pop()
-    if stream is None:
-        stream = cuda.current_stream(device).cuda_stream
-    else:
-        stream = int(getattr(stream, "cuda_stream", stream))
+    stream = cuda.current_stream(device).cuda_stream
     if device == cuda.current_device():
         _check(fn(*args, stream))
     else:
@@ -260,11 +277,12 @@ def _diff_desc(Q, K, V, lam, scale, causal, window, bounds, queries=None):
     return AttnDesc(B, H, N, d, scale, causal, _dtype_code(Q), H // Hkv if Hkv else 1, window, lo, hi), ptrs
 
 
-def attn_diff_fwd(Q, K, V, lam, O=None, O2=None, lse=None, scale: float = 0.0, stream=None, causal: bool = True,
-                  window: int = 0, bounds=None, for_backward: bool = True):
+@_on_stream
+def attn_diff_fwd(Q, K, V, lam, O=None, O2=None, lse=None, scale: float = 0.0, causal: bool = True, window: int = 0,
+                  bounds=None, for_backward: bool = True):
     """O, O2, lse = differential attention (A_1 - lam_h A_2) V of Q [B, 2H, N, d], K [B, 2H/g, N, d] (the maps of a
     head in neighbouring slices), V [B, H/g, N, 2d], lam [H] float32.  O2 = A_2 V and lse are what the backward
-    needs; for_backward=False leaves O2 out (returned as None)."""
+    needs; for_backward=False leaves O2 out (returned as None).  stream=: the stream to run on (keyword only)."""
     torch = _torch()
     desc, ptrs = _diff_desc(Q, K, V, lam, scale, causal, window, bounds)
     shape = (desc.B, desc.H, desc.N, 2 * desc.d)
@@ -276,7 +294,7 @@ def attn_diff_fwd(Q, K, V, lam, O=None, O2=None, lse=None, scale: float = 0.0, s
         lse = torch.empty(Q.shape[:3], dtype=torch.float32, device=Q.device)
     outs = (_want("O", O, shape, Q.dtype), None if O2 is None else _want("O2", O2, shape, Q.dtype),
             _want("lse", lse, Q.shape[:3], torch.float32))
-    _launch(lib.attn_diff_fwd, (Q, K, V, lam, O, O2, lse, *(bounds or ())), stream, ctypes.byref(desc), *ptrs, *outs)
+    _launch(lib.attn_diff_fwd, (Q, K, V, lam, O, O2, lse, *(bounds or ())), ctypes.byref(desc), *ptrs, *outs)
     return O, O2, lse
 
 
@@ -284,8 +302,9 @@ def attn_diff_bwd_workspace_bytes(desc: AttnDesc) -> int:
     return int(lib.attn_diff_bwd_workspace_bytes(ctypes.byref(desc)))
 
 
+@_on_stream
 def attn_diff_bwd(Q, K, V, lam, O, O2, dO, lse, dQ=None, dK=None, dV=None, dlam=None, workspace=None,
-                  scale: float = 0.0, stream=None, causal: bool = True, window: int = 0, bounds=None):
+                  scale: float = 0.0, causal: bool = True, window: int = 0, bounds=None):
     """dQ, dK, dV, dlam = recompute backward of attn_diff_fwd (its mask and scale given again)."""
     torch = _torch()
     desc, ptrs = _diff_desc(Q, K, V, lam, scale, causal, window, bounds)
@@ -300,8 +319,8 @@ def attn_diff_bwd(Q, K, V, lam, O, O2, dO, lse, dQ=None, dK=None, dV=None, dlam=
             _want("dlam", dlam, lam.shape, torch.float32))
     workspace = _workspace(lib.attn_diff_bwd_workspace_bytes(ctypes.byref(desc)), Q, workspace)
     _launch(lib.attn_diff_bwd, (Q, K, V, lam, O, O2, dO, lse, dQ, dK, dV, dlam, workspace if Q.numel() else None,
-                                *(bounds or ())), stream, ctypes.byref(desc), *ptrs, *ins, *outs,
-            _at("workspace", workspace), workspace.nbytes)
+                                *(bounds or ())), ctypes.byref(desc), *ptrs, *ins, *outs, _at("workspace", workspace),
+            workspace.nbytes)
     return dQ, dK, dV, dlam
 
 
@@ -309,7 +328,8 @@ def attn_diff_decode_workspace_bytes(desc: AttnDesc) -> int:
     return int(lib.attn_diff_decode_workspace_bytes(ctypes.byref(desc)))
 
 
-def attn_diff_decode(Q, K, V, lam, lens, O=None, workspace=None, scale: float = 0.0, stream=None, window: int = 0):
+@_on_stream
+def attn_diff_decode(Q, K, V, lam, lens, O=None, workspace=None, scale: float = 0.0, window: int = 0):
     """O [B, H, 1, 2d] = differential attention of one token per sequence, Q [B, 2H, 1, d], over a cache K
     [B, 2H/g, capacity, d], V [B, H/g, capacity, 2d] of which sequence b holds lens[b] keys (int32, on the device;
     the new token's among them).  A sequence without a key gives zeros."""
@@ -321,12 +341,13 @@ def attn_diff_decode(Q, K, V, lam, lens, O=None, workspace=None, scale: float = 
         O = torch.empty(shape, dtype=Q.dtype, device=Q.device)
     O_at = _want("O", O, shape, Q.dtype)
     workspace = _workspace(lib.attn_diff_decode_workspace_bytes(ctypes.byref(desc)), Q, workspace)
-    _launch(lib.attn_diff_decode, (Q, K, V, lam, lens, O, workspace if Q.numel() else None), stream,
-            ctypes.byref(desc), *ptrs, lens_at, O_at, _at("workspace", workspace), workspace.nbytes)
+    _launch(lib.attn_diff_decode, (Q, K, V, lam, lens, O, workspace if Q.numel() else None), ctypes.byref(desc), *ptrs,
+            lens_at, O_at, _at("workspace", workspace), workspace.nbytes)
     return O
 
 
-def attn_rope(xs, pos, freq, axis, outs=None, paired: str = "half", inverse: bool = False, stream=None):
+@_on_stream
+def attn_rope(xs, pos, freq, axis, outs=None, paired: str = "half", inverse: bool = False):
     """Rotary positions with several axes: pair i of each token of the [B, heads, N, d] views `xs` (one tensor or up to
     four, any strides with d contiguous) turns by freq[i] * pos[axis[i]]; pos [axes, B, N] or [axes, N] int32, freq
     [d/2] float32, axis [d/2] int32 (-1: the pair is copied unturned).  paired: "half" (coordinates i, i + d/2) or
@@ -366,7 +387,7 @@ def attn_rope(xs, pos, freq, axis, outs=None, paired: str = "half", inverse: boo
               _want("freq", freq, (d // 2,), torch.float32), _want("axis", axis, (d // 2,), torch.int32))
     desc = RopeDesc(B, N, d, axes, _dtype_code(xs[0]), ATTN_ROPE_HALF if paired == "half" else ATTN_ROPE_NEIGHBOUR,
                     bool(inverse), 0 if shared else N)
-    _launch(lib.attn_rope, (*xs, *outs, pos, freq, axis) if any(x.numel() for x in xs) else (), stream,
+    _launch(lib.attn_rope, (*xs, *outs, pos, freq, axis) if any(x.numel() for x in xs) else (),
             ctypes.byref(desc), tensors, len(xs), *tables)
     return outs[0] if single else outs
 

@@ -214,6 +214,12 @@ def test_streams_graphs_and_views_of_lam():
         got = run(x)
     for k in got:
         assert torch.equal(got[k], want[k]), k
+    for given in (st, st.cuda_stream):  # the stream as an argument, an object or its handle
+        O, O2, lse = fbd.attn_diff_fwd(*x[:4], stream=given)
+        dQ, dK, dV, dlam = fbd.attn_diff_bwd(*x[:4], O, O2, x[4], lse, stream=given)
+        st.synchronize()
+        for k, v in dict(O=O, O2=O2, lse=lse, dQ=dQ, dK=dK, dV=dV, dlam=dlam).items():
+            assert torch.equal(v, want[k]), k
     desc = fbd.AttnDesc(1, 3, 300, 64, 0.0, 1, fbd.ATTN_BF16, 1, 0, None, None)
     ws = torch.empty(fbd.attn_diff_bwd_workspace_bytes(desc), dtype=torch.uint8, device="cuda")
 
@@ -353,7 +359,10 @@ def test_decode_is_the_last_row_of_the_forward():
         Q, K, V, lam, _ = make(2, 4, 2, N, 64, "f32")
         O, _, _ = fbd.attn_diff_fwd(Q, K, V, lam)
         lens = torch.full((2,), N, dtype=torch.int32, device="cuda")
-        o = fbd.attn_diff_decode(Q[:, :, -1:].contiguous(), K, V, lam, lens)
+        st = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        o = fbd.attn_diff_decode(Q[:, :, -1:].contiguous(), K, V, lam, lens, stream=st)
+        st.synchronize()
         assert (o - O[:, :, -1:]).abs().max() <= 1e-5 * V.abs().max() * 2.1
 
 
