@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(kT, 2)
   constexpr int DV = 2 * D, NT = DV / 8;  // 8-column tiles of o
   extern __shared__ __align__(128) uint8_t sh[];
   const uint32_t s0 = ptx::smem_u32(sh);
+  ptx::grid_dependency_launch();
   const int split = blockIdx.x % nsplit, Hkv = H / G, chunks = (G + rows - 1) / rows;
   const int unit = blockIdx.x / nsplit;  // (b, key/value head, chunk of its query heads)
   const int r0 = unit % chunks * rows, n = unit / chunks % Hkv, b = unit / chunks / Hkv;
@@ -295,6 +296,7 @@ __global__ void __launch_bounds__(kT)
   extern __shared__ __align__(128) uint8_t sh[];
   float* sB = reinterpret_cast<float*>(sh);  // two tiles
   float *sQ = sB + 2 * kTile, *sP = sQ + 2 * RMAX * D, *sA = sP + 2 * RMAX * BK, *sM = sA + 2 * RMAX, *sL = sM + 2 * RMAX;
+  ptx::grid_dependency_launch();
   const int split = blockIdx.x % nsplit, Hkv = H / G, chunks = (G + rows - 1) / rows;
   const int unit = blockIdx.x / nsplit;  // (b, key/value head, chunk of its query heads)
   const int r0 = unit % chunks * rows, n = unit / chunks % Hkv, b = unit / chunks / Hkv;

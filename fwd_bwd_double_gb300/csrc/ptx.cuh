@@ -144,6 +144,9 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// Let the kernel launched behind this one be set up once every block of this one has got here or
+// ended.
+__device__ __forceinline__ void grid_dependency_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 // Wait until the kernels before this one in the stream, which it may have been launched ahead
 // of, have completed and their writes are visible (no effect in an ordinary launch).
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

@@ -736,6 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                const __grid_constant__ CUtensorMap tmdQ, const __grid_constant__ CUtensorMap tmdK,
                const __grid_constant__ CUtensorMap tmdV, const __grid_constant__ Args p) {
+  ptx::grid_dependency_launch();
   const int ncol = p.nb * p.BHkv, x = static_cast<int>(blockIdx.x);
   if (x < ncol)
     col_pass<DV, WIN>(p, x, tmQ, tmdO, tmK, tmV, tmdK, tmdV);
@@ -762,6 +763,7 @@ __global__ void __launch_bounds__(256)
                 const __nv_bfloat16* __restrict__ dO, const float* __restrict__ lse, const float* __restrict__ lam,
                 float* __restrict__ stats, int64_t N, unsigned per_head, unsigned H, int causal, Band bd) {
   constexpr int W = DV / 16;  // columns per thread
+  ptx::grid_dependency_launch();
   const unsigned bh = blockIdx.x / per_head, blk = blockIdx.x - bh * per_head;
   const int row = static_cast<int>(blk * 16 + (threadIdx.x >> 4)), part = static_cast<int>(threadIdx.x & 15);
   const bool live = row < N;
