@@ -254,7 +254,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = threadIdx.x & 127;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + L::cS + m * BN + lane_off, tO = tmem + L::cO + lane_off;
-    const float slack = kSlack / c;
+    // (finite also for the smallest scales: -inf + slack has to stay below a row's first maximum)
+    const float slack = fminf(kSlack / c, 3e38f);
     const uint64_t c2 = tc::pk2f(c, c);
     int T = 0;
     for (int x = static_cast<int>(blockIdx.x), n = 0; x >= 0; x = next_item(n, wait, true), ++n) {

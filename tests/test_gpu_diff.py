@@ -199,6 +199,21 @@ def test_repeats_bit_for_bit():
             assert torch.equal(a[name], b[name]), (dtype, name)
 
 
+def test_smallest_scales():
+    """A scale whose product with every score vanishes: uniform weights over the visible keys."""
+    import fwd_bwd_double_gb300 as fbd
+    torch = _t()
+    Q, K, V, lam, _ = make(1, 2, 1, 300, 64, "bf16")
+    O, O2, lse = fbd.attn_diff_fwd(Q, K, V, lam, scale=1.2e-38)
+    n = torch.arange(1, 301, device="cuda", dtype=torch.float64)
+    want = V.double().cumsum(2) / n[:, None]
+    # P = 1 exactly; O2 = the sum of bf16 values in fp32, 1 / l and their product, then one bf16 rounding
+    size = V.double().abs().cumsum(2) / n[:, None]
+    assert ((O2.double() - want).abs() <= 2**-8 * want.abs() + 300 * 2**-24 * size).all()
+    assert ((lse.double() - n.log()).abs() <= 2**-22 * (1 + n.log())).all()
+    assert torch.isfinite(O).all()
+
+
 def test_streams_graphs_and_views_of_lam():
     """On another stream; captured twice over one workspace and replayed in turn on new data; lam a
     slice of a larger tensor (4-byte aligned)."""
