@@ -212,11 +212,17 @@ def _on_stream(call):
     def wrapped(*args, stream=None, **kwargs):
         if stream is None:
             return call(*args, **kwargs)
-        cuda = _torch().cuda
-        if not isinstance(stream, cuda.Stream):  # a handle: a stream of the tensors' device
-            t = args[0] if args else next(iter(kwargs.values()))
-            t = t if _torch().is_tensor(t) else t[0]
-            stream = cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=t.device)
+        torch, cuda = _torch(), _torch().cuda
+        given = (t for v in (*args, *kwargs.values()) for t in (v if isinstance(v, (list, tuple)) else (v,)))
+        device = next((t.device for t in given if torch.is_tensor(t) and t.is_cuda), None)
+        if device is None:  # refused there, or nothing to launch
+            return call(*args, **kwargs)
+        if isinstance(stream, cuda.Stream):
+            if stream.device != device:
+                raise FbdError(1, f"a stream of {stream.device} for tensors on {device}")
+        else:  # a handle: a stream of the tensors' device, 0 (and cudaStreamLegacy, 1) its default one
+            handle = int(getattr(stream, "cuda_stream", stream))
+            stream = cuda.ExternalStream(handle, device=device) if handle > 1 else cuda.default_stream(device)
         with cuda.stream(stream):
             return call(*args, **kwargs)
 

@@ -182,3 +182,13 @@ def test_binding_refuses_shapes_types_and_places():
         with pytest.raises(FbdError):
             f()
             raise AssertionError(f"case {k} was accepted")
+
+
+@pytest.mark.parametrize("stream", [0, 1 << 40])
+def test_refuses_host_tensors_given_a_stream(stream):
+    import torch
+    Q, V, lam = torch.zeros(1, 4, 8, 64), torch.zeros(1, 2, 8, 128), torch.zeros(2)
+    with pytest.raises(FbdError):
+        fbd.attn_diff_fwd(Q, Q, V, lam, stream=stream)
+    with pytest.raises(FbdError):
+        fbd.attn_rope([], torch.zeros(1, 8, dtype=torch.int32), lam, lam, stream=stream)

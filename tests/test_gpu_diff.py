@@ -214,6 +214,26 @@ def test_smallest_scales():
     assert torch.isfinite(O).all()
 
 
+def test_given_streams(monkeypatch):
+    """The stream a call runs on: an object, its handle, the default stream's handle 0 under another
+    stream, keywords in any order."""
+    import fwd_bwd_double_gb300 as fbd
+    torch = _t()
+    Q, K, V, lam, _ = make(1, 2, 1, 130, 64, "bf16")
+    seen = []
+    launch = fbd._launch
+    monkeypatch.setattr(fbd, "_launch", lambda *a: (seen.append(torch.cuda.current_stream()), launch(*a)))
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        fbd.attn_diff_fwd(Q, K, V, lam)
+        fbd.attn_diff_fwd(Q, K, V, lam, stream=0)
+    fbd.attn_diff_fwd(scale=0.5, Q=Q, K=K, V=V, lam=lam, stream=st)
+    fbd.attn_diff_fwd(Q, K, V, lam, stream=st.cuda_stream)
+    assert [s.cuda_stream for s in seen] == [st.cuda_stream, 0, st.cuda_stream, st.cuda_stream]
+    torch.cuda.synchronize()
+
+
 def test_streams_graphs_and_views_of_lam():
     """On another stream; captured twice over one workspace and replayed in turn on new data; lam a
     slice of a larger tensor (4-byte aligned)."""
