@@ -328,7 +328,9 @@ attn_status_t attn_bwd_projected_dS(const attn_desc_t* desc, const void* Q, cons
  * Masks (causal, full, window, document bounds), types, scale, alignment, streams and
  * errors are those of attn_fwd, with these differences: d in {32, 64} (else
  * ATTN_ERR_UNSUPPORTED), B*H < 2^30 and B*H*ceil(N/128) < 2^28 (else ATTN_ERR_INVALID_ARG),
- * and lam, dlam and lens need only their element's alignment.
+ * and lam, dlam and lens need only their element's alignment.  In attn_diff_fwd and
+ * attn_diff_bwd, as in attn_fwd, a mask makes a key's weight 0, which an infinity or NaN in
+ * that key's row of K, V (or a query's of Q, dO) passes through: padding has to be finite.
  * Kernels: bf16 attn_diff_fwd and attn_diff_bwd on the tcgen05/TMA tensor-core kernels (P, and
  * dS in the backward, rounded to bf16 for their products, all sums fp32); bf16 attn_diff_decode
  * on warp-level matrix products; float32 in fp32 on the CUDA cores.  Every output is the same
@@ -383,7 +385,8 @@ attn_status_t attn_diff_decode(const attn_desc_t* desc, const void* Q, const voi
  * [B, heads, N, d] view with strides of its own (d contiguous), so that a projection's
  * [B,N,heads,d] output is turned and laid out as [B,H,N,d] in one pass, or back.  y may be
  * exactly x (same address and strides); otherwise no y may share an element with any x or
- * other y.  That is checked for a contiguous x and its contiguous y (ATTN_ERR_INVALID_ARG). */
+ * other y, nor with pos, freq and axis.  That is checked for a contiguous x and its
+ * contiguous y (ATTN_ERR_INVALID_ARG). */
 #define ATTN_ROPE_MAX_TENSORS 4
 #define ATTN_ROPE_HALF 0      /* pair i: coordinates i and i + d/2 */
 #define ATTN_ROPE_NEIGHBOUR 1 /* pair i: coordinates 2i and 2i + 1 */
