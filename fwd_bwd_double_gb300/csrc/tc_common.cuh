@@ -32,6 +32,14 @@ __device__ __forceinline__ uint32_t sw128(int row, int chunk) {
   return static_cast<uint32_t>(row * 128 + ((chunk ^ (row & 7)) << 4));
 }
 
+// Bits from .. to of a word (none where they do not meet it).  A bit tested per element takes one
+// instruction, the two bounds compared with it two.
+__device__ __forceinline__ uint32_t bits_between(int from, int to) {
+  const uint32_t below = to < 0 ? 0u : 0xffffffffu >> (31 - min(to, 31));
+  const uint32_t above = from > 31 ? 0u : 0xffffffffu << max(from, 0);
+  return below & above;
+}
+
 // A descriptor moved by `bytes` within shared memory: the start address sits in
 // bits 0-13 of the low word in 16-byte units, and every operand of these kernels
 // lies in the first 256 KB, so the move never carries out of the low word.  The

@@ -285,9 +285,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int ch = 0; ch < 4; ++ch)
             if (ch * 32 + 31 > klim0 || ch * 32 < klo31) {
+              // (two comparisons a score: 314 against 292 us at H48 N8000 for a window of 1024)
+              const uint32_t see = tc::bits_between(klo - ch * 32, klim - ch * 32);
 #pragma unroll
               for (int t = 0; t < 32; ++t)
-                if (ch * 32 + t > klim || ch * 32 + t < klo) v[ch][t] = __float_as_uint(-INFINITY);
+                if (!(see & (1u << t))) v[ch][t] = __float_as_uint(-INFINITY);
             }
         }
         float mx[8];
