@@ -257,14 +257,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (finite also for the smallest scales: -inf + slack has to stay below a row's first maximum)
     const float slack = fminf(kSlack / c, 3e38f);
     const uint64_t c2 = tc::pk2f(c, c);
+    // A row block with this thread's row's bound, the last row's, and its head's lam: looked up
+    // before the last row block's epilogue (after it: 292 against 283 us at H48 N8000 for a window of 1024).
+    struct Row {
+      Item it;
+      int lo_row, lo_last;
+      float lm;
+    };
+    auto row_at = [&](int x) {
+      Row w;
+      w.it = item_at(x);
+      w.lm = lam[w.it.bh % H];
+      w.lo_row = (WIN && causal) ? bd.row_lo(w.it.bh, static_cast<int64_t>(w.it.rb) * BM + r) : 0;
+      w.lo_last = (WIN && causal) ? bd.row_lo(w.it.bh, min(w.it.rb * BM + BM - 1, N - 1)) : 0;
+      return w;
+    };
     int T = 0;
-    for (int x = static_cast<int>(blockIdx.x), n = 0; x >= 0; x = next_item(n, wait, true), ++n) {
-      const Item it = item_at(x);
-      const int bh = it.bh, rb = it.rb, j0 = it.j0, nkv = it.nkv;
-      const float lm = lam[bh % H];
+    Row next = row_at(static_cast<int>(blockIdx.x));
+    for (int x = static_cast<int>(blockIdx.x), n = 0; x >= 0; ++n) {
+      const Item it = next.it;
+      const int bh = it.bh, rb = it.rb, j0 = it.j0, nkv = it.nkv, lo_row = next.lo_row, lo_last = next.lo_last;
+      const float lm = next.lm;
       const int64_t row = static_cast<int64_t>(rb) * BM + r;
-      const int lo_row = (WIN && causal) ? bd.row_lo(bh, row) : 0;
-      const int lo_last = (WIN && causal) ? bd.row_lo(bh, min(rb * BM + BM - 1, N - 1)) : 0;
       float mref = -INFINITY, l = 0.f;
       for (int j = 0; j < nkv; ++j, ++T) {
         const int kb = j0 + j;
@@ -349,6 +363,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += x.x + x.y;
       }
       // ------------------------------------------------------------------ epilogue
+      x = next_item(n, wait, true);
+      if (x >= 0) next = row_at(x);
       const float inv = 1.f / l;
       if (row < N) lse[(2 * static_cast<int64_t>(bh) + m) * N + row] = mref * scale + logf(l);
       wait(o_full, n & 1);
