@@ -313,9 +313,10 @@ __device__ __forceinline__ void row_pass(const Args& p, int block, const CUtenso
           ptx::mbar_arrive(dp_cons);
         }
         if (masked) {
+          const uint32_t see = tc::bits_between(klo, klim);
 #pragma unroll
           for (int u = 0; u < 32; ++u)
-            if (u > klim || u < klo) v[u] = 0u;
+            if (!(see & (1u << u))) v[u] = 0u;
         }
 #pragma unroll
         for (int u = 0; u < 32; u += 2) {
@@ -617,6 +618,7 @@ __device__ __forceinline__ void col_pass(const Args& p, int block, const CUtenso
           // queries u of the block's 32 the key is seen by: from .. to
           const int from = causal ? key - i * BW - c0 : (key < N ? 0 : kC);
           const int to = min((WIN && causal ? khi : N - 1), N - 1) - i * BW - c0;
+          const uint32_t see = tc::bits_between(from, to);
 #pragma unroll
           for (int u = 0; u < kC; u += 4) {
             const float4 L = *reinterpret_cast<const float4*>(sSt + m * BW + u);
@@ -626,7 +628,7 @@ __device__ __forceinline__ void col_pass(const Args& p, int block, const CUtenso
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               if constexpr (decltype(mk)::value)
-                if (u + x < from || u + x > to) p[x] = 0.f;
+                if (!(see & (1u << (u + x)))) p[x] = 0.f;
               v[u + x] = __float_as_uint(p[x]);
             }
           }
