@@ -234,6 +234,38 @@ def test_given_streams(monkeypatch):
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("d", [32, 64])
+def test_calls_at_once(d):
+    """Training steps on one stream, forwards of plain attention and a token over a cache on another:
+    the bits of the calls on their own."""
+    import fwd_bwd_double_gb300 as fbd
+    torch = _t()
+    x = make(2, 6, 2, 1500, d, "bf16")
+    Q, K, V, lam, _ = make(3, 4, 2, 2000, d, "bf16", 1)
+    q, lens = Q[:, :, -1:].contiguous(), torch.tensor([2000, 0, 77], dtype=torch.int32, device="cuda")
+    P, R, S = (torch.randn(2, 4, 1500, d, device="cuda").bfloat16() for _ in range(3))
+
+    def other():
+        return (fbd.attn_diff_decode(q, K, V, lam, lens), *fbd.attn_diff_fwd(Q, K, V, lam), *fbd.attn_fwd(P, R, S))
+
+    want, want_other = run(x), other()
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    got, got_other = [], []
+    for _ in range(4):
+        with torch.cuda.stream(a):
+            got.append(run(x))
+        with torch.cuda.stream(b):
+            got_other.append(other())
+    torch.cuda.synchronize()
+    fbd.attn_device_status()
+    for g, o in zip(got, got_other):
+        for k in want:
+            assert torch.equal(g[k], want[k]), k
+        for u, v in zip(o, want_other):
+            assert torch.equal(u, v)
+
+
 def test_streams_graphs_and_views_of_lam():
     """On another stream; captured twice over one workspace and replayed in turn on new data; lam a
     slice of a larger tensor (4-byte aligned)."""
