@@ -98,6 +98,13 @@ struct BoundedWaitT {
     }
   }
 };
+// The last wait of a CTA in which a wait has given up, for copies or products of its own that are
+// still in flight: without the abort flag, for 2 s at most.
+__device__ __forceinline__ void settle(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 0; it < (1u << 20); ++it)
+    if (mbar_try_wait_hint(bar, parity, 100000u) || globaltimer_ns() - t0 > 2000000000ull) return;
+}
 // The waits of the attention kernels give up after 2 s.
 using BoundedWait = BoundedWaitT<2000000000ull>;
 

@@ -60,6 +60,20 @@ __device__ __forceinline__ void named_sync(int id, int n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
 
+// The same barrier (of a multiple of 32 threads), and whether `x` is true for all of them.
+__device__ __forceinline__ bool named_all(int id, int n, bool x) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.s32 p, %3, 0;\n\t"
+      "barrier.red.and.pred q, %1, %2, p;\n\t"
+      "selp.s32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(n), "r"(static_cast<int>(x))
+      : "memory");
+  return r != 0;
+}
+
 // Grid order of the 1-D grids: slices (batch, head) go in groups of 8, so the
 // streamed tiles of one group (K, V, ... of 8 heads) stay resident in L2 while its
 // CTAs run; within a group, block index k = 0 (the heaviest causal block) comes

@@ -26,7 +26,10 @@
 // P is rounded to bf16 for its product; the sums l are of the unrounded fp32 values.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "diff.h"
+#include "handover.h"
 #include "ptx.cuh"
 #include "tc_common.cuh"
 
@@ -61,6 +64,34 @@ struct Lay {
 };
 static_assert(Lay<64>::bytes <= 232448, "shared memory");
 
+// The primitives of a role in the hand-over to the next row block (handover.h): a whole warp's, or
+// one thread's.
+template <bool WARP>
+struct Role {
+  ptx::BoundedWait wait;
+  uint64_t *known, *free;
+  const void* answer_at;
+  int lane;
+  __device__ __forceinline__ bool wait_free(int n) const { return wait(free, n & 1); }
+  __device__ __forceinline__ bool wait_known(int n) const {
+    const bool ok = wait(known, n & 1);
+    return WARP ? __all_sync(0xffffffffu, ok) : ok;
+  }
+  __device__ __forceinline__ void request() const {
+    ptx::mbar_expect_tx(known, 16);
+    ptx::clc_request(const_cast<void*>(answer_at), known);
+  }
+  __device__ __forceinline__ int answer() const {
+    const int x = ptx::clc_block(answer_at);
+    ptx::fence_proxy_async_smem();
+    return x;
+  }
+  __device__ __forceinline__ void taken() const {
+    if (WARP) __syncwarp();
+    if (!WARP || lane == 0) ptx::mbar_arrive(free);
+  }
+};
+
 // WIN: a banded causal mask is in force (window and/or document bounds).
 template <int D, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -85,8 +116,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* q_empty = o_empty + 1;        // the row block's last S_1, S_2 done
   uint64_t* x_full = q_empty + 1;         // the next row block is known
   uint64_t* x_empty = x_full + 1;         // ... and every role has taken it
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(x_empty + 1);
+  uint64_t* settled = x_empty + 1;        // after a wait that gave up: the products in flight done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(settled + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* started = abort_flag + 1;  // Q loads, key blocks' loads, requests (the TMA thread's)
   float* sInv = reinterpret_cast<float*>(sm + L::oInv);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -103,16 +136,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     it.nkv = (causal ? it.rb + 1 : nrb) - it.j0;
     return it;
   };
-  // The row block after the n-th (-1: none), for a whole warp or for one thread of it.
-  auto next_item = [&](int n, const auto& w, bool whole_warp) {
-    bool known = w(x_full, n & 1);
-    if (whole_warp) known = __all_sync(0xffffffffu, known);
-    if (!known) return -1;  // a wait has given up: the CTA ends
-    const int x = ptx::clc_block(sm + L::oClc);
-    ptx::fence_proxy_async_smem();
-    if (whole_warp) __syncwarp();
-    if (!whole_warp || lane == 0) ptx::mbar_arrive(x_empty);
-    return x;
+  // A role's side of the hand-over to the next row block, for a whole warp or for one thread of it.
+  auto role = [&](const ptx::BoundedWait& w, auto whole) {
+    return Role<decltype(whole)::value>{w, x_full, x_empty, sm + L::oClc, lane};
   };
 
   auto load_q = [&](const Item& it) {
@@ -147,6 +173,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::mbar_init(q_empty, 1);
     ptx::mbar_init(x_full, 1);
     ptx::mbar_init(x_empty, 10);  // the TMA thread, the MMA warp, eight softmax warps
+    ptx::mbar_init(settled, 1);
+    started[0] = started[1] = started[2] = 0;
     *abort_flag = (ptx::smem_u32(sm) & 1023u) ? 1 : 0;  // the swizzled tiles need 1024-byte alignment
     if (*abort_flag) atomicOr(&g_err, FBD_ERR_TIMEOUT);
     ptx::fence_mbar_init();
@@ -171,24 +199,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 8) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0 && ok) {
-      int T = 0;
-      for (int x = static_cast<int>(blockIdx.x), n = 0; x >= 0; x = next_item(n, wait, false), ++n) {
+      const auto me = role(wait, std::false_type{});
+      int T = 0, nq = 1, asked = 0;
+      for (int x = static_cast<int>(blockIdx.x), n = 0; x >= 0; ++n) {
         const Item it = item_at(x);
         if (n > 0) {
-          wait(q_empty, (n - 1) & 1);
+          if (!wait(q_empty, (n - 1) & 1)) break;
           load_q(it);
+          ++nq;
         }
-        for (int j = 0; j < it.nkv; ++j, ++T) {
+        int j = 0;
+        for (; j < it.nkv; ++j, ++T) {
           if (n == 0 && j < NS) continue;  // (issued above)
-          if (T >= NS) wait(&empty[T % NS], ((T / NS) - 1) & 1);
+          if (T >= NS && !wait(&empty[T % NS], ((T / NS) - 1) & 1)) break;
           load(it, j, T);
         }
         // Ask for the next row block now, a few key blocks before this one ends: asked for sooner,
         // it would wait here while other SMs run out.
-        if (n > 0) wait(x_empty, (n - 1) & 1);
-        ptx::mbar_expect_tx(x_full, 16);
-        ptx::clc_request(sm + L::oClc, x_full);
+        if (j < it.nkv || !handover::ask(me, n)) break;
+        ++asked;
+        x = handover::take(me, n);
       }
+      started[0] = nq, started[1] = T, started[2] = asked;
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------- MMA issuer
@@ -206,8 +238,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc::desc_add(dK, so + tc::kmajor_off(BN, k)), idS, k > 0 ? 1u : 0u);
         ptx::mma_commit_e(&s_full[m]);
       };
+      const auto me = role(wait, std::true_type{});
       int T = 0;
-      for (int x = static_cast<int>(blockIdx.x), n = 0; x >= 0; x = next_item(n, wait, true), ++n) {
+      for (int x = static_cast<int>(blockIdx.x), n = 0; x >= 0; x = handover::take(me, n), ++n) {
         const int nkv = item_at(x).nkv;
         wait(q_full, n & 1);
         wait(&k_full[T % NS], (T / NS) & 1);
@@ -272,6 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       w.lo_last = (WIN && causal) ? bd.row_lo(w.it.bh, min(w.it.rb * BM + BM - 1, N - 1)) : 0;
       return w;
     };
+    const auto me = role(wait, std::true_type{});
     int T = 0;
     Row next = row_at(static_cast<int>(blockIdx.x));
     for (int x = static_cast<int>(blockIdx.x), n = 0; x >= 0; ++n) {
@@ -363,13 +397,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += x.x + x.y;
       }
       // ------------------------------------------------------------------ epilogue
-      x = next_item(n, wait, true);
+      x = handover::take(me, n);
       if (x >= 0) next = row_at(x);
       const float inv = 1.f / l;
       if (row < N) lse[(2 * static_cast<int64_t>(bh) + m) * N + row] = mref * scale + logf(l);
       wait(o_full, n & 1);
       if (m == 1) sInv[r] = inv;  // (map 1 is done with the last row block's: it has taken part in this one)
-      tc::named_sync(1, 256);
+      // (both maps' warps go on to the same row block, or none does: they meet at barriers in each)
+      x = handover::agree(x, [](bool some) { return tc::named_all(1, 256, some); });
       ptx::tc_fence_after();
       if (m == 0 || with_O2) {
         const float w = m == 0 ? -lm * sInv[r] : inv;  // of O_2's columns
@@ -416,6 +451,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   ptx::tc_fence_before();
   __syncthreads();
+  // A wait has given up: loads, an answer and products may still be on their way into this CTA's
+  // shared memory and TMEM, which others get when it ends.
+  if (*abort_flag != 0) {
+    if (threadIdx.x == 8 * 32) {
+      const int nq = started[0], T = started[1], asked = started[2];
+      if (nq > 0) ptx::settle(q_full, (nq - 1) & 1);
+      for (int s = 0; s < NS && s < T; ++s) {
+        ptx::settle(&k_full[s], ((T - 1 - s) / NS) & 1);
+        ptx::settle(&v_full[s], ((T - 1 - s) / NS) & 1);
+      }
+      if (asked > 0) ptx::settle(x_full, (asked - 1) & 1);
+    }
+    if (warp == 9) {
+      ptx::mma_commit_e(settled);
+      ptx::settle(settled, 0);
+    }
+  }
   if (warp == 9) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 512);
