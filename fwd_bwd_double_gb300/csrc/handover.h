@@ -49,5 +49,9 @@ FBD_HD int agree(int x, const All& all) {
   return all(x >= 0) ? x : -1;
 }
 
+// Parity of the last phase that `fills` fills of a ring of `stages` have begun in stage s < fills:
+// what a CTA that gave up waits for before it ends.
+FBD_HD int last_phase(int fills, int stages, int s) { return ((fills - 1 - s) / stages) & 1; }
+
 }  // namespace handover
 }  // namespace fbd

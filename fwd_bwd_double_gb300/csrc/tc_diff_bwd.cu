@@ -27,6 +27,7 @@
 #include <type_traits>
 
 #include "diff.h"
+#include "handover.h"
 #include "ptx.cuh"
 #include "tc_common.cuh"
 
@@ -81,6 +82,25 @@ __device__ __forceinline__ void init_abort(uint8_t* sm, volatile int* abort_flag
   if (*abort_flag) atomicOr(&g_err, FBD_ERR_TIMEOUT);
 }
 
+// After the roles have met, in a CTA where a wait has given up: loads and products may still be on
+// their way into its shared memory and TMEM, which others get when it ends.  started: the loads
+// begun in each ring of stages; the first ones come with the held block's.
+__device__ __forceinline__ void teardown(volatile int* abort_flag, uint64_t* settled, volatile int* started,
+                                         uint64_t* held, uint64_t* ring0, uint64_t* ring1) {
+  if (*abort_flag == 0) return;
+  if (threadIdx.x == kCW * 32) {
+    if (started[0] > 0) ptx::settle(held, 0);
+    for (int s = 0; s < NS; ++s) {
+      if (s < started[0]) ptx::settle(&ring0[s], handover::last_phase(started[0], NS, s));
+      if (s < started[1]) ptx::settle(&ring1[s], handover::last_phase(started[1], NS, s));
+    }
+  }
+  if (threadIdx.x / 32 == kCW + 1) {
+    ptx::mma_commit_e(settled);
+    ptx::settle(settled, 0);
+  }
+}
+
 struct Args {
   const float* lam;
   const float* stats;
@@ -117,6 +137,8 @@ __device__ __forceinline__ void row_pass(const Args& p, int block, const CUtenso
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dq_done + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* sRed = reinterpret_cast<float*>(sm + L::oBar + 160);  // [kCW]
+  uint64_t* settled = reinterpret_cast<uint64_t*>(sm + L::oBar + 224);  // see teardown()
+  volatile int* started = reinterpret_cast<volatile int*>(settled + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float *lam = p.lam, *stats = p.stats;
@@ -161,7 +183,9 @@ __device__ __forceinline__ void row_pass(const Args& p, int block, const CUtenso
     }
     ptx::mbar_init(dp_full, 1);
     ptx::mbar_init(dp_cons, kCW * 32);
+    ptx::mbar_init(settled, 1);
     init_abort(sm, abort_flag);
+    started[0] = started[1] = *abort_flag ? 0 : min(nt, NS);
     ptx::fence_mbar_init();
     if (!*abort_flag) {
       ptx::mbar_expect_tx(held_full, L::kBlock);
@@ -190,10 +214,12 @@ __device__ __forceinline__ void row_pass(const Args& p, int block, const CUtenso
     if (lane == 0 && ok) {
       for (int t = NS; t < nt; ++t) {
         const int s = t % NS, ph = ((t / NS) - 1) & 1;
-        wait(&v_empty[s], ph);
+        if (!wait(&v_empty[s], ph)) break;
         load_v(t);
-        wait(&k_empty[s], ph);
+        started[1] = t + 1;
+        if (!wait(&k_empty[s], ph)) break;
         load_k(t);
+        started[0] = t + 1;
       }
     }
   } else if (warp == kCW + 1) {
@@ -370,6 +396,7 @@ __device__ __forceinline__ void row_pass(const Args& p, int block, const CUtenso
 
   ptx::tc_fence_before();
   __syncthreads();
+  teardown(abort_flag, settled, started, held_full, k_full, v_full);
   if (warp == kCW + 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 512);
@@ -411,6 +438,8 @@ __device__ __forceinline__ void col_pass(const Args& p, int block, const CUtenso
   uint64_t* st_full = out_done + 1;  // the block's statistics in shared memory
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(st_full + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint64_t* settled = reinterpret_cast<uint64_t*>(sm + L::oBar + 224);  // see teardown()
+  volatile int* started = reinterpret_cast<volatile int*>(settled + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float *lam = p.lam, *stats = p.stats;
@@ -454,7 +483,9 @@ __device__ __forceinline__ void col_pass(const Args& p, int block, const CUtenso
     ptx::mbar_init(ready, kCW * 32);
     ptx::mbar_init(out_done, 1);
     ptx::mbar_init(st_full, 32);
+    ptx::mbar_init(settled, 1);
     init_abort(sm, abort_flag);
+    started[0] = started[1] = *abort_flag ? 0 : min(nt, NS);
     ptx::fence_mbar_init();
     if (!*abort_flag) {
       ptx::mbar_expect_tx(held_full, L::kBlock);
@@ -484,10 +515,12 @@ __device__ __forceinline__ void col_pass(const Args& p, int block, const CUtenso
     if (lane == 0 && ok) {
       for (int t = NS; t < nt; ++t) {
         const int s = t % NS, ph = ((t / NS) - 1) & 1;
-        wait(&a_empty[s], ph);
+        if (!wait(&a_empty[s], ph)) break;
         load_a(t);
-        wait(&b_empty[s], ph);
+        started[0] = t + 1;
+        if (!wait(&b_empty[s], ph)) break;
         load_b(t);
+        started[1] = t + 1;
       }
     }
   } else if (warp == kCW + 1) {
@@ -723,6 +756,7 @@ __device__ __forceinline__ void col_pass(const Args& p, int block, const CUtenso
 
   ptx::tc_fence_before();
   __syncthreads();
+  teardown(abort_flag, settled, started, held_full, a_full, b_full);
   if (warp == kCW + 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 512);

@@ -458,8 +458,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nq = started[0], T = started[1], asked = started[2];
       if (nq > 0) ptx::settle(q_full, (nq - 1) & 1);
       for (int s = 0; s < NS && s < T; ++s) {
-        ptx::settle(&k_full[s], ((T - 1 - s) / NS) & 1);
-        ptx::settle(&v_full[s], ((T - 1 - s) / NS) & 1);
+        ptx::settle(&k_full[s], handover::last_phase(T, NS, s));
+        ptx::settle(&v_full[s], handover::last_phase(T, NS, s));
       }
       if (asked > 0) ptx::settle(x_full, (asked - 1) & 1);
     }

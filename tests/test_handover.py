@@ -135,12 +135,40 @@ int main(int argc, char** argv) {
 """
 
 
-def test_every_role_leaves(tmp_path):
+RING = r"""
+#include <cstdio>
+#include "handover.h"
+
+int main() {
+  for (int stages = 1; stages <= 4; ++stages)
+    for (int fills = 0; fills <= 20; ++fills) {
+      int begun[4] = {0, 0, 0, 0};  // fills of each stage: the last one is phase begun - 1
+      for (int t = 0; t < fills; ++t) ++begun[t % stages];
+      for (int s = 0; s < stages; ++s) {
+        if ((begun[s] > 0) != (s < fills)) return std::printf("stage %d of %d after %d fills\n", s, stages, fills), 1;
+        if (begun[s] > 0 && fbd::handover::last_phase(fills, stages, s) != ((begun[s] - 1) & 1))
+          return std::printf("phase of stage %d of %d after %d fills\n", s, stages, fills), 1;
+      }
+    }
+  return 0;
+}
+"""
+
+
+def run_on_host(tmp_path, source, *args):
     cxx = shutil.which("g++") or shutil.which("c++")
     if cxx is None:
         pytest.skip("no C++ compiler")
     src, exe = tmp_path / "handover.cpp", tmp_path / "handover"
-    src.write_text(DRIVER)
+    src.write_text(source)
     subprocess.run([cxx, "-O2", "-std=c++17", "-pthread", "-I" + CSRC, str(src), "-o", str(exe)], check=True)
-    r = subprocess.run([str(exe), "400"], capture_output=True, text=True, timeout=300)
+    r = subprocess.run([str(exe), *args], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stdout
+
+
+def test_every_role_leaves(tmp_path):
+    run_on_host(tmp_path, DRIVER, "400")
+
+
+def test_phases_a_cta_that_gave_up_waits_for(tmp_path):
+    run_on_host(tmp_path, RING)
