@@ -18,11 +18,13 @@
 // run in order, so S_m overwrites P_m only once it has been read.  P_m V starts on the first
 // 64 keys' P while the rest is exponentiated.
 //
-// The reference maximum M_m moves only when a row's maximum passes it by more than 2^8 in
-// the probabilities (P_m <= 2^8, l and O_m in fp32): most blocks then rescale nothing.  Moving it
-// with every maximum took 569 against 452 us at B4 H6 N8192; what it buys, a largest P of exactly
-// 1, is a little accuracy where attention is nearly one-hot (keys with a shared mean of norm 40:
-// O within 1.8e-3 against 2.1e-3 of 64-bit values, dQ 1.9e-2 against 2.1e-2).
+// The reference maximum M_m moves only when a row's maximum passes it so far that the new largest P
+// would be above a quarter of the row's sum so far (or above 2^8; P_m <= 2^8, l and O_m in fp32):
+// most blocks then rescale nothing, and a weight that makes up more than a fifth of its row is 1
+// exactly, so its product is not rounded.  That matters where attention is nearly one-hot (keys with
+// a shared mean of norm 40, queries near copies of keys): dQ within 1.89e-2 and 1.97e-2 of 64-bit
+// values, as with a maximum that always moves (1.88e-2, 1.96e-2); 2.07e-2 and 2.10e-2 at 2^8 alone.
+// B4 H6 N8192: 447 us, 563 if it always moves, 445 at 2^8 alone; H48 N8000, window 1024: 290, 333, 282.
 // P is rounded to bf16 for its product; the sums l are of the unrounded fp32 values.
 #include <cuda_bf16.h>
 
@@ -46,7 +48,8 @@ constexpr int NS = 2;
 constexpr int kThreads = 384;
 constexpr int kRegs = 208, kRegsOther = 80;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kSlack = 8.f;  // log2 of the largest P
+constexpr float kSlack = 256.f;  // the largest P
+constexpr float kShare = .25f;   // ... and its share of the row's sum so far, where it is above 1
 
 template <int D>
 struct Lay {
@@ -287,8 +290,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = threadIdx.x & 127;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + L::cS + m * BN + lane_off, tO = tmem + L::cO + lane_off;
-    // (finite also for the smallest scales: -inf + slack has to stay below a row's first maximum)
-    const float slack = fminf(kSlack / c, 3e38f);
     const uint64_t c2 = tc::pk2f(c, c);
     // A row block with this thread's row's bound, the last row's, and its head's lam: looked up
     // before the last row block's epilogue (after it: 292 against 283 us at H48 N8000 for a window of 1024).
@@ -351,7 +352,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int u = 0; u < 8; ++u) mx[u] = fmaxf(mx[u], fmaxf(tc::f(v[ch][t + u]), tc::f(v[ch][t + 8 + u])));
 #pragma unroll
         for (int u = 1; u < 8; ++u) mx[0] = fmaxf(mx[0], mx[u]);
-        const bool moved = mx[0] > mref + slack;  // always at the first visible key (mref = -inf)
+        // (always at the first visible key: mref = -inf)
+        const bool moved = ptx::ex2((mx[0] - mref) * c) > fminf(fmaxf(kShare * l, 1.f), kSlack);
         const float mnew = moved ? mx[0] : mref;
         const float alpha = moved ? ptx::ex2((mref - mnew) * c) : 1.f;
         if (j > 0 && __any_sync(0xffffffffu, moved)) {
