@@ -3,9 +3,11 @@
 // `inverse` turns back, which is the gradient (the map is orthogonal).
 //
 // Bound by reading and writing each element once (16 bytes per thread and half).  Angles
-// are exact before they are rounded: freq / 2 pi as a 64-bit fraction of a turn times the
-// integer position, modulo 2^64, is the fraction of a turn left over, so a position in
-// the millions loses nothing (an fp32 product freq * pos would lose its low bits there).
+// are within 2^-32 of a turn (1.5e-9 radians) before they are rounded, at every int32 position
+// and for |freq| up to 2^40: freq / 2 pi as a 64-bit fraction of a turn, within 2^-64, times the
+// integer position, modulo 2^64, is the fraction of a turn left over (an fp32 product freq * pos
+// would lose its low bits in the thousands, a double's quotient its own far out: 2e-6 radians
+// at freq 6.9, 3e-3 at 1e4).
 // A thread holds the sines of its pairs and applies them to several heads.
 #include <cuda_bf16.h>
 
@@ -20,6 +22,21 @@ constexpr int kT = 256;
 constexpr int kMaxPairs = 128;
 
 constexpr int kHU = 4;  // heads whose loads are in flight together
+
+constexpr double kInv2PiHead = 0x1.45f306dc9c883p-3, kInv2PiTail = -0x1.6b01ec5417056p-57;  // 1 / 2 pi
+
+// x in units of 2^-64, modulo 2^64 (its whole part drops out), rounded to the nearest: from the bits of
+// a double, since floating point in 64 bits is slow (B2 N1001, 12 heads of 128 in float32: 8.0 us, with
+// rint and a conversion 8.9).
+__device__ __forceinline__ unsigned long long fraction(double x) {
+  const long long b = __double_as_longlong(x);
+  const unsigned long long m = (b & 0xfffffffffffffll) | 0x10000000000000ll;
+  const int up = static_cast<int>(b >> 52 & 0x7ff) - (1075 - 64);
+  unsigned long long v = 0;
+  if (up >= 0 && up < 64) v = m << up;
+  if (up < 0 && up > -64) v = ((m >> (-up - 1)) + 1) >> 1;
+  return b < 0 ? 0ull - v : v;
+}
 
 // 16 bytes as floats.
 __device__ __forceinline__ void widen(const uint4& v, float (&x)[4]) {
@@ -47,9 +64,10 @@ __global__ void __launch_bounds__(kT)
   __shared__ int sAx[kMaxPairs];
   const int pairs = a.d / 2, per = pairs / W;  // threads per token
   for (int i = threadIdx.x; i < pairs; i += kT) {
-    double t = static_cast<double>(freq[i]) * 0.15915494309189533577;  // turns per step (1 / 2 pi)
-    t -= floor(t);
-    sT[i] = __double2ull_rz(t * 18446744073709551616.0);
+    // Turns per step: freq times 1 / 2 pi held as a sum of two doubles (106 bits), the first
+    // product's rounding error recovered by fma; the whole turns drop out of each part.
+    const double f = static_cast<double>(freq[i]), head = f * kInv2PiHead;
+    sT[i] = fraction(head) + fraction(fma(f, kInv2PiTail, fma(f, kInv2PiHead, -head)));
     const int ax = axis[i];
     sAx[i] = ax < a.axes ? ax : -1;
   }
@@ -67,7 +85,8 @@ __global__ void __launch_bounds__(kT)
     if (ax >= 0) {
       const long long p = pos[ax * a.pos_axis + b * a.pos_batch + n];
       const unsigned long long turn = static_cast<unsigned long long>(p) * sT[i];  // mod 2^64: whole turns drop out
-      sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f, &sn[u], &cs[u]);
+      const int frac = static_cast<int>((turn + 0x80000000ull) >> 32);  // to the nearest 2^-32 of a turn
+      sincospif(static_cast<float>(frac) * 4.656612873077393e-10f, &sn[u], &cs[u]);
       if (a.inverse) sn[u] = -sn[u];
     }
   }

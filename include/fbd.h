@@ -380,7 +380,8 @@ attn_status_t attn_diff_decode(const attn_desc_t* desc, const void* Q, const voi
  *   pos [axes, B, N] int32 (pos_batch_stride = 0: [axes, N], shared by the batch);
  *   freq [d/2] float32 (finite), radians per step; axis [d/2] int32: the axis each pair
  *   turns with, outside 0 .. axes - 1: the pair is copied unturned.
- * Angles are exact before rounding for every int32 position.
+ * Angles are within 2^-32 of a turn before they are rounded to float32, for every int32 position and
+ * |freq| up to 2^40 (larger ones turn by a less exact angle).
  * Up to ATTN_ROPE_MAX_TENSORS tensors with the same tokens in one launch, each a
  * [B, heads, N, d] view with strides of its own (d contiguous), so that a projection's
  * [B,N,heads,d] output is turned and laid out as [B,H,N,d] in one pass, or back.  y may be

@@ -1,11 +1,61 @@
-"""Differential attention and the rotary on the GPU where they can go wrong: weights nearly one-hot."""
+"""Differential attention and the rotary on the GPU where they can go wrong: weights nearly one-hot, angles of
+far positions."""
 import math
+from fractions import Fraction
 
 import pytest
 
 from test_gpu_diff import _lib, _t, check, run  # noqa: F401  (_lib: the fixture that builds)
 
 pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------- far positions turned
+def inverse_of_two_pi(bits=320):
+    """1 / 2 pi as a fraction within 2^-bits, from Machin's formula pi = 16 arctan(1/5) - 4 arctan(1/239)."""
+    one = 1 << (bits + 32)
+
+    def arctan(n):
+        term, total, k = one // n, 0, 0
+        while term:
+            total += (-1) ** k * (term // (2 * k + 1))
+            term, k = term // (n * n), k + 1
+        return total
+
+    return Fraction(one, 2 * (16 * arctan(5) - 4 * arctan(239)))
+
+
+@pytest.mark.parametrize("paired", ["half", "neighbour"])
+def test_angles_of_far_positions(paired):
+    """Frequencies from 1e-30 to 2^40 of both signs at the farthest int32 positions, against angles
+    reduced in rational arithmetic."""
+    import fwd_bwd_double_gb300 as fbd
+    torch = _t()
+    d = 64
+    freq = torch.tensor([1e-30, 1e-4, 0.03, 1.0, 6.9, 100.0, 1e4, 1e6, 2.0 ** 31, 2.0 ** 40, 3.3, 0.7, 12.5, 777.0, 4e8, 2.5],
+                        dtype=torch.float32)
+    freq = torch.cat([freq, -freq])
+    pos = torch.tensor([0, 1, -1, 1000, -4097, 12000000, -99999999, (1 << 31) - 1, -(1 << 31)], dtype=torch.int32)
+    N = pos.numel()
+    x = torch.randn(1, 2, N, d, generator=torch.Generator().manual_seed(0))
+    C = inverse_of_two_pi()
+    angle = torch.empty(N, d // 2, dtype=torch.float64)
+    for i, f in enumerate(freq.tolist()):
+        for n, p in enumerate(pos.tolist()):
+            turn = Fraction(f) * p * C
+            angle[n, i] = 2 * math.pi * float(turn - round(turn))
+    c, s = torch.cos(angle), torch.sin(angle)
+    z = x.double()
+    u, v = (z[..., :d // 2], z[..., d // 2:]) if paired == "half" else (z[..., 0::2], z[..., 1::2])
+    a, b = u * c - v * s, u * s + v * c
+    want = torch.cat([a, b], -1) if paired == "half" else torch.stack([a, b], -1).flatten(-2)
+    got = fbd.attn_rope(x.cuda(), pos.cuda()[None], freq.cuda(), torch.zeros(d // 2, dtype=torch.int32, device="cuda"),
+                        paired=paired).cpu().double()
+    # the angle within 2^-32 of a turn (below 2^-29 radians) and its rounding to float32 (2^-24 of half a
+    # turn, below 2^-22), of a pair's length below sqrt 2 of the largest coordinate; sine, cosine, two
+    # products and their sum: each half a step, 2^-24, of terms no larger than that: 2^-21 in all
+    tol = (2.0 ** -21 + math.sqrt(2) * (2.0 ** -29 + 2.0 ** -22)) * x.abs().max().item()
+    assert (got - want).abs().max().item() <= tol
 
 
 # ------------------------------------------------------- rows with one dominating weight
