@@ -9,7 +9,8 @@
 //
 // bf16 on warp-level matrix products (m16n8k16): rows 0-7 of a tile are the heads' first maps,
 // rows 8-15 their second ones, so one product P V serves both maps, and S is Q_1 K_1^T with
-// rows 8-15 zero plus Q_2 K_2^T with rows 0-7 zero.  (tcgen05 has 128 rows to fill.)  Each of
+// rows 8-15 zero and Q_2 K_2^T with rows 0-7 zero, of which the other rows are kept (zeros times an
+// infinite key of the other map are NaN).  (tcgen05 has 128 rows to fill.)  Each of
 // four warps takes 16 of a tile's 64 keys with a softmax of its own; the four are joined at
 // the end.  Three 32 KB stages of 16-byte asynchronous copies, two CTAs an SM: 192 KB in
 // flight on each SM.  P is rounded to bf16 for its product; sums, maxima and o are fp32.
@@ -171,20 +172,21 @@ __global__ void __launch_bounds__(kT, 2)
     const uint32_t st = s0 + static_cast<uint32_t>((t % NS) * St::bytes);
     float s[2][4];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      s[u][0] = s[u][1] = s[u][2] = s[u][3] = 0.f;
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int m = 0; m < 2; ++m) {
+        float sm[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) {
           uint32_t f[4];
           ldm4(st + m * St::kK + at<D * 2>(warp * 16 + u * 8 + (lane & 7), k * 4 + (lane >> 3)), f);
 #pragma unroll
           for (int x = 0; x < 2; ++x)
-            mma(s[u], m == 0 ? qa[0][2 * k + x][0] : 0u, m == 1 ? qa[1][2 * k + x][0] : 0u,
+            mma(sm, m == 0 ? qa[0][2 * k + x][0] : 0u, m == 1 ? qa[1][2 * k + x][0] : 0u,
                 m == 0 ? qa[0][2 * k + x][1] : 0u, m == 1 ? qa[1][2 * k + x][1] : 0u, f[2 * x], f[2 * x + 1]);
         }
-    }
+        s[u][2 * m] = sm[2 * m], s[u][2 * m + 1] = sm[2 * m + 1];
+      }
     if (t == nt - 1) {
       const int64_t k0 = kb + static_cast<int64_t>(t) * MK + warp * 16 + q4 * 2;
 #pragma unroll

@@ -1,13 +1,42 @@
-"""Differential attention and the rotary on the GPU where they can go wrong: weights nearly one-hot, angles of
-far positions."""
+"""Differential attention and the rotary on the GPU where they can go wrong: weights nearly one-hot, infinite
+scores, angles of far positions."""
 import math
 from fractions import Fraction
 
 import pytest
 
-from test_gpu_diff import _lib, _t, check, run  # noqa: F401  (_lib: the fixture that builds)
+from test_gpu_diff import _lib, _t, check, decode_reference, make, run  # noqa: F401  (_lib: the fixture that builds)
 
 pytestmark = pytest.mark.gpu
+
+
+# -------------------------------------------------------------- infinities among the keys
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [32, 64])
+def test_an_infinite_score_is_its_own_maps(d, dtype):
+    """Visible keys with an infinity in one map, their scores minus infinity: weight 0 in that map, the
+    other map's as if nothing were there; over a cache and in the forward."""
+    import diff_reference as R
+    import fwd_bwd_double_gb300 as fbd
+    torch = _t()
+    B, H, g, N = 2, 4, 2, 200
+    Q, K, V, lam, _ = make(B, H, g, N, d, dtype)
+    Q[:, 0::2, :, 5], Q[:, 1::2, :, d - 1] = -Q[:, 0::2, :, 5].abs() - 0.5, Q[:, 1::2, :, d - 1].abs() + 0.5
+    K[:, 0::2, 3::7, 5] = math.inf            # first maps
+    K[:, 1::2, 4::9, d - 1] = -math.inf       # second maps
+    lens = torch.tensor([N, 77], dtype=torch.int32, device="cuda")
+    q = Q[:, :, -1:].contiguous()
+    got = fbd.attn_diff_decode(q, K, V, lam, lens)
+    want, tol = decode_reference(q, K, V, lam, lens, g)
+    assert torch.isfinite(want).all() and torch.isfinite(got).all()
+    assert ((got.double() - want).abs() <= tol).all()
+    O, O2, lse = fbd.attn_diff_fwd(Q, K, V, lam)
+    A, A2, L, P = R.forward(Q, K, V, lam, g, R.visible(N, "causal", device="cuda"))
+    e, h = (2.0 ** -8 + R.FP32, 2.0 ** -8) if dtype == "bf16" else (R.FP32, 2.0 ** -24)
+    mag = P @ V.double().unsqueeze(2).repeat_interleave(g, 1).abs()
+    assert ((O2.double() - A2).abs() <= e * mag[:, :, 1] + h * A2.abs()).all()
+    assert ((O.double() - A).abs() <= e * (mag[:, :, 0] + lam.abs()[:, None, None] * mag[:, :, 1]) + h * A.abs()).all()
+    assert ((lse.double() - L).abs() <= R.FP32 * (1 + L.abs())).all()
 
 
 # ------------------------------------------------------------------- far positions turned
