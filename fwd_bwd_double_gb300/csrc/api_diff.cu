@@ -184,6 +184,20 @@ attn_status_t attn_rope(const attn_rope_desc_t* desc, const attn_rope_tensor_t* 
     if (h < 0 || h > 65535 || (heads += h) > 65535) return fail(ATTN_ERR_INVALID_ARG, "0 to 65535 heads in all%s");
   }
   if (heads * B * N == 0) return ATTN_OK;
+  // Byte ranges without gaps: what each y writes and each x reads where its strides leave none, and the
+  // tables.  (Views with gaps may lie between one another, as a projection's heads do: not checked.)
+  struct Range {
+    uintptr_t lo, hi;
+    bool meets(const Range& o) const { return lo < o.hi && o.lo < hi; }
+  };
+  const auto table = [](const void* p, int64_t words) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    return Range{at, at + static_cast<uintptr_t>(4 * words)};
+  };
+  const Range tables[3] = {table(pos, a.axes * a.pos_axis), table(freq, d / 2), table(axis, d / 2)};
+  Range xr[ATTN_ROPE_MAX_TENSORS], yr[ATTN_ROPE_MAX_TENSORS];
+  int nx = 0, ny = 0;
+  bool meet = false;
   int n = 0;
   for (int t = 0; t < count; ++t) {
     const attn_rope_tensor_t& z = tensors[t];
@@ -196,6 +210,7 @@ attn_status_t attn_rope(const attn_rope_desc_t* desc, const attn_rope_tensor_t* 
     r.x = z.x, r.y = z.y, r.heads = static_cast<int>(z.heads);
     bool same = ax == ay;
     int64_t xe = d, ye = d;  // elements from the first to behind the last
+    int64_t xn = d;          // elements of x, one that it repeats counted once
     for (int k = 0; k < 3; ++k) {
       if (size[k] == 1) continue;  // a stride that is never taken (left 0)
       const int64_t sx = z.x_stride[k], sy = z.y_stride[k], most = (int64_t(1) << 58) / size[k];
@@ -204,6 +219,7 @@ attn_status_t attn_rope(const attn_rope_desc_t* desc, const attn_rope_tensor_t* 
       if (sx * e % 16 || sy * e % 16) return fail(ATTN_ERR_ALIGNMENT, "strides must be multiples of 16 bytes%s");
       r.xs[k] = sx, r.ys[k] = sy;
       xe += sx * (size[k] - 1), ye += sy * (size[k] - 1);
+      if (sx > 0) xn *= size[k];
       same = same && sx == sy;
     }
     // y's rows apart: in order of stride, each stride past all that lies below it
@@ -221,9 +237,19 @@ attn_status_t attn_rope(const attn_rope_desc_t* desc, const attn_rope_tensor_t* 
       below += r.ys[k] * (size[k] - 1);
     }
     const int64_t elems = B * z.heads * N * d;
-    if (!same && xe == elems && ye == elems && ax < ay + ye * e && ay < ax + xe * e)
-      return fail(ATTN_ERR_INVALID_ARG, "y overlaps x%s");
+    const Range x{ax, ax + static_cast<uintptr_t>(xe * e)}, y{ay, ay + static_cast<uintptr_t>(ye * e)};
+    if (xe == xn && !same) {  // (x and y the same: y's checks below are x's)
+      for (int k = 0; k < ny; ++k) meet = meet || x.meets(yr[k]);
+      xr[nx++] = x;
+    }
+    if (ye == elems) {
+      for (int k = 0; k < nx; ++k) meet = meet || y.meets(xr[k]);
+      for (int k = 0; k < ny; ++k) meet = meet || y.meets(yr[k]);
+      for (int k = 0; k < 3; ++k) meet = meet || y.meets(tables[k]);
+      yr[ny++] = y;
+    }
   }
+  if (meet) return fail(ATTN_ERR_INVALID_ARG, "an output overlaps an input, a table or another output%s");
   a.heads = static_cast<int>(heads);
   attn_status_t s;
   if ((s = check_small("pos", pos)) != ATTN_OK || (s = check_small("freq", freq)) != ATTN_OK ||

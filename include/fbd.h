@@ -386,8 +386,8 @@ attn_status_t attn_diff_decode(const attn_desc_t* desc, const void* Q, const voi
  * [B, heads, N, d] view with strides of its own (d contiguous), so that a projection's
  * [B,N,heads,d] output is turned and laid out as [B,H,N,d] in one pass, or back.  y may be
  * exactly x (same address and strides); otherwise no y may share an element with any x or
- * other y, nor with pos, freq and axis.  That is checked for a contiguous x and its
- * contiguous y (ATTN_ERR_INVALID_ARG). */
+ * other y, nor with pos, freq and axis.  That is checked (ATTN_ERR_INVALID_ARG) between the tables
+ * and those x and y that have no gaps; views with gaps may lie between one another. */
 #define ATTN_ROPE_MAX_TENSORS 4
 #define ATTN_ROPE_HALF 0      /* pair i: coordinates i and i + d/2 */
 #define ATTN_ROPE_NEIGHBOUR 1 /* pair i: coordinates 2i and 2i + 1 */
