@@ -1,5 +1,5 @@
 """Differential attention and the rotary on the GPU where they can go wrong: weights nearly one-hot, infinite
-scores, angles of far positions."""
+scores, angles of far positions, two streams at once."""
 import math
 from fractions import Fraction
 
@@ -8,6 +8,66 @@ import pytest
 from test_gpu_diff import _lib, _t, check, decode_reference, make, run  # noqa: F401  (_lib: the fixture that builds)
 
 pytestmark = pytest.mark.gpu
+
+
+# --------------------------------------------------------------------- two streams at once
+@pytest.mark.parametrize("d", [32, 64])
+def test_two_streams_at_the_same_time(d):
+    """Training steps of both types in a graph on one stream, forwards, plain attention, a token over a
+    cache and the rotary in a graph on another, replayed together several times: their intervals
+    overlap and every output has the bits of the calls on their own."""
+    import fwd_bwd_double_gb300 as fbd
+    torch = _t()
+    x, f = make(2, 6, 2, 1500, d, "bf16"), make(1, 4, 2, 500, d, "f32", 2)
+    y = make(3, 4, 2, 2000, d, "bf16", 1)
+    Q, K, V, lam, _ = y
+    q, lens = Q[:, :, -1:].contiguous(), torch.tensor([2000, 0, 77], dtype=torch.int32, device="cuda")
+    P, R, S = (torch.randn(2, 4, 1500, d, device="cuda").bfloat16() for _ in range(3))
+    pos = torch.arange(2000, device="cuda", dtype=torch.int32)[None]
+    freq, axis = torch.rand(d // 2, device="cuda"), torch.zeros(d // 2, dtype=torch.int32, device="cuda")
+
+    def step(x):
+        O, O2, lse = fbd.attn_diff_fwd(*x[:4])
+        return (O, O2, lse, *fbd.attn_diff_bwd(*x[:4], O, O2, x[4], lse))
+
+    def one():
+        return (*step(x), *step(f))
+
+    def other():
+        return (fbd.attn_diff_decode(q, K, V, lam, lens), *step(y), *fbd.attn_fwd(P, R, S),
+                *fbd.attn_rope((Q, K), pos, freq, axis))
+
+    want = [one(), other()]
+    torch.cuda.synchronize()
+    times, graphs, got = 12, [], []
+    for calls in (one, other):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            for _ in range(times):
+                out = calls()
+        graphs.append(gr)
+        got.append(out)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for out in got:
+            for t in out:
+                t.zero_()
+        start = torch.cuda.Event(enable_timing=True)
+        ends = [[torch.cuda.Event(enable_timing=True) for _ in range(2)] for _ in range(2)]
+        start.record()
+        for st, gr, (a, b) in zip(streams, graphs, ends):
+            st.wait_event(start)
+            with torch.cuda.stream(st):
+                a.record()
+                gr.replay()
+                b.record()
+        torch.cuda.synchronize()
+        (a0, a1), (b0, b1) = [[start.elapsed_time(e) for e in pair] for pair in ends]
+        assert min(a1, b1) - max(a0, b0) > 0.5 * min(a1 - a0, b1 - b0), (a0, a1, b0, b1)
+        for g, w in zip(got, want):
+            for u, v in zip(g, w):
+                assert torch.equal(u, v)
+    fbd.attn_device_status()
 
 
 # -------------------------------------------------------------- infinities among the keys
