@@ -1,13 +1,60 @@
 """Differential attention and the rotary on the GPU where they can go wrong: weights nearly one-hot, infinite
-scores, angles of far positions, two streams at once."""
+scores, angles of far positions, two streams at once, offsets past 2^31 elements."""
 import math
 from fractions import Fraction
 
 import pytest
 
-from test_gpu_diff import _lib, _t, check, decode_reference, make, run  # noqa: F401  (_lib: the fixture that builds)
+from test_gpu_diff import _lib, _t, check, decode_reference, dt, make, run  # noqa: F401  (_lib: the fixture that builds)
 
 pytestmark = pytest.mark.gpu
+
+
+# -------------------------------------------------------------- offsets past 2^31 elements
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_the_last_head_past_2_31_elements(dtype):
+    """17 heads of 2^20 tokens: the last head of every tensor begins at 2^31 elements.  Forward, backward,
+    a token over the cache and the rotary, which also reads and writes a projection's layout there."""
+    import fwd_bwd_double_gb300 as fbd
+    torch = _t()
+    H, N, d, W = 17, 1 << 20, 64, 40
+    if torch.cuda.mem_get_info()[0] < 160 << 30:
+        pytest.skip("needs 160 GB of device memory")
+    gen = torch.Generator(device="cuda").manual_seed(0)
+
+    def big(heads, width):  # the last head's values random, the others' zero
+        x = torch.zeros(1, heads, N, width, dtype=dt(dtype), device="cuda")
+        x[:, -(heads // H):] = torch.randn(1, heads // H, N, width, generator=gen, device="cuda").to(dt(dtype))
+        assert (heads - heads // H) * N * width == 1 << 31
+        return x
+
+    Q, K, V, dO = big(2 * H, d), big(2 * H, d), big(H, 2 * d), big(H, 2 * d)
+    lam = torch.full((H,), 0.5, device="cuda")
+    last = (*(t[:, -(t.shape[1] // H):].contiguous() for t in (Q, K, V)), lam[-1:], dO[:, -1:].contiguous())
+    a, b = run((Q, K, V, lam, dO), window=W), run(last, window=W)
+    for k in b:
+        got = a[k][-1:] if k == "dlam" else a[k][:, -(a[k].shape[1] // H):]
+        assert torch.equal(got, b[k]), k
+    del a, b, dO
+    lens = torch.tensor([N], dtype=torch.int32, device="cuda")
+    o = fbd.attn_diff_decode(Q[:, :, -1:].contiguous(), K, V, lam, lens)
+    want, tol = decode_reference(last[0][:, :, -1:], last[1], last[2], last[3], lens, 1)
+    assert ((o[:, -1:].double() - want).abs() <= tol).all()
+    del K, V
+    pos = torch.arange(N, device="cuda", dtype=torch.int32)[None]
+    freq, axis = torch.rand(d // 2, device="cuda"), torch.zeros(d // 2, dtype=torch.int32, device="cuda")
+    turned = fbd.attn_rope(last[0], pos, freq, axis)
+    assert torch.equal(fbd.attn_rope(Q, pos, freq, axis)[:, -2:], turned)
+    del Q
+    # [B, N, heads, d]: the last token begins past 2^31 elements
+    proj = torch.zeros(1, N, 2 * H, d, dtype=dt(dtype), device="cuda")
+    proj[:, :, -2:] = last[0].transpose(1, 2)
+    y = fbd.attn_rope(proj.transpose(1, 2), pos, freq, axis)
+    assert torch.equal(y[:, -2:], turned)
+    proj.zero_()
+    fbd.attn_rope(y, pos, freq, axis, inverse=True, outs=proj.transpose(1, 2))
+    assert torch.equal(proj[:, :, -2:].transpose(1, 2), fbd.attn_rope(turned, pos, freq, axis, inverse=True))
+    assert not proj[:, :, :-2].any()
 
 
 # --------------------------------------------------------------------- two streams at once
