@@ -257,6 +257,8 @@ def _at(name, t):
 
 def _want(name, t, shape, dtype):
     """The address of t, contiguous and of that shape and type."""
+    if t is None:
+        raise FbdError(1, f"{name} is None")
     if t.shape != shape or t.dtype != dtype:
         raise FbdError(1, f"{name} must be {dtype} {tuple(shape)} (got {t.dtype} {tuple(t.shape)})")
     return _at(name, t)
@@ -265,8 +267,8 @@ def _want(name, t, shape, dtype):
 def _diff_desc(Q, K, V, lam, scale, causal, window, bounds, queries=None):
     """Descriptor of a differential attention call (queries: 1 for a token over a cache, None where Q has the keys'
     length) and the addresses of Q, K, V and lam, their shapes and types checked."""
-    if Q.dim() != 4 or K.dim() != 4 or V.dim() != 4:
-        raise FbdError(1, "Q, K and V must be 4-dimensional")
+    if any(t is None or t.dim() != 4 for t in (Q, K, V)):
+        raise FbdError(1, "Q, K and V must be 4-dimensional tensors")
     dtype = Q.dtype
     B, maps, _, d = Q.shape
     _, kmaps, N, _ = K.shape
@@ -361,10 +363,10 @@ def attn_rope(xs, pos, freq, axis, outs=None, paired: str = "half", inverse: boo
     tensors when not given; views of any strides when given, x itself among them), one tensor for one."""
     torch = _torch()
     single = torch.is_tensor(xs)
-    xs = [xs] if single else list(xs)
+    xs = [xs] if single else list(xs or ())
     if not 1 <= len(xs) <= ATTN_ROPE_MAX_TENSORS:
         raise FbdError(1, f"1 to {ATTN_ROPE_MAX_TENSORS} tensors, got {len(xs)}")
-    if any(x.dim() != 4 for x in xs):
+    if any(x is None or x.dim() != 4 for x in xs):
         raise FbdError(1, "tensors must be [B, heads, N, d]")
     if outs is None:
         outs = [torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in xs]
@@ -386,7 +388,7 @@ def attn_rope(xs, pos, freq, axis, outs=None, paired: str = "half", inverse: boo
         if heads and B and N and (xs_[3] != 1 or ys_[3] != 1):
             raise FbdError(1, "the last dimension must be contiguous")
         t.x, t.y, t.heads, t.x_stride[:], t.y_stride[:] = x.data_ptr(), y.data_ptr(), heads, xs_[:3], ys_[:3]
-    if pos.dim() not in (2, 3):
+    if pos is None or pos.dim() not in (2, 3):
         raise FbdError(1, "pos must be [axes, B, N] or [axes, N]")
     axes, shared = pos.shape[0], pos.dim() == 2
     tables = (_want("pos", pos, (axes, N) if shared else (axes, B, N), torch.int32),

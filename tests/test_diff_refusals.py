@@ -1,5 +1,5 @@
 """Refusals of the differential attention and rotary entry points that need no GPU (fake pointers,
-never dereferenced): rotary outputs over another tensor or over a table."""
+never dereferenced): rotary outputs over another tensor or over a table; an input left out."""
 import ctypes
 
 import pytest
@@ -7,6 +7,7 @@ import pytest
 import __graft_entry__
 
 __graft_entry__.build()
+import fwd_bwd_double_gb300 as fbd  # noqa: E402
 from fwd_bwd_double_gb300 import RopeDesc, RopeTensor, lib  # noqa: E402
 
 INVALID = 1
@@ -38,3 +39,26 @@ def rope(x0=X0, y0=Y0, x1=X1, y1=Y1, pos=POS, freq=FREQ, axis=AXIS, xs=None):
 def test_rope_refuses_outputs_over_other_tensors_and_tables(kw):
     assert rope(**kw) == INVALID
     assert b"overlaps" in lib.attn_last_error()
+
+
+def test_binding_refuses_an_input_left_out():
+    """None for a tensor, O2 above all, which a forward without the backward's output returns."""
+    import torch
+    Q, V, lam, lse = torch.zeros(1, 4, 8, 32), torch.zeros(1, 2, 8, 64), torch.zeros(2), torch.zeros(1, 4, 8)
+    ins = (Q, Q, V, lam, V, V, V, lse)
+    for k in range(len(ins)):
+        with pytest.raises(fbd.FbdError):
+            fbd.attn_diff_bwd(*(None if u == k else t for u, t in enumerate(ins)))
+    for k in range(4):
+        with pytest.raises(fbd.FbdError):
+            fbd.attn_diff_fwd(*(None if u == k else t for u, t in enumerate(ins[:4])))
+    token = (Q[:, :, :1].contiguous(), Q, V, lam, torch.zeros(1, dtype=torch.int32))
+    for k in range(5):
+        with pytest.raises(fbd.FbdError):
+            fbd.attn_diff_decode(*(None if u == k else t for u, t in enumerate(token)))
+    tables = (torch.zeros(1, 8, dtype=torch.int32), torch.zeros(16), torch.zeros(16, dtype=torch.int32))
+    for k in range(4):
+        with pytest.raises(fbd.FbdError):
+            fbd.attn_rope(*(None if u == k else t for u, t in enumerate((Q, *tables))))
+    with pytest.raises(fbd.FbdError):
+        fbd.attn_rope((Q, None), *tables)
