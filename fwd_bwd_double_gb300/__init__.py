@@ -282,6 +282,7 @@ def _diff_desc(Q, K, V, lam, scale, causal, window, bounds, queries=None):
     lo = hi = None
     if bounds is not None:
         lo, hi = (_want(name, t, (B, N), _torch().int32) for name, t in zip(("seg_lo", "seg_hi"), bounds))
+    window = max(-1, min(window, max(N, 1)))  # (the field has 32 bits; N or more is no window)
     return AttnDesc(B, H, N, d, scale, causal, _dtype_code(Q), H // Hkv if Hkv else 1, window, lo, hi), ptrs
 
 

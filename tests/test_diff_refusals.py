@@ -62,3 +62,14 @@ def test_binding_refuses_an_input_left_out():
             fbd.attn_rope(*(None if u == k else t for u, t in enumerate((Q, *tables))))
     with pytest.raises(fbd.FbdError):
         fbd.attn_rope((Q, None), *tables)
+
+
+@pytest.mark.parametrize("window,taken", [(0, 0), (5, 5), (8, 8), (1 << 31, 8), ((1 << 32) + 5, 8), (1 << 70, 8), (-1, -1),
+                                          (5 - (1 << 32), -1)])
+def test_a_window_past_32_bits_is_none(window, taken):
+    """The descriptor's window has 32 bits: one as wide as the sequence or wider is no window at all;
+    a negative one stays negative, which is refused."""
+    import torch
+    Q, V, lam = torch.zeros(1, 4, 8, 32), torch.zeros(1, 2, 8, 64), torch.zeros(2)
+    desc, _ = fbd._diff_desc(Q, Q, V, lam, 0.0, True, window, None)
+    assert desc.window == taken
