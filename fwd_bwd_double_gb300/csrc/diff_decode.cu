@@ -43,7 +43,7 @@ Plan make_plan(const Problem& p) {
   // 128 keys.  Measured at 3, 4, 6 and 8 CTAs an SM: 54.8, 52.6, 50.7, 52.6 us for 32 ragged contexts
   // of up to 8192 keys, 124, 120, 124, 128 us for one of 131072, 29.6, 30.1, 35.0, 39.1 us for one
   // key/value head and 8 query heads over 40000 (the join grows with the splits); float32, 64 heads
-  // over 8192: 179, 152, 143, 127 us.
+  // over 8192: 179, 152, 143, 127 us (that shape alone, so the rule stays at two waves for both types).
   const int64_t fit = p.dtype == ATTN_BF16 ? 2 : 3;
   const int64_t base = p.BHkv * q.chunks;
   const int64_t want = base > 0 ? (2 * fit * 152 + base - 1) / base : 1;
