@@ -1,6 +1,6 @@
 """Python binding of libfbd: exact attention (causal by default) forward, backward (GProj) and
 backward-over-backward on GB300; differential attention (forward, backward, one token over a
-cache) and multi-axis rotary positions.
+cache) and multi-axis rotary positions; normed heads, a paged cache and the attention over it.
 
 Argument marshalling only.  Every computation runs in the CUDA kernels of
 ``libfbd.so`` behind the C ABI declared in ``include/fbd.h``; PyTorch is used for
@@ -15,13 +15,15 @@ import os
 
 from . import _lib
 from ._lib import (ATTN_BF16, ATTN_COL_PASS, ATTN_F32, ATTN_ROPE_HALF, ATTN_ROPE_MAX_TENSORS,  # noqa: F401
-                   ATTN_ROPE_NEIGHBOUR, ATTN_ROW_PASS, AttnDesc, FbdError, RopeDesc, RopeTensor, lib, status_name)
+                   ATTN_ROPE_NEIGHBOUR, ATTN_ROW_PASS, AttnDesc, Cache, FbdError, NewTokens, NormGrad, NormTensor, RopeDesc,
+                   RopeTensor, lib, status_name)
 
 __all__ = [
     "attn_fwd", "attn_bwd", "attn_bob", "attn_bwd_passes", "attn_bob_passes", "ATTN_ROW_PASS", "ATTN_COL_PASS", "attn_bwd_workspace_bytes", "attn_bob_workspace_bytes",
     "attn_bob_static", "attn_bwd_projected_dS", "attn_segment_bounds",
     "attn_diff_fwd", "attn_diff_bwd", "attn_diff_bwd_workspace_bytes", "attn_diff_decode",
-    "attn_diff_decode_workspace_bytes", "attn_rope", "attn_device_status", "attn_check_wait_timeout",
+    "attn_diff_decode_workspace_bytes", "attn_rope", "attn_qk_norm", "attn_qk_norm_bwd", "attn_cache_append",
+    "attn_paged", "attn_paged_workspace_bytes", "attn_device_status", "attn_check_wait_timeout",
     "attn_status_string", "attn_version", "make_desc",
     "FbdError", "AttnDesc", "ATTN_F32", "ATTN_BF16", "lib",
 ]
@@ -399,6 +401,227 @@ def attn_rope(xs, pos, freq, axis, outs=None, paired: str = "half", inverse: boo
     _launch(lib.attn_rope, (*xs, *outs, pos, freq, axis) if any(x.numel() for x in xs) else (),
             ctypes.byref(desc), tensors, len(xs), *tables)
     return outs[0] if single else outs
+
+
+def _view(name, x, shape, dtype, strides):
+    """The address of a view [B, heads, N, d] of that shape and type, its last dimension contiguous; its strides of the
+    other three into `strides`."""
+    if x is None:
+        raise FbdError(1, f"{name} is None")
+    if x.shape != shape or x.dtype != dtype:
+        raise FbdError(1, f"{name} must be {dtype} {tuple(shape)} (got {x.dtype} {tuple(x.shape)})")
+    s = x.stride()
+    if s[3] != 1 and x.numel():
+        raise FbdError(1, f"the last dimension of {name} must be contiguous")
+    strides[:] = s[:3]
+    return x.data_ptr()
+
+
+def _angles(pos, freq, axis, B, N, d, own_pos=False):
+    """(axes, shared, addresses of pos, freq, axis) of a rotary's tables, all None where nothing turns; own_pos: pos may
+    be left out alone (the tokens' own positions)."""
+    torch = _torch()
+    if pos is None and freq is None and axis is None:
+        return 1, True, (None, None, None)
+    at = None
+    axes, shared = 1, True
+    if pos is not None or not own_pos:
+        if pos is None or pos.dim() not in (2, 3):
+            raise FbdError(1, "pos must be [axes, B, N] or [axes, N]")
+        axes, shared = pos.shape[0], pos.dim() == 2
+        at = _want("pos", pos, (axes, N) if shared else (axes, B, N), torch.int32)
+    return axes, shared, (at, _want("freq", freq, (d // 2,), torch.float32), _want("axis", axis, (d // 2,), torch.int32))
+
+
+def _norm_desc(xs, pos, freq, axis, paired):
+    """Descriptor of a call on normed heads, the shape [B, heads, N, d] of its first tensor, and its tables."""
+    if not 1 <= len(xs) <= ATTN_ROPE_MAX_TENSORS:
+        raise FbdError(1, f"1 to {ATTN_ROPE_MAX_TENSORS} tensors, got {len(xs)}")
+    if any(x is None or x.dim() != 4 for x in xs):
+        raise FbdError(1, "tensors must be [B, heads, N, d]")
+    if paired not in ("half", "neighbour"):
+        raise FbdError(1, f"paired must be 'half' or 'neighbour' (got {paired!r})")
+    B, _, N, d = xs[0].shape
+    axes, shared, tables = _angles(pos, freq, axis, B, N, d)
+    desc = RopeDesc(B, N, d, axes, _dtype_code(xs[0]), ATTN_ROPE_HALF if paired == "half" else ATTN_ROPE_NEIGHBOUR, 0,
+                    0 if shared else N)
+    return desc, (B, N, d), tables
+
+
+def _listed(ts, n, what):
+    """A tensor, None or a list of n of them as a list."""
+    if ts is None:
+        return [None] * n
+    ts = [ts] if _torch().is_tensor(ts) else list(ts)
+    if len(ts) != n:
+        raise FbdError(1, f"{n} tensors and {len(ts)} {what}")
+    return ts
+
+
+@_on_stream
+def attn_qk_norm(xs, weights=None, pos=None, freq=None, axis=None, outs=None, paired: str = "half", eps: float = 1e-6):
+    """RMS norm over d of each head's vector, z = w x / sqrt(mean x^2 + eps), then the turn of attn_rope, in one pass over
+    the [B, heads, N, d] views `xs` (one tensor or up to four, any strides with d contiguous).  weights: float32 [d] per
+    tensor (None: ones).  pos, freq, axis: as in attn_rope, all None: no turn.  Returns `outs` (contiguous [B, heads, N, d]
+    tensors when not given; views when given, x itself among them), one tensor for one."""
+    torch = _torch()
+    single = torch.is_tensor(xs)
+    xs = [xs] if single else list(xs or ())
+    desc, (B, N, d), tables = _norm_desc(xs, pos, freq, axis, paired)
+    weights = _listed(weights, len(xs), "weights")
+    outs = [torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in xs] if outs is None else _listed(outs, len(xs), "outputs")
+    tensors = (NormTensor * len(xs))()
+    for t, x, w, y in zip(tensors, xs, weights, outs):
+        shape = (B, x.shape[1], N, d)
+        t.x, t.y = _view("x", x, shape, xs[0].dtype, t.x_stride), _view("an output", y, shape, xs[0].dtype, t.y_stride)
+        t.w, t.heads = None if w is None else _want("weight", w, (d,), torch.float32), shape[1]
+    _launch(lib.attn_qk_norm, (*xs, *outs, *weights, pos, freq, axis) if any(x.numel() for x in xs) else (),
+            ctypes.byref(desc), tensors, len(xs), eps, *tables)
+    return outs[0] if single else outs
+
+
+@_on_stream
+def attn_qk_norm_bwd(xs, dys, weights=None, pos=None, freq=None, axis=None, dxs=None, dweights=None, workspace=None,
+                     paired: str = "half", eps: float = 1e-6):
+    """dxs, dweights = gradient of attn_qk_norm at xs for the gradients dys of its outputs (the tables, weights and eps
+    given again).  dxs: contiguous tensors when not given, x or dy itself among those given; dweights: float32 [d] per
+    tensor, None where its weight is None.  One tensor each for one tensor."""
+    torch = _torch()
+    single = torch.is_tensor(xs)
+    xs = [xs] if single else list(xs or ())
+    desc, (B, N, d), tables = _norm_desc(xs, pos, freq, axis, paired)
+    dys = _listed(dys, len(xs), "gradients")
+    weights = _listed(weights, len(xs), "weights")
+    dxs = [torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in xs] if dxs is None else _listed(dxs, len(xs), "dxs")
+    dweights = [None if w is None else torch.empty_like(w) for w in weights] if dweights is None else \
+        _listed(dweights, len(xs), "dweights")
+    tensors = (NormGrad * len(xs))()
+    dtype = xs[0].dtype
+    for t, x, dy, dx, w, dw in zip(tensors, xs, dys, dxs, weights, dweights):
+        shape = (B, x.shape[1], N, d)
+        t.x, t.dy, t.dx = (_view("x", x, shape, dtype, t.x_stride), _view("dy", dy, shape, dtype, t.dy_stride),
+                           _view("dx", dx, shape, dtype, t.dx_stride))
+        t.w = None if w is None else _want("weight", w, (d,), torch.float32)
+        t.dw = None if dw is None else _want("dweight", dw, (d,), torch.float32)
+        t.heads = shape[1]
+    workspace = _workspace(lib.attn_qk_norm_bwd_workspace_bytes(ctypes.byref(desc), tensors, len(xs)), xs[0], workspace)
+    some = any(x.numel() for x in xs)
+    _launch(lib.attn_qk_norm_bwd, (*xs, *dys, *dxs, *weights, *dweights, pos, freq, axis, workspace) if some else dweights,
+            ctypes.byref(desc), tensors, len(xs), eps, *tables, _at("workspace", workspace), workspace.nbytes)
+    return (dxs[0], dweights[0]) if single else (dxs, dweights)
+
+
+def _cache_of(cache, heads, d, dtype, B):
+    """The C structure of a cache (K, V, table)."""
+    try:
+        K, V, table = cache
+    except (TypeError, ValueError):
+        raise FbdError(1, "a cache is (K, V, table)") from None
+    if K is None or V is None or table is None or K.dim() != 4:
+        raise FbdError(1, "a cache is K and V [pages, heads, page_size, d] and table [B, width]")
+    c = Cache()
+    shape = (K.shape[0], heads, K.shape[2], d)
+    c.K, c.V = _view("K of the cache", K, shape, dtype, c.k_stride), _view("V of the cache", V, shape, dtype, c.v_stride)
+    c.table = _want("table", table, (B, table.shape[-1] if table.dim() else 0), _torch().int32)
+    c.pages, c.page_size, c.width = K.shape[0], K.shape[2], table.shape[1]
+    return c, (K, V, table)
+
+
+def _sequences(lens, cu, batch):
+    """(B, addresses of cu and lens) of a call's sequences; batch: of its [batch, heads, N, d] tensors."""
+    torch = _torch()
+    if lens is None or lens.dim() != 1:
+        raise FbdError(1, "lens must be an int32 [B] tensor")
+    B = lens.shape[0]
+    if batch != (B if cu is None else 1):
+        raise FbdError(1, f"{batch} batch rows for {B} sequences" + ("" if cu is None else " of packed tokens (one batch row)"))
+    return B, (None if cu is None else _want("cu", cu, (B + 1,), torch.int32), _want("lens", lens, (B,), torch.int32))
+
+
+@_on_stream
+def attn_cache_append(K, V, cache, lens, cu=None, Q=None, Q_out=None, weights=None, pos=None, freq=None, axis=None,
+                      paired: str = "half", eps: float = 1e-6):
+    """The new tokens' K and V [B, Hkv, N, d] into the pages of `cache` = (K, V [pages, Hkv, page_size, d], table [B, width]
+    int32), the keys normed and turned on the way, and the queries Q [B, H, N, d] too if given.  lens [B] int32: the keys
+    each sequence holds then; cu [B + 1] int32: packed tokens, views [1, heads, N, d] of which sequence b has the rows
+    cu[b] .. cu[b + 1] - 1.  weights = (wq, wk), float32 [d] or None each: the norm of attn_qk_norm (None: no norm).
+    freq, axis: attn_rope's tables (None: no turn), pos None: the tokens' positions in their sequences.  Returns Q_out
+    (a contiguous tensor when not given, Q itself among those given; rows of no sequence stay as they were), None
+    without Q."""
+    torch = _torch()
+    if any(x is None or x.dim() != 4 for x in (K, V)) or (Q is not None and Q.dim() != 4):
+        raise FbdError(1, "tensors must be [B, heads, N, d]")
+    if paired not in ("half", "neighbour"):
+        raise FbdError(1, f"paired must be 'half' or 'neighbour' (got {paired!r})")
+    dtype = K.dtype
+    batch, Hkv, N, d = K.shape
+    B, (cu_at, lens_at) = _sequences(lens, cu, batch)
+    H = Hkv if Q is None else Q.shape[1]
+    if (Hkv == 0) != (H == 0) or (Hkv and H % Hkv):
+        raise FbdError(1, f"key/value heads ({Hkv}) must divide query heads ({H})")
+    c, parts = _cache_of(cache, Hkv, d, dtype, B)
+    t = NewTokens()
+    t.K, t.V = _view("K", K, K.shape, dtype, t.k_stride), _view("V", V, K.shape, dtype, t.v_stride)
+    if Q is None and Q_out is not None:
+        raise FbdError(1, "Q_out without Q")
+    if Q is not None:
+        if Q_out is None:
+            Q_out = torch.empty(Q.shape, dtype=dtype, device=Q.device)
+        shape = (batch, H, N, d)
+        t.Q, t.Q_out = _view("Q", Q, shape, dtype, t.q_stride), _view("Q_out", Q_out, shape, dtype, t.q_out_stride)
+    wq, wk = (None, None) if weights is None else _listed(weights, 2, "weights")
+    t.q_weight, t.k_weight = (None if w is None else _want("weight", w, (d,), torch.float32) for w in (wq, wk))
+    axes, shared, (t.pos, t.freq, t.axis) = _angles(pos, freq, axis, batch, N, d, own_pos=True)
+    t.pos_batch_stride, t.axes = 0 if shared else N, axes
+    t.paired = ATTN_ROPE_HALF if paired == "half" else ATTN_ROPE_NEIGHBOUR
+    t.normed, t.eps = weights is not None, eps
+    desc = AttnDesc(B, H, N, d, 0.0, 1, _dtype_code(K), H // Hkv if Hkv else 1, 0, None, None)
+    _launch(lib.attn_cache_append, (K, V, *parts, lens, cu, Q, Q_out, wq, wk, pos, freq, axis) if K.numel() else (),
+            ctypes.byref(desc), ctypes.byref(t), ctypes.byref(c), cu_at, lens_at)
+    return Q_out
+
+
+def attn_paged_workspace_bytes(desc: AttnDesc, max_new: int = 0) -> int:
+    return int(lib.attn_paged_workspace_bytes(ctypes.byref(desc), int(max_new)))
+
+
+_Strides = ctypes.c_int64 * 3
+
+
+@_on_stream
+def attn_paged(Q, cache, lens, cu=None, O=None, lse=None, workspace=None, scale: float = 0.0, causal: bool = True,
+               window: int = 0, max_new: int = 0):
+    """O, lse = attention of the new tokens Q [B, H, N, d] over a paged cache = (K, V [pages, Hkv, page_size, d], table
+    [B, width] int32) that holds lens [B] int32 keys of each sequence, the new tokens' own among them (they are its last
+    ones).  cu [B + 1] int32: packed tokens, Q [1, H, N, d], sequence b has the rows cu[b] .. cu[b + 1] - 1.  Q, K, V and O
+    are views of any strides with d contiguous; O is given its memory token by token ([B, N, H, d]) when it is not given,
+    as a layer's output projection takes it.  lse float32 [B, H, N].  max_new: the most new tokens of a sequence, where the
+    host knows it (1 when each has one: chooses the kernel, nothing else).  A token that sees no key gives O = 0, lse =
+    -inf; rows of no sequence stay as they were."""
+    torch = _torch()
+    if Q is None or Q.dim() != 4:
+        raise FbdError(1, "Q must be [B, H, N, d]")
+    dtype = Q.dtype
+    batch, H, N, d = Q.shape
+    B, (cu_at, lens_at) = _sequences(lens, cu, batch)
+    Hkv = cache[0].shape[1] if isinstance(cache, (tuple, list)) and len(cache) == 3 and getattr(cache[0], "ndim", 0) == 4 else 0
+    if (Hkv == 0) != (H == 0) or (Hkv and H % Hkv):
+        raise FbdError(1, f"key/value heads ({Hkv}) must divide query heads ({H})")
+    c, parts = _cache_of(cache, Hkv, d, dtype, B)
+    if O is None:
+        O = torch.empty((batch, N, H, d), dtype=dtype, device=Q.device).transpose(1, 2)
+    if lse is None:
+        lse = torch.empty((batch, H, N), dtype=torch.float32, device=Q.device)
+    qs, os_ = _Strides(), _Strides()
+    Q_at, O_at = _view("Q", Q, Q.shape, dtype, qs), _view("O", O, Q.shape, dtype, os_)
+    lse_at = _want("lse", lse, (batch, H, N), torch.float32)
+    window = max(-1, min(window, (1 << 31) - 1))  # (the field has 32 bits; a cache's capacity or more is no window)
+    desc = AttnDesc(B, H, N, d, scale, causal, _dtype_code(Q), H // Hkv if Hkv else 1, window, None, None)
+    max_new = N if cu is None else min(max_new, N)
+    workspace = _workspace(lib.attn_paged_workspace_bytes(ctypes.byref(desc), max_new), Q, workspace)
+    _launch(lib.attn_paged, (Q, *parts, lens, cu, O, lse, workspace) if Q.numel() and B else (), ctypes.byref(desc), Q_at, qs,
+            ctypes.byref(c), cu_at, lens_at, max_new, O_at, os_, lse_at, _at("workspace", workspace), workspace.nbytes)
+    return O, lse
 
 
 def attn_device_status(stream=None) -> int:

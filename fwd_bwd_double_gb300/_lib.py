@@ -48,6 +48,32 @@ class RopeTensor(ctypes.Structure):
                 ("x_stride", ctypes.c_int64 * 3), ("y_stride", ctypes.c_int64 * 3)]
 
 
+class NormTensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("w", ctypes.c_void_p), ("heads", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64 * 3), ("y_stride", ctypes.c_int64 * 3)]
+
+
+class NormGrad(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("dy", ctypes.c_void_p), ("dx", ctypes.c_void_p), ("w", ctypes.c_void_p),
+                ("dw", ctypes.c_void_p), ("heads", ctypes.c_int64), ("x_stride", ctypes.c_int64 * 3),
+                ("dy_stride", ctypes.c_int64 * 3), ("dx_stride", ctypes.c_int64 * 3)]
+
+
+class Cache(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("table", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("width", ctypes.c_int64), ("k_stride", ctypes.c_int64 * 3),
+                ("v_stride", ctypes.c_int64 * 3)]
+
+
+class NewTokens(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("Q", ctypes.c_void_p), ("Q_out", ctypes.c_void_p),
+                ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3), ("q_stride", ctypes.c_int64 * 3),
+                ("q_out_stride", ctypes.c_int64 * 3), ("k_weight", ctypes.c_void_p), ("q_weight", ctypes.c_void_p),
+                ("pos", ctypes.c_void_p), ("freq", ctypes.c_void_p), ("axis", ctypes.c_void_p),
+                ("pos_batch_stride", ctypes.c_int64), ("axes", ctypes.c_int32), ("paired", ctypes.c_int32),
+                ("normed", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
 _P = ctypes.c_void_p
 _D = ctypes.POINTER(AttnDesc)
 PROTOTYPES = {
@@ -68,6 +94,15 @@ PROTOTYPES = {
     "attn_diff_decode_workspace_bytes": (ctypes.c_size_t, [_D]),
     "attn_diff_decode": (ctypes.c_int, [_D] + [_P] * 7 + [ctypes.c_size_t, _P]),
     "attn_rope": (ctypes.c_int, [ctypes.POINTER(RopeDesc), ctypes.POINTER(RopeTensor), ctypes.c_int, _P, _P, _P, _P]),
+    "attn_qk_norm": (ctypes.c_int, [ctypes.POINTER(RopeDesc), ctypes.POINTER(NormTensor), ctypes.c_int, ctypes.c_float,
+                                    _P, _P, _P, _P]),
+    "attn_qk_norm_bwd_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(RopeDesc), ctypes.POINTER(NormGrad), ctypes.c_int]),
+    "attn_qk_norm_bwd": (ctypes.c_int, [ctypes.POINTER(RopeDesc), ctypes.POINTER(NormGrad), ctypes.c_int, ctypes.c_float,
+                                        _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "attn_cache_append": (ctypes.c_int, [_D, ctypes.POINTER(NewTokens), ctypes.POINTER(Cache), _P, _P, _P]),
+    "attn_paged_workspace_bytes": (ctypes.c_size_t, [_D, ctypes.c_int64]),
+    "attn_paged": (ctypes.c_int, [_D, _P, ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(Cache), _P, _P, ctypes.c_int64, _P,
+                                  ctypes.POINTER(ctypes.c_int64), _P, _P, ctypes.c_size_t, _P]),
     "attn_device_status": (ctypes.c_int, [_P]),
     "attn_check_wait_timeout": (ctypes.c_int, [_P]),
     "attn_status_string": (ctypes.c_char_p, [ctypes.c_int]),

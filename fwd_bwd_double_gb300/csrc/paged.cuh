@@ -1,0 +1,165 @@
+// How the attention over a paged cache is cut into work, shared by its kernels.
+//
+// An item is a run of new tokens of one sequence with `gt` query heads of a key/value head: the rows
+// (token, head) of a tile.  Its cost is its key blocks (two units each where it fills two tiles) and a
+// constant.  All items stand on a line, sequence by sequence, tile by tile, the heads of a tile side
+// by side, and each CTA takes an equal stretch of it, cut between key blocks: ragged batches spread
+// evenly, and a long context with few rows is shared by all SMs.  An item that lies in several
+// stretches leaves its parts (o unnormalised, maximum, sum) in the workspace, at most two a CTA, and
+// a last launch joins them in a fixed order.
+#pragma once
+#include "diff.h"
+#include "paged.h"
+#include "ptx.cuh"
+#include "tc_common.cuh"
+
+namespace fbd {
+namespace paged {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct Cut {
+  int gt;      // query heads handled together (divides the heads of a key/value head)
+  int nv;      // groups of gt query heads
+  int per_kv;  // ... of a key/value head
+  int tile;    // tokens of a tile
+  int step;    // tokens of an item (tile, or 2 tile: then an item of more than `tile` tokens costs double)
+  int BN;      // keys of a block
+  int over;    // cost of an item beside its blocks
+  int least;   // units of a stretch, at the least
+  int ctas;
+};
+struct Work {
+  Seqs seqs;
+  Cut cut;
+  int causal, window;
+};
+// What the planning launch leaves in front of the workspace.
+struct Head {
+  int64_t total, stretch;
+};
+struct Start {  // the item in which a CTA's stretch begins (b < 0: none)
+  int64_t pos;  // of the item on the line
+  int b, tile, vh, pad;
+};
+struct Tail {  // the item that begins in a CTA's stretch and goes on behind it
+  int b, tile, vh, parts;  // parts 0: none
+};
+// Workspace: Head, Start[ctas], Tail[ctas], the line position behind each of the B sequences, then two slots
+// per CTA of `rows` rows: o [rows][D], (max in powers of two, sum) [rows].  Slot 2p holds CTA p's part of
+// an item that began before, slot 2p + 1 of one that begins here and goes on.
+struct Space {
+  Head* head;
+  Start* start;
+  Tail* tail;
+  int64_t* ends;
+  float* slots;
+  int64_t slot;  // floats of a slot
+  int rows, D;
+  static int64_t header(int ctas, int64_t B) {
+    return (static_cast<int64_t>(sizeof(Head)) + ctas * static_cast<int64_t>(sizeof(Start) + sizeof(Tail)) + B * 8 + 255) /
+           256 * 256;
+  }
+  static size_t bytes(int ctas, int64_t B, int rows, int D) {
+    return static_cast<size_t>(header(ctas, B)) + 2ull * ctas * rows * (D + 2) * sizeof(float);
+  }
+  static Space at(void* ws, int ctas, int64_t B, int rows, int D) {
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    Space s;
+    s.head = reinterpret_cast<Head*>(w);
+    s.start = reinterpret_cast<Start*>(w + sizeof(Head));
+    s.tail = reinterpret_cast<Tail*>(w + sizeof(Head) + ctas * sizeof(Start));
+    s.ends = reinterpret_cast<int64_t*>(s.tail + ctas);
+    s.slots = reinterpret_cast<float*>(w + header(ctas, B));
+    s.slot = static_cast<int64_t>(rows) * (D + 2);
+    s.rows = rows, s.D = D;
+    return s;
+  }
+  __device__ __forceinline__ float* o(int k, int row) const { return slots + k * slot + static_cast<int64_t>(row) * D; }
+  __device__ __forceinline__ float2* ml(int k, int row) const {
+    return reinterpret_cast<float2*>(slots + k * slot + static_cast<int64_t>(rows) * D) + row;
+  }
+};
+
+struct Blocks {
+  int j0, n;  // key blocks j0 .. j0 + n - 1 (at least one, which may be hidden from every row)
+};
+// The key blocks that tokens t0 .. t1 - 1 of a sequence see.
+__device__ __forceinline__ Blocks blocks_of(const Work& w, const Seq& s, int t0, int t1) {
+  const int hi = w.causal ? min(max(s.start + t1, 0), s.len) : s.len;
+  const int64_t l = static_cast<int64_t>(s.start) + t0 - w.window + 1;
+  const int lo = w.window > 0 && l > 0 ? static_cast<int>(l) : 0;
+  if (hi <= lo) return Blocks{0, 1};
+  const int j0 = lo / w.cut.BN;
+  return Blocks{j0, (hi + w.cut.BN - 1) / w.cut.BN - j0};
+}
+
+// The items of a CTA's stretch, one after another.
+struct Walk {
+  int64_t pos, from, to, stretch;  // this item on the line; the stretch
+  int b, tile, vh;
+  Seq s;
+  int t0, t1, j0, n, weight;
+  int k0, k1;             // this CTA's blocks of the item: k0 .. k1 - 1
+  int64_t end;            // the item's last block on the line
+
+  __device__ __forceinline__ void set_tile(const Work& w) {
+    t0 = tile * w.cut.step, t1 = min(s.n, t0 + w.cut.step);
+    const Blocks k = blocks_of(w, s, t0, t1);
+    j0 = k.j0, n = k.n;
+    weight = t1 - t0 > w.cut.tile ? 2 : 1;
+  }
+  __device__ __forceinline__ void set_range() {
+    end = pos + static_cast<int64_t>(weight) * (n - 1);
+    k0 = from > pos ? static_cast<int>(min(static_cast<int64_t>(n), (from - pos + weight - 1) / weight)) : 0;
+    k1 = end >= to ? static_cast<int>(max(static_cast<int64_t>(0), (to - pos + weight - 1) / weight)) : n;
+  }
+  // false: nothing to do
+  __device__ __forceinline__ bool begin(const Work& w, const Space& sp, int p) {
+    const Start st = sp.start[p];
+    if (st.b < 0) return false;
+    const Head h = *sp.head;
+    stretch = h.stretch;
+    from = stretch * p, to = min(from + stretch, h.total);
+    pos = st.pos, b = st.b, tile = st.tile, vh = st.vh;
+    s = seq_at(w.seqs, b);
+    set_tile(w);
+    set_range();
+    return k0 < k1 || next(w);  // (the stretch may begin behind the item's last block)
+  }
+  // the next item with blocks in the stretch
+  __device__ __forceinline__ bool next(const Work& w) {
+    do {
+      pos += static_cast<int64_t>(weight) * n + w.cut.over;
+      if (pos >= to) return false;
+      if (++vh == w.cut.nv) {
+        vh = 0;
+        ++tile;
+        if (static_cast<int64_t>(tile) * w.cut.step >= s.n) {
+          tile = 0;
+          do {
+            if (++b >= w.seqs.B) return false;
+            s = seq_at(w.seqs, b);
+          } while (s.n == 0);
+        }
+        set_tile(w);
+      }
+      set_range();
+    } while (k0 >= k1);
+    return true;
+  }
+  __device__ __forceinline__ bool whole() const { return k0 == 0 && k1 == n; }
+  __device__ __forceinline__ int slot(int p) const { return k0 > 0 ? 2 * p : 2 * p + 1; }
+  // the CTAs whose stretches this item's blocks lie in, from this one on
+  __device__ __forceinline__ int parts(int p) const { return static_cast<int>(end / stretch) - p + 1; }
+};
+
+// Where the outputs of a call go.
+struct Out {
+  void* O;
+  float* lse;
+  int64_t os[3], ls[2];
+};
+
+}  // namespace paged
+}  // namespace fbd

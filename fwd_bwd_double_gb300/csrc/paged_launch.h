@@ -1,0 +1,24 @@
+// Launches of the attention over a paged cache: the plan and the join around each of its kernels.
+#pragma once
+#include "paged.cuh"
+
+namespace fbd {
+namespace paged {
+
+cudaError_t plan(const Work& w, const Space& sp, cudaStream_t st);
+// tile_rows: rows of a slot that a tile takes.
+cudaError_t join(const Work& w, const Space& sp, const Out& out, int dtype, int d, int tile_rows, cudaStream_t st);
+
+// The query heads handled together by a kernel whose tiles have `rows` rows: all that share a
+// key/value head where `few` new tokens of them fit a tile (K and V are then read once), else the
+// divisor of the group that leaves the fewest rows of a tile empty (the larger of two alike).
+inline int heads_together(int group, int rows, int64_t few) {
+  if (few > 0 && few * group <= rows) return group;
+  int best = 1;
+  for (int k = 1; k <= group && k <= rows; ++k)
+    if (group % k == 0 && rows / k * k >= rows / best * best) best = k;
+  return best;
+}
+
+}  // namespace paged
+}  // namespace fbd

@@ -1,0 +1,187 @@
+// The planning launch of the attention over a paged cache (one block), and the launch that joins the
+// parts of items that several CTAs shared.
+#include <cuda_bf16.h>
+
+#include "paged.cuh"
+#include "paged_launch.h"
+
+namespace fbd {
+namespace paged {
+namespace {
+
+constexpr int kT = 1024;
+
+__device__ __forceinline__ int64_t tile_units(const Work& w, const Seq& s, int tile) {
+  const int t0 = tile * w.cut.step, t1 = min(s.n, t0 + w.cut.step);
+  const Blocks k = blocks_of(w, s, t0, t1);
+  return static_cast<int64_t>(t1 - t0 > w.cut.tile ? 2 : 1) * k.n + w.cut.over;
+}
+
+__device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+__global__ void __launch_bounds__(kT) plan_kernel(const Work w, const Space sp) {
+  __shared__ int64_t carry, part[kT / 32];
+  ptx::grid_dependency_launch();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, B = w.seqs.B;
+  int64_t* ends = sp.ends;
+  for (int b = warp; b < B; b += kT / 32) {
+    const Seq s = seq_at(w.seqs, b);
+    const int tiles = static_cast<int>((static_cast<int64_t>(s.n) + w.cut.step - 1) / w.cut.step);
+    int64_t v = 0;
+    for (int t = lane; t < tiles; t += 32) v += tile_units(w, s, t);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0) ends[b] = v * w.cut.nv;
+  }
+  if (threadIdx.x == 0) carry = 0;
+  __syncthreads();
+  for (int b0 = 0; b0 < B; b0 += kT) {
+    const int b = b0 + threadIdx.x;
+    int64_t v = warp_scan(b < B ? ends[b] : 0, lane);
+    if (lane == 31) part[warp] = v;
+    __syncthreads();
+    if (warp == 0) part[lane] = warp_scan(part[lane], lane);
+    __syncthreads();
+    v += carry + (warp > 0 ? part[warp - 1] : 0);
+    if (b < B) ends[b] = v;
+    __syncthreads();
+    if (threadIdx.x == kT - 1) carry = v;
+    __syncthreads();
+  }
+  const int64_t total = carry;
+  const int64_t even = (total + w.cut.ctas - 1) / w.cut.ctas, stretch = even > w.cut.least ? even : w.cut.least;
+  if (threadIdx.x == 0) *sp.head = Head{total, stretch};
+  for (int p = warp; p < w.cut.ctas; p += kT / 32) {
+    const int64_t x = stretch * p;
+    if (x >= total) {
+      if (lane == 0) sp.start[p] = Start{0, -1, 0, 0, 0};
+      continue;
+    }
+    int lo = -1, hi = B - 1;  // the first sequence that ends behind x
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (ends[mid] > x) hi = mid; else lo = mid;
+    }
+    const Seq s = seq_at(w.seqs, hi);
+    const int tiles = static_cast<int>((static_cast<int64_t>(s.n) + w.cut.step - 1) / w.cut.step);
+    int64_t base = hi > 0 ? ends[hi - 1] : 0;
+    for (int t0 = 0; t0 < tiles; t0 += 32) {
+      const int t = t0 + lane;
+      const int64_t u = t < tiles ? tile_units(w, s, t) : 0, cum = base + warp_scan(u * w.cut.nv, lane);
+      const unsigned behind = __ballot_sync(0xffffffffu, cum > x);
+      if (behind != 0) {
+        if (lane == __ffs(behind) - 1) {
+          const int64_t at = cum - u * w.cut.nv, vh = (x - at) / u;
+          sp.start[p] = Start{at + vh * u, hi, t, static_cast<int>(vh), 0};
+        }
+        break;
+      }
+      base = __shfl_sync(0xffffffffu, cum, 31);
+    }
+  }
+}
+
+__device__ __forceinline__ void put(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float4 v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(ptx::pack_bf16(v.x, v.y), ptx::pack_bf16(v.z, v.w));
+}
+
+constexpr int kJ = 256;
+constexpr int kRows = 8;  // rows of a block
+
+// Block (p, chunk): rows of the item that begins in CTA p's stretch and goes on behind it.  A row's columns
+// are d / 4 threads' (rounded up to a power of two); such groups take a row each, or, where the
+// parts are many, parts of one row after another.
+template <typename T>
+__global__ void __launch_bounds__(kJ) join_kernel(const Work w, const Space sp, const Out out, int d, int tile_rows) {
+  __shared__ float4 sum[kJ];
+  __shared__ float sl[kJ], sm[kJ];
+  ptx::grid_dependency_wait();
+  const Tail q = sp.tail[blockIdx.x];
+  if (q.parts == 0) return;
+  const Seq s = seq_at(w.seqs, q.b);
+  const int t0 = q.tile * w.cut.step, t1 = min(s.n, t0 + w.cut.step), gt = w.cut.gt;
+  const int rows = (t1 - t0) * gt, p = blockIdx.x;
+  int C = 8;
+  while (C * 4 < d) C *= 2;
+  const int groups = kJ / C, g = threadIdx.x / C, col = (threadIdx.x & (C - 1)) * 4;
+  const bool wide = q.parts > 2 * groups;  // groups share a row
+  const int r0 = blockIdx.y * kRows, r1 = min(rows, r0 + kRows);
+  for (int rr = r0; rr < r1; rr += wide ? 1 : groups) {
+    const int row = rr + (wide ? 0 : g);
+    const bool live = row < r1;
+    const int t = live ? row / gt : 0, hh = live ? row - t * gt : 0;
+    const int tl = t / w.cut.tile, at = tl * tile_rows + (t - tl * w.cut.tile) * gt + hh;  // in a slot
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (live) {
+      for (int k = wide ? g : 0; k < q.parts; k += wide ? groups : 1) {
+        const int slot = k == 0 ? 2 * p + 1 : 2 * (p + k);
+        const float2 x = *sp.ml(slot, at);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (col < d) v = *reinterpret_cast<const float4*>(sp.o(slot, at) + col);
+        const float mn = fmaxf(m, x.x), sub = mn == -INFINITY ? 0.f : mn;
+        const float a = ptx::ex2(m - sub), b = ptx::ex2(x.x - sub);
+        m = mn, l = fmaf(l, a, x.y * b);
+        o.x = fmaf(o.x, a, v.x * b), o.y = fmaf(o.y, a, v.y * b);
+        o.z = fmaf(o.z, a, v.z * b), o.w = fmaf(o.w, a, v.w * b);
+      }
+    }
+    if (wide) {
+      __syncthreads();  // the row before has been read
+      sum[threadIdx.x] = o, sm[threadIdx.x] = m, sl[threadIdx.x] = l;
+      __syncthreads();
+      if (g == 0) {
+        for (int k = 1; k < groups; ++k) {
+          const int u = k * C + threadIdx.x;
+          const float4 v = sum[u];
+          const float mn = fmaxf(m, sm[u]), sub = mn == -INFINITY ? 0.f : mn;
+          const float a = ptx::ex2(m - sub), b = ptx::ex2(sm[u] - sub);
+          m = mn, l = fmaf(l, a, sl[u] * b);
+          o.x = fmaf(o.x, a, v.x * b), o.y = fmaf(o.y, a, v.y * b);
+          o.z = fmaf(o.z, a, v.z * b), o.w = fmaf(o.w, a, v.w * b);
+        }
+      }
+    }
+    if (live && (!wide || g == 0)) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // (a row that sees no key: 0)
+      const int64_t h = static_cast<int64_t>(q.vh) * gt + hh, pos = s.row0 + t0 + t;
+      if (col < d)
+        put(static_cast<T*>(out.O) + s.batch * out.os[0] + h * out.os[1] + pos * out.os[2] + col,
+            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+      if (col == 0 && out.lse != nullptr)
+        out.lse[s.batch * out.ls[0] + h * out.ls[1] + pos] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t plan(const Work& w, const Space& sp, cudaStream_t st) {
+  plan_kernel<<<1, kT, 0, st>>>(w, sp);
+  return cudaGetLastError();
+}
+
+cudaError_t join(const Work& w, const Space& sp, const Out& out, int dtype, int d, int tile_rows, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(w.cut.ctas), static_cast<unsigned>((w.cut.step * w.cut.gt + kRows - 1) / kRows));
+  cfg.blockDim = dim3(kJ);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return dtype == ATTN_BF16 ? cudaLaunchKernelEx(&cfg, join_kernel<__nv_bfloat16>, w, sp, out, d, tile_rows)
+                            : cudaLaunchKernelEx(&cfg, join_kernel<float>, w, sp, out, d, tile_rows);
+}
+
+}  // namespace paged
+}  // namespace fbd

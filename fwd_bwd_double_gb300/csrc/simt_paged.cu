@@ -1,0 +1,270 @@
+// Attention of new tokens over a paged cache on the CUDA cores: online softmax over blocks of 64 keys, fp32
+// throughout.
+//
+// A CTA of 256 threads holds R rows (tokens times the query heads that share a key/value head) and streams
+// K and V through shared memory; a row belongs to 16 threads of a half-warp, R / 16 rows to a thread,
+// so that scores, maxima and probabilities pass between them by shuffles and a row of shared memory.
+// Keys that the sequence does not hold are not read; a key hidden from a row has weight 0 there and its
+// value is left out of the sum, whatever it is.
+#include <cuda_bf16.h>
+
+#include "paged_launch.h"
+
+namespace fbd {
+namespace paged {
+namespace {
+
+constexpr int kT = 256, BN = 64;
+
+template <int D, int R>
+struct Lay {
+  static constexpr int PK = D + 4, PP = BN + 4;
+  static constexpr int oQ = 0, oK = oQ + R * D, oV = oK + BN * PK, oP = oV + BN * D, oRow = oP + R * PP;
+  static constexpr int bytes = 4 * oRow + BN * 8 * 2;
+};
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p);
+template <>
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+template <>
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  return make_float4(tc::bf16_lo(v.x), tc::bf16_hi(v.x), tc::bf16_lo(v.y), tc::bf16_hi(v.y));
+}
+__device__ __forceinline__ void put2(float* p, float x, float y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); }
+__device__ __forceinline__ void put2(__nv_bfloat16* p, float x, float y) {
+  *reinterpret_cast<uint32_t*>(p) = ptx::pack_bf16(x, y);
+}
+
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(kT)
+    paged_kernel(const Work w, const Space sp, const Out out, const T* __restrict__ Q, const T* __restrict__ K,
+                 const T* __restrict__ V, int64_t qs0, int64_t qs1, int64_t qs2, int64_t ks0, int64_t ks1, int64_t ks2,
+                 int64_t vs0, int64_t vs1, int64_t vs2, float c) {
+  using L = Lay<D, R>;
+  constexpr int RT = R / 16, C2 = D / 32;  // rows, pairs of columns of a thread
+  extern __shared__ __align__(16) float sh[];
+  float *sQ = sh + L::oQ, *sK = sh + L::oK, *sV = sh + L::oV, *sP = sh + L::oP;
+  int64_t* sRow = reinterpret_cast<int64_t*>(sh + L::oRow);  // [2][BN]: offsets of the block's keys, values (-1: none)
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, p = blockIdx.x, gt = w.cut.gt;
+  ptx::grid_dependency_wait();
+  ptx::grid_dependency_launch();
+  Tail tail{0, 0, 0, 0};
+  Walk it;
+  for (bool more = it.begin(w, sp, p); more; more = it.next(w)) {
+    const Seq& s = it.s;
+    const int rows = (it.t1 - it.t0) * gt, kvh = it.vh / w.cut.per_kv;
+    const int64_t h0 = static_cast<int64_t>(it.vh) * gt;
+    __syncthreads();
+    for (int u = threadIdx.x; u < R * D / 4; u += kT) {
+      const int r = u / (D / 4), cc = u % (D / 4) * 4, t = r / gt;
+      float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < rows) q = load4(Q + s.batch * qs0 + (h0 + r - t * gt) * qs1 + static_cast<int64_t>(s.row0 + it.t0 + t) * qs2 + cc);
+      *reinterpret_cast<float4*>(sQ + r * D + cc) = make_float4(q.x * c, q.y * c, q.z * c, q.w * c);
+    }
+    int first[RT], last[RT];  // keys that the thread's rows see
+    float m[RT], l[RT], acc[RT][C2][2];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int t = it.t0 + (ty * RT + i) / gt;
+      const int64_t at = static_cast<int64_t>(s.start) + t;
+      last[i] = w.causal ? static_cast<int>(at < s.len ? at : s.len - 1) : s.len - 1;
+      const int64_t f = w.window > 0 ? at - w.window + 1 : 0;
+      first[i] = static_cast<int>(f > 0 ? f : 0);
+      m[i] = -INFINITY, l[i] = 0.f;
+#pragma unroll
+      for (int x = 0; x < C2; ++x) acc[i][x][0] = acc[i][x][1] = 0.f;
+    }
+    const int64_t at0 = static_cast<int64_t>(s.start) + it.t0, at1 = static_cast<int64_t>(s.start) + it.t1 - 1;
+    for (int k = it.k0; k < it.k1; ++k) {
+      const int64_t key0 = static_cast<int64_t>(it.j0 + k) * BN;
+      __syncthreads();  // the block before has been read
+      if (threadIdx.x < BN) {
+        const int64_t j = key0 + threadIdx.x;
+        int page = -1;
+        int e = 0;
+        if (j < s.len) {
+          e = static_cast<int>(j) / w.seqs.page;
+          page = page_at(w.seqs, it.b, e);
+        }
+        const int64_t slot = j - static_cast<int64_t>(e) * w.seqs.page;
+        sRow[threadIdx.x] = page < 0 ? -1 : page * ks0 + kvh * ks1 + slot * ks2;
+        sRow[BN + threadIdx.x] = page < 0 ? -1 : page * vs0 + kvh * vs1 + slot * vs2;
+      }
+      __syncthreads();
+      bool gap = false;
+      for (int u = threadIdx.x; u < BN * D / 4; u += kT) {
+        const int r = u / (D / 4), cc = u % (D / 4) * 4;
+        const int64_t ko = sRow[r], vo = sRow[BN + r];
+        gap = gap || ko < 0;
+        const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4*>(sK + r * L::PK + cc) = ko < 0 ? z : load4(K + ko + cc);
+        *reinterpret_cast<float4*>(sV + r * D + cc) = vo < 0 ? z : load4(V + vo + cc);
+      }
+      // some row does not see some key of the block
+      const bool part = __syncthreads_or(gap) || (w.causal && key0 + BN - 1 > at0) || (w.window > 0 && key0 <= at1 - w.window);
+      float sc[RT][4];
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) sc[i][x] = 0.f;
+#pragma unroll 8
+      for (int d = 0; d < D; d += 4) {
+        float4 kk[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) kk[x] = *reinterpret_cast<const float4*>(sK + (tx + 16 * x) * L::PK + d);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const float4 q = *reinterpret_cast<const float4*>(sQ + (ty * RT + i) * D + d);
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            sc[i][x] = fmaf(q.x, kk[x].x, fmaf(q.y, kk[x].y, fmaf(q.z, kk[x].z, fmaf(q.w, kk[x].w, sc[i][x]))));
+        }
+      }
+      float alpha[RT];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        if (part) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int64_t j = key0 + tx + 16 * x;
+            if (j < first[i] || j > last[i] || sRow[tx + 16 * x] < 0) sc[i][x] = -INFINITY;
+          }
+        }
+        float t = fmaxf(fmaxf(sc[i][0], sc[i][1]), fmaxf(sc[i][2], sc[i][3]));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+        const float mn = fmaxf(m[i], t), sub = mn == -INFINITY ? 0.f : mn;
+        alpha[i] = ptx::ex2(m[i] - sub);
+        m[i] = mn;
+        float z = 0.f;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float e = ptx::ex2(sc[i][x] - sub);
+          z += e;
+          sP[(ty * RT + i) * L::PP + tx + 16 * x] = e;
+        }
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        l[i] = fmaf(l[i], alpha[i], z);
+      }
+      __syncwarp();
+      // The block's sums, then added to the running ones: a chain of additions as long as the context would
+      // lose bits with its square root.
+      float o[RT][C2][2];
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int x = 0; x < C2; ++x) o[i][x][0] = o[i][x][1] = 0.f;
+      for (int j = 0; j < BN; j += 4) {
+        float4 e[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) e[i] = *reinterpret_cast<const float4*>(sP + (ty * RT + i) * L::PP + j);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          float2 v[C2];
+#pragma unroll
+          for (int x = 0; x < C2; ++x) v[x] = *reinterpret_cast<const float2*>(sV + (j + u) * D + tx * 2 + 32 * x);
+#pragma unroll
+          for (int i = 0; i < RT; ++i) {
+            const float f = u == 0 ? e[i].x : u == 1 ? e[i].y : u == 2 ? e[i].z : e[i].w;
+            if (part && f == 0.f) continue;  // (hidden: 0 times an infinity would be NaN)
+#pragma unroll
+            for (int x = 0; x < C2; ++x) o[i][x][0] = fmaf(f, v[x].x, o[i][x][0]), o[i][x][1] = fmaf(f, v[x].y, o[i][x][1]);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int x = 0; x < C2; ++x)
+          acc[i][x][0] = fmaf(acc[i][x][0], alpha[i], o[i][x][0]), acc[i][x][1] = fmaf(acc[i][x][1], alpha[i], o[i][x][1]);
+    }
+    const bool whole = it.whole();
+    const int slot = it.slot(p);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int r = ty * RT + i;
+      if (r >= rows) break;
+      if (!whole) {
+#pragma unroll
+        for (int x = 0; x < C2; ++x) put2(sp.o(slot, r) + tx * 2 + 32 * x, acc[i][x][0], acc[i][x][1]);
+        if (tx == 0) *sp.ml(slot, r) = make_float2(m[i], l[i]);
+        continue;
+      }
+      const int t = r / gt;
+      const int64_t h = h0 + r - t * gt, pos = s.row0 + it.t0 + t;
+      const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];  // (a row that sees no key: 0)
+      T* dst = static_cast<T*>(out.O) + s.batch * out.os[0] + h * out.os[1] + pos * out.os[2];
+#pragma unroll
+      for (int x = 0; x < C2; ++x) put2(dst + tx * 2 + 32 * x, acc[i][x][0] * inv, acc[i][x][1] * inv);
+      if (tx == 0 && out.lse != nullptr)
+        out.lse[s.batch * out.ls[0] + h * out.ls[1] + pos] =
+            l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.69314718055994531f;
+    }
+    if (!whole && it.k0 == 0) tail = Tail{it.b, it.tile, it.vh, it.parts(p)};
+  }
+  if (threadIdx.x == 0) sp.tail[p] = tail;
+}
+
+template <typename T, int D, int R>
+cudaError_t launch(const PagedArgs& a, const Work& w, const Space& sp, const Out& out, cudaStream_t st) {
+  auto kern = paged_kernel<T, D, R>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D, R>::bytes);
+  if (e != cudaSuccess) return e;
+  if ((e = plan(w, sp, st)) != cudaSuccess) return e;
+  e = launch_behind(kern, w.cut.ctas, kT, Lay<D, R>::bytes, st, w, sp, out, static_cast<const T*>(a.Q), static_cast<const T*>(a.K),
+                    static_cast<const T*>(a.V), a.qs[0], a.qs[1], a.qs[2], a.ks[0], a.ks[1], a.ks[2], a.vs[0], a.vs[1],
+                    a.vs[2], a.scale * kLog2e);
+  if (e != cudaSuccess) return e;
+  return join(w, sp, out, a.dtype, D, R, st);
+}
+
+template <typename T, int D>
+cudaError_t rows(const PagedArgs& a, const Work& w, const Space& sp, const Out& out, cudaStream_t st) {
+  return sp.rows == 16 ? launch<T, D, 16>(a, w, sp, out, st) : launch<T, D, 64>(a, w, sp, out, st);
+}
+
+// 16 rows a tile where the new tokens of a sequence fit them, else 64.
+int tile_rows(const PagedArgs& a) { return a.max_new * (a.H / a.Hkv) <= 16 ? 16 : 64; }
+
+Work work_of(const PagedArgs& a) {
+  Work w;
+  const int R = tile_rows(a), g = a.H / a.Hkv;
+  w.seqs = a.seqs, w.causal = a.causal, w.window = a.window;
+  w.cut.gt = heads_together(g, R, R == 16 ? a.max_new : 0);
+  w.cut.nv = a.H / w.cut.gt, w.cut.per_kv = g / w.cut.gt;
+  w.cut.tile = w.cut.step = R / w.cut.gt;
+  w.cut.BN = BN, w.cut.over = 1, w.cut.least = 4;
+  const int smem = R == 16 ? 4 * (BN * 2 * a.d) : 4 * (BN * 2 * a.d + 64 * a.d);
+  w.cut.ctas = 152 * (smem <= 50000 ? 3 : smem <= 100000 ? 2 : 1);
+  return w;
+}
+
+}  // namespace
+
+size_t simt_bytes(const PagedArgs& a) {
+  const Work w = work_of(a);
+  return Space::bytes(w.cut.ctas, a.seqs.B, tile_rows(a), a.d);
+}
+
+cudaError_t simt_paged(const PagedArgs& a, void* ws, cudaStream_t st) {
+  const Work w = work_of(a);
+  const Space sp = Space::at(ws, w.cut.ctas, a.seqs.B, tile_rows(a), a.d);
+  const Out out{a.O, a.lse, {a.os[0], a.os[1], a.os[2]}, {a.ls[0], a.ls[1]}};
+  if (a.dtype == ATTN_BF16) {
+    using T = __nv_bfloat16;
+    return a.d == 32 ? rows<T, 32>(a, w, sp, out, st) : a.d == 64 ? rows<T, 64>(a, w, sp, out, st) : a.d == 96 ? rows<T, 96>(a, w, sp, out, st)
+           : a.d == 128 ? rows<T, 128>(a, w, sp, out, st) : rows<T, 256>(a, w, sp, out, st);
+  }
+  return a.d == 32 ? rows<float, 32>(a, w, sp, out, st) : a.d == 64 ? rows<float, 64>(a, w, sp, out, st) : a.d == 96 ? rows<float, 96>(a, w, sp, out, st)
+         : a.d == 128 ? rows<float, 128>(a, w, sp, out, st) : rows<float, 256>(a, w, sp, out, st);
+}
+
+}  // namespace paged
+
+size_t paged_bytes(const PagedArgs& a) { return paged::simt_bytes(a); }
+cudaError_t paged_attention(const PagedArgs& a, void* ws, cudaStream_t st) { return paged::simt_paged(a, ws, st); }
+
+}  // namespace fbd

@@ -409,6 +409,116 @@ typedef struct {
 attn_status_t attn_rope(const attn_rope_desc_t* desc, const attn_rope_tensor_t* tensors, int count,
                         const int32_t* pos, const float* freq, const int32_t* axis, void* stream);
 
+/* ---------------------------------------------------------------------------------
+ * Normed heads, and a paged cache with the attention over it: what stands before and around an
+ * attention layer that is trained with normed queries and keys, and served.  The source pages have no
+ * counterpart.  d in {32, 64, 96, 128, 256}; bf16 and float32; views of any strides (d contiguous,
+ * multiples of 16 bytes); weights float32.  Integer arrays, weights and lse need only their element's
+ * alignment.  Overlaps are checked between arrays and views without gaps (ATTN_ERR_INVALID_ARG);
+ * views with gaps may lie between one another.  Every output is the same bits on every call. */
+
+/* RMS norm of each head's vector, then the rotary of attn_rope, in one pass:
+ *   r = (mean_k x_k^2 + eps)^(-1/2),  z_k = w_k x_k r,  y = z turned by its token's position.
+ * desc is attn_rope's (inverse = 0); pos, freq and axis all NULL: nothing turns.  Up to
+ * ATTN_ROPE_MAX_TENSORS tensors with the same tokens, a weight [d] each (NULL: ones).  y may be exactly x
+ * (same address and strides).  Squares, sums and r are float32 (values up to 1e18); one rounding of y. */
+typedef struct {
+  const void* x;
+  void* y;
+  const float* w;
+  int64_t heads;
+  int64_t x_stride[3], y_stride[3]; /* of (batch, head, position) in elements, as in attn_rope */
+} attn_norm_tensor_t;
+attn_status_t attn_qk_norm(const attn_rope_desc_t* desc, const attn_norm_tensor_t* tensors, int count, float eps,
+                           const int32_t* pos, const float* freq, const int32_t* axis, void* stream);
+
+/* Its gradient, from x, w and dy (r is formed again):
+ *   dz = dy turned back,  dw_k = sum over batch, heads and tokens of dz_k x_k r,
+ *   dx_k = r (w_k dz_k - x_k r^2 mean_m(w_m dz_m x_m)).
+ * dw may be NULL (not formed); it is written also when there are no tokens (zeros), and summed in a
+ * fixed order.  dx may be exactly x or exactly dy.
+ *   workspace: >= attn_qk_norm_bwd_workspace_bytes(desc, tensors, count) bytes (it reads the heads alone),
+ *   16-byte aligned, contents ignored on entry.  Calls that may run at the same time need one each. */
+typedef struct {
+  const void* x;
+  const void* dy;
+  void* dx;
+  const float* w;
+  float* dw;
+  int64_t heads;
+  int64_t x_stride[3], dy_stride[3], dx_stride[3];
+} attn_norm_grad_t;
+size_t attn_qk_norm_bwd_workspace_bytes(const attn_rope_desc_t* desc, const attn_norm_grad_t* tensors, int count);
+attn_status_t attn_qk_norm_bwd(const attn_rope_desc_t* desc, const attn_norm_grad_t* tensors, int count, float eps,
+                               const int32_t* pos, const float* freq, const int32_t* axis, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* A paged cache: K and V as views [pages, Hkv, page_size, d], and per sequence the pages that hold its
+ * keys in order: key j of sequence b is slot j % page_size of page table[b][j / page_size].
+ *   page_size: a multiple of 16, up to 2^20 (else ATTN_ERR_UNSUPPORTED); width * page_size <= 2^31 - 4096.
+ *   A table entry outside 0 .. pages - 1 is no page: nothing is written there, and the keys that
+ *   would lie there are hidden from every token (as pages given up behind a window may be).
+ * The sequences of a call: desc->B of them, lens [B] int32 (device) the keys each holds, its new
+ * tokens' among them; new token t of the n of a sequence stands at position lens[b] - n + t.
+ *   cu [B + 1] int32 (device), non-decreasing: packed tokens; the tensors are [1, heads, N, d] and sequence
+ *   b has the rows cu[b] .. cu[b + 1] - 1 (rows of no sequence are left as they were);
+ *   cu NULL: [B, heads, N, d], N new tokens for every sequence.
+ * The tables and lengths are read on the device: nothing outside the tensors is touched whatever they
+ * hold.  lens below 0 reads as 0; keys past width * page_size are not held. */
+typedef struct {
+  void* K;
+  void* V;
+  const int32_t* table; /* [B, width] */
+  int64_t pages, page_size, width;
+  int64_t k_stride[3], v_stride[3]; /* of (page, head, slot), in elements; positive */
+} attn_cache_t;
+
+/* New keys and values into the pages of a cache, the keys normed and turned on the way as attn_qk_norm
+ * does, the new tokens' queries too if given; one launch.
+ *   desc: B, H, N, d, dtype, group (Hkv = H / group heads of K and V); the rest is not used.
+ *   K, V [.., Hkv, N, d]; Q and Q_out [.., H, N, d] or both NULL (Q_out may be exactly Q).
+ *   normed = 1: the RMS norm with k_weight, q_weight [d] (NULL: ones) and eps; V is copied.
+ *   freq, axis: the rotary's tables (both NULL: nothing turns); pos NULL: the tokens' positions in their
+ *   sequences (axes = 1), else [axes, B, N] (pos_batch_stride = N) or [axes, N] (0; packed tokens).
+ *   A token whose position is outside the table or has no page is not written (its query is).  Two tokens
+ *   with the same slot: either may stay.  The cache may not overlap the new tokens. */
+typedef struct {
+  const void* K;
+  const void* V;
+  const void* Q;
+  void* Q_out;
+  int64_t k_stride[3], v_stride[3], q_stride[3], q_out_stride[3]; /* of (batch, head, position) */
+  const float* k_weight;
+  const float* q_weight;
+  const int32_t* pos;
+  const float* freq;
+  const int32_t* axis;
+  int64_t pos_batch_stride;
+  int32_t axes;
+  int32_t paired; /* ATTN_ROPE_HALF or ATTN_ROPE_NEIGHBOUR */
+  int32_t normed;
+  float eps;
+} attn_new_tokens_t;
+attn_status_t attn_cache_append(const attn_desc_t* desc, const attn_new_tokens_t* tokens, const attn_cache_t* cache,
+                                const int32_t* cu, const int32_t* lens, void* stream);
+
+/* Attention of the new tokens of each sequence (a prompt, a chunk of one, a few proposed tokens or one
+ * next token) over the keys the cache holds, their own among them:
+ *   O = softmax(s Q K^T + mask) V,  lse the natural log-sum-exp [.., H, N] float32 (NULL: not written).
+ *   desc: B, H, N, d, scale, dtype, group, causal = 1: a token at position p sees the keys j <= p, with
+ *   window W > 0 only j > p - W; causal = 0: every key.  No document bounds (ATTN_ERR_UNSUPPORTED).
+ *   Q, O: [.., H, N, d] views with strides of (batch, head, position), positive.
+ *   A token that sees no key gives O = 0 and lse = -inf.  A key that a token does not see has no part
+ *   in its result, whatever the cache holds there.
+ *   max_new: the most new tokens that a sequence has, as far as the host knows (0: not known; N where
+ *   cu is NULL).  It chooses the kernel and may change roundings, nothing else.
+ *   workspace: >= attn_paged_workspace_bytes(desc, max_new) bytes, 16-byte aligned, contents ignored on
+ *   entry.  Calls that may run at the same time need one each. */
+size_t attn_paged_workspace_bytes(const attn_desc_t* desc, int64_t max_new);
+attn_status_t attn_paged(const attn_desc_t* desc, const void* Q, const int64_t* q_stride, const attn_cache_t* cache,
+                         const int32_t* cu, const int32_t* lens, int64_t max_new, void* O, const int64_t* o_stride,
+                         float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronises `stream` and reports (then clears) the device-side status word:
  * ATTN_ERR_TIMEOUT if any kernel's bounded wait gave up since the last call,
  * ATTN_ERR_LAUNCH if the stream holds a CUDA error, else ATTN_OK. */
