@@ -15,6 +15,8 @@
 #include "diff.h"
 #include "fbd.h"
 #include "internal.h"
+#include "paged.h"
+#include "tmap.h"
 
 namespace {
 thread_local char g_last_error[256] = "";
@@ -317,7 +319,7 @@ attn_status_t attn_device_status(void* stream) {
   const uint32_t flags = fbd::tc_fwd_take_error() | fbd::tc_bwd_take_error() | fbd::tc_bwd_wide_take_error() | fbd::tc_bwd_fused_take_error() |
                          fbd::tc_bob_take_error() | fbd::tc_bob128_take_error() | fbd::tc32_take_error() |
                          fbd::selftest_take_error() | fbd::tc_diff_fwd_take_error() |
-                         fbd::tc_diff_bwd_take_error();
+                         fbd::tc_diff_bwd_take_error() | fbd::tc_paged_take_error();
   if (flags != 0) return fail(ATTN_ERR_TIMEOUT, "a device-side bounded wait gave up%s");
   return ATTN_OK;
 }
@@ -381,6 +383,20 @@ bool make_tmap_bf16(void* map_out, const void* base, int64_t N, int64_t d, int64
                   dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+bool make_tmap_view(void* map_out, const void* base, int rank, const int64_t* dims, const int64_t* strides, const int* box) {
+  EncodeFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t n[5], s[4];
+  cuuint32_t b[5], estr[5];
+  for (int k = 0; k < rank; ++k) {
+    n[k] = static_cast<cuuint64_t>(dims[k]), b[k] = static_cast<cuuint32_t>(box[k]), estr[k] = 1u;
+    if (k > 0) s[k - 1] = strides[k - 1] > 0 ? static_cast<cuuint64_t>(strides[k - 1]) * 2 : static_cast<cuuint64_t>(dims[0]) * 2;
+  }
+  return fn(static_cast<CUtensorMap*>(map_out), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank),
+            const_cast<void*>(base), n, s, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool make_tmap_f32_rows(void* map_out, const void* base, int64_t N, int64_t BH, int box_rows) {

@@ -60,6 +60,7 @@ __global__ void __launch_bounds__(kT) plan_kernel(const Work w, const Space sp) 
   if (threadIdx.x == 0) *sp.head = Head{total, stretch};
   for (int p = warp; p < w.cut.ctas; p += kT / 32) {
     const int64_t x = stretch * p;
+    if (lane == 0) sp.tail[p] = Tail{0, 0, 0, 0};
     if (x >= total) {
       if (lane == 0) sp.start[p] = Start{0, -1, 0, 0, 0};
       continue;
@@ -184,4 +185,14 @@ cudaError_t join(const Work& w, const Space& sp, const Out& out, int dtype, int 
 }
 
 }  // namespace paged
+
+namespace {
+bool on_tensor_cores(const PagedArgs& a) { return a.dtype == ATTN_BF16 && a.d <= 128; }
+}  // namespace
+
+size_t paged_bytes(const PagedArgs& a) { return on_tensor_cores(a) ? paged::tc_bytes(a) : paged::simt_bytes(a); }
+cudaError_t paged_attention(const PagedArgs& a, void* ws, cudaStream_t st) {
+  return on_tensor_cores(a) ? paged::tc_paged(a, ws, st) : paged::simt_paged(a, ws, st);
+}
+
 }  // namespace fbd

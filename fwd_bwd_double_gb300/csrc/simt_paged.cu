@@ -50,7 +50,6 @@ __global__ void __launch_bounds__(kT)
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, p = blockIdx.x, gt = w.cut.gt;
   ptx::grid_dependency_wait();
   ptx::grid_dependency_launch();
-  Tail tail{0, 0, 0, 0};
   Walk it;
   for (bool more = it.begin(w, sp, p); more; more = it.next(w)) {
     const Seq& s = it.s;
@@ -203,9 +202,8 @@ __global__ void __launch_bounds__(kT)
         out.lse[s.batch * out.ls[0] + h * out.ls[1] + pos] =
             l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.69314718055994531f;
     }
-    if (!whole && it.k0 == 0) tail = Tail{it.b, it.tile, it.vh, it.parts(p)};
+    if (threadIdx.x == 0 && !whole && it.k0 == 0) sp.tail[p] = Tail{it.b, it.tile, it.vh, it.parts(p)};
   }
-  if (threadIdx.x == 0) sp.tail[p] = tail;
 }
 
 template <typename T, int D, int R>
@@ -263,8 +261,4 @@ cudaError_t simt_paged(const PagedArgs& a, void* ws, cudaStream_t st) {
 }
 
 }  // namespace paged
-
-size_t paged_bytes(const PagedArgs& a) { return paged::simt_bytes(a); }
-cudaError_t paged_attention(const PagedArgs& a, void* ws, cudaStream_t st) { return paged::simt_paged(a, ws, st); }
-
 }  // namespace fbd

@@ -1,0 +1,589 @@
+// Attention of new tokens over a paged cache, bf16, on the tensor cores.
+//
+//   O = softmax(s Q K^T + mask) V over each sequence's pages
+// A tile's 128 rows are tokens times the query heads that share a key/value head, so that K and V are
+// loaded once for all of them.  Two tiles at once, per block of 128 keys and tile
+//   S_m = Q_m K^T            A and B from shared memory, accumulator in TMEM
+//   P_m = 2^(S_m c - M_m c)  online softmax, one row per thread, bf16 over S_m's columns
+//   O_m += P_m V             A = P_m from TMEM, B = V (MN-major)
+// The tiles take turns: while four warps exponentiate S_0, the tensor cores run P_1 V and the next S_1,
+// and the other way round.  Items of more tokens than a tile holds fill two tiles that see the same
+// blocks; of smaller ones both "tiles" hold the same rows and take the blocks in turn, and the two
+// softmaxes are joined at the end.
+//
+// Pages: a block is fetched in boxes of as many keys as divide the page's (16 .. 128), one lane of the
+// loading warp per box, which looks its page up; keys that the sequence does not hold, and entries
+// that are no page, are coordinates outside the tensor, which read as zeros without traffic.  Keys hidden
+// from a row are masked in its scores.  Their values are multiplied by weights of 0, which would make
+// an infinity or NaN there a NaN: in blocks that some row does not see whole, two warps make such
+// elements 0 before the product (and rows behind the last key, which may hold anything), and the
+// rows that do see them add them at the end.
+//
+// CTAs take the stretches of paged.cuh.  The reference maximum M_m moves as in the differential forward
+// (tc_diff_fwd.cu): when the new largest P would be above a quarter of the row's sum so far, or above 2^8.
+#include <cuda_bf16.h>
+
+#include "handover.h"
+#include "paged_launch.h"
+#include "tmap.h"
+
+namespace fbd {
+namespace paged {
+namespace {
+
+__device__ unsigned int g_err = 0;
+
+constexpr int BM = 128, BN = 128;
+// Warps 0-3: tile 0, 4-7: tile 1, 8: TMA, 9: MMA, 10, 11: values that a row must not see.  384 threads
+// launched with 168 registers; the softmax warps (a row of 128 scores each thread) take 208, the third
+// warpgroup's keep 80: 256 * 208 + 128 * 80 <= 384 * 168.
+constexpr int kThreads = 384;
+constexpr int kRegs = 208, kRegsOther = 80;
+constexpr float kSlack = 256.f;  // the largest P
+constexpr float kShare = .25f;   // ... and its share of the row's sum so far, where it is above 1
+
+template <int D>
+struct Lay {
+  static constexpr int kTile = BM * D * 2;       // Q tile, and a K or V entry of the ring
+  static constexpr int NS = D == 64 ? 8 : 5;
+  static constexpr int oRing = 2 * kTile;
+  static constexpr int oStat = oRing + NS * kTile;  // [2][128] (max, sum) of the second half of an item's blocks
+  static constexpr int oBar = oStat + 2 * BM * 8;
+  static constexpr int bytes = oBar + 512;
+  static constexpr uint32_t cS = 0, cO = 2 * BN;  // S_m at cS + m BN, O_m at cO + m D
+};
+static_assert(Lay<128>::bytes <= 232448 && Lay<64>::bytes <= 232448, "shared memory");
+
+// What the blocks of an item hide from some row.
+struct Hide {
+  int last, first;  // the last key that every row sees, the first one
+  __device__ __forceinline__ Hide(const Work& w, const Walk& it) {
+    const int64_t p0 = static_cast<int64_t>(it.s.start) + it.t0, p1 = static_cast<int64_t>(it.s.start) + it.t1 - 1;
+    last = w.causal ? static_cast<int>(min(p0, static_cast<int64_t>(it.s.len) - 1)) : it.s.len - 1;
+    const int64_t f = w.window > 0 ? p1 - w.window + 1 : 0;
+    first = static_cast<int>(max(f, static_cast<int64_t>(0)));
+  }
+  __device__ __forceinline__ bool in(int kb) const { return kb * BN + BN - 1 > last || kb * BN < first; }
+};
+
+// The ring's entries of an item: two tiles over the same blocks: K_0 V_0 K_1 V_1 ...; one tile whose blocks
+// go to both in turn: K_0 K_1 V_0 K_2 V_1 K_3 ...; 2 n in all.
+struct Order {
+  int base, n;
+  bool pair;  // both tiles see the same blocks
+  __device__ __forceinline__ int count(int m) const { return pair ? n : (n + 1 - m) / 2; }  // blocks of tile m
+  __device__ __forceinline__ int block(int m, int j) const { return pair ? j : 2 * j + m; }
+  __device__ __forceinline__ int V(int i) const {
+    return pair ? base + 2 * i + 1 : base + min(n, 2) + i + min(i, max(n - 2, 0));
+  }
+  __device__ __forceinline__ int K(int i) const { return pair ? base + 2 * i : i < 2 ? base + i : V(i - 2) + 1; }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                 const __grid_constant__ CUtensorMap tmV, const Work w, const Space sp, const Out out,
+                 const __nv_bfloat16* __restrict__ Vg, int64_t vs0, int64_t vs1, int64_t vs2, int d, int box,
+                 float scale, float c) {
+  using L = Lay<D>;
+  constexpr int NS = L::NS, SL = D / 64;  // slabs of 64 columns
+  extern __shared__ __align__(1024) uint8_t sm[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::oBar);
+  uint64_t* q_full = bars;
+  uint64_t* q_empty = bars + 1;      // the item's last products with Q done
+  uint64_t* s_full = bars + 2;       // [2] S_m in TMEM (and the previous P_m V done)
+  uint64_t* p_half = s_full + 2;     // [2] P_m of the first 64 keys in TMEM, O_m rescaled
+  uint64_t* p_ready = p_half + 2;    // [2] of all keys
+  uint64_t* o_full = p_ready + 2;
+  uint64_t* o_empty = o_full + 1;    // O_0, O_1 read by the epilogue
+  uint64_t* settled = o_empty + 1;   // after a wait that gave up: the products in flight done
+  uint64_t* full = settled + 1;      // [NS]
+  uint64_t* empty = full + NS;       // [NS]
+  uint64_t* v_ok = empty + NS;       // [NS] values that some row does not see are finite
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_ok + NS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* started = abort_flag + 1;                                 // Q loads, ring entries (the TMA warp's)
+  volatile uint32_t* hidden = reinterpret_cast<volatile uint32_t*>(started + 2);  // [16] of K entries: 16-key runs without a page
+  volatile int* spoilt = reinterpret_cast<volatile int*>(hidden + 16);    // [8] of items: n + 1 where values were made 0
+  float2* stat = reinterpret_cast<float2*>(sm + L::oStat);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, p = blockIdx.x;
+  const int gt = w.cut.gt, tq = w.cut.tile;
+  if (threadIdx.x == 8 * 32) {
+    ptx::prefetch_tmap(&tmQ);
+    ptx::prefetch_tmap(&tmK);
+    ptx::prefetch_tmap(&tmV);
+    ptx::mbar_init(q_full, 1);
+    ptx::mbar_init(q_empty, 1);
+    for (int m = 0; m < 2; ++m) {
+      ptx::mbar_init(&s_full[m], 2);  // the products' end and the warp that issued them
+      ptx::mbar_init(&p_half[m], 128);
+      ptx::mbar_init(&p_ready[m], 128);
+    }
+    ptx::mbar_init(o_full, 2);
+    ptx::mbar_init(o_empty, 256);
+    ptx::mbar_init(settled, 1);
+    for (int s = 0; s < NS; ++s) {
+      ptx::mbar_init(&full[s], 1);
+      ptx::mbar_init(&empty[s], 1);
+      ptx::mbar_init(&v_ok[s], 2);
+    }
+    for (int s = 0; s < 8; ++s) spoilt[s] = 0;
+    started[0] = started[1] = 0;
+    *abort_flag = (ptx::smem_u32(sm) & 1023u) ? 1 : 0;  // the swizzled tiles need 1024-byte alignment
+    if (*abort_flag) atomicOr(&g_err, FBD_ERR_TIMEOUT);
+    ptx::fence_mbar_init();
+  }
+  if (warp == 9) {
+    ptx::tmem_alloc(tmem_slot, 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const ptx::BoundedWait wait{abort_flag, &g_err};
+  const bool ok = *abort_flag == 0;
+  ptx::grid_dependency_wait();  // the plan
+  ptx::grid_dependency_launch();
+  Walk it;
+  bool more = it.begin(w, sp, p) && ok;
+  auto order = [&](int base) { return Order{base, it.k1 - it.k0, it.weight == 2}; };
+
+  if (warp >= 8) ptx::setmaxnreg_dec<kRegsOther>();
+  if (warp == 8) {
+    // ------------------------------------------------------------ TMA producer
+    int E = 0, n = 0, nq = 0;
+    bool go = true;
+    const int per = BN / box;             // boxes of an entry along its keys
+    const int c0 = lane % SL, g0 = lane / SL;  // this lane's box
+    // Entry e: block kb of K or V.
+    auto load = [&](const CUtensorMap* map, bool key, int kb, int kvh) {
+      const int s = E % NS;
+      const int k0 = kb * BN + g0 * box;
+      const int en = k0 / w.seqs.page;
+      const int pg = g0 < per && k0 < it.s.len ? page_at(w.seqs, it.b, en) : -1;
+      if (E >= NS) go = wait(&empty[s], ((E / NS) - 1) & 1) && go;
+      if (!__all_sync(0xffffffffu, go)) {
+        go = false;
+        return;
+      }
+      if (key) {
+        const uint32_t run = g0 < per && pg < 0 && k0 < it.s.len ? ((1u << (box / 16)) - 1u) << (g0 * (box / 16)) : 0u;
+        const uint32_t all = __reduce_or_sync(0xffffffffu, run);
+        if (lane == 0) hidden[E & 15] = all;
+      }
+      if (lane == 0) ptx::mbar_expect_tx(&full[s], L::kTile);
+      __syncwarp();
+      if (g0 < per)
+        ptx::tma_load_4d(sm + L::oRing + s * L::kTile + c0 * BN * 128 + g0 * box * 128, map, &full[s], c0 * 64,
+                    pg < 0 ? 0 : k0 - en * w.seqs.page, kvh, pg);
+      ++E;
+    };
+    for (; more && go; more = it.next(w), ++n) {
+      const int tiles = it.weight, kvh = it.vh / w.cut.per_kv;
+      const Order o = order(0);
+      if (n > 0) go = wait(q_empty, (n - 1) & 1) && go;
+      if (!__all_sync(0xffffffffu, go)) break;
+      ++nq;
+      if (lane == 0) {
+        ptx::mbar_expect_tx(q_full, tiles * SL * gt * tq * 128);
+        for (int m = 0; m < tiles; ++m)
+          for (int u = 0; u < SL; ++u)
+            ptx::tma_load_5d(sm + m * L::kTile + u * BM * 128, &tmQ, q_full, u * 64, 0, it.s.row0 + it.t0 + m * tq, it.vh, it.s.batch);
+      }
+      const int b0 = it.j0 + it.k0;
+      if (o.pair) {
+        for (int j = 0; j < o.n && go; ++j) {
+          load(&tmK, true, b0 + j, kvh);
+          if (go) load(&tmV, false, b0 + j, kvh);
+        }
+      } else {
+        load(&tmK, true, b0, kvh);
+        if (go && o.n > 1) load(&tmK, true, b0 + 1, kvh);
+        for (int j = 0; j < o.n && go; ++j) {
+          load(&tmV, false, b0 + j, kvh);
+          if (go && j + 2 < o.n) load(&tmK, true, b0 + j + 2, kvh);
+        }
+      }
+    }
+    if (lane == 0) started[0] = nq, started[1] = E;
+  } else if (warp == 9) {
+    // ------------------------------------------------------------- MMA issuer
+    constexpr uint32_t idS = ptx::idesc_bf16(BM, BN, 0, 0);
+    constexpr uint32_t idO = ptx::idesc_bf16(BM, D, 0, 1);
+    const uint64_t dQ = tc::kmajor_desc(ptx::smem_u32(sm), BM, 0);
+    const uint64_t dK = tc::kmajor_desc(ptx::smem_u32(sm + L::oRing), BN, 0);
+    const uint64_t dV = tc::mnmajor_desc(ptx::smem_u32(sm + L::oRing), BN, 0);
+    int base = 0, n = 0, T0 = 0, T1 = 0, masked = 0;
+    for (; more; more = it.next(w), ++n) {
+      const Order o = order(base);
+      const Hide hide(w, it);
+      const int b0 = it.j0 + it.k0, n0 = o.count(0), n1 = o.count(1);
+      int left = n0 + n1;  // products with Q still to issue
+      auto issue_s = [&](int m, int j) {
+        const int e = o.K(o.block(m, j)), s = e % NS;
+        if (!o.pair || m == 0) wait(&full[s], (e / NS) & 1);
+        ptx::tc_fence_after();
+        const uint32_t so = static_cast<uint32_t>(s * L::kTile), qo = o.pair && m == 1 ? L::kTile : 0;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          ptx::mma_ss_e(tmem + L::cS + m * BN, tc::desc_add(dQ, qo + tc::kmajor_off(BM, k)),
+                        tc::desc_add(dK, so + tc::kmajor_off(BN, k)), idS, k > 0 ? 1u : 0u);
+        ptx::mma_commit_e(&s_full[m]);
+        if (lane == 0) ptx::mbar_arrive(&s_full[m]);
+        if (!o.pair || m == 1) ptx::mma_commit_e(&empty[s]);
+        if (--left == 0) ptx::mma_commit_e(q_empty);
+      };
+      wait(q_full, n & 1);
+      issue_s(0, 0);
+      if (n1 > 0) issue_s(1, 0);
+      for (int j = 0; j < n0; ++j) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          if (j >= (m == 0 ? n0 : n1)) continue;
+          const int T = m == 0 ? T0++ : T1++;
+          const int i = o.block(m, j), e = o.V(i), s = e % NS;
+          if (!o.pair || m == 0) {
+            if (hide.in(b0 + i)) {
+              wait(&v_ok[masked % NS], (masked / NS) & 1);
+              ++masked;
+            } else {
+              wait(&full[s], (e / NS) & 1);
+            }
+          }
+          wait(&p_half[m], T & 1);
+          if (j == 0 && m == 0 && n > 0) wait(o_empty, (n - 1) & 1);
+          ptx::tc_fence_after();
+          const uint32_t so = static_cast<uint32_t>(s * L::kTile);
+#pragma unroll
+          for (int k = 0; k < BN / 16; ++k) {
+            if (k == BN / 32) {
+              wait(&p_ready[m], T & 1);
+              ptx::tc_fence_after();
+            }
+            ptx::mma_ts_e(tmem + L::cO + m * D, tmem + L::cS + m * BN + k * 8, tc::desc_add(dV, so + k * 2048), idO,
+                          (j > 0 || k > 0) ? 1u : 0u);
+          }
+          if (!o.pair || m == 1) ptx::mma_commit_e(&empty[s]);
+          if (j + 1 < (m == 0 ? n0 : n1)) issue_s(m, j + 1);
+        }
+      }
+      ptx::mma_commit_e(o_full);
+      if (lane == 0) ptx::mbar_arrive(o_full);
+      base += 2 * o.n;
+    }
+  } else if (warp >= 10) {
+    // ------------------------- values that some row does not see: made 0 where they are not finite
+    int base = 0, n = 0, masked = 0, seen = 0;
+    for (; more; more = it.next(w), ++n) {
+      const Order o = order(base);
+      const Hide hide(w, it);
+      const int b0 = it.j0 + it.k0;
+      for (int i = 0; i < o.n; ++i) {
+        const int e = o.V(i), s = e % NS;
+        // every entry up to this one in turn: a barrier two phases back would look complete
+        for (; seen <= e; ++seen) wait(&full[seen % NS], (seen / NS) & 1);
+        if (!hide.in(b0 + i)) continue;
+        uint8_t* V = sm + L::oRing + s * L::kTile;
+        const int held = min(max(it.s.len - (b0 + i) * BN, 0), BN);  // keys behind them may hold anything
+        bool some = false;
+#pragma unroll
+        for (int r = threadIdx.x - 320; r < BN; r += 64) {
+          for (int u = 0; u < SL; ++u)
+#pragma unroll
+            for (int ch = 0; ch < 8; ++ch) {
+              uint4* at = reinterpret_cast<uint4*>(V + u * BN * 128 + tc::sw128(r, ch));
+              if (r >= held) {
+                *at = make_uint4(0, 0, 0, 0);
+                continue;
+              }
+              const uint4 x = *at;
+              uint32_t y[4] = {x.x, x.y, x.z, x.w};
+              bool bad = false;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if ((y[k] & 0x7f80u) == 0x7f80u) y[k] &= 0xffff0000u, bad = true;
+                if ((y[k] & 0x7f800000u) == 0x7f800000u) y[k] &= 0x0000ffffu, bad = true;
+              }
+              if (bad) *at = make_uint4(y[0], y[1], y[2], y[3]), some = true;
+            }
+        }
+        if (some) spoilt[n & 7] = n + 1;
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&v_ok[masked % NS]);
+        ++masked;
+      }
+      base += 2 * o.n;
+    }
+  } else {
+    ptx::setmaxnreg_inc<kRegs>();
+    // --------------------------- softmax of tile m: thread r owns row r
+    const int m = warp >> 2;
+    const int r = threadIdx.x & 127;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + L::cS + m * BN + lane_off, tO = tmem + L::cO + lane_off;
+    const uint64_t c2 = tc::pk2f(c, c);
+    const int rt = r / gt, rh = r - rt * gt;  // this row's token of the tile, and its head
+    int T = 0, base = 0, n = 0, shared = 0;
+    for (; more; more = it.next(w), ++n) {
+      const Order o = order(base);
+      const int nb = o.count(m), b0 = it.j0 + it.k0;
+      const int tok = it.t0 + (o.pair ? m * tq : 0) + rt;
+      const bool live = rt < tq && tok < it.t1;
+      // the keys that this row sees
+      const int64_t at = static_cast<int64_t>(it.s.start) + tok;
+      const int last = w.causal ? static_cast<int>(max(min(at, static_cast<int64_t>(it.s.len) - 1), static_cast<int64_t>(-1))) : it.s.len - 1;
+      const int64_t f0 = w.window > 0 ? at - w.window + 1 : 0;
+      const int first = static_cast<int>(min(max(f0, static_cast<int64_t>(0)), static_cast<int64_t>(0x7fffffff)));
+      // bounds grow with the row: the warp's first row has the first last key, its last row the last first one
+      const int last0 = __shfl_sync(0xffffffffu, last, 0), first31 = __shfl_sync(0xffffffffu, first, 31);
+      float mref = -INFINITY, l = 0.f;
+      for (int j = 0; j < nb; ++j, ++T) {
+        const int i = o.block(m, j), key0 = (b0 + i) * BN;
+        wait(&s_full[m], T & 1);
+        ptx::tc_fence_after();
+        uint32_t v[4][32];
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) ptx::tmem_ld32(tS + ch * 32, v[ch]);
+        const uint32_t hid = hidden[o.K(i) & 15];
+        ptx::tmem_wait_ld();
+        if (key0 + BN - 1 > last0 || key0 < first31 || hid != 0) {
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch)
+            if (key0 + ch * 32 + 31 > last0 || key0 + ch * 32 < first31 || hid != 0) {
+              uint32_t see = tc::bits_between(first - key0 - ch * 32, last - key0 - ch * 32);
+              if (hid & (1u << (2 * ch))) see &= 0xffff0000u;
+              if (hid & (2u << (2 * ch))) see &= 0x0000ffffu;
+#pragma unroll
+              for (int t = 0; t < 32; ++t)
+                if (!(see & (1u << t))) v[ch][t] = __float_as_uint(-INFINITY);
+            }
+        }
+        float mx[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) mx[u] = -INFINITY;
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch)
+#pragma unroll
+          for (int t = 0; t < 32; t += 16)
+#pragma unroll
+            for (int u = 0; u < 8; ++u) mx[u] = fmaxf(mx[u], fmaxf(tc::f(v[ch][t + u]), tc::f(v[ch][t + 8 + u])));
+#pragma unroll
+        for (int u = 1; u < 8; ++u) mx[0] = fmaxf(mx[0], mx[u]);
+        // (always at the first visible key: mref = -inf)
+        const bool moved = ptx::ex2((mx[0] - mref) * c) > fminf(fmaxf(kShare * l, 1.f), kSlack);
+        const float mnew = moved ? mx[0] : mref;
+        const float alpha = moved ? ptx::ex2((mref - mnew) * c) : 1.f;
+        if (j > 0 && __any_sync(0xffffffffu, moved)) {
+          const uint64_t a2 = tc::pk2f(alpha, alpha);
+#pragma unroll 1
+          for (int x0 = 0; x0 < D; x0 += 16) {  // 16 columns at a time: the scores hold 128 registers
+            uint32_t q[16];
+            ptx::tmem_ld16(tO + m * D + x0, q);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int t = 0; t < 16; t += 2) {
+              const float2 x = tc::unpk2(tc::mul2(tc::pk2(q[t], q[t + 1]), a2));
+              q[t] = __float_as_uint(x.x);
+              q[t + 1] = __float_as_uint(x.y);
+            }
+            ptx::tmem_st16(tO + m * D + x0, q);
+          }
+        }
+        l *= alpha;
+        mref = mnew;
+        // a row that has seen no key yet subtracts 0, not -inf: every term is 2^-inf = 0
+        const float nm = mref == -INFINITY ? 0.f : -mref * c;
+        const uint64_t nm2 = tc::pk2f(nm, nm);
+        uint64_t rs[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int t = 0; t < 32; t += 2) {
+            const float2 arg = tc::unpk2(tc::fma2(tc::pk2(v[ch][t], v[ch][t + 1]), c2, nm2));
+            const float p0 = ptx::ex2(arg.x), p1 = ptx::ex2(arg.y);
+            rs[(t >> 1) & 3] = tc::add2(rs[(t >> 1) & 3], tc::pk2f(p0, p1));
+            pk[t >> 1] = ptx::pack_bf16(p0, p1);
+          }
+          ptx::tmem_st16(tS + ch * 16, pk);
+          if (ch & 1) {
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(ch == 1 ? &p_half[m] : &p_ready[m]);
+          }
+        }
+        const float2 x = tc::unpk2(tc::add2(tc::add2(rs[0], rs[1]), tc::add2(rs[2], rs[3])));
+        l += x.x + x.y;
+      }
+      // ------------------------------------------------------------------ epilogue
+      float a0 = 1.f, a1 = 0.f;  // weights of this tile's sums and of the other's
+      if (!o.pair) {
+        float2* mine = stat + (shared & 1) * BM + r;
+        if (m == 1) *mine = make_float2(mref, l);
+        tc::named_sync(1, 256);
+        ++shared;
+        if (m == 0) {
+          const float2 z = *mine;
+          const float top = fmaxf(mref, z.x), sub = top == -INFINITY ? 0.f : top * c;
+          a0 = mref == -INFINITY ? 0.f : ptx::ex2(fmaf(mref, c, -sub)), a1 = z.x == -INFINITY ? 0.f : ptx::ex2(fmaf(z.x, c, -sub));
+          l = l * a0 + z.y * a1, mref = top;
+        }
+      }
+      wait(o_full, n & 1);
+      ptx::tc_fence_after();
+      if (o.pair || m == 0) {
+        const bool whole = it.whole(), both = !o.pair && o.count(1) > 0;
+        const int slot = it.slot(p);
+        const int srow = (o.pair ? m * BM : 0) + r;
+        const int64_t h = static_cast<int64_t>(it.vh) * gt + rh, pos = it.s.row0 + tok;
+        const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;  // (a row that sees no key: 0)
+        a0 *= inv, a1 *= inv;
+        const bool bad = spoilt[n & 7] == n + 1;
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(out.O) + it.s.batch * out.os[0] + h * out.os[1] + pos * out.os[2];
+#pragma unroll 1
+        for (int ch = 0; ch < D / 32; ++ch) {
+          uint32_t a[32], b[32];
+          ptx::tmem_ld32(tO + (o.pair ? m * D : 0) + ch * 32, a);
+          if (both) ptx::tmem_ld32(tO + D + ch * 32, b);
+          ptx::tmem_wait_ld();
+          if (ch == D / 32 - 1) {
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(o_empty);
+          }
+#pragma unroll
+          for (int t = 0; t < 32; ++t) {
+            float x = tc::f(a[t]) * a0;
+            if (both) x = fmaf(tc::f(b[t]), a1, x);
+            if (l == 0.f) x = 0.f;
+            a[t] = __float_as_uint(x);
+          }
+          if (!live || ch * 32 >= d) continue;
+          if (bad) {
+            // The values made 0 that this row does see (one by one from the cache).
+            const Hide hide(w, it);
+            const int kvh = it.vh / w.cut.per_kv;
+            for (int i = 0; i < o.n; ++i) {
+              if (!hide.in(b0 + i)) continue;
+              for (int k = max((b0 + i) * BN, first); k <= min((b0 + i) * BN + BN - 1, last); ++k) {
+                const int pg = page_at(w.seqs, it.b, k / w.seqs.page);
+                if (pg < 0) continue;
+                const __nv_bfloat16* src = Vg + pg * vs0 + kvh * vs1 + static_cast<int64_t>(k % w.seqs.page) * vs2 + ch * 32;
+#pragma unroll
+                for (int t = 0; t < 32; ++t) {
+                  const float x = __bfloat162float(src[t]);
+                  if (!isfinite(x)) a[t] = __float_as_uint(tc::f(a[t]) + x);
+                }
+              }
+            }
+          }
+          if (whole) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              uint32_t pk[4];
+#pragma unroll
+              for (int t = 0; t < 4; ++t) pk[t] = ptx::pack_bf16(tc::f(a[u * 8 + 2 * t]), tc::f(a[u * 8 + 2 * t + 1]));
+              *reinterpret_cast<uint4*>(dst + ch * 32 + u * 8) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            }
+          } else {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              *reinterpret_cast<uint4*>(sp.o(slot, srow) + ch * 32 + u * 4) =
+                  make_uint4(a[u * 4], a[u * 4 + 1], a[u * 4 + 2], a[u * 4 + 3]);
+          }
+        }
+        if (live) {
+          if (!whole)
+            *sp.ml(slot, srow) = make_float2(mref == -INFINITY ? mref : mref * c, l);
+          else if (out.lse != nullptr)
+            out.lse[it.s.batch * out.ls[0] + h * out.ls[1] + pos] = l == 0.f ? -INFINITY : fmaf(mref, scale, logf(l));
+        }
+      } else {
+        ptx::mbar_arrive(o_empty);
+      }
+      base += 2 * o.n;
+      if (threadIdx.x == 0 && !it.whole() && it.k0 == 0) sp.tail[p] = Tail{it.b, it.tile, it.vh, it.parts(p)};
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  // A wait has given up: loads and products may still be on their way into this CTA's shared memory and
+  // TMEM, which others get when it ends.
+  if (*abort_flag != 0) {
+    if (threadIdx.x == 8 * 32) {
+      const int nq = started[0], E = started[1];
+      if (nq > 0) ptx::settle(q_full, (nq - 1) & 1);
+      for (int s = 0; s < NS && s < E; ++s) ptx::settle(&full[s], handover::last_phase(E, NS, s));
+    }
+    if (warp == 9) {
+      ptx::mma_commit_e(settled);
+      ptx::settle(settled, 0);
+    }
+  }
+  if (warp == 9) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t launch(const PagedArgs& a, const Work& w, const Space& sp, const Out& out, cudaStream_t st) {
+  alignas(64) CUtensorMap mq, mk, mv;
+  const Cut& k = w.cut;
+  int box = BN;  // keys of a box: as many as divide a page's
+  while (a.seqs.page % box != 0) box /= 2;
+  const bool none = a.seqs.pages == 0;  // no key anywhere: a tensor that is never read
+  const int64_t q_dims[5] = {a.d, k.gt, a.seqs.N, k.nv, a.seqs.cu != nullptr ? 1 : a.seqs.B};
+  const int64_t q_str[4] = {a.qs[1], a.qs[2], a.qs[1] * k.gt, a.qs[0]};
+  const int q_box[5] = {64, k.gt, k.tile, 1, 1};
+  const int64_t kv_dims[4] = {a.d, a.seqs.page, a.Hkv, none ? 1 : a.seqs.pages};
+  const int64_t k_str[3] = {a.ks[2], a.ks[1], a.ks[0]}, v_str[3] = {a.vs[2], a.vs[1], a.vs[0]};
+  const int kv_box[4] = {64, box, 1, 1};
+  if (!make_tmap_view(&mq, a.Q, 5, q_dims, q_str, q_box) || !make_tmap_view(&mk, none ? a.Q : a.K, 4, kv_dims, k_str, kv_box) ||
+      !make_tmap_view(&mv, none ? a.Q : a.V, 4, kv_dims, v_str, kv_box))
+    return cudaErrorInvalidValue;
+  auto kern = paged_kernel<D>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::bytes);
+  if (e != cudaSuccess) return e;
+  if ((e = plan(w, sp, st)) != cudaSuccess) return e;
+  e = launch_behind(kern, k.ctas, kThreads, Lay<D>::bytes, st, mq, mk, mv, w, sp, out, static_cast<const __nv_bfloat16*>(a.V), a.vs[0], a.vs[1], a.vs[2], a.d, box, a.scale, a.scale * kLog2e);
+  if (e != cudaSuccess) return e;
+  return join(w, sp, out, a.dtype, a.d, BM, st);
+}
+
+Work work_of(const PagedArgs& a) {
+  Work w;
+  const int g = a.H / a.Hkv;
+  w.seqs = a.seqs, w.causal = a.causal, w.window = a.window;
+  w.cut.gt = heads_together(g, BM, a.max_new);
+  w.cut.nv = a.H / w.cut.gt, w.cut.per_kv = g / w.cut.gt;
+  w.cut.tile = BM / w.cut.gt, w.cut.step = 2 * w.cut.tile;
+  w.cut.BN = BN, w.cut.over = 2, w.cut.least = 8, w.cut.ctas = 152;
+  return w;
+}
+
+}  // namespace
+
+size_t tc_bytes(const PagedArgs& a) { return Space::bytes(152, a.seqs.B, 2 * BM, a.d <= 64 ? 64 : 128); }
+
+cudaError_t tc_paged(const PagedArgs& a, void* ws, cudaStream_t st) {
+  const Work w = work_of(a);
+  const Space sp = Space::at(ws, w.cut.ctas, a.seqs.B, 2 * BM, a.d <= 64 ? 64 : 128);
+  const Out out{a.O, a.lse, {a.os[0], a.os[1], a.os[2]}, {a.ls[0], a.ls[1]}};
+  // d = 32 runs the kernel of 64 columns and d = 96 that of 128: TMA fills the columns past d with zeros.
+  return a.d <= 64 ? launch<64>(a, w, sp, out, st) : launch<128>(a, w, sp, out, st);
+}
+
+}  // namespace paged
+
+uint32_t tc_paged_take_error() {
+  uint32_t v = 0, z = 0;
+  if (cudaMemcpyFromSymbol(&v, paged::g_err, sizeof(v)) != cudaSuccess) return 0;
+  if (v) cudaMemcpyToSymbol(paged::g_err, &z, sizeof(z));
+  return v;
+}
+
+}  // namespace fbd
