@@ -49,35 +49,58 @@ struct Lay {
   static constexpr int oRing = 2 * kTile;
   static constexpr int oStat = oRing + NS * kTile;  // [2][128] (max, sum) of the second half of an item's blocks
   static constexpr int oBar = oStat + 2 * BM * 8;
-  static constexpr int bytes = oBar + 512;
+  static constexpr int oItem = oBar + 512;
+  static constexpr int bytes = oItem + 8 * 64;
   static constexpr uint32_t cS = 0, cO = 2 * BN;  // S_m at cS + m BN, O_m at cO + m D
 };
 static_assert(Lay<128>::bytes <= 232448 && Lay<64>::bytes <= 232448, "shared memory");
 
-// What the blocks of an item hide from some row.
-struct Hide {
+// An item as the loading warp gives it to the others, through a ring in shared memory.
+struct Item {
+  int n;            // blocks b0 .. b0 + n - 1; 0: there are no more items
+  int b0;
+  int pair;         // two tiles see the same blocks; else both hold one tile's rows and take the blocks in turn
+  int t0, t1;       // its tokens
+  int start, len;   // of its sequence (paged.h)
   int last, first;  // the last key that every row sees, the first one
-  __device__ __forceinline__ Hide(const Work& w, const Walk& it) {
-    const int64_t p0 = static_cast<int64_t>(it.s.start) + it.t0, p1 = static_cast<int64_t>(it.s.start) + it.t1 - 1;
-    last = w.causal ? static_cast<int>(min(p0, static_cast<int64_t>(it.s.len) - 1)) : it.s.len - 1;
-    const int64_t f = w.window > 0 ? p1 - w.window + 1 : 0;
-    first = static_cast<int>(max(f, static_cast<int64_t>(0)));
-  }
-  __device__ __forceinline__ bool in(int kb) const { return kb * BN + BN - 1 > last || kb * BN < first; }
+  int slot;         // of its part of a shared item, -1: it is whole
+  int b, batch, row0, vh, kvh, pad;
+  // some row does not see some key of the block
+  __device__ __forceinline__ bool hides(int kb) const { return kb * BN + BN - 1 > last || kb * BN < first; }
+  __device__ __forceinline__ int count(int m) const { return pair ? n : (n + 1 - m) / 2; }  // blocks of tile m
 };
 
 // The ring's entries of an item: two tiles over the same blocks: K_0 V_0 K_1 V_1 ...; one tile whose blocks
 // go to both in turn: K_0 K_1 V_0 K_2 V_1 K_3 ...; 2 n in all.
 struct Order {
   int base, n;
-  bool pair;  // both tiles see the same blocks
-  __device__ __forceinline__ int count(int m) const { return pair ? n : (n + 1 - m) / 2; }  // blocks of tile m
+  bool pair;
   __device__ __forceinline__ int block(int m, int j) const { return pair ? j : 2 * j + m; }
   __device__ __forceinline__ int V(int i) const {
     return pair ? base + 2 * i + 1 : base + min(n, 2) + i + min(i, max(n - 2, 0));
   }
   __device__ __forceinline__ int K(int i) const { return pair ? base + 2 * i : i < 2 ? base + i : V(i - 2) + 1; }
 };
+
+// Values that were made 0 for the rows that do not see them, added to a row that does (`o` or `part`, its
+// first d columns): one by one from the cache.
+__device__ __noinline__ void add_spoilt(const Work& w, const Item& it, int first, int last, const __nv_bfloat16* V, int64_t s0,
+                                        int64_t s2, int d, __nv_bfloat16* o, float* part) {
+  for (int i = 0; i < it.n; ++i) {
+    if (!it.hides(it.b0 + i)) continue;
+    for (int k = max((it.b0 + i) * BN, first); k <= min((it.b0 + i) * BN + BN - 1, last); ++k) {
+      const int pg = page_at(w.seqs, it.b, k / w.seqs.page);
+      if (pg < 0) continue;
+      const __nv_bfloat16* v = V + pg * s0 + static_cast<int64_t>(k % w.seqs.page) * s2;
+      for (int x = 0; x < d; ++x) {
+        const float y = __bfloat162float(v[x]);
+        if (isfinite(y)) continue;
+        if (part != nullptr) part[x] += y;
+        else o[x] = __float2bfloat16(__bfloat162float(o[x]) + y);
+      }
+    }
+  }
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -96,16 +119,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* p_ready = p_half + 2;    // [2] of all keys
   uint64_t* o_full = p_ready + 2;
   uint64_t* o_empty = o_full + 1;    // O_0, O_1 read by the epilogue
-  uint64_t* settled = o_empty + 1;   // after a wait that gave up: the products in flight done
+  uint64_t* x_full = o_empty + 1;    // tile 1's maxima and sums are there for tile 0
+  uint64_t* settled = x_full + 1;    // after a wait that gave up: the products in flight done
   uint64_t* full = settled + 1;      // [NS]
   uint64_t* empty = full + NS;       // [NS]
   uint64_t* v_ok = empty + NS;       // [NS] values that some row does not see are finite
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_ok + NS);
+  uint64_t* known = v_ok + NS;       // [8] items
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(known + 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* started = abort_flag + 1;                                 // Q loads, ring entries (the TMA warp's)
-  volatile uint32_t* hidden = reinterpret_cast<volatile uint32_t*>(started + 2);  // [16] of K entries: 16-key runs without a page
+  volatile uint8_t* hidden = reinterpret_cast<volatile uint8_t*>(started + 2);  // [2][8] of tile m's blocks: 16-key runs without a page
   volatile int* spoilt = reinterpret_cast<volatile int*>(hidden + 16);    // [8] of items: n + 1 where values were made 0
   float2* stat = reinterpret_cast<float2*>(sm + L::oStat);
+  Item* items = reinterpret_cast<Item*>(sm + L::oItem);
+  static_assert(sizeof(Item) == 64 && (12 + 3 * NS + 8) * 8 + 4 * 4 + 16 + 32 <= 512, "the barriers' region");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, p = blockIdx.x;
   const int gt = w.cut.gt, tq = w.cut.tile;
@@ -122,13 +149,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     ptx::mbar_init(o_full, 2);
     ptx::mbar_init(o_empty, 256);
+    ptx::mbar_init(x_full, 128);
     ptx::mbar_init(settled, 1);
     for (int s = 0; s < NS; ++s) {
       ptx::mbar_init(&full[s], 1);
       ptx::mbar_init(&empty[s], 1);
       ptx::mbar_init(&v_ok[s], 2);
     }
-    for (int s = 0; s < 8; ++s) spoilt[s] = 0;
+    for (int s = 0; s < 8; ++s) ptx::mbar_init(&known[s], 1), spoilt[s] = 0;
     started[0] = started[1] = 0;
     *abort_flag = (ptx::smem_u32(sm) & 1023u) ? 1 : 0;  // the swizzled tiles need 1024-byte alignment
     if (*abort_flag) atomicOr(&g_err, FBD_ERR_TIMEOUT);
@@ -146,68 +174,92 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool ok = *abort_flag == 0;
   ptx::grid_dependency_wait();  // the plan
   ptx::grid_dependency_launch();
-  Walk it;
-  bool more = it.begin(w, sp, p) && ok;
-  auto order = [&](int base) { return Order{base, it.k1 - it.k0, it.weight == 2}; };
+  // Item n, once it is known (ring of 8: the loading warp is three items ahead at most, since it waits for the
+  // products with Q of the one before, and those for the softmax of the one before that).
+  auto item = [&](int n) -> const Item* {
+    wait(&known[n & 7], (n >> 3) & 1);
+    const Item* it = items + (n & 7);
+    // (a whole warp goes on or leaves; warps may leave at different times, since they meet only at barriers
+    // whose waits are bounded)
+    return __all_sync(0xffffffffu, *abort_flag == 0 && *reinterpret_cast<const volatile int*>(&it->n) > 0) ? it : nullptr;
+  };
 
   if (warp >= 8) ptx::setmaxnreg_dec<kRegsOther>();
   if (warp == 8) {
     // ------------------------------------------------------------ TMA producer
-    int E = 0, n = 0, nq = 0;
-    bool go = true;
-    const int per = BN / box;             // boxes of an entry along its keys
+    Walk it;
+    bool more = it.begin(w, sp, p) && ok, go = true;
+    int E = 0, n = 0, nq = 0, T0 = 0, T1 = 0;
+    const int per = BN / box;                  // boxes of an entry along its keys
     const int c0 = lane % SL, g0 = lane / SL;  // this lane's box
-    // Entry e: block kb of K or V.
-    auto load = [&](const CUtensorMap* map, bool key, int kb, int kvh) {
+    // The next entry: block kb of K (for tiles m0 .. m1) or V.
+    auto load = [&](const CUtensorMap* map, int m0, int m1, int kb, int kvh) {
       const int s = E % NS;
       const int k0 = kb * BN + g0 * box;
       const int en = k0 / w.seqs.page;
       const int pg = g0 < per && k0 < it.s.len ? page_at(w.seqs, it.b, en) : -1;
       if (E >= NS) go = wait(&empty[s], ((E / NS) - 1) & 1) && go;
-      if (!__all_sync(0xffffffffu, go)) {
-        go = false;
-        return;
-      }
-      if (key) {
+      go = __all_sync(0xffffffffu, go);
+      if (!go) return;
+      if (m0 <= m1) {
         const uint32_t run = g0 < per && pg < 0 && k0 < it.s.len ? ((1u << (box / 16)) - 1u) << (g0 * (box / 16)) : 0u;
         const uint32_t all = __reduce_or_sync(0xffffffffu, run);
-        if (lane == 0) hidden[E & 15] = all;
+        if (lane == 0) {
+          if (m0 == 0) hidden[T0 & 7] = static_cast<uint8_t>(all);
+          if (m1 == 1) hidden[8 + (T1 & 7)] = static_cast<uint8_t>(all);
+        }
+        T0 += m0 == 0, T1 += m1 == 1;
       }
       if (lane == 0) ptx::mbar_expect_tx(&full[s], L::kTile);
       __syncwarp();
       if (g0 < per)
         ptx::tma_load_4d(sm + L::oRing + s * L::kTile + c0 * BN * 128 + g0 * box * 128, map, &full[s], c0 * 64,
-                    pg < 0 ? 0 : k0 - en * w.seqs.page, kvh, pg);
+                         pg < 0 ? 0 : k0 - en * w.seqs.page, kvh, pg);
       ++E;
     };
     for (; more && go; more = it.next(w), ++n) {
-      const int tiles = it.weight, kvh = it.vh / w.cut.per_kv;
-      const Order o = order(0);
+      const int tiles = it.weight, kvh = it.vh / w.cut.per_kv, nb = it.k1 - it.k0, b0 = it.j0 + it.k0;
       if (n > 0) go = wait(q_empty, (n - 1) & 1) && go;
-      if (!__all_sync(0xffffffffu, go)) break;
+      go = __all_sync(0xffffffffu, go);
+      if (!go) break;
       ++nq;
       if (lane == 0) {
+        Item& x = items[n & 7];
+        x.n = nb, x.b0 = b0, x.pair = it.weight == 2, x.t0 = it.t0, x.t1 = it.t1, x.start = it.s.start, x.len = it.s.len;
+        const int64_t p0 = static_cast<int64_t>(it.s.start) + it.t0, p1 = static_cast<int64_t>(it.s.start) + it.t1 - 1;
+        x.last = w.causal ? static_cast<int>(min(p0, static_cast<int64_t>(it.s.len) - 1)) : it.s.len - 1;
+        x.first = w.window > 0 ? static_cast<int>(max(p1 - w.window + 1, static_cast<int64_t>(0))) : 0;
+        x.slot = it.whole() ? -1 : it.slot(p);
+        x.b = it.b, x.batch = it.s.batch, x.row0 = it.s.row0, x.vh = it.vh, x.kvh = kvh;
+        ptx::mbar_arrive(&known[n & 7]);
+        if (!it.whole() && it.k0 == 0) sp.tail[p] = Tail{it.b, it.tile, it.vh, it.parts(p)};
         ptx::mbar_expect_tx(q_full, tiles * SL * gt * tq * 128);
         for (int m = 0; m < tiles; ++m)
           for (int u = 0; u < SL; ++u)
-            ptx::tma_load_5d(sm + m * L::kTile + u * BM * 128, &tmQ, q_full, u * 64, 0, it.s.row0 + it.t0 + m * tq, it.vh, it.s.batch);
+            ptx::tma_load_5d(sm + m * L::kTile + u * BM * 128, &tmQ, q_full, u * 64, 0, it.s.row0 + it.t0 + m * tq, it.vh,
+                             it.s.batch);
       }
-      const int b0 = it.j0 + it.k0;
-      if (o.pair) {
-        for (int j = 0; j < o.n && go; ++j) {
-          load(&tmK, true, b0 + j, kvh);
-          if (go) load(&tmV, false, b0 + j, kvh);
+      if (tiles == 2) {
+        for (int j = 0; j < nb && go; ++j) {
+          load(&tmK, 0, 1, b0 + j, kvh);
+          if (go) load(&tmV, 1, 0, b0 + j, kvh);
         }
       } else {
-        load(&tmK, true, b0, kvh);
-        if (go && o.n > 1) load(&tmK, true, b0 + 1, kvh);
-        for (int j = 0; j < o.n && go; ++j) {
-          load(&tmV, false, b0 + j, kvh);
-          if (go && j + 2 < o.n) load(&tmK, true, b0 + j + 2, kvh);
+        load(&tmK, 0, 0, b0, kvh);
+        if (go && nb > 1) load(&tmK, 1, 1, b0 + 1, kvh);
+        for (int j = 0; j < nb && go; ++j) {
+          load(&tmV, 1, 0, b0 + j, kvh);
+          if (go && j + 2 < nb) load(&tmK, j & 1, j & 1, b0 + j + 2, kvh);
         }
       }
     }
-    if (lane == 0) started[0] = nq, started[1] = E;
+    if (lane == 0) {
+      if (go) {
+        items[n & 7].n = 0;
+        ptx::mbar_arrive(&known[n & 7]);
+      }
+      started[0] = nq, started[1] = E;
+    }
   } else if (warp == 9) {
     // ------------------------------------------------------------- MMA issuer
     constexpr uint32_t idS = ptx::idesc_bf16(BM, BN, 0, 0);
@@ -216,10 +268,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dK = tc::kmajor_desc(ptx::smem_u32(sm + L::oRing), BN, 0);
     const uint64_t dV = tc::mnmajor_desc(ptx::smem_u32(sm + L::oRing), BN, 0);
     int base = 0, n = 0, T0 = 0, T1 = 0, masked = 0;
-    for (; more; more = it.next(w), ++n) {
-      const Order o = order(base);
-      const Hide hide(w, it);
-      const int b0 = it.j0 + it.k0, n0 = o.count(0), n1 = o.count(1);
+    for (const Item* it; (it = item(n)) != nullptr; ++n) {
+      const Order o{base, it->n, it->pair != 0};
+      const int b0 = it->b0, n0 = it->count(0), n1 = it->count(1);
       int left = n0 + n1;  // products with Q still to issue
       auto issue_s = [&](int m, int j) {
         const int e = o.K(o.block(m, j)), s = e % NS;
@@ -245,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int T = m == 0 ? T0++ : T1++;
           const int i = o.block(m, j), e = o.V(i), s = e % NS;
           if (!o.pair || m == 0) {
-            if (hide.in(b0 + i)) {
+            if (it->hides(b0 + i)) {
               wait(&v_ok[masked % NS], (masked / NS) & 1);
               ++masked;
             } else {
@@ -276,17 +327,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 10) {
     // ------------------------- values that some row does not see: made 0 where they are not finite
     int base = 0, n = 0, masked = 0, seen = 0;
-    for (; more; more = it.next(w), ++n) {
-      const Order o = order(base);
-      const Hide hide(w, it);
-      const int b0 = it.j0 + it.k0;
+    for (const Item* it; (it = item(n)) != nullptr; ++n) {
+      const Order o{base, it->n, it->pair != 0};
+      const int b0 = it->b0;
       for (int i = 0; i < o.n; ++i) {
         const int e = o.V(i), s = e % NS;
         // every entry up to this one in turn: a barrier two phases back would look complete
         for (; seen <= e; ++seen) wait(&full[seen % NS], (seen / NS) & 1);
-        if (!hide.in(b0 + i)) continue;
+        if (!it->hides(b0 + i)) continue;
         uint8_t* V = sm + L::oRing + s * L::kTile;
-        const int held = min(max(it.s.len - (b0 + i) * BN, 0), BN);  // keys behind them may hold anything
+        const int held = min(max(it->len - (b0 + i) * BN, 0), BN);  // keys behind them may hold anything
         bool some = false;
 #pragma unroll
         for (int r = threadIdx.x - 320; r < BN; r += 64) {
@@ -326,28 +376,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + L::cS + m * BN + lane_off, tO = tmem + L::cO + lane_off;
     const uint64_t c2 = tc::pk2f(c, c);
     const int rt = r / gt, rh = r - rt * gt;  // this row's token of the tile, and its head
-    int T = 0, base = 0, n = 0, shared = 0;
-    for (; more; more = it.next(w), ++n) {
-      const Order o = order(base);
-      const int nb = o.count(m), b0 = it.j0 + it.k0;
-      const int tok = it.t0 + (o.pair ? m * tq : 0) + rt;
-      const bool live = rt < tq && tok < it.t1;
-      // the keys that this row sees
-      const int64_t at = static_cast<int64_t>(it.s.start) + tok;
-      const int last = w.causal ? static_cast<int>(max(min(at, static_cast<int64_t>(it.s.len) - 1), static_cast<int64_t>(-1))) : it.s.len - 1;
-      const int64_t f0 = w.window > 0 ? at - w.window + 1 : 0;
-      const int first = static_cast<int>(min(max(f0, static_cast<int64_t>(0)), static_cast<int64_t>(0x7fffffff)));
+    int T = 0, shared = 0;
+    const Item* it;
+    for (int n = 0; (it = item(n)) != nullptr; ++n) {
+      const int nb = it->count(m);
+      const bool pair = it->pair != 0;
+      // the keys that this row sees: its token's position less the window, up to that position or the last key
+      int last, first;
+      {
+        const int tok = it->t0 + (pair ? m * tq : 0) + rt;
+        const int64_t at = static_cast<int64_t>(it->start) + tok, end = it->len - 1;
+        last = static_cast<int>(w.causal ? max(min(at, end), static_cast<int64_t>(-1)) : end);
+        const int64_t f = w.window > 0 ? at - w.window + 1 : 0;
+        first = static_cast<int>(min(max(f, static_cast<int64_t>(0)), static_cast<int64_t>(0x7fffffff)));
+      }
       // bounds grow with the row: the warp's first row has the first last key, its last row the last first one
       const int last0 = __shfl_sync(0xffffffffu, last, 0), first31 = __shfl_sync(0xffffffffu, first, 31);
+      int key0 = (it->b0 + (pair ? 0 : m)) * BN;
       float mref = -INFINITY, l = 0.f;
-      for (int j = 0; j < nb; ++j, ++T) {
-        const int i = o.block(m, j), key0 = (b0 + i) * BN;
+      for (int j = 0; j < nb; ++j, ++T, key0 += pair ? BN : 2 * BN) {
         wait(&s_full[m], T & 1);
         ptx::tc_fence_after();
         uint32_t v[4][32];
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch) ptx::tmem_ld32(tS + ch * 32, v[ch]);
-        const uint32_t hid = hidden[o.K(i) & 15];
+        const uint32_t hid = hidden[m * 8 + (T & 7)];
         ptx::tmem_wait_ld();
         if (key0 + BN - 1 > last0 || key0 < first31 || hid != 0) {
 #pragma unroll
@@ -420,66 +473,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // ------------------------------------------------------------------ epilogue
       float a0 = 1.f, a1 = 0.f;  // weights of this tile's sums and of the other's
-      if (!o.pair) {
+      if (!pair && it->n > 1) {  // (tile 1 of the item after next waits for this one's epilogue: two buffers)
         float2* mine = stat + (shared & 1) * BM + r;
-        if (m == 1) *mine = make_float2(mref, l);
-        tc::named_sync(1, 256);
-        ++shared;
-        if (m == 0) {
+        if (m == 1) {
+          *mine = make_float2(mref, l);
+          ptx::mbar_arrive(x_full);
+        } else {
+          wait(x_full, shared & 1);
           const float2 z = *mine;
           const float top = fmaxf(mref, z.x), sub = top == -INFINITY ? 0.f : top * c;
           a0 = mref == -INFINITY ? 0.f : ptx::ex2(fmaf(mref, c, -sub)), a1 = z.x == -INFINITY ? 0.f : ptx::ex2(fmaf(z.x, c, -sub));
           l = l * a0 + z.y * a1, mref = top;
         }
+        ++shared;
       }
       wait(o_full, n & 1);
       ptx::tc_fence_after();
-      if (o.pair || m == 0) {
-        const bool whole = it.whole(), both = !o.pair && o.count(1) > 0;
-        const int slot = it.slot(p);
-        const int srow = (o.pair ? m * BM : 0) + r;
-        const int64_t h = static_cast<int64_t>(it.vh) * gt + rh, pos = it.s.row0 + tok;
-        const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;  // (a row that sees no key: 0)
+      if (pair || m == 0) {
+        const int slot = it->slot, tok = it->t0 + (pair ? m * tq : 0) + rt;
+        const bool both = !pair && it->n > 1, live = rt < tq && tok < it->t1;
+        const int64_t h = static_cast<int64_t>(it->vh) * gt + rh, pos = it->row0 + tok;
+        const float inv = slot >= 0 ? 1.f : l == 0.f ? 0.f : 1.f / l;  // (a row that sees no key: 0)
         a0 *= inv, a1 *= inv;
-        const bool bad = spoilt[n & 7] == n + 1;
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(out.O) + it.s.batch * out.os[0] + h * out.os[1] + pos * out.os[2];
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(out.O) + it->batch * out.os[0] + h * out.os[1] + pos * out.os[2];
+        float* part = slot >= 0 ? sp.o(slot, (pair ? m * BM : 0) + r) : nullptr;
 #pragma unroll 1
         for (int ch = 0; ch < D / 32; ++ch) {
           uint32_t a[32], b[32];
-          ptx::tmem_ld32(tO + (o.pair ? m * D : 0) + ch * 32, a);
+          ptx::tmem_ld32(tO + (pair ? m * D : 0) + ch * 32, a);
           if (both) ptx::tmem_ld32(tO + D + ch * 32, b);
           ptx::tmem_wait_ld();
           if (ch == D / 32 - 1) {
             ptx::tc_fence_before();
             ptx::mbar_arrive(o_empty);
           }
+          if (!live || ch * 32 >= d) continue;
 #pragma unroll
           for (int t = 0; t < 32; ++t) {
             float x = tc::f(a[t]) * a0;
             if (both) x = fmaf(tc::f(b[t]), a1, x);
-            if (l == 0.f) x = 0.f;
-            a[t] = __float_as_uint(x);
+            a[t] = l == 0.f ? 0u : __float_as_uint(x);
           }
-          if (!live || ch * 32 >= d) continue;
-          if (bad) {
-            // The values made 0 that this row does see (one by one from the cache).
-            const Hide hide(w, it);
-            const int kvh = it.vh / w.cut.per_kv;
-            for (int i = 0; i < o.n; ++i) {
-              if (!hide.in(b0 + i)) continue;
-              for (int k = max((b0 + i) * BN, first); k <= min((b0 + i) * BN + BN - 1, last); ++k) {
-                const int pg = page_at(w.seqs, it.b, k / w.seqs.page);
-                if (pg < 0) continue;
-                const __nv_bfloat16* src = Vg + pg * vs0 + kvh * vs1 + static_cast<int64_t>(k % w.seqs.page) * vs2 + ch * 32;
-#pragma unroll
-                for (int t = 0; t < 32; ++t) {
-                  const float x = __bfloat162float(src[t]);
-                  if (!isfinite(x)) a[t] = __float_as_uint(tc::f(a[t]) + x);
-                }
-              }
-            }
-          }
-          if (whole) {
+          if (part == nullptr) {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               uint32_t pk[4];
@@ -490,21 +525,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-              *reinterpret_cast<uint4*>(sp.o(slot, srow) + ch * 32 + u * 4) =
-                  make_uint4(a[u * 4], a[u * 4 + 1], a[u * 4 + 2], a[u * 4 + 3]);
+              *reinterpret_cast<uint4*>(part + ch * 32 + u * 4) = make_uint4(a[u * 4], a[u * 4 + 1], a[u * 4 + 2], a[u * 4 + 3]);
           }
         }
         if (live) {
-          if (!whole)
-            *sp.ml(slot, srow) = make_float2(mref == -INFINITY ? mref : mref * c, l);
+          if (spoilt[n & 7] == n + 1) add_spoilt(w, *it, first, last, Vg + it->kvh * vs1, vs0, vs2, d, dst, part);
+          if (part != nullptr)
+            *sp.ml(slot, (pair ? m * BM : 0) + r) = make_float2(mref == -INFINITY ? mref : mref * c, l);
           else if (out.lse != nullptr)
-            out.lse[it.s.batch * out.ls[0] + h * out.ls[1] + pos] = l == 0.f ? -INFINITY : fmaf(mref, scale, logf(l));
+            out.lse[it->batch * out.ls[0] + h * out.ls[1] + pos] = l == 0.f ? -INFINITY : fmaf(mref, scale, logf(l));
         }
       } else {
         ptx::mbar_arrive(o_empty);
       }
-      base += 2 * o.n;
-      if (threadIdx.x == 0 && !it.whole() && it.k0 == 0) sp.tail[p] = Tail{it.b, it.tile, it.vh, it.parts(p)};
     }
   }
 
