@@ -24,7 +24,7 @@ struct Cut {
   int per_kv;  // ... of a key/value head
   int tile;    // tokens of a tile
   int step;    // tokens of an item (tile, or 2 tile: then an item of more than `tile` tokens costs double)
-  int BN;      // keys of a block
+  int shift;   // a block holds 1 << shift keys
   int over;    // cost of an item beside its blocks
   int least;   // units of a stretch, at the least
   int ctas;
@@ -90,8 +90,8 @@ __device__ __forceinline__ Blocks blocks_of(const Work& w, const Seq& s, int t0,
   const int64_t l = static_cast<int64_t>(s.start) + t0 - w.window + 1;
   const int lo = w.window > 0 && l > 0 ? static_cast<int>(l) : 0;
   if (hi <= lo) return Blocks{0, 1};
-  const int j0 = lo / w.cut.BN;
-  return Blocks{j0, (hi + w.cut.BN - 1) / w.cut.BN - j0};
+  const int j0 = lo >> w.cut.shift;
+  return Blocks{j0, ((hi - 1) >> w.cut.shift) + 1 - j0};
 }
 
 // The items of a CTA's stretch, one after another.

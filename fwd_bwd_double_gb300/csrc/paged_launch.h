@@ -6,8 +6,8 @@ namespace fbd {
 namespace paged {
 
 cudaError_t plan(const Work& w, const Space& sp, cudaStream_t st);
-// tile_rows: rows of a slot that a tile takes.
-cudaError_t join(const Work& w, const Space& sp, const Out& out, int dtype, int d, int tile_rows, cudaStream_t st);
+// tile_rows: rows of a slot that a tile takes; few: the most new tokens of a sequence, as far as is known.
+cudaError_t join(const Work& w, const Space& sp, const Out& out, int dtype, int d, int tile_rows, int64_t few, cudaStream_t st);
 
 // The query heads handled together by a kernel whose tiles have `rows` rows: all that share a
 // key/value head where `few` new tokens of them fit a tile (K and V are then read once), else the

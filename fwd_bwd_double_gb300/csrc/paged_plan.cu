@@ -26,25 +26,32 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
   return v;
 }
 
+constexpr int kNear = 2048;  // sequences whose ends are kept in shared memory
+
 __global__ void __launch_bounds__(kT) plan_kernel(const Work w, const Space sp) {
-  __shared__ int64_t carry, part[kT / 32];
+  __shared__ int64_t carry, part[kT / 32], near[kNear];
   ptx::grid_dependency_launch();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, B = w.seqs.B;
-  int64_t* ends = sp.ends;
-  for (int b = warp; b < B; b += kT / 32) {
-    const Seq s = seq_at(w.seqs, b);
-    const int tiles = static_cast<int>((static_cast<int64_t>(s.n) + w.cut.step - 1) / w.cut.step);
-    int64_t v = 0;
-    for (int t = lane; t < tiles; t += 32) v += tile_units(w, s, t);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (lane == 0) ends[b] = v * w.cut.nv;
-  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, B = w.seqs.B, step = w.cut.step;
+  int64_t* ends = B <= kNear ? near : sp.ends;
   if (threadIdx.x == 0) carry = 0;
-  __syncthreads();
   for (int b0 = 0; b0 < B; b0 += kT) {
     const int b = b0 + threadIdx.x;
-    int64_t v = warp_scan(b < B ? ends[b] : 0, lane);
+    // A sequence's tiles: its thread's, the warp's together where they are many.
+    int64_t v = 0;
+    Seq s{};
+    if (b < B) s = seq_at(w.seqs, b);
+    for (int t = 0; t < 4 && static_cast<int64_t>(t) * step < s.n; ++t) v += tile_units(w, s, t);
+    for (unsigned many = __ballot_sync(0xffffffffu, s.n > 4ll * step); many != 0; many &= many - 1) {
+      const int from = __ffs(many) - 1;
+      const Seq q = seq_at(w.seqs, b0 + warp * 32 + from);
+      int64_t u = 0;
+      for (int64_t t = 4 + lane; t * step < q.n; t += 32) u += tile_units(w, q, static_cast<int>(t));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+      if (lane == from) v += u;
+    }
+    v = warp_scan(v * w.cut.nv, lane);
+    __syncthreads();  // `part` and `carry` of the round before
     if (lane == 31) part[warp] = v;
     __syncthreads();
     if (warp == 0) part[lane] = warp_scan(part[lane], lane);
@@ -53,38 +60,60 @@ __global__ void __launch_bounds__(kT) plan_kernel(const Work w, const Space sp) 
     if (b < B) ends[b] = v;
     __syncthreads();
     if (threadIdx.x == kT - 1) carry = v;
-    __syncthreads();
   }
+  __syncthreads();
   const int64_t total = carry;
   const int64_t even = (total + w.cut.ctas - 1) / w.cut.ctas, stretch = even > w.cut.least ? even : w.cut.least;
   if (threadIdx.x == 0) *sp.head = Head{total, stretch};
-  for (int p = warp; p < w.cut.ctas; p += kT / 32) {
+  for (int p0 = warp * 32; p0 < w.cut.ctas; p0 += kT) {
+    const int p = p0 + lane;
     const int64_t x = stretch * p;
-    if (lane == 0) sp.tail[p] = Tail{0, 0, 0, 0};
-    if (x >= total) {
-      if (lane == 0) sp.start[p] = Start{0, -1, 0, 0, 0};
-      continue;
-    }
-    int lo = -1, hi = B - 1;  // the first sequence that ends behind x
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (ends[mid] > x) hi = mid; else lo = mid;
-    }
-    const Seq s = seq_at(w.seqs, hi);
-    const int tiles = static_cast<int>((static_cast<int64_t>(s.n) + w.cut.step - 1) / w.cut.step);
-    int64_t base = hi > 0 ? ends[hi - 1] : 0;
-    for (int t0 = 0; t0 < tiles; t0 += 32) {
-      const int t = t0 + lane;
-      const int64_t u = t < tiles ? tile_units(w, s, t) : 0, cum = base + warp_scan(u * w.cut.nv, lane);
-      const unsigned behind = __ballot_sync(0xffffffffu, cum > x);
-      if (behind != 0) {
-        if (lane == __ffs(behind) - 1) {
-          const int64_t at = cum - u * w.cut.nv, vh = (x - at) / u;
-          sp.start[p] = Start{at + vh * u, hi, t, static_cast<int>(vh), 0};
-        }
-        break;
+    const bool some = p < w.cut.ctas && x < total;
+    int hi = B - 1;  // the first sequence that ends behind x
+    Seq s{};
+    int64_t base = 0;
+    if (some) {
+      for (int lo = -1; hi - lo > 1;) {
+        const int mid = (lo + hi) >> 1;
+        if (ends[mid] > x) hi = mid; else lo = mid;
       }
-      base = __shfl_sync(0xffffffffu, cum, 31);
+      s = seq_at(w.seqs, hi);
+      base = hi > 0 ? ends[hi - 1] : 0;
+    }
+    if (p < w.cut.ctas) {
+      sp.tail[p] = Tail{0, 0, 0, 0};
+      if (!some) sp.start[p] = Start{0, -1, 0, 0, 0};
+    }
+    // ... and its tile that does: looked for by the thread where there are few, else by the warp
+    bool found = !some;
+    for (int t = 0; !found && t < 4 && static_cast<int64_t>(t) * step < s.n; ++t) {
+      const int64_t u = tile_units(w, s, t), all = u * w.cut.nv;
+      if (base + all > x) {
+        const int64_t vh = (x - base) / u;
+        sp.start[p] = Start{base + vh * u, hi, t, static_cast<int>(vh), 0};
+        found = true;
+      } else {
+        base += all;
+      }
+    }
+    for (unsigned rest = __ballot_sync(0xffffffffu, !found); rest != 0; rest &= rest - 1) {
+      const int from = __ffs(rest) - 1, qb = __shfl_sync(0xffffffffu, hi, from);
+      const int64_t at0 = __shfl_sync(0xffffffffu, base, from), y = __shfl_sync(0xffffffffu, x, from);
+      const Seq q = seq_at(w.seqs, qb);
+      int64_t at = at0;
+      for (int64_t t0 = 4; t0 * step < q.n; t0 += 32) {
+        const int64_t t = t0 + lane;
+        const int64_t u = t * step < q.n ? tile_units(w, q, static_cast<int>(t)) : 0, cum = at + warp_scan(u * w.cut.nv, lane);
+        const unsigned behind = __ballot_sync(0xffffffffu, cum > y);
+        if (behind != 0) {
+          if (lane == __ffs(behind) - 1) {
+            const int64_t b = cum - u * w.cut.nv, vh = (y - b) / u;
+            sp.start[p0 + from] = Start{b + vh * u, qb, static_cast<int>(t), static_cast<int>(vh), 0};
+          }
+          break;
+        }
+        at = __shfl_sync(0xffffffffu, cum, 31);
+      }
     }
   }
 }
@@ -95,13 +124,12 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, float4 v) {
 }
 
 constexpr int kJ = 256;
-constexpr int kRows = 8;  // rows of a block
 
-// Block (p, chunk): rows of the item that begins in CTA p's stretch and goes on behind it.  A row's columns
+// Block (p, y): every gridDim.y-th run of `per` rows of the item that begins in CTA p's stretch and goes on behind it.  A row's columns
 // are d / 4 threads' (rounded up to a power of two); such groups take a row each, or, where the
 // parts are many, parts of one row after another.
 template <typename T>
-__global__ void __launch_bounds__(kJ) join_kernel(const Work w, const Space sp, const Out out, int d, int tile_rows) {
+__global__ void __launch_bounds__(kJ) join_kernel(const Work w, const Space sp, const Out out, int d, int tile_rows, int per) {
   __shared__ float4 sum[kJ];
   __shared__ float sl[kJ], sm[kJ];
   ptx::grid_dependency_wait();
@@ -114,8 +142,8 @@ __global__ void __launch_bounds__(kJ) join_kernel(const Work w, const Space sp, 
   while (C * 4 < d) C *= 2;
   const int groups = kJ / C, g = threadIdx.x / C, col = (threadIdx.x & (C - 1)) * 4;
   const bool wide = q.parts > 2 * groups;  // groups share a row
-  const int r0 = blockIdx.y * kRows, r1 = min(rows, r0 + kRows);
-  for (int rr = r0; rr < r1; rr += wide ? 1 : groups) {
+  for (int r0 = blockIdx.y * per; r0 < rows; r0 += gridDim.y * per)
+  for (int rr = r0, r1 = min(rows, r0 + per); rr < r1; rr += wide ? 1 : groups) {
     const int row = rr + (wide ? 0 : g);
     const bool live = row < r1;
     const int t = live ? row / gt : 0, hh = live ? row - t * gt : 0;
@@ -123,6 +151,7 @@ __global__ void __launch_bounds__(kJ) join_kernel(const Work w, const Space sp, 
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (live) {
+#pragma unroll 4
       for (int k = wide ? g : 0; k < q.parts; k += wide ? groups : 1) {
         const int slot = k == 0 ? 2 * p + 1 : 2 * (p + k);
         const float2 x = *sp.ml(slot, at);
@@ -170,9 +199,12 @@ cudaError_t plan(const Work& w, const Space& sp, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-cudaError_t join(const Work& w, const Space& sp, const Out& out, int dtype, int d, int tile_rows, cudaStream_t st) {
+cudaError_t join(const Work& w, const Space& sp, const Out& out, int dtype, int d, int tile_rows, int64_t few, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(w.cut.ctas), static_cast<unsigned>((w.cut.step * w.cut.gt + kRows - 1) / kRows));
+  // A row a block where items have few (each then has many parts), else eight.
+  const int64_t rows = (few < w.cut.step ? few : w.cut.step) * w.cut.gt;
+  const int per = rows <= 32 ? 1 : 8;
+  cfg.gridDim = dim3(static_cast<unsigned>(w.cut.ctas), static_cast<unsigned>((rows + per - 1) / per));
   cfg.blockDim = dim3(kJ);
   cfg.stream = st;
   cudaLaunchAttribute attr{};
@@ -180,8 +212,8 @@ cudaError_t join(const Work& w, const Space& sp, const Out& out, int dtype, int 
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return dtype == ATTN_BF16 ? cudaLaunchKernelEx(&cfg, join_kernel<__nv_bfloat16>, w, sp, out, d, tile_rows)
-                            : cudaLaunchKernelEx(&cfg, join_kernel<float>, w, sp, out, d, tile_rows);
+  return dtype == ATTN_BF16 ? cudaLaunchKernelEx(&cfg, join_kernel<__nv_bfloat16>, w, sp, out, d, tile_rows, per)
+                            : cudaLaunchKernelEx(&cfg, join_kernel<float>, w, sp, out, d, tile_rows, per);
 }
 
 }  // namespace paged

@@ -216,7 +216,7 @@ cudaError_t launch(const PagedArgs& a, const Work& w, const Space& sp, const Out
                     static_cast<const T*>(a.V), a.qs[0], a.qs[1], a.qs[2], a.ks[0], a.ks[1], a.ks[2], a.vs[0], a.vs[1],
                     a.vs[2], a.scale * kLog2e);
   if (e != cudaSuccess) return e;
-  return join(w, sp, out, a.dtype, D, R, st);
+  return join(w, sp, out, a.dtype, D, R, a.max_new, st);
 }
 
 template <typename T, int D>
@@ -234,7 +234,7 @@ Work work_of(const PagedArgs& a) {
   w.cut.gt = heads_together(g, R, R == 16 ? a.max_new : 0);
   w.cut.nv = a.H / w.cut.gt, w.cut.per_kv = g / w.cut.gt;
   w.cut.tile = w.cut.step = R / w.cut.gt;
-  w.cut.BN = BN, w.cut.over = 1, w.cut.least = 4;
+  w.cut.shift = 6, w.cut.over = 1, w.cut.least = 4;
   const int smem = R == 16 ? 4 * (BN * 2 * a.d) : 4 * (BN * 2 * a.d + 64 * a.d);
   w.cut.ctas = 152 * (smem <= 50000 ? 3 : smem <= 100000 ? 2 : 1);
   return w;

@@ -13,8 +13,10 @@
 //
 // Pages: a block is fetched in boxes of as many keys as divide the page's (16 .. 128), one lane of the
 // loading warp per box, which looks its page up; keys that the sequence does not hold, and entries
-// that are no page, are coordinates outside the tensor, which read as zeros without traffic.  Keys hidden
-// from a row are masked in its scores.  Their values are multiplied by weights of 0, which would make
+// that are no page, are coordinates outside the tensor, which read as zeros without traffic.  The lanes'
+// copies are issued one after another (about 75 cycles each), so where the strides allow it a box takes all
+// d columns, in groups of eight keys (group, slab of 64 columns, key: MMA operands of either major), else
+// a slab of them.  Keys hidden from a row are masked in its scores.  Their values are multiplied by weights of 0, which would make
 // an infinity or NaN there a NaN: in blocks that some row does not see whole, two warps make such
 // elements 0 before the product (and rows behind the last key, which may hold anything), and the
 // rows that do see them add them at the end.
@@ -45,15 +47,25 @@ constexpr float kShare = .25f;   // ... and its share of the row's sum so far, w
 template <int D>
 struct Lay {
   static constexpr int kTile = BM * D * 2;       // Q tile, and a K or V entry of the ring
-  static constexpr int NS = D == 64 ? 8 : 5;
+  static constexpr int NS = D == 64 ? 8 : 4;
+  static constexpr int kOut = 32 * 80;           // a warp's outputs on their way: 64 bytes of each row
   static constexpr int oRing = 2 * kTile;
-  static constexpr int oStat = oRing + NS * kTile;  // [2][128] (max, sum) of the second half of an item's blocks
+  static constexpr int oOut = oRing + NS * kTile;
+  static constexpr int oStat = oOut + 8 * kOut;  // [2][128] (max, sum) of the second half of an item's blocks
   static constexpr int oBar = oStat + 2 * BM * 8;
   static constexpr int oItem = oBar + 512;
   static constexpr int bytes = oItem + 8 * 64;
   static constexpr uint32_t cS = 0, cO = 2 * BN;  // S_m at cS + m BN, O_m at cO + m D
 };
 static_assert(Lay<128>::bytes <= 232448 && Lay<64>::bytes <= 232448, "shared memory");
+
+// How K and V lie in the cache and in the ring.
+struct Pages {
+  int box;       // keys of a box
+  int whole;     // a box takes all columns: its last coordinate is page * mul + head
+  int mul;
+  int sbo, slab; // bytes from eight keys to the next, from 64 columns to the next
+};
 
 // An item as the loading warp gives it to the others, through a ring in shared memory.
 struct Item {
@@ -106,7 +118,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV, const Work w, const Space sp, const Out out,
-                 const __nv_bfloat16* __restrict__ Vg, int64_t vs0, int64_t vs1, int64_t vs2, int d, int box,
+                 const __nv_bfloat16* __restrict__ Vg, int64_t vs0, int64_t vs1, int64_t vs2, int d, Pages pg,
                  float scale, float c) {
   using L = Lay<D>;
   constexpr int NS = L::NS, SL = D / 64;  // slabs of 64 columns
@@ -190,19 +202,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     Walk it;
     bool more = it.begin(w, sp, p) && ok, go = true;
     int E = 0, n = 0, nq = 0, T0 = 0, T1 = 0;
-    const int per = BN / box;                  // boxes of an entry along its keys
-    const int c0 = lane % SL, g0 = lane / SL;  // this lane's box
+    const int box = pg.box, per = BN / box;    // boxes of an entry along its keys
+    const int c0 = pg.whole ? 0 : lane % SL, g0 = pg.whole ? lane : lane / SL;  // this lane's box
     // The next entry: block kb of K (for tiles m0 .. m1) or V.
     auto load = [&](const CUtensorMap* map, int m0, int m1, int kb, int kvh) {
       const int s = E % NS;
       const int k0 = kb * BN + g0 * box;
       const int en = k0 / w.seqs.page;
-      const int pg = g0 < per && k0 < it.s.len ? page_at(w.seqs, it.b, en) : -1;
+      const int page = g0 < per && k0 < it.s.len ? page_at(w.seqs, it.b, en) : -1;
       if (E >= NS) go = wait(&empty[s], ((E / NS) - 1) & 1) && go;
       go = __all_sync(0xffffffffu, go);
       if (!go) return;
       if (m0 <= m1) {
-        const uint32_t run = g0 < per && pg < 0 && k0 < it.s.len ? ((1u << (box / 16)) - 1u) << (g0 * (box / 16)) : 0u;
+        const uint32_t run = g0 < per && page < 0 && k0 < it.s.len ? ((1u << (box / 16)) - 1u) << (g0 * (box / 16)) : 0u;
         const uint32_t all = __reduce_or_sync(0xffffffffu, run);
         if (lane == 0) {
           if (m0 == 0) hidden[T0 & 7] = static_cast<uint8_t>(all);
@@ -212,9 +224,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (lane == 0) ptx::mbar_expect_tx(&full[s], L::kTile);
       __syncwarp();
-      if (g0 < per)
-        ptx::tma_load_4d(sm + L::oRing + s * L::kTile + c0 * BN * 128 + g0 * box * 128, map, &full[s], c0 * 64,
-                         pg < 0 ? 0 : k0 - en * w.seqs.page, kvh, pg);
+      if (g0 < per) {
+        uint8_t* dst = sm + L::oRing + s * L::kTile + (g0 * box >> 3) * pg.sbo + c0 * pg.slab;
+        const int slot = page < 0 ? 0 : k0 - en * w.seqs.page;
+        if (pg.whole)
+          ptx::tma_load_5d(dst, map, &full[s], 0, 0, 0, slot >> 3, page < 0 ? -1 : page * pg.mul + kvh);
+        else
+          ptx::tma_load_4d(dst, map, &full[s], c0 * 64, slot, kvh, page);
+      }
       ++E;
     };
     for (; more && go; more = it.next(w), ++n) {
@@ -265,8 +282,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t idS = ptx::idesc_bf16(BM, BN, 0, 0);
     constexpr uint32_t idO = ptx::idesc_bf16(BM, D, 0, 1);
     const uint64_t dQ = tc::kmajor_desc(ptx::smem_u32(sm), BM, 0);
-    const uint64_t dK = tc::kmajor_desc(ptx::smem_u32(sm + L::oRing), BN, 0);
-    const uint64_t dV = tc::mnmajor_desc(ptx::smem_u32(sm + L::oRing), BN, 0);
+    const uint64_t dK = ptx::sdesc_sw128(ptx::smem_u32(sm + L::oRing), 16, pg.sbo);
+    const uint64_t dV = ptx::sdesc_sw128(ptx::smem_u32(sm + L::oRing), pg.slab, pg.sbo);
     int base = 0, n = 0, T0 = 0, T1 = 0, masked = 0;
     for (const Item* it; (it = item(n)) != nullptr; ++n) {
       const Order o{base, it->n, it->pair != 0};
@@ -280,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
           ptx::mma_ss_e(tmem + L::cS + m * BN, tc::desc_add(dQ, qo + tc::kmajor_off(BM, k)),
-                        tc::desc_add(dK, so + tc::kmajor_off(BN, k)), idS, k > 0 ? 1u : 0u);
+                        tc::desc_add(dK, so + (k >> 2) * pg.slab + (k & 3) * 32), idS, k > 0 ? 1u : 0u);
         ptx::mma_commit_e(&s_full[m]);
         if (lane == 0) ptx::mbar_arrive(&s_full[m]);
         if (!o.pair || m == 1) ptx::mma_commit_e(&empty[s]);
@@ -313,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               wait(&p_ready[m], T & 1);
               ptx::tc_fence_after();
             }
-            ptx::mma_ts_e(tmem + L::cO + m * D, tmem + L::cS + m * BN + k * 8, tc::desc_add(dV, so + k * 2048), idO,
+            ptx::mma_ts_e(tmem + L::cO + m * D, tmem + L::cS + m * BN + k * 8, tc::desc_add(dV, so + k * 2 * pg.sbo), idO,
                           (j > 0 || k > 0) ? 1u : 0u);
           }
           if (!o.pair || m == 1) ptx::mma_commit_e(&empty[s]);
@@ -338,26 +355,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t* V = sm + L::oRing + s * L::kTile;
         const int held = min(max(it->len - (b0 + i) * BN, 0), BN);  // keys behind them may hold anything
         bool some = false;
-#pragma unroll
         for (int r = threadIdx.x - 320; r < BN; r += 64) {
-          for (int u = 0; u < SL; ++u)
+          uint8_t* row = V + (r >> 3) * pg.sbo + (r & 7) * 128;
+          for (int u = 0; u < SL; ++u, row += pg.slab) {
+            uint4* at = reinterpret_cast<uint4*>(row);  // (its 16-byte pieces in another order)
+            if (r >= held) {
 #pragma unroll
-            for (int ch = 0; ch < 8; ++ch) {
-              uint4* at = reinterpret_cast<uint4*>(V + u * BN * 128 + tc::sw128(r, ch));
-              if (r >= held) {
-                *at = make_uint4(0, 0, 0, 0);
-                continue;
-              }
-              const uint4 x = *at;
-              uint32_t y[4] = {x.x, x.y, x.z, x.w};
-              bool bad = false;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                if ((y[k] & 0x7f80u) == 0x7f80u) y[k] &= 0xffff0000u, bad = true;
-                if ((y[k] & 0x7f800000u) == 0x7f800000u) y[k] &= 0x0000ffffu, bad = true;
-              }
-              if (bad) *at = make_uint4(y[0], y[1], y[2], y[3]), some = true;
+              for (int ch = 0; ch < 8; ++ch) at[ch] = make_uint4(0, 0, 0, 0);
+              continue;
             }
+            uint32_t top = 0;  // an exponent of ones carries into the sign's place
+            uint4 x[8];
+#pragma unroll
+            for (int ch = 0; ch < 8; ++ch) x[ch] = at[ch ^ (r & 7)];
+#pragma unroll
+            for (int ch = 0; ch < 8; ++ch)
+              top |= ((x[ch].x & 0x7f807f80u) + 0x00800080u) | ((x[ch].y & 0x7f807f80u) + 0x00800080u) |
+                     ((x[ch].z & 0x7f807f80u) + 0x00800080u) | ((x[ch].w & 0x7f807f80u) + 0x00800080u);
+            if ((top & 0x80008000u) == 0) continue;
+            some = true;
+            uint16_t* e = reinterpret_cast<uint16_t*>(row);
+            for (int k = 0; k < 64; ++k)
+              if ((e[k] & 0x7f80u) == 0x7f80u) e[k] = 0;
+          }
         }
         if (some) spoilt[n & 7] = n + 1;
         ptx::fence_proxy_async_smem();
@@ -376,6 +396,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + L::cS + m * BN + lane_off, tO = tmem + L::cO + lane_off;
     const uint64_t c2 = tc::pk2f(c, c);
     const int rt = r / gt, rh = r - rt * gt;  // this row's token of the tile, and its head
+    uint8_t* mine_out = sm + L::oOut + warp * L::kOut;
+    // 64 bytes of each live row of the warp to `to`, its own row's address.
+    auto put_rows = [&](const uint32_t (&x)[16], uint8_t* to, bool live) {
+      __syncwarp();
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        *reinterpret_cast<uint4*>(mine_out + lane * 80 + u * 16) = make_uint4(x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
+      __syncwarp();
+      const unsigned rows = __ballot_sync(0xffffffffu, live);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int row = u * 8 + (lane >> 2);
+        uint8_t* at = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), row));
+        const uint4 v = *reinterpret_cast<const uint4*>(mine_out + row * 80 + (lane & 3) * 16);
+        if (rows >> row & 1) *reinterpret_cast<uint4*>(at + (lane & 3) * 16) = v;
+      }
+    };
     int T = 0, shared = 0;
     const Item* it;
     for (int n = 0; (it = item(n)) != nullptr; ++n) {
@@ -507,27 +544,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tc_fence_before();
             ptx::mbar_arrive(o_empty);
           }
-          if (!live || ch * 32 >= d) continue;
+          if (ch * 32 >= d) continue;  // columns past d are padding
 #pragma unroll
           for (int t = 0; t < 32; ++t) {
             float x = tc::f(a[t]) * a0;
             if (both) x = fmaf(tc::f(b[t]), a1, x);
             a[t] = l == 0.f ? 0u : __float_as_uint(x);
           }
+          // Through shared memory, so that four threads write 64 bytes of a row: a row per thread straight to memory
+          // took 12 thousand cycles of an item.
           if (part == nullptr) {
+            uint32_t pk[16];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              uint32_t pk[4];
-#pragma unroll
-              for (int t = 0; t < 4; ++t) pk[t] = ptx::pack_bf16(tc::f(a[u * 8 + 2 * t]), tc::f(a[u * 8 + 2 * t + 1]));
-              *reinterpret_cast<uint4*>(dst + ch * 32 + u * 8) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-            }
+            for (int t = 0; t < 16; ++t) pk[t] = ptx::pack_bf16(tc::f(a[2 * t]), tc::f(a[2 * t + 1]));
+            put_rows(pk, reinterpret_cast<uint8_t*>(dst) + ch * 64, live);
           } else {
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-              *reinterpret_cast<uint4*>(part + ch * 32 + u * 4) = make_uint4(a[u * 4], a[u * 4 + 1], a[u * 4 + 2], a[u * 4 + 3]);
+            put_rows(reinterpret_cast<const uint32_t(&)[16]>(a[0]), reinterpret_cast<uint8_t*>(part) + ch * 128, live);
+            put_rows(reinterpret_cast<const uint32_t(&)[16]>(a[16]), reinterpret_cast<uint8_t*>(part) + ch * 128 + 64, live);
           }
         }
+        __syncwarp();
         if (live) {
           if (spoilt[n & 7] == n + 1) add_spoilt(w, *it, first, last, Vg + it->kvh * vs1, vs0, vs2, d, dst, part);
           if (part != nullptr)
@@ -566,25 +602,45 @@ template <int D>
 cudaError_t launch(const PagedArgs& a, const Work& w, const Space& sp, const Out& out, cudaStream_t st) {
   alignas(64) CUtensorMap mq, mk, mv;
   const Cut& k = w.cut;
-  int box = BN;  // keys of a box: as many as divide a page's
-  while (a.seqs.page % box != 0) box /= 2;
   const bool none = a.seqs.pages == 0;  // no key anywhere: a tensor that is never read
   const int64_t q_dims[5] = {a.d, k.gt, a.seqs.N, k.nv, a.seqs.cu != nullptr ? 1 : a.seqs.B};
   const int64_t q_str[4] = {a.qs[1], a.qs[2], a.qs[1] * k.gt, a.qs[0]};
   const int q_box[5] = {64, k.gt, k.tile, 1, 1};
-  const int64_t kv_dims[4] = {a.d, a.seqs.page, a.Hkv, none ? 1 : a.seqs.pages};
-  const int64_t k_str[3] = {a.ks[2], a.ks[1], a.ks[0]}, v_str[3] = {a.vs[2], a.vs[1], a.vs[0]};
-  const int kv_box[4] = {64, box, 1, 1};
-  if (!make_tmap_view(&mq, a.Q, 5, q_dims, q_str, q_box) || !make_tmap_view(&mk, none ? a.Q : a.K, 4, kv_dims, k_str, kv_box) ||
-      !make_tmap_view(&mv, none ? a.Q : a.V, 4, kv_dims, v_str, kv_box))
-    return cudaErrorInvalidValue;
+  if (!make_tmap_view(&mq, a.Q, 5, q_dims, q_str, q_box)) return cudaErrorInvalidValue;
+  Pages pg;
+  pg.box = BN;  // as many keys as divide a page's
+  while (a.seqs.page % pg.box != 0) pg.box /= 2;
+  // All columns in a box: of whole slabs, and pages a multiple of the heads' stride apart (K and V alike, and
+  // within a coordinate).
+  const int64_t pages = none ? 1 : a.seqs.pages, one = a.Hkv == 1 ? 1 : 0;
+  const int64_t k_mul = one ? 1 : pages == 1 ? 0 : a.ks[0] / a.ks[1], v_mul = one ? 1 : pages == 1 ? 0 : a.vs[0] / a.vs[1];
+  const int64_t heads = (pages - 1) * k_mul + a.Hkv;
+  pg.whole = a.d % 64 == 0 && !none && k_mul == v_mul && heads < (int64_t(1) << 31) &&
+             (one || pages == 1 || (a.ks[0] % a.ks[1] == 0 && a.vs[0] % a.vs[1] == 0));
+  pg.mul = static_cast<int>(k_mul);
+  const void *K = none ? a.Q : a.K, *V = none ? a.Q : a.V;
+  bool made;
+  if (pg.whole) {
+    pg.slab = 1024, pg.sbo = D / 64 * 1024;
+    const int64_t dims[5] = {64, 8, a.d / 64, a.seqs.page / 8, heads};
+    const int64_t k_str[4] = {a.ks[2], 64, 8 * a.ks[2], one ? a.ks[0] : a.ks[1]}, v_str[4] = {a.vs[2], 64, 8 * a.vs[2], one ? a.vs[0] : a.vs[1]};
+    const int boxes[5] = {64, 8, static_cast<int>(a.d) / 64, pg.box / 8, 1};
+    made = make_tmap_view(&mk, K, 5, dims, k_str, boxes) && make_tmap_view(&mv, V, 5, dims, v_str, boxes);
+  } else {
+    pg.slab = BN * 128, pg.sbo = 1024;
+    const int64_t dims[4] = {a.d, a.seqs.page, a.Hkv, pages};
+    const int64_t k_str[3] = {a.ks[2], a.ks[1], a.ks[0]}, v_str[3] = {a.vs[2], a.vs[1], a.vs[0]};
+    const int boxes[4] = {64, pg.box, 1, 1};
+    made = make_tmap_view(&mk, K, 4, dims, k_str, boxes) && make_tmap_view(&mv, V, 4, dims, v_str, boxes);
+  }
+  if (!made) return cudaErrorInvalidValue;
   auto kern = paged_kernel<D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::bytes);
   if (e != cudaSuccess) return e;
   if ((e = plan(w, sp, st)) != cudaSuccess) return e;
-  e = launch_behind(kern, k.ctas, kThreads, Lay<D>::bytes, st, mq, mk, mv, w, sp, out, static_cast<const __nv_bfloat16*>(a.V), a.vs[0], a.vs[1], a.vs[2], a.d, box, a.scale, a.scale * kLog2e);
+  e = launch_behind(kern, k.ctas, kThreads, Lay<D>::bytes, st, mq, mk, mv, w, sp, out, static_cast<const __nv_bfloat16*>(a.V), a.vs[0], a.vs[1], a.vs[2], a.d, pg, a.scale, a.scale * kLog2e);
   if (e != cudaSuccess) return e;
-  return join(w, sp, out, a.dtype, a.d, BM, st);
+  return join(w, sp, out, a.dtype, a.d, BM, a.max_new, st);
 }
 
 Work work_of(const PagedArgs& a) {
@@ -594,7 +650,7 @@ Work work_of(const PagedArgs& a) {
   w.cut.gt = heads_together(g, BM, a.max_new);
   w.cut.nv = a.H / w.cut.gt, w.cut.per_kv = g / w.cut.gt;
   w.cut.tile = BM / w.cut.gt, w.cut.step = 2 * w.cut.tile;
-  w.cut.BN = BN, w.cut.over = 2, w.cut.least = 8, w.cut.ctas = 152;
+  w.cut.shift = 7, w.cut.over = 2, w.cut.least = 8, w.cut.ctas = 152;
   return w;
 }
 
