@@ -20,11 +20,13 @@ inline int heads_together(int group, int rows, int64_t few) {
   return best;
 }
 
-// The kernels: CUDA cores (simt_paged.cu), tensor cores (tc_paged.cu).
+// The kernels: CUDA cores (simt_paged.cu, float32), tensor cores (tc_paged.cu, bf16 up to d = 128; tc_paged_wide.cu, d = 256).
 size_t simt_bytes(const PagedArgs& a);
 cudaError_t simt_paged(const PagedArgs& a, void* ws, cudaStream_t st);
 size_t tc_bytes(const PagedArgs& a);
 cudaError_t tc_paged(const PagedArgs& a, void* ws, cudaStream_t st);
+size_t tc_wide_bytes(const PagedArgs& a);
+cudaError_t tc_paged_wide(const PagedArgs& a, void* ws, cudaStream_t st);
 
 }  // namespace paged
 }  // namespace fbd

@@ -218,13 +218,13 @@ cudaError_t join(const Work& w, const Space& sp, const Out& out, int dtype, int 
 
 }  // namespace paged
 
-namespace {
-bool on_tensor_cores(const PagedArgs& a) { return a.dtype == ATTN_BF16 && a.d <= 128; }
-}  // namespace
-
-size_t paged_bytes(const PagedArgs& a) { return on_tensor_cores(a) ? paged::tc_bytes(a) : paged::simt_bytes(a); }
+size_t paged_bytes(const PagedArgs& a) {
+  return a.dtype != ATTN_BF16 ? paged::simt_bytes(a) : a.d <= 128 ? paged::tc_bytes(a) : paged::tc_wide_bytes(a);
+}
 cudaError_t paged_attention(const PagedArgs& a, void* ws, cudaStream_t st) {
-  return on_tensor_cores(a) ? paged::tc_paged(a, ws, st) : paged::simt_paged(a, ws, st);
+  return a.dtype != ATTN_BF16 ? paged::simt_paged(a, ws, st)
+         : a.d <= 128         ? paged::tc_paged(a, ws, st)
+                              : paged::tc_paged_wide(a, ws, st);
 }
 
 }  // namespace fbd

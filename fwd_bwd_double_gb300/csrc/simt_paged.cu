@@ -1,13 +1,11 @@
-// Attention of new tokens over a paged cache on the CUDA cores: online softmax over blocks of 64 keys, fp32
-// throughout.
+// Attention of new tokens over a paged cache in float32, on the CUDA cores: online softmax over blocks of 64
+// keys, fp32 throughout.
 //
 // A CTA of 256 threads holds R rows (tokens times the query heads that share a key/value head) and streams
 // K and V through shared memory; a row belongs to 16 threads of a half-warp, R / 16 rows to a thread,
 // so that scores, maxima and probabilities pass between them by shuffles and a row of shared memory.
 // Keys that the sequence does not hold are not read; a key hidden from a row has weight 0 there and its
 // value is left out of the sum, whatever it is.
-#include <cuda_bf16.h>
-
 #include "paged_launch.h"
 
 namespace fbd {
@@ -23,24 +21,13 @@ struct Lay {
   static constexpr int bytes = 4 * oRow + BN * 8 * 2;
 };
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T* p);
-template <>
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-template <>
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
-  return make_float4(tc::bf16_lo(v.x), tc::bf16_hi(v.x), tc::bf16_lo(v.y), tc::bf16_hi(v.y));
-}
 __device__ __forceinline__ void put2(float* p, float x, float y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); }
-__device__ __forceinline__ void put2(__nv_bfloat16* p, float x, float y) {
-  *reinterpret_cast<uint32_t*>(p) = ptx::pack_bf16(x, y);
-}
 
-template <typename T, int D, int R>
+template <int D, int R>
 __global__ void __launch_bounds__(kT)
-    paged_kernel(const Work w, const Space sp, const Out out, const T* __restrict__ Q, const T* __restrict__ K,
-                 const T* __restrict__ V, int64_t qs0, int64_t qs1, int64_t qs2, int64_t ks0, int64_t ks1, int64_t ks2,
+    paged_kernel(const Work w, const Space sp, const Out out, const float* __restrict__ Q, const float* __restrict__ K,
+                 const float* __restrict__ V, int64_t qs0, int64_t qs1, int64_t qs2, int64_t ks0, int64_t ks1, int64_t ks2,
                  int64_t vs0, int64_t vs1, int64_t vs2, float c) {
   using L = Lay<D, R>;
   constexpr int RT = R / 16, C2 = D / 32;  // rows, pairs of columns of a thread
@@ -195,7 +182,7 @@ __global__ void __launch_bounds__(kT)
       const int t = r / gt;
       const int64_t h = h0 + r - t * gt, pos = s.row0 + it.t0 + t;
       const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];  // (a row that sees no key: 0)
-      T* dst = static_cast<T*>(out.O) + s.batch * out.os[0] + h * out.os[1] + pos * out.os[2];
+      float* dst = static_cast<float*>(out.O) + s.batch * out.os[0] + h * out.os[1] + pos * out.os[2];
 #pragma unroll
       for (int x = 0; x < C2; ++x) put2(dst + tx * 2 + 32 * x, acc[i][x][0] * inv, acc[i][x][1] * inv);
       if (tx == 0 && out.lse != nullptr)
@@ -206,22 +193,22 @@ __global__ void __launch_bounds__(kT)
   }
 }
 
-template <typename T, int D, int R>
+template <int D, int R>
 cudaError_t launch(const PagedArgs& a, const Work& w, const Space& sp, const Out& out, cudaStream_t st) {
-  auto kern = paged_kernel<T, D, R>;
+  auto kern = paged_kernel<D, R>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D, R>::bytes);
   if (e != cudaSuccess) return e;
   if ((e = plan(w, sp, st)) != cudaSuccess) return e;
-  e = launch_behind(kern, w.cut.ctas, kT, Lay<D, R>::bytes, st, w, sp, out, static_cast<const T*>(a.Q), static_cast<const T*>(a.K),
-                    static_cast<const T*>(a.V), a.qs[0], a.qs[1], a.qs[2], a.ks[0], a.ks[1], a.ks[2], a.vs[0], a.vs[1],
+  e = launch_behind(kern, w.cut.ctas, kT, Lay<D, R>::bytes, st, w, sp, out, static_cast<const float*>(a.Q), static_cast<const float*>(a.K),
+                    static_cast<const float*>(a.V), a.qs[0], a.qs[1], a.qs[2], a.ks[0], a.ks[1], a.ks[2], a.vs[0], a.vs[1],
                     a.vs[2], a.scale * kLog2e);
   if (e != cudaSuccess) return e;
   return join(w, sp, out, a.dtype, D, R, a.max_new, st);
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t rows(const PagedArgs& a, const Work& w, const Space& sp, const Out& out, cudaStream_t st) {
-  return sp.rows == 16 ? launch<T, D, 16>(a, w, sp, out, st) : launch<T, D, 64>(a, w, sp, out, st);
+  return sp.rows == 16 ? launch<D, 16>(a, w, sp, out, st) : launch<D, 64>(a, w, sp, out, st);
 }
 
 // 16 rows a tile where the new tokens of a sequence fit them, else 64.
@@ -251,13 +238,8 @@ cudaError_t simt_paged(const PagedArgs& a, void* ws, cudaStream_t st) {
   const Work w = work_of(a);
   const Space sp = Space::at(ws, w.cut.ctas, a.seqs.B, tile_rows(a), a.d);
   const Out out{a.O, a.lse, {a.os[0], a.os[1], a.os[2]}, {a.ls[0], a.ls[1]}};
-  if (a.dtype == ATTN_BF16) {
-    using T = __nv_bfloat16;
-    return a.d == 32 ? rows<T, 32>(a, w, sp, out, st) : a.d == 64 ? rows<T, 64>(a, w, sp, out, st) : a.d == 96 ? rows<T, 96>(a, w, sp, out, st)
-           : a.d == 128 ? rows<T, 128>(a, w, sp, out, st) : rows<T, 256>(a, w, sp, out, st);
-  }
-  return a.d == 32 ? rows<float, 32>(a, w, sp, out, st) : a.d == 64 ? rows<float, 64>(a, w, sp, out, st) : a.d == 96 ? rows<float, 96>(a, w, sp, out, st)
-         : a.d == 128 ? rows<float, 128>(a, w, sp, out, st) : rows<float, 256>(a, w, sp, out, st);
+  return a.d == 32 ? rows<32>(a, w, sp, out, st) : a.d == 64 ? rows<64>(a, w, sp, out, st) : a.d == 96 ? rows<96>(a, w, sp, out, st)
+         : a.d == 128 ? rows<128>(a, w, sp, out, st) : rows<256>(a, w, sp, out, st);
 }
 
 }  // namespace paged

@@ -26,8 +26,7 @@
 #include <cuda_bf16.h>
 
 #include "handover.h"
-#include "paged_launch.h"
-#include "tmap.h"
+#include "tc_paged.cuh"
 
 namespace fbd {
 namespace paged {
@@ -35,20 +34,16 @@ namespace {
 
 __device__ unsigned int g_err = 0;
 
-constexpr int BM = 128, BN = 128;
 // Warps 0-3: tile 0, 4-7: tile 1, 8: TMA, 9: MMA, 10, 11: values that a row must not see.  384 threads
 // launched with 168 registers; the softmax warps (a row of 128 scores each thread) take 208, the third
 // warpgroup's keep 80: 256 * 208 + 128 * 80 <= 384 * 168.
 constexpr int kThreads = 384;
 constexpr int kRegs = 208, kRegsOther = 80;
-constexpr float kSlack = 256.f;  // the largest P
-constexpr float kShare = .25f;   // ... and its share of the row's sum so far, where it is above 1
 
 template <int D>
 struct Lay {
   static constexpr int kTile = BM * D * 2;       // Q tile, and a K or V entry of the ring
   static constexpr int NS = D == 64 ? 8 : 4;
-  static constexpr int kOut = 32 * 80;           // a warp's outputs on their way: 64 bytes of each row
   static constexpr int oRing = 2 * kTile;
   static constexpr int oOut = oRing + NS * kTile;
   static constexpr int oStat = oOut + 8 * kOut;  // [2][128] (max, sum) of the second half of an item's blocks
@@ -58,61 +53,6 @@ struct Lay {
   static constexpr uint32_t cS = 0, cO = 2 * BN;  // S_m at cS + m BN, O_m at cO + m D
 };
 static_assert(Lay<128>::bytes <= 232448 && Lay<64>::bytes <= 232448, "shared memory");
-
-// How K and V lie in the cache and in the ring.
-struct Pages {
-  int box;       // keys of a box
-  int whole;     // a box takes all columns: its last coordinate is page * mul + head
-  int mul;
-  int sbo, slab; // bytes from eight keys to the next, from 64 columns to the next
-};
-
-// An item as the loading warp gives it to the others, through a ring in shared memory.
-struct Item {
-  int n;            // blocks b0 .. b0 + n - 1; 0: there are no more items
-  int b0;
-  int pair;         // two tiles see the same blocks; else both hold one tile's rows and take the blocks in turn
-  int t0, t1;       // its tokens
-  int start, len;   // of its sequence (paged.h)
-  int last, first;  // the last key that every row sees, the first one
-  int slot;         // of its part of a shared item, -1: it is whole
-  int b, batch, row0, vh, kvh, pad;
-  // some row does not see some key of the block
-  __device__ __forceinline__ bool hides(int kb) const { return kb * BN + BN - 1 > last || kb * BN < first; }
-  __device__ __forceinline__ int count(int m) const { return pair ? n : (n + 1 - m) / 2; }  // blocks of tile m
-};
-
-// The ring's entries of an item: two tiles over the same blocks: K_0 V_0 K_1 V_1 ...; one tile whose blocks
-// go to both in turn: K_0 K_1 V_0 K_2 V_1 K_3 ...; 2 n in all.
-struct Order {
-  int base, n;
-  bool pair;
-  __device__ __forceinline__ int block(int m, int j) const { return pair ? j : 2 * j + m; }
-  __device__ __forceinline__ int V(int i) const {
-    return pair ? base + 2 * i + 1 : base + min(n, 2) + i + min(i, max(n - 2, 0));
-  }
-  __device__ __forceinline__ int K(int i) const { return pair ? base + 2 * i : i < 2 ? base + i : V(i - 2) + 1; }
-};
-
-// Values that were made 0 for the rows that do not see them, added to a row that does (`o` or `part`, its
-// first d columns): one by one from the cache.
-__device__ __noinline__ void add_spoilt(const Work& w, const Item& it, int first, int last, const __nv_bfloat16* V, int64_t s0,
-                                        int64_t s2, int d, __nv_bfloat16* o, float* part) {
-  for (int i = 0; i < it.n; ++i) {
-    if (!it.hides(it.b0 + i)) continue;
-    for (int k = max((it.b0 + i) * BN, first); k <= min((it.b0 + i) * BN + BN - 1, last); ++k) {
-      const int pg = page_at(w.seqs, it.b, k / w.seqs.page);
-      if (pg < 0) continue;
-      const __nv_bfloat16* v = V + pg * s0 + static_cast<int64_t>(k % w.seqs.page) * s2;
-      for (int x = 0; x < d; ++x) {
-        const float y = __bfloat162float(v[x]);
-        if (isfinite(y)) continue;
-        if (part != nullptr) part[x] += y;
-        else o[x] = __float2bfloat16(__bfloat162float(o[x]) + y);
-      }
-    }
-  }
-}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -352,33 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // every entry up to this one in turn: a barrier two phases back would look complete
         for (; seen <= e; ++seen) wait(&full[seen % NS], (seen / NS) & 1);
         if (!it->hides(b0 + i)) continue;
-        uint8_t* V = sm + L::oRing + s * L::kTile;
-        const int held = min(max(it->len - (b0 + i) * BN, 0), BN);  // keys behind them may hold anything
-        bool some = false;
-        for (int r = threadIdx.x - 320; r < BN; r += 64) {
-          uint8_t* row = V + (r >> 3) * pg.sbo + (r & 7) * 128;
-          for (int u = 0; u < SL; ++u, row += pg.slab) {
-            uint4* at = reinterpret_cast<uint4*>(row);  // (its 16-byte pieces in another order)
-            if (r >= held) {
-#pragma unroll
-              for (int ch = 0; ch < 8; ++ch) at[ch] = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            uint32_t top = 0;  // an exponent of ones carries into the sign's place
-            uint4 x[8];
-#pragma unroll
-            for (int ch = 0; ch < 8; ++ch) x[ch] = at[ch ^ (r & 7)];
-#pragma unroll
-            for (int ch = 0; ch < 8; ++ch)
-              top |= ((x[ch].x & 0x7f807f80u) + 0x00800080u) | ((x[ch].y & 0x7f807f80u) + 0x00800080u) |
-                     ((x[ch].z & 0x7f807f80u) + 0x00800080u) | ((x[ch].w & 0x7f807f80u) + 0x00800080u);
-            if ((top & 0x80008000u) == 0) continue;
-            some = true;
-            uint16_t* e = reinterpret_cast<uint16_t*>(row);
-            for (int k = 0; k < 64; ++k)
-              if ((e[k] & 0x7f80u) == 0x7f80u) e[k] = 0;
-          }
-        }
+        const bool some = hide_values(sm + L::oRing + s * L::kTile, BN, min(max(it->len - (b0 + i) * BN, 0), BN), SL, pg);
         if (some) spoilt[n & 7] = n + 1;
         ptx::fence_proxy_async_smem();
         __syncwarp();
@@ -396,23 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + L::cS + m * BN + lane_off, tO = tmem + L::cO + lane_off;
     const uint64_t c2 = tc::pk2f(c, c);
     const int rt = r / gt, rh = r - rt * gt;  // this row's token of the tile, and its head
-    uint8_t* mine_out = sm + L::oOut + warp * L::kOut;
-    // 64 bytes of each live row of the warp to `to`, its own row's address.
-    auto put_rows = [&](const uint32_t (&x)[16], uint8_t* to, bool live) {
-      __syncwarp();
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        *reinterpret_cast<uint4*>(mine_out + lane * 80 + u * 16) = make_uint4(x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
-      __syncwarp();
-      const unsigned rows = __ballot_sync(0xffffffffu, live);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int row = u * 8 + (lane >> 2);
-        uint8_t* at = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), row));
-        const uint4 v = *reinterpret_cast<const uint4*>(mine_out + row * 80 + (lane & 3) * 16);
-        if (rows >> row & 1) *reinterpret_cast<uint4*>(at + (lane & 3) * 16) = v;
-      }
-    };
+    uint8_t* stage = sm + L::oOut + warp * kOut;
     int T = 0, shared = 0;
     const Item* it;
     for (int n = 0; (it = item(n)) != nullptr; ++n) {
@@ -557,10 +455,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t pk[16];
 #pragma unroll
             for (int t = 0; t < 16; ++t) pk[t] = ptx::pack_bf16(tc::f(a[2 * t]), tc::f(a[2 * t + 1]));
-            put_rows(pk, reinterpret_cast<uint8_t*>(dst) + ch * 64, live);
+            put_rows(stage, pk, reinterpret_cast<uint8_t*>(dst) + ch * 64, live);
           } else {
-            put_rows(reinterpret_cast<const uint32_t(&)[16]>(a[0]), reinterpret_cast<uint8_t*>(part) + ch * 128, live);
-            put_rows(reinterpret_cast<const uint32_t(&)[16]>(a[16]), reinterpret_cast<uint8_t*>(part) + ch * 128 + 64, live);
+            put_rows(stage, reinterpret_cast<const uint32_t(&)[16]>(a[0]), reinterpret_cast<uint8_t*>(part) + ch * 128, live);
+            put_rows(stage, reinterpret_cast<const uint32_t(&)[16]>(a[16]), reinterpret_cast<uint8_t*>(part) + ch * 128 + 64, live);
           }
         }
         __syncwarp();
@@ -601,44 +499,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D>
 cudaError_t launch(const PagedArgs& a, const Work& w, const Space& sp, const Out& out, cudaStream_t st) {
   alignas(64) CUtensorMap mq, mk, mv;
-  const Cut& k = w.cut;
-  const bool none = a.seqs.pages == 0;  // no key anywhere: a tensor that is never read
-  const int64_t q_dims[5] = {a.d, k.gt, a.seqs.N, k.nv, a.seqs.cu != nullptr ? 1 : a.seqs.B};
-  const int64_t q_str[4] = {a.qs[1], a.qs[2], a.qs[1] * k.gt, a.qs[0]};
-  const int q_box[5] = {64, k.gt, k.tile, 1, 1};
-  if (!make_tmap_view(&mq, a.Q, 5, q_dims, q_str, q_box)) return cudaErrorInvalidValue;
   Pages pg;
-  pg.box = BN;  // as many keys as divide a page's
-  while (a.seqs.page % pg.box != 0) pg.box /= 2;
-  // All columns in a box: of whole slabs, and pages a multiple of the heads' stride apart (K and V alike, and
-  // within a coordinate).
-  const int64_t pages = none ? 1 : a.seqs.pages, one = a.Hkv == 1 ? 1 : 0;
-  const int64_t k_mul = one ? 1 : pages == 1 ? 0 : a.ks[0] / a.ks[1], v_mul = one ? 1 : pages == 1 ? 0 : a.vs[0] / a.vs[1];
-  const int64_t heads = (pages - 1) * k_mul + a.Hkv;
-  pg.whole = a.d % 64 == 0 && !none && k_mul == v_mul && heads < (int64_t(1) << 31) &&
-             (one || pages == 1 || (a.ks[0] % a.ks[1] == 0 && a.vs[0] % a.vs[1] == 0));
-  pg.mul = static_cast<int>(k_mul);
-  const void *K = none ? a.Q : a.K, *V = none ? a.Q : a.V;
-  bool made;
-  if (pg.whole) {
-    pg.slab = 1024, pg.sbo = D / 64 * 1024;
-    const int64_t dims[5] = {64, 8, a.d / 64, a.seqs.page / 8, heads};
-    const int64_t k_str[4] = {a.ks[2], 64, 8 * a.ks[2], one ? a.ks[0] : a.ks[1]}, v_str[4] = {a.vs[2], 64, 8 * a.vs[2], one ? a.vs[0] : a.vs[1]};
-    const int boxes[5] = {64, 8, static_cast<int>(a.d) / 64, pg.box / 8, 1};
-    made = make_tmap_view(&mk, K, 5, dims, k_str, boxes) && make_tmap_view(&mv, V, 5, dims, v_str, boxes);
-  } else {
-    pg.slab = BN * 128, pg.sbo = 1024;
-    const int64_t dims[4] = {a.d, a.seqs.page, a.Hkv, pages};
-    const int64_t k_str[3] = {a.ks[2], a.ks[1], a.ks[0]}, v_str[3] = {a.vs[2], a.vs[1], a.vs[0]};
-    const int boxes[4] = {64, pg.box, 1, 1};
-    made = make_tmap_view(&mk, K, 4, dims, k_str, boxes) && make_tmap_view(&mv, V, 4, dims, v_str, boxes);
-  }
-  if (!made) return cudaErrorInvalidValue;
+  if (!make_maps(a, w.cut, BN, D / 64, &mq, &mk, &mv, pg)) return cudaErrorInvalidValue;
   auto kern = paged_kernel<D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::bytes);
   if (e != cudaSuccess) return e;
   if ((e = plan(w, sp, st)) != cudaSuccess) return e;
-  e = launch_behind(kern, k.ctas, kThreads, Lay<D>::bytes, st, mq, mk, mv, w, sp, out, static_cast<const __nv_bfloat16*>(a.V), a.vs[0], a.vs[1], a.vs[2], a.d, pg, a.scale, a.scale * kLog2e);
+  e = launch_behind(kern, w.cut.ctas, kThreads, Lay<D>::bytes, st, mq, mk, mv, w, sp, out,
+                    static_cast<const __nv_bfloat16*>(a.V), a.vs[0], a.vs[1], a.vs[2], a.d, pg, a.scale, a.scale * kLog2e);
   if (e != cudaSuccess) return e;
   return join(w, sp, out, a.dtype, a.d, BM, a.max_new, st);
 }
