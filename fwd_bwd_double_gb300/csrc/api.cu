@@ -320,7 +320,7 @@ attn_status_t attn_device_status(void* stream) {
                          fbd::tc_bob_take_error() | fbd::tc_bob128_take_error() | fbd::tc32_take_error() |
                          fbd::selftest_take_error() | fbd::tc_diff_fwd_take_error() |
                          fbd::tc_diff_bwd_take_error() | fbd::tc_paged_take_error() |
-                         fbd::tc_paged_wide_take_error();
+                         fbd::tc_paged_wide_take_error() | fbd::token_paged_take_error();
   if (flags != 0) return fail(ATTN_ERR_TIMEOUT, "a device-side bounded wait gave up%s");
   return ATTN_OK;
 }

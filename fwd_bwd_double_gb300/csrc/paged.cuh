@@ -94,6 +94,66 @@ __device__ __forceinline__ Blocks blocks_of(const Work& w, const Seq& s, int t0,
   return Blocks{j0, ((hi - 1) >> w.cut.shift) + 1 - j0};
 }
 
+// The units of a tile of a sequence, all groups of heads.
+__device__ __forceinline__ int64_t tile_units(const Work& w, const Seq& s, int tile) {
+  const int t0 = tile * w.cut.step, t1 = min(s.n, t0 + w.cut.step);
+  const Blocks k = blocks_of(w, s, t0, t1);
+  return static_cast<int64_t>(t1 - t0 > w.cut.tile ? 2 : 1) * k.n + w.cut.over;
+}
+__device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+// The plan for one CTA, by one warp of its own (every lane gets it): for calls whose sequences have few tiles, where
+// it costs less than a launch.
+__device__ __forceinline__ void plan_here(const Work& w, int p, Head& head, Start& start) {
+  const int lane = threadIdx.x & 31, B = w.seqs.B, step = w.cut.step;
+  auto units = [&](int b) {
+    int64_t v = 0;
+    if (b < B) {
+      const Seq s = seq_at(w.seqs, b);
+      for (int64_t t = 0; t * step < s.n; ++t) v += tile_units(w, s, static_cast<int>(t));
+    }
+    return v * w.cut.nv;
+  };
+  int64_t total = 0;
+  const int64_t mine = units(lane);  // (the first 32 sequences are looked at once)
+  for (int b0 = 0; b0 < B; b0 += 32) total += b0 == 0 ? mine : units(b0 + lane);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  const int64_t even = (total + w.cut.ctas - 1) / w.cut.ctas;
+  head = Head{total, even > w.cut.least ? even : w.cut.least};
+  start = Start{0, -1, 0, 0, 0};
+  const int64_t x = head.stretch * p;
+  if (x >= total) return;
+  int64_t at = 0;
+  for (int b0 = 0; b0 < B; b0 += 32) {
+    const int64_t v = b0 == 0 ? mine : units(b0 + lane), cum = at + warp_scan(v, lane);
+    const unsigned behind = __ballot_sync(0xffffffffu, cum > x);
+    if (behind == 0) {
+      at = __shfl_sync(0xffffffffu, cum, 31);
+      continue;
+    }
+    const int from = __ffs(behind) - 1;
+    int64_t base = __shfl_sync(0xffffffffu, cum - v, from);
+    const Seq s = seq_at(w.seqs, b0 + from);
+    for (int t = 0;; ++t) {
+      const int64_t u = tile_units(w, s, t);
+      if (base + u * w.cut.nv > x) {
+        const int64_t vh = (x - base) / u;
+        start = Start{base + vh * u, b0 + from, t, static_cast<int>(vh), 0};
+        return;
+      }
+      base += u * w.cut.nv;
+    }
+  }
+}
+
 // The items of a CTA's stretch, one after another.
 struct Walk {
   int64_t pos, from, to, stretch;  // this item on the line; the stretch
@@ -115,10 +175,9 @@ struct Walk {
     k1 = end >= to ? static_cast<int>(max(static_cast<int64_t>(0), (to - pos + weight - 1) / weight)) : n;
   }
   // false: nothing to do
-  __device__ __forceinline__ bool begin(const Work& w, const Space& sp, int p) {
-    const Start st = sp.start[p];
+  __device__ __forceinline__ bool begin(const Work& w, const Space& sp, int p) { return begin(w, *sp.head, sp.start[p], p); }
+  __device__ __forceinline__ bool begin(const Work& w, const Head& h, const Start& st, int p) {
     if (st.b < 0) return false;
-    const Head h = *sp.head;
     stretch = h.stretch;
     from = stretch * p, to = min(from + stretch, h.total);
     pos = st.pos, b = st.b, tile = st.tile, vh = st.vh;

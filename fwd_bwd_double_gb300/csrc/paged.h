@@ -117,5 +117,6 @@ size_t paged_bytes(const PagedArgs& a);
 cudaError_t paged_attention(const PagedArgs& a, void* ws, cudaStream_t st);
 uint32_t tc_paged_take_error();
 uint32_t tc_paged_wide_take_error();
+uint32_t token_paged_take_error();
 
 }  // namespace fbd

@@ -25,6 +25,10 @@ size_t simt_bytes(const PagedArgs& a);
 cudaError_t simt_paged(const PagedArgs& a, void* ws, cudaStream_t st);
 size_t tc_bytes(const PagedArgs& a);
 cudaError_t tc_paged(const PagedArgs& a, void* ws, cudaStream_t st);
+// ... and warp-level products for up to 16 rows of a sequence (paged_token.cu, bf16).
+inline bool few_rows(const PagedArgs& a) { return a.max_new * (a.H / a.Hkv) <= 16; }
+size_t token_bytes(const PagedArgs& a);
+cudaError_t token_paged(const PagedArgs& a, void* ws, cudaStream_t st);
 size_t tc_wide_bytes(const PagedArgs& a);
 cudaError_t tc_paged_wide(const PagedArgs& a, void* ws, cudaStream_t st);
 

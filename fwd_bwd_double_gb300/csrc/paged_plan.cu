@@ -11,21 +11,6 @@ namespace {
 
 constexpr int kT = 1024;
 
-__device__ __forceinline__ int64_t tile_units(const Work& w, const Seq& s, int tile) {
-  const int t0 = tile * w.cut.step, t1 = min(s.n, t0 + w.cut.step);
-  const Blocks k = blocks_of(w, s, t0, t1);
-  return static_cast<int64_t>(t1 - t0 > w.cut.tile ? 2 : 1) * k.n + w.cut.over;
-}
-
-__device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
-  }
-  return v;
-}
-
 constexpr int kNear = 2048;  // sequences whose ends are kept in shared memory
 
 __global__ void __launch_bounds__(kT) plan_kernel(const Work w, const Space sp) {
@@ -65,55 +50,32 @@ __global__ void __launch_bounds__(kT) plan_kernel(const Work w, const Space sp) 
   const int64_t total = carry;
   const int64_t even = (total + w.cut.ctas - 1) / w.cut.ctas, stretch = even > w.cut.least ? even : w.cut.least;
   if (threadIdx.x == 0) *sp.head = Head{total, stretch};
-  for (int p0 = warp * 32; p0 < w.cut.ctas; p0 += kT) {
-    const int p = p0 + lane;
+  for (int p = warp; p < w.cut.ctas; p += kT / 32) {
     const int64_t x = stretch * p;
-    const bool some = p < w.cut.ctas && x < total;
+    if (lane == 0) sp.tail[p] = Tail{0, 0, 0, 0};
+    if (x >= total) {
+      if (lane == 0) sp.start[p] = Start{0, -1, 0, 0, 0};
+      continue;
+    }
     int hi = B - 1;  // the first sequence that ends behind x
-    Seq s{};
-    int64_t base = 0;
-    if (some) {
-      for (int lo = -1; hi - lo > 1;) {
-        const int mid = (lo + hi) >> 1;
-        if (ends[mid] > x) hi = mid; else lo = mid;
-      }
-      s = seq_at(w.seqs, hi);
-      base = hi > 0 ? ends[hi - 1] : 0;
+    for (int lo = -1; hi - lo > 1;) {
+      const int mid = (lo + hi) >> 1;
+      if (ends[mid] > x) hi = mid; else lo = mid;
     }
-    if (p < w.cut.ctas) {
-      sp.tail[p] = Tail{0, 0, 0, 0};
-      if (!some) sp.start[p] = Start{0, -1, 0, 0, 0};
-    }
-    // ... and its tile that does: looked for by the thread where there are few, else by the warp
-    bool found = !some;
-    for (int t = 0; !found && t < 4 && static_cast<int64_t>(t) * step < s.n; ++t) {
-      const int64_t u = tile_units(w, s, t), all = u * w.cut.nv;
-      if (base + all > x) {
-        const int64_t vh = (x - base) / u;
-        sp.start[p] = Start{base + vh * u, hi, t, static_cast<int>(vh), 0};
-        found = true;
-      } else {
-        base += all;
-      }
-    }
-    for (unsigned rest = __ballot_sync(0xffffffffu, !found); rest != 0; rest &= rest - 1) {
-      const int from = __ffs(rest) - 1, qb = __shfl_sync(0xffffffffu, hi, from);
-      const int64_t at0 = __shfl_sync(0xffffffffu, base, from), y = __shfl_sync(0xffffffffu, x, from);
-      const Seq q = seq_at(w.seqs, qb);
-      int64_t at = at0;
-      for (int64_t t0 = 4; t0 * step < q.n; t0 += 32) {
-        const int64_t t = t0 + lane;
-        const int64_t u = t * step < q.n ? tile_units(w, q, static_cast<int>(t)) : 0, cum = at + warp_scan(u * w.cut.nv, lane);
-        const unsigned behind = __ballot_sync(0xffffffffu, cum > y);
-        if (behind != 0) {
-          if (lane == __ffs(behind) - 1) {
-            const int64_t b = cum - u * w.cut.nv, vh = (y - b) / u;
-            sp.start[p0 + from] = Start{b + vh * u, qb, static_cast<int>(t), static_cast<int>(vh), 0};
-          }
-          break;
+    const Seq s = seq_at(w.seqs, hi);
+    int64_t at = hi > 0 ? ends[hi - 1] : 0;
+    for (int64_t t0 = 0; t0 * step < s.n; t0 += 32) {  // ... and its tile that does
+      const int64_t t = t0 + lane;
+      const int64_t u = t * step < s.n ? tile_units(w, s, static_cast<int>(t)) : 0, cum = at + warp_scan(u * w.cut.nv, lane);
+      const unsigned behind = __ballot_sync(0xffffffffu, cum > x);
+      if (behind != 0) {
+        if (lane == __ffs(behind) - 1) {
+          const int64_t b = cum - u * w.cut.nv, vh = (x - b) / u;
+          sp.start[p] = Start{b + vh * u, hi, static_cast<int>(t), static_cast<int>(vh), 0};
         }
-        at = __shfl_sync(0xffffffffu, cum, 31);
+        break;
       }
+      at = __shfl_sync(0xffffffffu, cum, 31);
     }
   }
 }
@@ -219,10 +181,11 @@ cudaError_t join(const Work& w, const Space& sp, const Out& out, int dtype, int 
 }  // namespace paged
 
 size_t paged_bytes(const PagedArgs& a) {
-  return a.dtype != ATTN_BF16 ? paged::simt_bytes(a) : a.d <= 128 ? paged::tc_bytes(a) : paged::tc_wide_bytes(a);
+  return a.dtype != ATTN_BF16 ? paged::simt_bytes(a) : paged::few_rows(a) ? paged::token_bytes(a) : a.d <= 128 ? paged::tc_bytes(a) : paged::tc_wide_bytes(a);
 }
 cudaError_t paged_attention(const PagedArgs& a, void* ws, cudaStream_t st) {
   return a.dtype != ATTN_BF16 ? paged::simt_paged(a, ws, st)
+         : paged::few_rows(a) ? paged::token_paged(a, ws, st)
          : a.d <= 128         ? paged::tc_paged(a, ws, st)
                               : paged::tc_paged_wide(a, ws, st);
 }

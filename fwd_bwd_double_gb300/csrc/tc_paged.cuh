@@ -31,8 +31,8 @@ struct Item {
   int last, first;  // the last key that every row sees, the first one
   int slot;         // of its part of a shared item, -1: it is whole
   int b, batch, row0, vh, kvh, pad;
-  // some row does not see some key of the block
-  __device__ __forceinline__ bool hides(int kb) const { return kb * BN + BN - 1 > last || kb * BN < first; }
+  // some row does not see some key of the block (of `keys` keys)
+  __device__ __forceinline__ bool hides(int kb, int keys = BN) const { return kb * keys + keys - 1 > last || kb * keys < first; }
   __device__ __forceinline__ int count(int m) const { return pair ? n : (n + 1 - m) / 2; }  // blocks of tile m
 };
 
@@ -51,10 +51,11 @@ struct Order {
 // Values that were made 0 for the rows that do not see them, added to a row that does (`o` or `part`, its
 // first d columns): one by one from the cache.
 static __device__ __noinline__ void add_spoilt(const Work& w, const Item& it, int first, int last, const __nv_bfloat16* V, int64_t s0,
-                                        int64_t s2, int d, __nv_bfloat16* o, float* part) {
+                                        int64_t s2, int d, __nv_bfloat16* o, float* part, int keys = BN) {
   for (int i = 0; i < it.n; ++i) {
-    if (!it.hides(it.b0 + i)) continue;
-    for (int k = max((it.b0 + i) * BN, first); k <= min((it.b0 + i) * BN + BN - 1, last); ++k) {
+    const int k0 = (it.b0 + i) * keys;
+    if (!it.hides(it.b0 + i, keys)) continue;
+    for (int k = max(k0, first); k <= min(k0 + keys - 1, last); ++k) {
       const int pg = page_at(w.seqs, it.b, k / w.seqs.page);
       if (pg < 0) continue;
       const __nv_bfloat16* v = V + pg * s0 + static_cast<int64_t>(k % w.seqs.page) * s2;
@@ -118,13 +119,13 @@ __device__ __forceinline__ bool hide_values(uint8_t* V, int keys, int held, int 
   return some;
 }
 
-// Tensor maps of Q (a tile's tokens and heads), K and V in entries of `keys` keys and `slabs` slabs of 64 columns.
+// Tensor maps of Q (a tile's tokens and heads; mq may be null), K and V in entries of `keys` keys and `slabs` slabs of 64 columns.
 inline bool make_maps(const PagedArgs& a, const Cut& k, int keys, int slabs, void* mq, void* mk, void* mv, Pages& pg) {
   const bool none = a.seqs.pages == 0;  // no key anywhere: a tensor that is never read
   const int64_t q_dims[5] = {a.d, k.gt, a.seqs.N, k.nv, a.seqs.cu != nullptr ? 1 : a.seqs.B};
   const int64_t q_str[4] = {a.qs[1], a.qs[2], a.qs[1] * k.gt, a.qs[0]};
   const int q_box[5] = {64, k.gt, k.tile, 1, 1};
-  if (!make_tmap_view(mq, a.Q, 5, q_dims, q_str, q_box)) return false;
+  if (mq != nullptr && !make_tmap_view(mq, a.Q, 5, q_dims, q_str, q_box)) return false;
   pg.box = keys;  // as many keys as divide a page's
   while (a.seqs.page % pg.box != 0) pg.box /= 2;
   // All columns in a box: of whole slabs, and pages a multiple of the heads' stride apart (K and V alike, and
