@@ -87,69 +87,102 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, float4 v) {
 
 constexpr int kJ = 256;
 
-// Block (p, y): every gridDim.y-th run of `per` rows of the item that begins in CTA p's stretch and goes on behind it.  A row's columns
-// are d / 4 threads' (rounded up to a power of two); such groups take a row each, or, where the
-// parts are many, parts of one row after another.
 template <typename T>
-__global__ void __launch_bounds__(kJ) join_kernel(const Work w, const Space sp, const Out out, int d, int tile_rows, int per) {
+__device__ __forceinline__ void put_row(const Work& w, const Out& out, const Seq& s, const Tail& q, int row, int t0, int col, int d,
+                                        float4 o, float m, float l) {
+  const int t = row / w.cut.gt, hh = row - t * w.cut.gt;
+  const float inv = l == 0.f ? 0.f : 1.f / l;  // (a row that sees no key: 0)
+  const int64_t h = static_cast<int64_t>(q.vh) * w.cut.gt + hh, pos = s.row0 + t0 + t;
+  if (col < d)
+    put(static_cast<T*>(out.O) + s.batch * out.os[0] + h * out.os[1] + pos * out.os[2] + col,
+        make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+  if (col == 0 && out.lse != nullptr)
+    out.lse[s.batch * out.ls[0] + h * out.ls[1] + pos] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
+// Block (p, y): every gridDim.y-th run of rows of the item that begins in CTA p's stretch and goes on behind it.  A
+// row's columns are d / 4 threads' (rounded up to a power of two).  Few parts: such groups take a row each;
+// many: a row at a time, its parts' weights formed once and the parts shared by the groups.
+template <typename T>
+__global__ void __launch_bounds__(kJ) join_kernel(const Work w, const Space sp, const Out out, int d, int tile_rows) {
+  __shared__ float weight[kMaxCtas];
   __shared__ float4 sum[kJ];
-  __shared__ float sl[kJ], sm[kJ];
+  __shared__ float total[2];
   ptx::grid_dependency_wait();
   const Tail q = sp.tail[blockIdx.x];
   if (q.parts == 0) return;
   const Seq s = seq_at(w.seqs, q.b);
   const int t0 = q.tile * w.cut.step, t1 = min(s.n, t0 + w.cut.step), gt = w.cut.gt;
-  const int rows = (t1 - t0) * gt, p = blockIdx.x;
+  const int rows = (t1 - t0) * gt, p = blockIdx.x, parts = q.parts;
   int C = 8;
   while (C * 4 < d) C *= 2;
   const int groups = kJ / C, g = threadIdx.x / C, col = (threadIdx.x & (C - 1)) * 4;
-  const bool wide = q.parts > 2 * groups;  // groups share a row
-  for (int r0 = blockIdx.y * per; r0 < rows; r0 += gridDim.y * per)
-  for (int rr = r0, r1 = min(rows, r0 + per); rr < r1; rr += wide ? 1 : groups) {
-    const int row = rr + (wide ? 0 : g);
-    const bool live = row < r1;
-    const int t = live ? row / gt : 0, hh = live ? row - t * gt : 0;
-    const int tl = t / w.cut.tile, at = tl * tile_rows + (t - tl * w.cut.tile) * gt + hh;  // in a slot
-    float m = -INFINITY, l = 0.f;
+  auto in_slot = [&](int row) {
+    const int t = row / gt, tl = t / w.cut.tile;
+    return tl * tile_rows + (t - tl * w.cut.tile) * gt + row - t * gt;
+  };
+  auto slot_of = [&](int k) { return k == 0 ? 2 * p + 1 : 2 * (p + k); };
+  if (parts <= 4) {
+    for (int row = blockIdx.y * groups + g; row < rows; row += gridDim.y * groups) {
+      const int at = in_slot(row);
+      float2 x[4];
+      float4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        x[k] = make_float2(-INFINITY, 0.f), v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k >= parts) continue;
+        x[k] = *sp.ml(slot_of(k), at);
+        if (col < d) v[k] = *reinterpret_cast<const float4*>(sp.o(slot_of(k), at) + col);
+      }
+      const float m = fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x)), sub = m == -INFINITY ? 0.f : m;
+      float l = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float f = ptx::ex2(x[k].x - sub);
+        l = fmaf(f, x[k].y, l);
+        o.x = fmaf(f, v[k].x, o.x), o.y = fmaf(f, v[k].y, o.y), o.z = fmaf(f, v[k].z, o.z), o.w = fmaf(f, v[k].w, o.w);
+      }
+      put_row<T>(w, out, s, q, row, t0, col, d, o, m, l);
+    }
+    return;
+  }
+  for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+    const int at = in_slot(row);
+    __syncthreads();  // the row before has been read
+    if (threadIdx.x < 32) {
+      float m = -INFINITY, l = 0.f;
+      for (int k = threadIdx.x; k < parts; k += 32) m = fmaxf(m, sp.ml(slot_of(k), at)->x);
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+      const float sub = m == -INFINITY ? 0.f : m;
+      for (int k = threadIdx.x; k < parts; k += 32) {
+        const float2 x = *sp.ml(slot_of(k), at);
+        const float f = ptx::ex2(x.x - sub);
+        weight[k] = f, l = fmaf(f, x.y, l);
+      }
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+      if (threadIdx.x == 0) total[0] = m, total[1] = l;
+    }
+    __syncthreads();
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (live) {
-#pragma unroll 4
-      for (int k = wide ? g : 0; k < q.parts; k += wide ? groups : 1) {
-        const int slot = k == 0 ? 2 * p + 1 : 2 * (p + k);
-        const float2 x = *sp.ml(slot, at);
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (col < d) v = *reinterpret_cast<const float4*>(sp.o(slot, at) + col);
-        const float mn = fmaxf(m, x.x), sub = mn == -INFINITY ? 0.f : mn;
-        const float a = ptx::ex2(m - sub), b = ptx::ex2(x.x - sub);
-        m = mn, l = fmaf(l, a, x.y * b);
-        o.x = fmaf(o.x, a, v.x * b), o.y = fmaf(o.y, a, v.y * b);
-        o.z = fmaf(o.z, a, v.z * b), o.w = fmaf(o.w, a, v.w * b);
+    if (col < d) {
+#pragma unroll 8
+      for (int k = g; k < parts; k += groups) {
+        const float4 v = *reinterpret_cast<const float4*>(sp.o(slot_of(k), at) + col);
+        const float f = weight[k];
+        o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y), o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
       }
     }
-    if (wide) {
-      __syncthreads();  // the row before has been read
-      sum[threadIdx.x] = o, sm[threadIdx.x] = m, sl[threadIdx.x] = l;
-      __syncthreads();
-      if (g == 0) {
-        for (int k = 1; k < groups; ++k) {
-          const int u = k * C + threadIdx.x;
-          const float4 v = sum[u];
-          const float mn = fmaxf(m, sm[u]), sub = mn == -INFINITY ? 0.f : mn;
-          const float a = ptx::ex2(m - sub), b = ptx::ex2(sm[u] - sub);
-          m = mn, l = fmaf(l, a, sl[u] * b);
-          o.x = fmaf(o.x, a, v.x * b), o.y = fmaf(o.y, a, v.y * b);
-          o.z = fmaf(o.z, a, v.z * b), o.w = fmaf(o.w, a, v.w * b);
-        }
+    sum[threadIdx.x] = o;
+    __syncthreads();
+    if (g == 0) {
+      for (int k = 1; k < groups; ++k) {
+        const float4 v = sum[k * C + threadIdx.x];
+        o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
       }
-    }
-    if (live && (!wide || g == 0)) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;  // (a row that sees no key: 0)
-      const int64_t h = static_cast<int64_t>(q.vh) * gt + hh, pos = s.row0 + t0 + t;
-      if (col < d)
-        put(static_cast<T*>(out.O) + s.batch * out.os[0] + h * out.os[1] + pos * out.os[2] + col,
-            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-      if (col == 0 && out.lse != nullptr)
-        out.lse[s.batch * out.ls[0] + h * out.ls[1] + pos] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+      put_row<T>(w, out, s, q, row, t0, col, d, o, total[0], total[1]);
     }
   }
 }
@@ -163,10 +196,9 @@ cudaError_t plan(const Work& w, const Space& sp, cudaStream_t st) {
 
 cudaError_t join(const Work& w, const Space& sp, const Out& out, int dtype, int d, int tile_rows, int64_t few, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
-  // A row a block where items have few (each then has many parts), else eight.
+  // Blocks for up to eight rows of an item (a row each where the parts are many, eight or four rows each where few).
   const int64_t rows = (few < w.cut.step ? few : w.cut.step) * w.cut.gt;
-  const int per = rows <= 32 ? 1 : 8;
-  cfg.gridDim = dim3(static_cast<unsigned>(w.cut.ctas), static_cast<unsigned>((rows + per - 1) / per));
+  cfg.gridDim = dim3(static_cast<unsigned>(w.cut.ctas), static_cast<unsigned>(rows <= 8 ? rows : rows <= 32 ? 8 : 32));
   cfg.blockDim = dim3(kJ);
   cfg.stream = st;
   cudaLaunchAttribute attr{};
@@ -174,8 +206,8 @@ cudaError_t join(const Work& w, const Space& sp, const Out& out, int dtype, int 
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return dtype == ATTN_BF16 ? cudaLaunchKernelEx(&cfg, join_kernel<__nv_bfloat16>, w, sp, out, d, tile_rows, per)
-                            : cudaLaunchKernelEx(&cfg, join_kernel<float>, w, sp, out, d, tile_rows, per);
+  return dtype == ATTN_BF16 ? cudaLaunchKernelEx(&cfg, join_kernel<__nv_bfloat16>, w, sp, out, d, tile_rows)
+                            : cudaLaunchKernelEx(&cfg, join_kernel<float>, w, sp, out, d, tile_rows);
 }
 
 }  // namespace paged

@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D>::per_sm)
     Walk it;
     bool more = it.begin(w, head, start, p) && *abort_flag == 0, go = true;
     int E = 0, n = 0;
-    const int box = pg.box, per = MK / box;
+    const int per = MK / pg.box;
     const int c0 = pg.whole ? 0 : lane % SL, g0 = pg.whole ? lane : lane / SL;  // this lane's box
     Tail tail{0, 0, 0, 0};
     for (; more && go; more = it.next(w), ++n) {
@@ -116,32 +116,20 @@ __global__ void __launch_bounds__(kThreads, Lay<D>::per_sm)
         ptx::mbar_arrive(&known[n & 7]);
       }
       if (!it.whole() && it.k0 == 0) tail = Tail{it.b, it.tile, it.vh, it.parts(p)};
-      for (int j = 0; j < nb; ++j) {
-        const int s = E % NS, k0 = (b0 + j) * MK + g0 * box, en = k0 / w.seqs.page;
-        const int page = g0 < per && k0 < it.s.len ? page_at(w.seqs, it.b, en) : -1;
+      Box x = box_at(w, pg, it.s, it.b, b0 * MK, g0, per);
+      for (int j = 0; j < nb; ++j, ++E) {
+        const int s = E % NS;
         if (E >= NS) go = wait(&empty[s], ((E / NS) - 1) & 1) && go;
         go = __all_sync(0xffffffffu, go);
         if (!go) break;
-        const uint32_t run = g0 < per && page < 0 && k0 < it.s.len ? ((1u << (box / 16)) - 1u) << (g0 * (box / 16)) : 0u;
-        const uint32_t all = __reduce_or_sync(0xffffffffu, run);
         if (lane == 0) {
-          hidden[s] = static_cast<uint8_t>(all);
+          hidden[s] = static_cast<uint8_t>(x.hidden);
           ptx::mbar_expect_tx(&full[s], 2 * L::kTile);
         }
         __syncwarp();
-        if (g0 < per) {
-          uint8_t* dst = sm + s * 2 * L::kTile + (g0 * box >> 3) * pg.sbo + c0 * pg.slab;
-          const int slot = page < 0 ? 0 : k0 - en * w.seqs.page;
-          if (pg.whole) {
-            const int at = page < 0 ? -1 : page * pg.mul + kvh;
-            ptx::tma_load_5d(dst, &tmK, &full[s], 0, 0, 0, slot >> 3, at);
-            ptx::tma_load_5d(dst + L::kTile, &tmV, &full[s], 0, 0, 0, slot >> 3, at);
-          } else {
-            ptx::tma_load_4d(dst, &tmK, &full[s], c0 * 64, slot, kvh, page);
-            ptx::tma_load_4d(dst + L::kTile, &tmV, &full[s], c0 * 64, slot, kvh, page);
-          }
-        }
-        ++E;
+        load_box(sm + s * 2 * L::kTile, &tmK, &full[s], pg, x, g0, per, c0, kvh);
+        load_box(sm + (s * 2 + 1) * L::kTile, &tmV, &full[s], pg, x, g0, per, c0, kvh);
+        if (j + 1 < nb) x = box_at(w, pg, it.s, it.b, (b0 + j + 1) * MK, g0, per);  // (looked up before the wait)
       }
     }
     if (lane == 0) {

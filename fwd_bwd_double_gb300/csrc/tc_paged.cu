@@ -142,36 +142,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     Walk it;
     bool more = it.begin(w, sp, p) && ok, go = true;
     int E = 0, n = 0, nq = 0, T0 = 0, T1 = 0;
-    const int box = pg.box, per = BN / box;    // boxes of an entry along its keys
+    const int per = BN / pg.box;                                                // boxes of an entry along its keys
     const int c0 = pg.whole ? 0 : lane % SL, g0 = pg.whole ? lane : lane / SL;  // this lane's box
-    // The next entry: block kb of K (for tiles m0 .. m1) or V.
-    auto load = [&](const CUtensorMap* map, int m0, int m1, int kb, int kvh) {
+    auto box = [&](int kb) { return box_at(w, pg, it.s, it.b, kb * BN, g0, per); };
+    // The next entry: K (for tiles m0 .. m1) or V.
+    auto load = [&](const CUtensorMap* map, int m0, int m1, const Box& x, int kvh) {
       const int s = E % NS;
-      const int k0 = kb * BN + g0 * box;
-      const int en = k0 / w.seqs.page;
-      const int page = g0 < per && k0 < it.s.len ? page_at(w.seqs, it.b, en) : -1;
       if (E >= NS) go = wait(&empty[s], ((E / NS) - 1) & 1) && go;
       go = __all_sync(0xffffffffu, go);
       if (!go) return;
-      if (m0 <= m1) {
-        const uint32_t run = g0 < per && page < 0 && k0 < it.s.len ? ((1u << (box / 16)) - 1u) << (g0 * (box / 16)) : 0u;
-        const uint32_t all = __reduce_or_sync(0xffffffffu, run);
-        if (lane == 0) {
-          if (m0 == 0) hidden[T0 & 7] = static_cast<uint8_t>(all);
-          if (m1 == 1) hidden[8 + (T1 & 7)] = static_cast<uint8_t>(all);
+      if (lane == 0) {
+        if (m0 <= m1) {
+          if (m0 == 0) hidden[T0 & 7] = static_cast<uint8_t>(x.hidden);
+          if (m1 == 1) hidden[8 + (T1 & 7)] = static_cast<uint8_t>(x.hidden);
         }
-        T0 += m0 == 0, T1 += m1 == 1;
+        ptx::mbar_expect_tx(&full[s], L::kTile);
       }
-      if (lane == 0) ptx::mbar_expect_tx(&full[s], L::kTile);
+      if (m0 <= m1) T0 += m0 == 0, T1 += m1 == 1;
       __syncwarp();
-      if (g0 < per) {
-        uint8_t* dst = sm + L::oRing + s * L::kTile + (g0 * box >> 3) * pg.sbo + c0 * pg.slab;
-        const int slot = page < 0 ? 0 : k0 - en * w.seqs.page;
-        if (pg.whole)
-          ptx::tma_load_5d(dst, map, &full[s], 0, 0, 0, slot >> 3, page < 0 ? -1 : page * pg.mul + kvh);
-        else
-          ptx::tma_load_4d(dst, map, &full[s], c0 * 64, slot, kvh, page);
-      }
+      load_box(sm + L::oRing + s * L::kTile, map, &full[s], pg, x, g0, per, c0, kvh);
       ++E;
     };
     for (; more && go; more = it.next(w), ++n) {
@@ -196,17 +185,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tma_load_5d(sm + m * L::kTile + u * BM * 128, &tmQ, q_full, u * 64, 0, it.s.row0 + it.t0 + m * tq, it.vh,
                              it.s.batch);
       }
+      // (a block's pages are looked up before the wait for room in the ring)
+      Box x = box(b0);
       if (tiles == 2) {
         for (int j = 0; j < nb && go; ++j) {
-          load(&tmK, 0, 1, b0 + j, kvh);
-          if (go) load(&tmV, 1, 0, b0 + j, kvh);
+          load(&tmK, 0, 1, x, kvh);
+          if (go) load(&tmV, 1, 0, x, kvh);
+          if (j + 1 < nb) x = box(b0 + j + 1);
         }
       } else {
-        load(&tmK, 0, 0, b0, kvh);
-        if (go && nb > 1) load(&tmK, 1, 1, b0 + 1, kvh);
+        Box y = x;
+        load(&tmK, 0, 0, x, kvh);
+        if (nb > 1) y = box(b0 + 1);
+        if (go && nb > 1) load(&tmK, 1, 1, y, kvh);
         for (int j = 0; j < nb && go; ++j) {
-          load(&tmV, 1, 0, b0 + j, kvh);
-          if (go && j + 2 < nb) load(&tmK, j & 1, j & 1, b0 + j + 2, kvh);
+          Box z = y;
+          if (j + 2 < nb) z = box(b0 + j + 2);
+          load(&tmV, 1, 0, x, kvh);
+          if (go && j + 2 < nb) load(&tmK, j & 1, j & 1, z, kvh);
+          x = y, y = z;
         }
       }
     }

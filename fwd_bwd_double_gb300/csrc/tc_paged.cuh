@@ -16,6 +16,7 @@ constexpr int kOut = 32 * 80;    // a warp's outputs on their way: 64 bytes of e
 // How K and V lie in the cache and in the ring.
 struct Pages {
   int box;       // keys of a box
+  int log;       // of the keys of a page to the base 2, -1 where they are no power of two
   int whole;     // a box takes all columns: its last coordinate is page * mul + head
   int mul;
   int sbo, slab; // bytes from eight keys to the next, from 64 columns to the next
@@ -67,6 +68,33 @@ static __device__ __noinline__ void add_spoilt(const Work& w, const Item& it, in
       }
     }
   }
+}
+
+// A lane's box of a run of keys (an entry of the ring, or two of the same keys): its place in the run, the page and the
+// slot there that it reads (page < 0: zeros), and of all the warp's the 16-key runs without a page.
+struct Box {
+  int page, slot;
+  uint32_t hidden;
+};
+// `keys` keys from k0 on, `per` boxes of them, this lane's the g-th.
+__device__ __forceinline__ Box box_at(const Work& w, const Pages& pg, const Seq& s, int b, int k0, int g, int per) {
+  const int key = k0 + g * pg.box, e = pg.log >= 0 ? key >> pg.log : key / w.seqs.page;
+  const bool mine = g < per && key < s.len;
+  Box x;
+  x.page = mine ? page_at(w.seqs, b, e) : -1;
+  x.slot = x.page < 0 ? 0 : key - e * w.seqs.page;
+  x.hidden = __reduce_or_sync(0xffffffffu, mine && x.page < 0 ? ((1u << (pg.box / 16)) - 1u) << (g * (pg.box / 16)) : 0u);
+  return x;
+}
+// The warp's copies (one lane's after another's).
+__device__ __forceinline__ void load_box(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, const Pages& pg, const Box& x, int g,
+                                         int per, int slab, int kvh) {
+  if (g >= per) return;
+  dst += (g * pg.box >> 3) * pg.sbo + slab * pg.slab;
+  if (pg.whole)
+    ptx::tma_load_5d(dst, map, bar, 0, 0, 0, x.slot >> 3, x.page < 0 ? -1 : x.page * pg.mul + kvh);
+  else
+    ptx::tma_load_4d(dst, map, bar, slab * 64, x.slot, kvh, x.page);
 }
 
 // 64 bytes of each live row of a warp to `to`, its own row's address, through `stage` (kOut bytes of the warp's own):
@@ -126,6 +154,9 @@ inline bool make_maps(const PagedArgs& a, const Cut& k, int keys, int slabs, voi
   const int64_t q_str[4] = {a.qs[1], a.qs[2], a.qs[1] * k.gt, a.qs[0]};
   const int q_box[5] = {64, k.gt, k.tile, 1, 1};
   if (mq != nullptr && !make_tmap_view(mq, a.Q, 5, q_dims, q_str, q_box)) return false;
+  pg.log = -1;
+  for (int k = 4; k <= 20; ++k)
+    if (a.seqs.page == 1 << k) pg.log = k;
   pg.box = keys;  // as many keys as divide a page's
   while (a.seqs.page % pg.box != 0) pg.box /= 2;
   // All columns in a box: of whole slabs, and pages a multiple of the heads' stride apart (K and V alike, and

@@ -103,33 +103,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     Walk it;
     bool more = it.begin(w, sp, p) && ok, go = true;
     int E = 0, n = 0, nq = 0, T = 0;
-    const int box = pg.box, per = HN / box;                                     // boxes of an entry along its keys
+    const int per = HN / pg.box;                                                // boxes of an entry along its keys
     const int c0 = pg.whole ? 0 : lane % SL, g0 = pg.whole ? lane : lane / SL;  // this lane's box
-    // The two entries of block kb of K or V.
-    auto load = [&](const CUtensorMap* map, bool key, int kb, int kvh) {
+    struct Block {
+      Box half[2];
+    };
+    auto box = [&](int kb) {
+      return Block{{box_at(w, pg, it.s, it.b, kb * BN, g0, per), box_at(w, pg, it.s, it.b, kb * BN + HN, g0, per)}};
+    };
+    // The two entries of a block of K or V.
+    auto load = [&](const CUtensorMap* map, bool key, const Block& x, int kvh) {
+#pragma unroll
       for (int h = 0; h < 2; ++h, ++E) {
         const int s = E % NS;
-        const int k0 = kb * BN + h * HN + g0 * box;
-        const int en = k0 / w.seqs.page;
-        const int page = g0 < per && k0 < it.s.len ? page_at(w.seqs, it.b, en) : -1;
         if (E >= NS) go = wait(&empty[s], ((E / NS) - 1) & 1) && go;
         go = __all_sync(0xffffffffu, go);
         if (!go) return;
-        if (key) {
-          const uint32_t run = g0 < per && page < 0 && k0 < it.s.len ? ((1u << (box / 16)) - 1u) << (g0 * (box / 16)) : 0u;
-          const uint32_t all = __reduce_or_sync(0xffffffffu, run);
-          if (lane == 0) hidden[(T & 7) * 2 + h] = static_cast<uint8_t>(all);
+        if (lane == 0) {
+          if (key) hidden[(T & 7) * 2 + h] = static_cast<uint8_t>(x.half[h].hidden);
+          ptx::mbar_expect_tx(&full[s], kEntry);
         }
-        if (lane == 0) ptx::mbar_expect_tx(&full[s], kEntry);
         __syncwarp();
-        if (g0 < per) {
-          uint8_t* dst = sm + oRing + s * kEntry + (g0 * box >> 3) * pg.sbo + c0 * pg.slab;
-          const int slot = page < 0 ? 0 : k0 - en * w.seqs.page;
-          if (pg.whole)
-            ptx::tma_load_5d(dst, map, &full[s], 0, 0, 0, slot >> 3, page < 0 ? -1 : page * pg.mul + kvh);
-          else
-            ptx::tma_load_4d(dst, map, &full[s], c0 * 64, slot, kvh, page);
-        }
+        load_box(sm + oRing + s * kEntry, map, &full[s], pg, x.half[h], g0, per, c0, kvh);
       }
       T += key;
     };
@@ -153,11 +148,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int u = 0; u < SL; ++u)
           ptx::tma_load_5d(sm + u * BM * 128, &tmQ, q_full, u * 64, 0, it.s.row0 + it.t0, it.vh, it.s.batch);
       }
-      load(&tmK, true, b0, kvh);
-      if (go && nb > 1) load(&tmK, true, b0 + 1, kvh);
+      // (a block's pages are looked up before the wait for room in the ring)
+      Block x = box(b0), y = x;
+      load(&tmK, true, x, kvh);
+      if (nb > 1) y = box(b0 + 1);
+      if (go && nb > 1) load(&tmK, true, y, kvh);
       for (int j = 0; j < nb && go; ++j) {
-        load(&tmV, false, b0 + j, kvh);
-        if (go && j + 2 < nb) load(&tmK, true, b0 + j + 2, kvh);
+        Block z = y;
+        if (j + 2 < nb) z = box(b0 + j + 2);
+        load(&tmV, false, x, kvh);
+        if (go && j + 2 < nb) load(&tmK, true, z, kvh);
+        x = y, y = z;
       }
     }
     if (lane == 0) {
