@@ -17,7 +17,7 @@
 // copies are issued one after another (about 75 cycles each), so where the strides allow it a box takes all
 // d columns, in groups of eight keys (group, slab of 64 columns, key: MMA operands of either major), else
 // a slab of them.  Keys hidden from a row are masked in its scores.  Their values are multiplied by weights of 0, which would make
-// an infinity or NaN there a NaN: in blocks that some row does not see whole, two warps make such
+// an infinity or NaN there a NaN: in blocks that some row does not see whole, a warp makes such
 // elements 0 before the product (and rows behind the last key, which may hold anything), and the
 // rows that do see them add them at the end.
 //
@@ -34,7 +34,7 @@ namespace {
 
 __device__ unsigned int g_err = 0;
 
-// Warps 0-3: tile 0, 4-7: tile 1, 8: TMA, 9: MMA, 10, 11: values that a row must not see.  384 threads
+// Warps 0-3: tile 0, 4-7: tile 1, 8: TMA, 9, 10: MMA of a tile each, 11: values that a row must not see.  384 threads
 // launched with 168 registers; the softmax warps (a row of 128 scores each thread) take 208, the third
 // warpgroup's keep 80: 256 * 208 + 128 * 80 <= 384 * 168.
 constexpr int kThreads = 384;
@@ -77,14 +77,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* empty = full + NS;       // [NS]
   uint64_t* v_ok = empty + NS;       // [NS] values that some row does not see are finite
   uint64_t* known = v_ok + NS;       // [8] items
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(known + 8);
+  uint64_t* turn = known + 8;        // [2] tile m may issue its next products
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* started = abort_flag + 1;                                 // Q loads, ring entries (the TMA warp's)
   volatile uint8_t* hidden = reinterpret_cast<volatile uint8_t*>(started + 2);  // [2][8] of tile m's blocks: 16-key runs without a page
   volatile int* spoilt = reinterpret_cast<volatile int*>(hidden + 16);    // [8] of items: n + 1 where values were made 0
   float2* stat = reinterpret_cast<float2*>(sm + L::oStat);
   Item* items = reinterpret_cast<Item*>(sm + L::oItem);
-  static_assert(sizeof(Item) == 64 && (12 + 3 * NS + 8) * 8 + 4 * 4 + 16 + 32 <= 512, "the barriers' region");
+  static_assert(sizeof(Item) == 64 && (12 + 3 * NS + 10) * 8 + 4 * 4 + 16 + 32 <= 512, "the barriers' region");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, p = blockIdx.x;
   const int gt = w.cut.gt, tq = w.cut.tile;
@@ -93,20 +94,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::prefetch_tmap(&tmK);
     ptx::prefetch_tmap(&tmV);
     ptx::mbar_init(q_full, 1);
-    ptx::mbar_init(q_empty, 1);
+    ptx::mbar_init(q_empty, 2);  // each tile's
     for (int m = 0; m < 2; ++m) {
       ptx::mbar_init(&s_full[m], 2);  // the products' end and the warp that issued them
       ptx::mbar_init(&p_half[m], 128);
       ptx::mbar_init(&p_ready[m], 128);
+      ptx::mbar_init(&turn[m], 1);
     }
-    ptx::mbar_init(o_full, 2);
+    ptx::mbar_init(o_full, 4);
     ptx::mbar_init(o_empty, 256);
     ptx::mbar_init(x_full, 128);
-    ptx::mbar_init(settled, 1);
+    ptx::mbar_init(settled, 2);
     for (int s = 0; s < NS; ++s) {
       ptx::mbar_init(&full[s], 1);
-      ptx::mbar_init(&empty[s], 1);
-      ptx::mbar_init(&v_ok[s], 2);
+      ptx::mbar_init(&empty[s], 3);  // each tile's, and the warp's that looks at values
+      ptx::mbar_init(&v_ok[s], 1);
     }
     for (int s = 0; s < 8; ++s) ptx::mbar_init(&known[s], 1), spoilt[s] = 0;
     started[0] = started[1] = 0;
@@ -214,71 +216,96 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       started[0] = nq, started[1] = E;
     }
-  } else if (warp == 9) {
-    // ------------------------------------------------------------- MMA issuer
+  } else if (warp == 9 || warp == 10) {
+    // ------------------------------------------------- MMA issuer of tile m
+    // (one warp for both tiles spends 1700 cycles of each product pair issuing, the products take 1024)
+    const int m = warp - 9;
     constexpr uint32_t idS = ptx::idesc_bf16(BM, BN, 0, 0);
     constexpr uint32_t idO = ptx::idesc_bf16(BM, D, 0, 1);
     const uint64_t dQ = tc::kmajor_desc(ptx::smem_u32(sm), BM, 0);
     const uint64_t dK = ptx::sdesc_sw128(ptx::smem_u32(sm + L::oRing), 16, pg.sbo);
     const uint64_t dV = ptx::sdesc_sw128(ptx::smem_u32(sm + L::oRing), pg.slab, pg.sbo);
-    int base = 0, n = 0, T0 = 0, T1 = 0, masked = 0;
+    const uint32_t tS = tmem + L::cS + m * BN, tO = tmem + L::cO + m * D;
+    int base = 0, n = 0, T = 0, masked = 0, seen = 0, turns = 0;
+    // Entry e, after those before it that are the other tile's.  A parity tells two neighbouring phases apart, so each
+    // consumer looks at every entry in turn, and an entry is filled again once all three have done with it.
+    auto pass = [&](int e) {
+      for (; seen < e; ++seen) {
+        wait(&full[seen % NS], (seen / NS) & 1);
+        if (lane == 0) ptx::mbar_arrive(&empty[seen % NS]);
+      }
+    };
+    auto loaded = [&](int e) {
+      pass(e);
+      wait(&full[e % NS], (e / NS) & 1);
+      seen = e + 1;
+    };
     for (const Item* it; (it = item(n)) != nullptr; ++n) {
       const Order o{base, it->n, it->pair != 0};
-      const int b0 = it->b0, n0 = it->count(0), n1 = it->count(1);
-      int left = n0 + n1;  // products with Q still to issue
-      auto issue_s = [&](int m, int j) {
+      const int b0 = it->b0, nb = it->count(m);
+      const uint32_t qo = o.pair && m == 1 ? L::kTile : 0;
+      auto issue_s = [&](int j) {
         const int e = o.K(o.block(m, j)), s = e % NS;
-        if (!o.pair || m == 0) wait(&full[s], (e / NS) & 1);
+        loaded(e);
         ptx::tc_fence_after();
-        const uint32_t so = static_cast<uint32_t>(s * L::kTile), qo = o.pair && m == 1 ? L::kTile : 0;
+        const uint32_t so = static_cast<uint32_t>(s * L::kTile);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          ptx::mma_ss_e(tmem + L::cS + m * BN, tc::desc_add(dQ, qo + tc::kmajor_off(BM, k)),
-                        tc::desc_add(dK, so + (k >> 2) * pg.slab + (k & 3) * 32), idS, k > 0 ? 1u : 0u);
+          ptx::mma_ss_e(tS, tc::desc_add(dQ, qo + tc::kmajor_off(BM, k)), tc::desc_add(dK, so + (k >> 2) * pg.slab + (k & 3) * 32),
+                        idS, k > 0 ? 1u : 0u);
         ptx::mma_commit_e(&s_full[m]);
         if (lane == 0) ptx::mbar_arrive(&s_full[m]);
-        if (!o.pair || m == 1) ptx::mma_commit_e(&empty[s]);
-        if (--left == 0) ptx::mma_commit_e(q_empty);
+        ptx::mma_commit_e(&empty[s]);
       };
+      int block = 0;  // blocks of the item whose values have been waited for
       wait(q_full, n & 1);
-      issue_s(0, 0);
-      if (n1 > 0) issue_s(1, 0);
-      for (int j = 0; j < n0; ++j) {
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          if (j >= (m == 0 ? n0 : n1)) continue;
-          const int T = m == 0 ? T0++ : T1++;
-          const int i = o.block(m, j), e = o.V(i), s = e % NS;
-          if (!o.pair || m == 0) {
-            if (it->hides(b0 + i)) {
-              wait(&v_ok[masked % NS], (masked / NS) & 1);
-              ++masked;
-            } else {
-              wait(&full[s], (e / NS) & 1);
-            }
+      if (nb > 0) issue_s(0);
+      if (nb <= 1) ptx::mma_commit_e(q_empty);
+      for (int j = 0; j < nb; ++j, ++T) {
+        const int i = o.block(m, j), e = o.V(i), s = e % NS;
+        loaded(e);
+        for (; block <= i; ++block)  // (in turn, too)
+          if (it->hides(b0 + block)) {
+            wait(&v_ok[masked % NS], (masked / NS) & 1);
+            ++masked;
           }
-          wait(&p_half[m], T & 1);
-          if (j == 0 && m == 0 && n > 0) wait(o_empty, (n - 1) & 1);
-          ptx::tc_fence_after();
-          const uint32_t so = static_cast<uint32_t>(s * L::kTile);
+        wait(&p_half[m], T & 1);
+        if (j == 0 && n > 0) wait(o_empty, (n - 1) & 1);
+        // Two tiles take turns, P V and the next S at a time: left to themselves their softmaxes fall into step,
+        // and the products wait for both at once.
+        if (o.pair && (m == 1 || turns > 0)) wait(&turn[m], (turns - 1 + m) & 1);
+        ptx::tc_fence_after();
+        const uint32_t so = static_cast<uint32_t>(s * L::kTile);
 #pragma unroll
-          for (int k = 0; k < BN / 16; ++k) {
-            if (k == BN / 32) {
-              wait(&p_ready[m], T & 1);
-              ptx::tc_fence_after();
-            }
-            ptx::mma_ts_e(tmem + L::cO + m * D, tmem + L::cS + m * BN + k * 8, tc::desc_add(dV, so + k * 2 * pg.sbo), idO,
-                          (j > 0 || k > 0) ? 1u : 0u);
+        for (int k = 0; k < BN / 16; ++k) {
+          if (k == BN / 32) {
+            wait(&p_ready[m], T & 1);
+            ptx::tc_fence_after();
           }
-          if (!o.pair || m == 1) ptx::mma_commit_e(&empty[s]);
-          if (j + 1 < (m == 0 ? n0 : n1)) issue_s(m, j + 1);
+          ptx::mma_ts_e(tO, tS + k * 8, tc::desc_add(dV, so + k * 2 * pg.sbo), idO, (j > 0 || k > 0) ? 1u : 0u);
+        }
+        ptx::mma_commit_e(&empty[s]);
+        if (j + 1 < nb) {
+          issue_s(j + 1);
+          if (j + 2 == nb) ptx::mma_commit_e(q_empty);
+        }
+        if (o.pair) {
+          if (lane == 0) ptx::mbar_arrive(&turn[1 - m]);
+          ++turns;
         }
       }
+      for (; block < o.n; ++block)  // (the other tile's last one)
+        if (it->hides(b0 + block)) {
+          wait(&v_ok[masked % NS], (masked / NS) & 1);
+          ++masked;
+        }
+      base += 2 * o.n;
+      pass(base);
+      if (nb == 0 && n > 0) wait(o_empty, (n - 1) & 1);  // (every item's, for the same reason)
       ptx::mma_commit_e(o_full);
       if (lane == 0) ptx::mbar_arrive(o_full);
-      base += 2 * o.n;
     }
-  } else if (warp >= 10) {
+  } else if (warp == 11) {
     // ------------------------- values that some row does not see: made 0 where they are not finite
     int base = 0, n = 0, masked = 0, seen = 0;
     for (const Item* it; (it = item(n)) != nullptr; ++n) {
@@ -286,9 +313,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int b0 = it->b0;
       for (int i = 0; i < o.n; ++i) {
         const int e = o.V(i), s = e % NS;
-        // every entry up to this one in turn: a barrier two phases back would look complete
-        for (; seen <= e; ++seen) wait(&full[seen % NS], (seen / NS) & 1);
+        for (; seen < e; ++seen) {  // (every entry in turn, as above)
+          wait(&full[seen % NS], (seen / NS) & 1);
+          if (lane == 0) ptx::mbar_arrive(&empty[seen % NS]);
+        }
         if (!it->hides(b0 + i)) continue;
+        wait(&full[s], (e / NS) & 1);
         const bool some = hide_values(sm + L::oRing + s * L::kTile, BN, min(max(it->len - (b0 + i) * BN, 0), BN), SL, pg);
         if (some) spoilt[n & 7] = n + 1;
         ptx::fence_proxy_async_smem();
@@ -297,6 +327,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++masked;
       }
       base += 2 * o.n;
+      for (; seen < base; ++seen) {
+        wait(&full[seen % NS], (seen / NS) & 1);
+        if (lane == 0) ptx::mbar_arrive(&empty[seen % NS]);
+      }
     }
   } else {
     ptx::setmaxnreg_inc<kRegs>();
@@ -482,10 +516,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (nq > 0) ptx::settle(q_full, (nq - 1) & 1);
       for (int s = 0; s < NS && s < E; ++s) ptx::settle(&full[s], handover::last_phase(E, NS, s));
     }
-    if (warp == 9) {
+    if (warp == 9 || warp == 10) {
       ptx::mma_commit_e(settled);
       ptx::settle(settled, 0);
     }
+    __syncthreads();
   }
   if (warp == 9) {
     ptx::tc_fence_after();

@@ -3,8 +3,9 @@
 //
 // One tile of 128 rows; S of the next block is formed while this one is exponentiated, in the other of
 // two S (P over the S it came from), so that the tensor cores wait for the softmax only where it is the
-// longer: 2048 cycles of products a block.  K and V come in entries of 64 keys (32 KB; Q takes 64 KB, so a ring of
-// four).  O is rescaled, where the maximum moved, once the product before has ended.
+// longer: 2048 cycles of products a block; S and P V are issued by a warp each.  K and V come in entries of 64 keys
+// (32 KB; Q takes 64 KB, so a ring of four: two operands of 128 keys).  O is rescaled, where the
+// maximum moved, once the product before has ended.
 #include <cuda_bf16.h>
 
 #include "handover.h"
@@ -17,10 +18,10 @@ namespace {
 __device__ unsigned int g_err = 0;
 
 constexpr int D = 256, HN = 64;  // columns; keys of an entry, half a block
-// Warps 0-3: softmax, 4: TMA, 5: MMA, 6, 7: values that a row must not see.
+// Warps 0-3: softmax, 4: TMA, 5: S, 6: P V, 7: values that a row must not see.
 constexpr int kThreads = 256;
 constexpr int NS = 4, SL = D / 64;
-constexpr int kQ = BM * D * 2, kEntry = HN * D * 2;
+constexpr int kQ = BM * D * 2, kEntry = HN * D * 2, kOperand = 2 * kEntry;
 constexpr int oRing = kQ, oOut = oRing + NS * kEntry, oBar = oOut + 4 * kOut, oItem = oBar + 512, kBytes = oItem + 8 * 64;
 static_assert(kBytes <= 232448, "shared memory");
 constexpr uint32_t cS = 0, cO = 2 * BN;  // S of an even (odd) block at cS (+ BN)
@@ -36,8 +37,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* s_full = bars + 2;      // [2] S in TMEM
   uint64_t* p_half = s_full + 2;    // [2] P of the first 64 keys in TMEM, O rescaled
   uint64_t* p_ready = p_half + 2;   // [2] of all keys
-  uint64_t* pv_done = p_ready + 2;  // the block's P V done
-  uint64_t* o_full = pv_done + 1;
+  uint64_t* pv_done = p_ready + 2;  // [2] the block's P V done
+  uint64_t* o_full = pv_done + 2;
   uint64_t* o_empty = o_full + 1;   // O read by the epilogue
   uint64_t* settled = o_empty + 1;  // after a wait that gave up: the products in flight done
   uint64_t* full = settled + 1;     // [NS]
@@ -63,15 +64,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&s_full[m], 2);  // the products' end and the warp that issued them
       ptx::mbar_init(&p_half[m], 128);
       ptx::mbar_init(&p_ready[m], 128);
+      ptx::mbar_init(&pv_done[m], 1);
     }
-    ptx::mbar_init(pv_done, 1);
     ptx::mbar_init(o_full, 2);
     ptx::mbar_init(o_empty, 128);
-    ptx::mbar_init(settled, 1);
+    ptx::mbar_init(settled, 2);
     for (int s = 0; s < NS; ++s) {
       ptx::mbar_init(&full[s], 1);
-      ptx::mbar_init(&empty[s], 1);
-      ptx::mbar_init(&v_ok[s], 2);
+      ptx::mbar_init(&empty[s], 3);  // of the three consumers: S, P V and the warp that looks at values
+      ptx::mbar_init(&v_ok[s], 1);
     }
     for (int s = 0; s < 8; ++s) ptx::mbar_init(&known[s], 1), spoilt[s] = 0;
     started[0] = started[1] = 0;
@@ -96,6 +97,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     wait(&known[n & 7], (n >> 3) & 1);
     const Item* it = items + (n & 7);
     return __all_sync(0xffffffffu, *abort_flag == 0 && *reinterpret_cast<const volatile int*>(&it->n) > 0) ? it : nullptr;
+  };
+
+  // A consumer's entries up to the e-th that are another's.  A parity tells two neighbouring phases apart, so each
+  // consumer looks at every entry in turn, and an entry is filled again once all three have done with it.
+  int seen = 0;
+  auto pass = [&](int e) {
+    for (; seen < e; ++seen) {
+      wait(&full[seen % NS], (seen / NS) & 1);
+      if (lane == 0) ptx::mbar_arrive(&empty[seen % NS]);
+    }
+  };
+  auto loaded = [&](int e) {
+    wait(&full[e % NS], (e / NS) & 1);
+    seen = e + 1;
   };
 
   if (warp == 4) {
@@ -124,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::mbar_expect_tx(&full[s], kEntry);
         }
         __syncwarp();
-        load_box(sm + oRing + s * kEntry, map, &full[s], pg, x.half[h], g0, per, c0, kvh);
+        load_box(sm + oRing + (s >> 1) * kOperand + h * 8 * pg.sbo, map, &full[s], pg, x.half[h], g0, per, c0, kvh);
       }
       T += key;
     };
@@ -169,75 +184,83 @@ __global__ void __launch_bounds__(kThreads, 1)
       started[0] = nq, started[1] = E;
     }
   } else if (warp == 5) {
-    // ------------------------------------------------------------- MMA issuer
-    constexpr uint32_t idS = ptx::idesc_bf16(BM, HN, 0, 0);
-    constexpr uint32_t idO = ptx::idesc_bf16(BM, D, 0, 1);
+    // ------------------------------------------------------------- S = Q K^T
+    constexpr uint32_t idS = ptx::idesc_bf16(BM, BN, 0, 0);
     const uint64_t dQ = tc::kmajor_desc(ptx::smem_u32(sm), BM, 0);
     const uint64_t dK = ptx::sdesc_sw128(ptx::smem_u32(sm + oRing), 16, pg.sbo);
+    int base = 0, n = 0, T = 0;
+    for (const Item* it; (it = item(n)) != nullptr; ++n) {
+      const Order o{base, it->n, false};
+      wait(q_full, n & 1);
+      for (int j = 0; j < o.n; ++j, ++T) {
+        const int e = 2 * o.K(j), s = e % NS;
+        pass(e);
+        loaded(e), loaded(e + 1);
+        // the block before the last has been multiplied with V: its P's columns are free
+        if (T >= 2) wait(&pv_done[T & 1], ((T >> 1) - 1) & 1);
+        ptx::tc_fence_after();
+        const uint32_t so = static_cast<uint32_t>((s >> 1) * kOperand);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          ptx::mma_ss_e(tmem + cS + (T & 1) * BN, tc::desc_add(dQ, tc::kmajor_off(BM, k)),
+                        tc::desc_add(dK, so + (k >> 2) * pg.slab + (k & 3) * 32), idS, k > 0 ? 1u : 0u);
+        ptx::mma_commit_e(&s_full[T & 1]);
+        if (lane == 0) ptx::mbar_arrive(&s_full[T & 1]);
+        ptx::mma_commit_e(&empty[s]);
+        ptx::mma_commit_e(&empty[s + 1]);
+      }
+      ptx::mma_commit_e(q_empty);
+      base += 2 * o.n;
+      pass(2 * base);
+    }
+  } else if (warp == 6) {
+    // ------------------------------------------------------------- O += P V
+    constexpr uint32_t idO = ptx::idesc_bf16(BM, D, 0, 1);
     const uint64_t dV = ptx::sdesc_sw128(ptx::smem_u32(sm + oRing), pg.slab, pg.sbo);
     int base = 0, n = 0, T = 0, masked = 0;
     for (const Item* it; (it = item(n)) != nullptr; ++n) {
       const Order o{base, it->n, false};
-      auto issue_s = [&](int j) {
-        const uint32_t to = tmem + cS + ((T + j) & 1) * BN;
-        for (int h = 0; h < 2; ++h) {
-          const int e = 2 * o.K(j) + h, s = e % NS;
-          wait(&full[s], (e / NS) & 1);
-          ptx::tc_fence_after();
-          const uint32_t so = static_cast<uint32_t>(s * kEntry);
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            ptx::mma_ss_e(to + h * HN, tc::desc_add(dQ, tc::kmajor_off(BM, k)),
-                          tc::desc_add(dK, so + (k >> 2) * pg.slab + (k & 3) * 32), idS, k > 0 ? 1u : 0u);
-          ptx::mma_commit_e(&empty[s]);
-        }
-        ptx::mma_commit_e(&s_full[(T + j) & 1]);
-        if (lane == 0) ptx::mbar_arrive(&s_full[(T + j) & 1]);
-        if (j == o.n - 1) ptx::mma_commit_e(q_empty);
-      };
-      wait(q_full, n & 1);
-      issue_s(0);
-      for (int j = 0; j < o.n; ++j) {
-        if (j + 1 < o.n) issue_s(j + 1);
-        const int b = (T + j) & 1, phase = ((T + j) >> 1) & 1;
-        const bool hides = it->hides(it->b0 + j);
-        if (hides) {
+      for (int j = 0; j < o.n; ++j, ++T) {
+        const int b = T & 1, phase = (T >> 1) & 1, e = 2 * o.V(j);
+        pass(e);
+        if (it->hides(it->b0 + j)) {
           wait(&v_ok[masked % NS], (masked / NS) & 1);
           ++masked;
         }
         wait(&p_half[b], phase);
         if (j == 0 && n > 0) wait(o_empty, (n - 1) & 1);
+#pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int e = 2 * o.V(j) + h, s = e % NS;
-          if (!hides) wait(&full[s], (e / NS) & 1);
+          const int s = (e + h) % NS;
+          loaded(e + h);
           if (h == 1) wait(&p_ready[b], phase);
           ptx::tc_fence_after();
-          const uint32_t so = static_cast<uint32_t>(s * kEntry);
+          const uint32_t so = static_cast<uint32_t>((s >> 1) * kOperand);
 #pragma unroll
-          for (int k = 0; k < HN / 16; ++k)
-            ptx::mma_ts_e(tmem + cO, tmem + cS + b * BN + (h * 4 + k) * 8, tc::desc_add(dV, so + k * 2 * pg.sbo), idO,
-                          (j > 0 || h > 0 || k > 0) ? 1u : 0u);
+          for (int k = h * 4; k < h * 4 + 4; ++k)
+            ptx::mma_ts_e(tmem + cO, tmem + cS + b * BN + k * 8, tc::desc_add(dV, so + k * 2 * pg.sbo), idO,
+                          (j > 0 || k > 0) ? 1u : 0u);
           ptx::mma_commit_e(&empty[s]);
         }
-        ptx::mma_commit_e(pv_done);
+        ptx::mma_commit_e(&pv_done[b]);
       }
       ptx::mma_commit_e(o_full);
       if (lane == 0) ptx::mbar_arrive(o_full);
-      base += 2 * o.n, T += o.n;
+      base += 2 * o.n;
+      pass(2 * base);
     }
-  } else if (warp >= 6) {
+  } else if (warp == 7) {
     // ------------------------- values that some row does not see: made 0 where they are not finite
-    int base = 0, n = 0, masked = 0, seen = 0;
+    int base = 0, n = 0, masked = 0;
     for (const Item* it; (it = item(n)) != nullptr; ++n) {
       const Order o{base, it->n, false};
       for (int j = 0; j < o.n; ++j) {
         const int e = 2 * o.V(j), key0 = (it->b0 + j) * BN;
-        // every entry up to these in turn: a barrier two phases back would look complete
-        for (; seen <= e + 1; ++seen) wait(&full[seen % NS], (seen / NS) & 1);
+        pass(e);
         if (!it->hides(it->b0 + j)) continue;
-        bool some = false;
-        for (int h = 0; h < 2; ++h)
-          some = hide_values(sm + oRing + (e + h) % NS * kEntry, HN, min(max(it->len - key0 - h * HN, 0), HN), SL, pg) || some;
+        wait(&full[e % NS], (e / NS) & 1);
+        wait(&full[(e + 1) % NS], ((e + 1) / NS) & 1);
+        const bool some = hide_values(sm + oRing + (e % NS >> 1) * kOperand, BN, min(max(it->len - key0, 0), BN), SL, pg);
         if (some) spoilt[n & 7] = n + 1;
         ptx::fence_proxy_async_smem();
         __syncwarp();
@@ -245,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++masked;
       }
       base += 2 * o.n;
+      pass(2 * base);
     }
   } else {
     // --------------------------- softmax: thread r owns row r
@@ -331,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (j > 0) {
-          wait(pv_done, (T - 1) & 1);
+          wait(&pv_done[b ^ 1], ((T - 1) >> 1) & 1);
           ptx::tc_fence_after();
         }
         if (rescale) {
@@ -408,10 +432,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (nq > 0) ptx::settle(q_full, (nq - 1) & 1);
       for (int s = 0; s < NS && s < E; ++s) ptx::settle(&full[s], handover::last_phase(E, NS, s));
     }
-    if (warp == 5) {
+    if (warp == 5 || warp == 6) {
       ptx::mma_commit_e(settled);
       ptx::settle(settled, 0);
     }
+    __syncthreads();
   }
   if (warp == 5) {
     ptx::tc_fence_after();
@@ -440,7 +465,7 @@ cudaError_t tc_paged_wide(const PagedArgs& a, void* ws, cudaStream_t st) {
   const Out out{a.O, a.lse, {a.os[0], a.os[1], a.os[2]}, {a.ls[0], a.ls[1]}};
   alignas(64) CUtensorMap mq, mk, mv;
   Pages pg;
-  if (!make_maps(a, w.cut, HN, SL, &mq, &mk, &mv, pg)) return cudaErrorInvalidValue;
+  if (!make_maps(a, w.cut, HN, SL, &mq, &mk, &mv, pg, BN)) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
   if (e != cudaSuccess) return e;
   if ((e = plan(w, sp, st)) != cudaSuccess) return e;
