@@ -56,116 +56,120 @@ __global__ void __launch_bounds__(kT) head_kernel(const HeadArgs a) {
   __shared__ int sAx[kMaxPairs];
   __shared__ __align__(16) float sW[4][2 * kMaxPairs];
   const int pairs = a.d / 2, per = pairs / W, LG = group_threads(a.d, W);
+  const int64_t gid = static_cast<int64_t>(blockIdx.x) * kT + threadIdx.x;
+  const int64_t tokens = a.B * a.N, token = gid / LG;
+  const int part = static_cast<int>(gid) & (LG - 1);
+  const bool in = token < tokens && part < per;  // (the others take part in the shuffles)
+  const bool packed = APPEND && a.seqs.cu != nullptr;
+  const int64_t b = in && !packed ? token / a.N : 0, n = in ? token - b * a.N : 0;
+  const int hb = blockIdx.y * a.per_thread;
+  const int he = min(hb + a.per_thread, a.heads);
+  const int c0 = HALF ? part * W : 2 * part * W, c1 = HALF ? c0 + pairs : c0 + W;
+  // kHU heads' loads at a time, the next ones' before these are worked on (y may be x, but no other head's).
+  struct Heads {
+    uint4 lo[kHU], hi[kHU];
+  };
+  auto locate = [&](int h, int& t) {  // head h of all tensors: the returned one of tensor t
+    t = 0;
+    while (h >= a.t[t].heads) h -= a.t[t].heads, ++t;
+    return h;
+  };
+  auto fetch = [&](int h, Heads& z) {
+#pragma unroll
+    for (int k = 0; k < kHU; ++k) {
+      z.lo[k] = z.hi[k] = make_uint4(0, 0, 0, 0);
+      if (h + k >= he || !in) continue;
+      int t;
+      const int hh = locate(h + k, t);
+      const T* x = static_cast<const T*>(a.t[t].x) + b * a.t[t].xs[0] + hh * a.t[t].xs[1] + n * a.t[t].xs[2];
+      z.lo[k] = *reinterpret_cast<const uint4*>(x + c0);
+      z.hi[k] = *reinterpret_cast<const uint4*>(x + c1);
+    }
+  };
+  Heads now, next;
+  fetch(hb, now);
+  // Behind those loads: the tables, and where the token belongs.
   if (a.freq != nullptr) angle_tables(a.freq, a.axis, pairs, a.axes, sT, sAx);
 #pragma unroll
   for (int t = 0; t < 4; ++t)
-    if (t < 4 && a.t[t].heads > 0 && a.t[t].norm)
+    if (a.t[t].heads > 0 && a.t[t].norm)
       for (int i = threadIdx.x; i < a.d; i += kT) sW[t][i] = a.t[t].w != nullptr ? a.t[t].w[i] : 1.f;
-  __syncthreads();
-  const int64_t gid = static_cast<int64_t>(blockIdx.x) * kT + threadIdx.x;
-  const int64_t tokens = a.B * a.N;
-  const int64_t token = gid / LG;
-  const int part = static_cast<int>(gid) & (LG - 1);
-  bool live = token < tokens && part < per;  // (the others take part in the shuffles)
-  int64_t b = 0, n = 0;
+  bool live = in;
   int at = 0, page = -1, slot = 0;  // its position in its sequence and its place in the cache
-  if (token < tokens) {
-    if (!APPEND) {
-      b = token / a.N, n = token - b * a.N;
-    } else {
-      const Seqs& q = a.seqs;
-      int s;
-      if (q.cu != nullptr) {  // the last sequence that begins at or before this row
-        n = token;
-        int lo = 0, hi = q.B;
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (q.cu[mid] <= n) lo = mid; else hi = mid;
-        }
-        s = lo;
-      } else {
-        s = static_cast<int>(token / a.N);
-        b = s, n = token - b * a.N;
+  if (APPEND && token < tokens) {
+    const Seqs& q = a.seqs;
+    int s = static_cast<int>(b);
+    if (packed) {  // the last sequence that begins at or before this row
+      int lo = 0, hi = q.B;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (q.cu[mid] <= token) lo = mid; else hi = mid;
       }
-      const Seq z = seq_at(q, s);
-      const int64_t t = n - z.row0;
-      live = live && t >= 0 && t < z.n;  // (a row of no sequence)
-      const int64_t p = static_cast<int64_t>(z.start) + t;
-      if (live && p >= 0 && p < q.cap) {
-        at = static_cast<int>(p);
-        const int e = at / q.page;
-        page = page_at(q, s, e), slot = at - e * q.page;
-      } else {
-        at = static_cast<int>(p);
-      }
+      s = lo;
     }
+    const Seq z = seq_at(q, s);
+    const int64_t t = (packed ? token : token - static_cast<int64_t>(s) * a.N) - z.row0;
+    live = live && t >= 0 && t < z.n;  // (a row of no sequence)
+    const int64_t p = static_cast<int64_t>(z.start) + t;
+    at = static_cast<int>(p);
+    if (live && p >= 0 && p < q.cap) {
+      const int e = at / q.page;
+      page = page_at(q, s, e), slot = at - e * q.page;
+    }
+  }
+  int pos[W];
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < W; ++u) {
+    const int ax = a.freq != nullptr && live ? sAx[part * W + u] : -1;
+    pos[u] = ax < 0 ? 0 : APPEND && a.pos == nullptr ? at : a.pos[ax * a.pos_axis + b * a.pos_batch + n];
   }
   float cs[W], sn[W];
 #pragma unroll
   for (int u = 0; u < W; ++u) {
-    const int i = part * W + u, ax = a.freq != nullptr && live ? sAx[i] : -1;
+    const int i = part * W + u;
     cs[u] = 1.f, sn[u] = 0.f;
-    if (ax >= 0) {
-      const int p = APPEND && a.pos == nullptr ? at : a.pos[ax * a.pos_axis + b * a.pos_batch + n];
-      angle::sincos_at(p, sT[i], &sn[u], &cs[u]);
-    }
+    if (a.freq != nullptr && live && sAx[i] >= 0) angle::sincos_at(pos[u], sT[i], &sn[u], &cs[u]);
   }
-  const int hb = blockIdx.y * a.per_thread;
-  const int he = min(hb + a.per_thread, a.heads);
-  const int c0 = HALF ? part * W : 2 * part * W, c1 = HALF ? c0 + pairs : c0 + W;
   for (int h = hb; h < he; h += kHU) {
-    // The loads of kHU heads before the first store (the compiler cannot reorder them: y may be x).
-    uint4 lo[kHU], hi[kHU];
-    T* y[kHU];
-    int tt[kHU];
+    if (h + kHU < he) fetch(h + kHU, next);
 #pragma unroll
     for (int k = 0; k < kHU; ++k) {
-      y[k] = nullptr;
-      tt[k] = -1;
-      lo[k] = hi[k] = make_uint4(0, 0, 0, 0);
       if (h + k >= he) break;
-      int t = 0, hh = h + k;  // head h + k of all tensors: head hh of tensor t
-      while (hh >= a.t[t].heads) hh -= a.t[t].heads, ++t;
-      tt[k] = t;
+      int t;
+      const int hh = locate(h + k, t);
       const HeadTensor& z = a.t[t];
-      if (!live || (APPEND && z.paged && page < 0)) continue;
-      const T* x = static_cast<const T*>(z.x) + b * z.xs[0] + hh * z.xs[1] + n * z.xs[2];
-      y[k] = static_cast<T*>(z.y) + hh * z.ys[1] +
+      const bool put = live && !(APPEND && z.paged && page < 0);
+      T* y = static_cast<T*>(z.y) + hh * z.ys[1] +
              (APPEND && z.paged ? page * z.ys[0] + slot * z.ys[2] : b * z.ys[0] + n * z.ys[2]);
-      lo[k] = *reinterpret_cast<const uint4*>(x + c0);
-      hi[k] = *reinterpret_cast<const uint4*>(x + c1);
-    }
-#pragma unroll
-    for (int k = 0; k < kHU; ++k) {
-      if (h + k >= he) break;
-      const HeadTensor& z = a.t[tt[k]];
       if (z.norm || z.turn) {
         float p[W], q[W];
-        angle::widen(lo[k], p);
-        angle::widen(hi[k], q);
+        angle::widen(now.lo[k], p);
+        angle::widen(now.hi[k], q);
         if (z.norm) {
           float ss = 0.f;
 #pragma unroll
           for (int u = 0; u < W; ++u) ss = fmaf(p[u], p[u], fmaf(q[u], q[u], ss));
           const float r = rsqrtf(group_sum(ss, LG) / static_cast<float>(a.d) + a.eps);
-          float w0[W], w1[W];
           if (part < per) {
-            take(sW[tt[k]], c0, w0);
-            take(sW[tt[k]], c1, w1);
+            float w0[W], w1[W];
+            take(sW[t], c0, w0);
+            take(sW[t], c1, w1);
 #pragma unroll
             for (int u = 0; u < W; ++u) p[u] *= r * w0[u], q[u] *= r * w1[u];
           }
         }
         if (z.turn) angle::turn<HALF>(p, q, cs, sn);
-        if (y[k] != nullptr) {
-          angle::stv(y[k] + c0, p);
-          angle::stv(y[k] + c1, q);
+        if (put) {
+          angle::stv(y + c0, p);
+          angle::stv(y + c1, q);
         }
-      } else if (y[k] != nullptr) {
-        *reinterpret_cast<uint4*>(y[k] + c0) = lo[k];
-        *reinterpret_cast<uint4*>(y[k] + c1) = hi[k];
+      } else if (put) {
+        *reinterpret_cast<uint4*>(y + c0) = now.lo[k];
+        *reinterpret_cast<uint4*>(y + c1) = now.hi[k];
       }
     }
+    now = next;
   }
 }
 
