@@ -6,7 +6,9 @@
 // that a warp holds whole groups; at d = 96 a quarter of them idle) takes a token: a thread holds
 // 16 bytes of each half of the head (neighbouring pairs: 32 bytes in a row), so that both
 // coordinates of its pairs are its own and the sum of squares is a few shuffles.  The sines of its
-// pairs serve all its heads.  Squares, sums and r are fp32; each output is rounded once.
+// pairs, times the weights, serve all its heads; arithmetic goes two floats an instruction.  The first heads'
+// loads are issued before the tables and the token's place are looked up, each next ones' before
+// these are worked on.  Squares, sums and r are fp32; each output is rounded once.
 #include <cuda_bf16.h>
 
 #include "angle.cuh"
@@ -18,7 +20,6 @@ namespace {
 
 constexpr int kT = 256;
 constexpr int kMaxPairs = 128;
-constexpr int kHU = 4;  // heads whose loads are in flight together
 
 // Threads per token: its pairs in pieces of W, rounded up to a power of two.
 __host__ __device__ inline int group_threads(int d, int W) {
@@ -27,17 +28,30 @@ __host__ __device__ inline int group_threads(int d, int W) {
   return n;
 }
 
-__device__ __forceinline__ float group_sum(float v, int LG) {
+template <int LG>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
   for (int o = LG / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// 2 W consecutive-per-piece floats of a table in shared memory.
-template <int W>
-__device__ __forceinline__ void take(const float* s, int c, float (&x)[W]) {
-#pragma unroll
-  for (int u = 0; u < W; u += 4) *reinterpret_cast<float4*>(x + u) = *reinterpret_cast<const float4*>(s + c + u);
+// 16 bytes as pairs of floats, and back.
+__device__ __forceinline__ void widen2(const uint4& v, uint64_t* x, float) { x[0] = tc::pk2(v.x, v.y), x[1] = tc::pk2(v.z, v.w); }
+__device__ __forceinline__ void widen2(const uint4& v, uint64_t* x, __nv_bfloat16) {
+  x[0] = tc::bf2_to_f2(v.x), x[1] = tc::bf2_to_f2(v.y), x[2] = tc::bf2_to_f2(v.z), x[3] = tc::bf2_to_f2(v.w);
 }
+__device__ __forceinline__ uint32_t pack2(uint64_t x) {
+  const float2 f = tc::unpk2(x);
+  return ptx::pack_bf16(f.x, f.y);
+}
+__device__ __forceinline__ void put2(float* p, const uint64_t* x) {
+  const float2 a = tc::unpk2(x[0]), b = tc::unpk2(x[1]);
+  *reinterpret_cast<float4*>(p) = make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void put2(__nv_bfloat16* p, const uint64_t* x) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack2(x[0]), pack2(x[1]), pack2(x[2]), pack2(x[3]));
+}
+__device__ __forceinline__ uint64_t both(float v) { return tc::pk2f(v, v); }
 
 // The frequencies' turns per step and their axes (outside 0 .. axes - 1: -1).
 __device__ __forceinline__ void angle_tables(const float* freq, const int* axis, int pairs, int axes,
@@ -49,235 +63,340 @@ __device__ __forceinline__ void angle_tables(const float* freq, const int* axis,
   }
 }
 
-template <typename T, bool HALF, bool APPEND>
-__global__ void __launch_bounds__(kT) head_kernel(const HeadArgs a) {
-  constexpr int W = 16 / sizeof(T);  // pairs per thread
+// A thread's part of a head: W packed pairs, of its first piece and then of its second.  Its coordinate pair u is
+// HALF: elements u of both pieces; else the neighbours 2u, 2u + 1 of the two in a row.
+template <typename T, bool HALF>
+struct Part {
+  static constexpr int W = 16 / sizeof(T);  // pairs of coordinates, and packed words
+  // (x0, x1) -> (x0 a + x1 nb, x0 c + x1 d) of every pair
+  uint64_t p[W], q[W];  // HALF: a, nb then c, d of two pairs each; else (a, c), (nb, d) of a pair each
+  __device__ __forceinline__ void set(int u, float a, float nb, float c, float d) {
+    if (HALF) {
+      const int k = u / 2;
+      const float2 A = tc::unpk2(p[k]), B = tc::unpk2(q[k]), C = tc::unpk2(p[W / 2 + k]), E = tc::unpk2(q[W / 2 + k]);
+      p[k] = u % 2 ? tc::pk2f(A.x, a) : tc::pk2f(a, 0.f), q[k] = u % 2 ? tc::pk2f(B.x, nb) : tc::pk2f(nb, 0.f);
+      p[W / 2 + k] = u % 2 ? tc::pk2f(C.x, c) : tc::pk2f(c, 0.f), q[W / 2 + k] = u % 2 ? tc::pk2f(E.x, d) : tc::pk2f(d, 0.f);
+    } else {
+      p[u] = tc::pk2f(a, c), q[u] = tc::pk2f(nb, d);
+    }
+  }
+  __device__ __forceinline__ void apply(const uint64_t (&x)[W], uint64_t (&y)[W]) const {
+    if (HALF) {
+#pragma unroll
+      for (int k = 0; k < W / 2; ++k) {
+        y[k] = tc::fma2(x[W / 2 + k], q[k], tc::mul2(x[k], p[k]));
+        y[W / 2 + k] = tc::fma2(x[W / 2 + k], q[W / 2 + k], tc::mul2(x[k], p[W / 2 + k]));
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < W; ++u) {
+        const float2 v = tc::unpk2(x[u]);
+        y[u] = tc::fma2(both(v.y), q[u], tc::mul2(both(v.x), p[u]));
+      }
+    }
+  }
+};
+
+template <int W>
+__device__ __forceinline__ float sum_squares(const uint64_t (&x)[W]) {
+  uint64_t s = tc::mul2(x[0], x[0]);
+#pragma unroll
+  for (int k = 1; k < W; ++k) s = tc::fma2(x[k], x[k], s);
+  const float2 f = tc::unpk2(s);
+  return f.x + f.y;
+}
+
+// W floats of a table from c0 on and W from c1 on (ones where it is null).
+template <int W>
+__device__ __forceinline__ void weights(const float* w, int c0, int c1, float (&w0)[W], float (&w1)[W]) {
+#pragma unroll
+  for (int u = 0; u < W; ++u) w0[u] = w1[u] = 1.f;
+  if (w == nullptr) return;
+#pragma unroll
+  for (int u = 0; u < W; ++u) w0[u] = __ldg(w + c0 + u), w1[u] = __ldg(w + c1 + u);  // (aligned to 4 bytes only)
+}
+
+constexpr int kHU = 3;      // heads whose loads are in flight together
+constexpr int kNear = 512;  // sequences of an append that are looked up in shared memory
+
+template <typename T, bool HALF, bool APPEND, int LG>
+__global__ void __launch_bounds__(kT, 2) head_kernel(const HeadArgs a) {
+  using P = Part<T, HALF>;
+  constexpr int W = P::W;
   __shared__ unsigned long long sT[kMaxPairs];
   __shared__ int sAx[kMaxPairs];
-  __shared__ __align__(16) float sW[4][2 * kMaxPairs];
-  const int pairs = a.d / 2, per = pairs / W, LG = group_threads(a.d, W);
-  const int64_t gid = static_cast<int64_t>(blockIdx.x) * kT + threadIdx.x;
-  const int64_t tokens = a.B * a.N, token = gid / LG;
-  const int part = static_cast<int>(gid) & (LG - 1);
-  const bool in = token < tokens && part < per;  // (the others take part in the shuffles)
+  __shared__ int sCu[APPEND ? kNear + 1 : 1], sLens[APPEND ? kNear : 1];
+  const int pairs = a.d / 2, per = pairs / W;
+  int t = 0;
+  while (static_cast<int>(blockIdx.y) >= a.first[t + 1]) ++t;
+  const HeadTensor& z = a.t[t];
+  const int hb = (blockIdx.y - a.first[t]) * a.per[t], heads = min(a.per[t], z.heads - hb);
+  const int part = threadIdx.x & (LG - 1);
+  const bool mine = part < per;  // (the others take part in the shuffles, on the first one's elements)
+  const int own = mine ? part : 0;
+  const int c0 = HALF ? own * W : 2 * own * W, c1 = HALF ? c0 + pairs : c0 + W;
   const bool packed = APPEND && a.seqs.cu != nullptr;
-  const int64_t b = in && !packed ? token / a.N : 0, n = in ? token - b * a.N : 0;
-  const int hb = blockIdx.y * a.per_thread;
-  const int he = min(hb + a.per_thread, a.heads);
-  const int c0 = HALF ? part * W : 2 * part * W, c1 = HALF ? c0 + pairs : c0 + W;
-  // kHU heads' loads at a time, the next ones' before these are worked on (y may be x, but no other head's).
+  const int64_t tokens = a.B * a.N;
+  constexpr int step = kT / LG;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * step;
+  struct Token {
+    int64_t i, b, n;
+    const T* x;
+  };
+  auto token_at = [&](int64_t base) {  // (behind the last one: the last one)
+    Token k;
+    k.i = min(base + threadIdx.x / LG, tokens - 1);
+    k.b = packed ? 0 : k.i / a.N, k.n = k.i - k.b * a.N;
+    k.x = static_cast<const T*>(z.x) + k.b * z.xs[0] + hb * z.xs[1] + k.n * z.xs[2];
+    return k;
+  };
   struct Heads {
     uint4 lo[kHU], hi[kHU];
   };
-  auto locate = [&](int h, int& t) {  // head h of all tensors: the returned one of tensor t
-    t = 0;
-    while (h >= a.t[t].heads) h -= a.t[t].heads, ++t;
-    return h;
-  };
-  auto fetch = [&](int h, Heads& z) {
+  auto fetch = [&](const T* x, int h, Heads& v) {  // (behind the last head: the last one)
 #pragma unroll
     for (int k = 0; k < kHU; ++k) {
-      z.lo[k] = z.hi[k] = make_uint4(0, 0, 0, 0);
-      if (h + k >= he || !in) continue;
-      int t;
-      const int hh = locate(h + k, t);
-      const T* x = static_cast<const T*>(a.t[t].x) + b * a.t[t].xs[0] + hh * a.t[t].xs[1] + n * a.t[t].xs[2];
-      z.lo[k] = *reinterpret_cast<const uint4*>(x + c0);
-      z.hi[k] = *reinterpret_cast<const uint4*>(x + c1);
+      const T* at = x + min(h + k, heads - 1) * z.xs[1];
+      v.lo[k] = *reinterpret_cast<const uint4*>(at + c0);
+      v.hi[k] = *reinterpret_cast<const uint4*>(at + c1);
     }
   };
   Heads now, next;
-  fetch(hb, now);
-  // Behind those loads: the tables, and where the token belongs.
-  if (a.freq != nullptr) angle_tables(a.freq, a.axis, pairs, a.axes, sT, sAx);
-#pragma unroll
-  for (int t = 0; t < 4; ++t)
-    if (a.t[t].heads > 0 && a.t[t].norm)
-      for (int i = threadIdx.x; i < a.d; i += kT) sW[t][i] = a.t[t].w != nullptr ? a.t[t].w[i] : 1.f;
-  bool live = in;
-  int at = 0, page = -1, slot = 0;  // its position in its sequence and its place in the cache
-  if (APPEND && token < tokens) {
-    const Seqs& q = a.seqs;
-    int s = static_cast<int>(b);
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * step;
+  Token tok = token_at(first);
+  fetch(tok.x, 0, now);
+  // Behind those loads: the tables.
+  const bool turn = z.turn;
+  if (turn) angle_tables(a.freq, a.axis, pairs, a.axes, sT, sAx);
+  float w0[W], w1[W];
+  weights<W>(z.norm ? z.w : nullptr, c0, c1, w0, w1);
+  const float inv = 1.f / static_cast<float>(a.d);
+  Seqs q = a.seqs;
+  if (APPEND && q.B <= kNear) {
+    for (int i = threadIdx.x; i <= q.B; i += kT) {
+      if (packed) sCu[i] = q.cu[i];
+      if (i < q.B) sLens[i] = q.lens[i];
+    }
+    if (packed) q.cu = sCu;
+    q.lens = sLens;
+  }
+  if (turn || APPEND) __syncthreads();
+  // A token's position in its sequence and its place in the cache (page as the table holds it, unused where
+  // it is none).
+  struct Place {
+    int at, page, slot;
+    bool live;
+  };
+  auto place_at = [&](const Token& k, int64_t base) {
+    Place x{0, -1, 0, mine && base + threadIdx.x / LG < tokens};
+    if (!APPEND) return x;
+    int s = static_cast<int>(packed ? 0 : k.b);
     if (packed) {  // the last sequence that begins at or before this row
       int lo = 0, hi = q.B;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (q.cu[mid] <= token) lo = mid; else hi = mid;
+        if (q.cu[mid] <= k.i) lo = mid; else hi = mid;
       }
       s = lo;
     }
-    const Seq z = seq_at(q, s);
-    const int64_t t = (packed ? token : token - static_cast<int64_t>(s) * a.N) - z.row0;
-    live = live && t >= 0 && t < z.n;  // (a row of no sequence)
-    const int64_t p = static_cast<int64_t>(z.start) + t;
-    at = static_cast<int>(p);
-    if (live && p >= 0 && p < q.cap) {
-      const int e = at / q.page;
-      page = page_at(q, s, e), slot = at - e * q.page;
+    const Seq e = seq_at(q, s);
+    const int64_t i = k.n - e.row0, p = e.start + i;
+    x.live = x.live && i >= 0 && i < e.n;  // (a row of no sequence)
+    x.at = static_cast<int>(p);
+    if (z.paged && x.live && p >= 0 && p < q.cap) {
+      const int entry = x.at / q.page;
+      x.page = __ldg(q.table + s * q.width + entry), x.slot = x.at - entry * q.page;
     }
-  }
-  int pos[W];
-  __syncthreads();
+    return x;
+  };
+  Place place = place_at(tok, first);
+  for (int64_t base = first; base < tokens; base += stride) {
+    const bool live = place.live;
+    const int at = place.at, slot = place.slot, page = place.page < q.pages ? place.page : -1;
+    P m;
+    {
+      int pos[W];
 #pragma unroll
-  for (int u = 0; u < W; ++u) {
-    const int ax = a.freq != nullptr && live ? sAx[part * W + u] : -1;
-    pos[u] = ax < 0 ? 0 : APPEND && a.pos == nullptr ? at : a.pos[ax * a.pos_axis + b * a.pos_batch + n];
-  }
-  float cs[W], sn[W];
+      for (int u = 0; u < W; ++u) {
+        const int ax = turn ? sAx[own * W + u] : -1;
+        pos[u] = ax < 0 ? 0 : APPEND && a.pos == nullptr ? at : a.pos[ax * a.pos_axis + tok.b * a.pos_batch + tok.n];
+      }
 #pragma unroll
-  for (int u = 0; u < W; ++u) {
-    const int i = part * W + u;
-    cs[u] = 1.f, sn[u] = 0.f;
-    if (a.freq != nullptr && live && sAx[i] >= 0) angle::sincos_at(pos[u], sT[i], &sn[u], &cs[u]);
-  }
-  for (int h = hb; h < he; h += kHU) {
-    if (h + kHU < he) fetch(h + kHU, next);
-#pragma unroll
-    for (int k = 0; k < kHU; ++k) {
-      if (h + k >= he) break;
-      int t;
-      const int hh = locate(h + k, t);
-      const HeadTensor& z = a.t[t];
-      const bool put = live && !(APPEND && z.paged && page < 0);
-      T* y = static_cast<T*>(z.y) + hh * z.ys[1] +
-             (APPEND && z.paged ? page * z.ys[0] + slot * z.ys[2] : b * z.ys[0] + n * z.ys[2]);
-      if (z.norm || z.turn) {
-        float p[W], q[W];
-        angle::widen(now.lo[k], p);
-        angle::widen(now.hi[k], q);
-        if (z.norm) {
-          float ss = 0.f;
-#pragma unroll
-          for (int u = 0; u < W; ++u) ss = fmaf(p[u], p[u], fmaf(q[u], q[u], ss));
-          const float r = rsqrtf(group_sum(ss, LG) / static_cast<float>(a.d) + a.eps);
-          if (part < per) {
-            float w0[W], w1[W];
-            take(sW[t], c0, w0);
-            take(sW[t], c1, w1);
-#pragma unroll
-            for (int u = 0; u < W; ++u) p[u] *= r * w0[u], q[u] *= r * w1[u];
-          }
-        }
-        if (z.turn) angle::turn<HALF>(p, q, cs, sn);
-        if (put) {
-          angle::stv(y + c0, p);
-          angle::stv(y + c1, q);
-        }
-      } else if (put) {
-        *reinterpret_cast<uint4*>(y + c0) = now.lo[k];
-        *reinterpret_cast<uint4*>(y + c1) = now.hi[k];
+      for (int u = 0; u < W; ++u) {
+        float cs = 1.f, sn = 0.f;
+        if (turn && sAx[own * W + u] >= 0) angle::sincos_at(pos[u], sT[own * W + u], &sn, &cs);
+        // the pair's weights: of its elements in the two pieces, or in a row through both
+        const float wa = HALF ? w0[u] : u < W / 2 ? w0[2 * u % W] : w1[2 * u % W];
+        const float wb = HALF ? w1[u] : u < W / 2 ? w0[(2 * u + 1) % W] : w1[(2 * u + 1) % W];
+        m.set(u, wa * cs, -wb * sn, wa * sn, wb * cs);
       }
     }
-    now = next;
+    const bool put = live && !(APPEND && z.paged && page < 0);
+    T* y = static_cast<T*>(z.y) + hb * z.ys[1] +
+           (APPEND && z.paged ? page * z.ys[0] + slot * z.ys[2] : tok.b * z.ys[0] + tok.n * z.ys[2]);
+    const T* x = tok.x;
+    tok = token_at(base + stride);
+    if (APPEND) place = place_at(tok, base + stride);  // (its page is not waited for here)
+    else place.live = mine && base + stride + threadIdx.x / LG < tokens;
+    for (int h = 0; h < heads; h += kHU) {
+      fetch(h + kHU < heads ? x : tok.x, h + kHU < heads ? h + kHU : 0, next);
+#pragma unroll
+      for (int k = 0; k < kHU; ++k) {
+        if (h + k >= heads) break;
+        T* to = y + (h + k) * z.ys[1];
+        if (z.norm || turn) {
+          uint64_t v[W], o[W];
+          widen2(now.lo[k], v, T{}), widen2(now.hi[k], v + W / 2, T{});
+          m.apply(v, o);
+          if (z.norm) {
+            const float ss = sum_squares(v);
+            const float r = rsqrtf(fmaf(group_sum<LG>(mine ? ss : 0.f), inv, a.eps));
+#pragma unroll
+            for (int u = 0; u < W; ++u) o[u] = tc::mul2(o[u], both(r));
+          }
+          if (put) {
+            put2(to + c0, o);
+            put2(to + c1, o + W / 2);
+          }
+        } else if (put) {
+          *reinterpret_cast<uint4*>(to + c0) = now.lo[k];
+          *reinterpret_cast<uint4*>(to + c1) = now.hi[k];
+        }
+      }
+      now = next;
+    }
   }
 }
 
-template <typename T, bool HALF>
-__global__ void __launch_bounds__(kT) grad_kernel(const HeadGradArgs a) {
+template <typename T, bool HALF, int LG>
+__global__ void __launch_bounds__(kT, 2) grad_kernel(const HeadGradArgs a) {
   constexpr int W = 16 / sizeof(T);
   __shared__ unsigned long long sT[kMaxPairs];
   __shared__ int sAx[kMaxPairs];
-  __shared__ __align__(16) float sW[2 * kMaxPairs];
   __shared__ float sum[kT / 32][2 * kMaxPairs];
+  __shared__ __align__(16) float sW[2 * kMaxPairs];
   ptx::grid_dependency_launch();
-  const int pairs = a.d / 2, per = pairs / W, LG = group_threads(a.d, W);
+  const int pairs = a.d / 2, per = pairs / W;
   int t = 0;
   while (static_cast<int>(blockIdx.y) >= a.first[t + 1]) ++t;
   const HeadGrad& z = a.t[t];
-  const int hb = (blockIdx.y - a.first[t]) * a.per, he = min(hb + a.per, z.heads);
-  if (a.freq != nullptr) angle_tables(a.freq, a.axis, pairs, a.axes, sT, sAx);
-  for (int i = threadIdx.x; i < a.d; i += kT) sW[i] = z.w != nullptr ? z.w[i] : 1.f;
-  __syncthreads();
+  const int hb = (blockIdx.y - a.first[t]) * a.per[t], heads = min(a.per[t], z.heads - hb);
   const int part = threadIdx.x & (LG - 1);
-  const int c0 = HALF ? part * W : 2 * part * W, c1 = HALF ? c0 + pairs : c0 + W;
-  const bool mine = part < per;
-  float w0[W], w1[W], g0[W], g1[W];
-#pragma unroll
-  for (int u = 0; u < W; ++u) w0[u] = w1[u] = g0[u] = g1[u] = 0.f;
-  if (mine) {
-    take(sW, c0, w0);
-    take(sW, c1, w1);
-  }
+  const bool mine = part < per, turn = a.freq != nullptr;
+  const int own = mine ? part : 0;
+  const int c0 = HALF ? own * W : 2 * own * W, c1 = HALF ? c0 + pairs : c0 + W;
   const int64_t tokens = a.B * a.N;
-  const int step = kT / LG;
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * step; base < tokens; base += static_cast<int64_t>(gridDim.x) * step) {
-    const int64_t token = base + threadIdx.x / LG;
-    const bool live = mine && token < tokens;
-    const int64_t b = live ? token / a.N : 0, n = live ? token - b * a.N : 0;
+  constexpr int step = kT / LG;
+  struct Token {
+    int64_t b, n;
+    const T *x, *dy;
+  };
+  auto token_at = [&](int64_t base) {  // (behind the last one: the last one)
+    Token k;
+    const int64_t i = min(base + threadIdx.x / LG, tokens - 1);
+    k.b = i / a.N, k.n = i - k.b * a.N;
+    k.x = static_cast<const T*>(z.x) + k.b * z.xs[0] + hb * z.xs[1] + k.n * z.xs[2];
+    k.dy = static_cast<const T*>(z.dy) + k.b * z.dys[0] + hb * z.dys[1] + k.n * z.dys[2];
+    return k;
+  };
+  // A head of x and dy at a time, the loads of the next but one, of the next token too, before it is worked on.
+  struct Head {
+    uint4 xl, xh, yl, yh;
+  };
+  auto fetch = [&](const Token& k, int h, Head& v) {
+    const T *x = k.x + h * z.xs[1], *dy = k.dy + h * z.dys[1];
+    v.xl = *reinterpret_cast<const uint4*>(x + c0), v.xh = *reinterpret_cast<const uint4*>(x + c1);
+    v.yl = *reinterpret_cast<const uint4*>(dy + c0), v.yh = *reinterpret_cast<const uint4*>(dy + c1);
+  };
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * step, stride = static_cast<int64_t>(gridDim.x) * step;
+  Token tok = token_at(first), then = token_at(first + stride);
+  Head now, next;
+  fetch(tok, 0, now);
+  if (heads > 1) fetch(tok, 1, next); else fetch(then, 0, next);
+  if (turn) angle_tables(a.freq, a.axis, pairs, a.axes, sT, sAx);
+  for (int i = threadIdx.x; i < a.d; i += kT) sW[i] = z.w != nullptr ? z.w[i] : 1.f;
+  uint64_t g[W];
+#pragma unroll
+  for (int k = 0; k < W; ++k) g[k] = 0;
+  __syncthreads();
+  const float inv = 1.f / static_cast<float>(a.d);
+  for (int64_t base = first; base < tokens; base += stride) {
+    const bool live = mine && base + threadIdx.x / LG < tokens;
     float cs[W], sn[W];
 #pragma unroll
     for (int u = 0; u < W; ++u) {
-      const int i = part * W + u, ax = a.freq != nullptr && live ? sAx[i] : -1;
+      const int i = own * W + u, ax = turn ? sAx[i] : -1;
       cs[u] = 1.f, sn[u] = 0.f;
-      if (ax >= 0) {
-        angle::sincos_at(a.pos[ax * a.pos_axis + b * a.pos_batch + n], sT[i], &sn[u], &cs[u]);
-        sn[u] = -sn[u];
-      }
+      if (ax >= 0) angle::sincos_at(a.pos[ax * a.pos_axis + tok.b * a.pos_batch + tok.n], sT[i], &sn[u], &cs[u]);
     }
-    constexpr int U = 2;  // heads whose loads are in flight together
-    for (int h = hb; h < he; h += U) {
-      uint4 xl[U], xh[U], yl[U], yh[U];
+    T* dx = static_cast<T*>(z.dx) + tok.b * z.dxs[0] + hb * z.dxs[1] + tok.n * z.dxs[2];
+    for (int h = 0; h < heads; ++h, dx += z.dxs[1]) {
+      uint64_t x[W], y[W], f[W];
+      widen2(now.xl, x, T{}), widen2(now.xh, x + W / 2, T{});
+      widen2(now.yl, y, T{}), widen2(now.yh, y + W / 2, T{});
+      now = next;
+      if (h + 2 < heads) fetch(tok, h + 2, next); else fetch(then, min(h + 2 - heads, heads - 1), next);
+      if (HALF) {  // the turn back
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        xl[k] = xh[k] = yl[k] = yh[k] = make_uint4(0, 0, 0, 0);
-        if (h + k >= he || !live) continue;
-        const T* x = static_cast<const T*>(z.x) + b * z.xs[0] + (h + k) * z.xs[1] + n * z.xs[2];
-        const T* dy = static_cast<const T*>(z.dy) + b * z.dys[0] + (h + k) * z.dys[1] + n * z.dys[2];
-        xl[k] = *reinterpret_cast<const uint4*>(x + c0), xh[k] = *reinterpret_cast<const uint4*>(x + c1);
-        yl[k] = *reinterpret_cast<const uint4*>(dy + c0), yh[k] = *reinterpret_cast<const uint4*>(dy + c1);
-      }
-#pragma unroll
-      for (int k = 0; k < U; ++k) {
-        if (h + k >= he) break;
-        float p[W], q[W], f[W], e[W];
-        angle::widen(xl[k], p);
-        angle::widen(xh[k], q);
-        angle::widen(yl[k], f);
-        angle::widen(yh[k], e);
-        angle::turn<HALF>(f, e, cs, sn);
-        float ss = 0.f, dot = 0.f;
+        for (int k = 0; k < W / 2; ++k) {
+          const uint64_t c2 = tc::pk2f(cs[2 * k], cs[2 * k + 1]), s2 = tc::pk2f(sn[2 * k], sn[2 * k + 1]);
+          const uint64_t n2 = tc::pk2f(-sn[2 * k], -sn[2 * k + 1]);
+          f[k] = tc::fma2(y[W / 2 + k], s2, tc::mul2(y[k], c2));
+          f[W / 2 + k] = tc::fma2(y[k], n2, tc::mul2(y[W / 2 + k], c2));
+        }
+      } else {
 #pragma unroll
         for (int u = 0; u < W; ++u) {
-          ss = fmaf(p[u], p[u], fmaf(q[u], q[u], ss));
-          dot = fmaf(w0[u] * f[u], p[u], fmaf(w1[u] * e[u], q[u], dot));
+          const float2 v = tc::unpk2(y[u]);
+          f[u] = tc::pk2f(fmaf(v.y, sn[u], v.x * cs[u]), fmaf(-v.x, sn[u], v.y * cs[u]));
         }
-        ss = group_sum(ss, LG), dot = group_sum(dot, LG);
-        const float inv = 1.f / static_cast<float>(a.d), r = rsqrtf(ss * inv + a.eps);
-        if (!live) continue;
-        const float m = dot * inv * r * r;
+      }
+      uint64_t dots = 0;
 #pragma unroll
-        for (int u = 0; u < W; ++u) {
-          g0[u] = fmaf(f[u], p[u] * r, g0[u]);
-          g1[u] = fmaf(e[u], q[u] * r, g1[u]);
-          p[u] = r * fmaf(-p[u], m, w0[u] * f[u]);
-          q[u] = r * fmaf(-q[u], m, w1[u] * e[u]);
+      for (int k = 0; k < W; k += 2) {
+        const uint4 w = *reinterpret_cast<const uint4*>(sW + (k < W / 2 ? c0 + 2 * k : c1 + 2 * (k - W / 2)));
+        y[k] = tc::mul2(tc::pk2(w.x, w.y), f[k]), y[k + 1] = tc::mul2(tc::pk2(w.z, w.w), f[k + 1]);
+        dots = tc::fma2(y[k], x[k], dots), dots = tc::fma2(y[k + 1], x[k + 1], dots);
+      }
+      const float2 dd = tc::unpk2(dots);
+      const float sq = sum_squares(x);
+      const float ss = group_sum<LG>(mine ? sq : 0.f), dot = group_sum<LG>(mine ? dd.x + dd.y : 0.f);
+      const float r = rsqrtf(fmaf(ss, inv, a.eps));
+      if (live) {
+        const uint64_t r2 = both(r), nm = both(-dot * inv * r * r);
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+          g[k] = tc::fma2(f[k], tc::mul2(x[k], r2), g[k]);
+          y[k] = tc::mul2(tc::fma2(x[k], nm, y[k]), r2);
         }
-        T* dx = static_cast<T*>(z.dx) + b * z.dxs[0] + (h + k) * z.dxs[1] + n * z.dxs[2];
-        angle::stv(dx + c0, p);
-        angle::stv(dx + c1, q);
+        put2(dx + c0, y);
+        put2(dx + c1, y + W / 2);
       }
     }
+    tok = then;
+    then = token_at(base + 2 * stride);
   }
   if (z.dw == nullptr) return;
   // This block's share of dw: over the groups of a warp, then over the warps.
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
-  for (int u = 0; u < W; ++u)
-    for (int o = LG; o < 32; o <<= 1) {
-      g0[u] += __shfl_xor_sync(0xffffffffu, g0[u], o);
-      g1[u] += __shfl_xor_sync(0xffffffffu, g1[u], o);
-    }
+  for (int k = 0; k < W; ++k)
+#pragma unroll
+    for (int o = LG; o < 32; o <<= 1) g[k] = tc::add2(g[k], __shfl_xor_sync(0xffffffffu, g[k], o));
   if (lane < per) {
 #pragma unroll
-    for (int u = 0; u < W; ++u) sum[warp][c0 + u] = g0[u], sum[warp][c1 + u] = g1[u];
+    for (int k = 0; k < W; ++k) {
+      const float2 v = tc::unpk2(g[k]);
+      const int c = k < W / 2 ? c0 + 2 * k : c1 + 2 * (k - W / 2);
+      sum[warp][c] = v.x, sum[warp][c + 1] = v.y;
+    }
   }
   __syncthreads();
   float* out = a.ws + (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * a.d;
   for (int i = threadIdx.x; i < a.d; i += kT) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kT / 32; ++w) v += sum[w][i];
+    for (int k = 0; k < kT / 32; ++k) v += sum[k][i];
     out[i] = v;
   }
 }
@@ -304,24 +423,56 @@ __global__ void __launch_bounds__(1024) weight_kernel(const HeadGradArgs a) {
   }
 }
 
-template <typename T, bool APPEND>
-cudaError_t run(HeadArgs a, bool half, cudaStream_t st) {
-  const int64_t threads = a.B * a.N * group_threads(a.d, 16 / static_cast<int>(sizeof(T)));
-  // Heads per thread: eight or four (whole groups of loads in flight) where that leaves a wave of
-  // threads on 152 SMs, so that the sines are shared.
-  const int64_t hp = a.heads * threads / (152 * 2048);
-  a.per_thread = hp >= 8 ? 8 : hp >= kHU ? kHU : 1;
-  const dim3 grid(static_cast<unsigned>((threads + kT - 1) / kT),
-                  static_cast<unsigned>((a.heads + a.per_thread - 1) / a.per_thread));
-  if (half)
-    head_kernel<T, true, APPEND><<<grid, kT, 0, st>>>(a);
-  else
-    head_kernel<T, false, APPEND><<<grid, kT, 0, st>>>(a);
+// Heads of a block row: up to `most`, a tensor's rows alike; the block rows before each tensor.
+void split_heads(int count, const int64_t* heads, int most, int* per, int* first) {
+  first[0] = 0;
+  for (int t = 0; t < 4; ++t) {
+    const int h = t < count ? static_cast<int>(heads[t]) : 0, rows = (h + most - 1) / most;
+    per[t] = rows > 0 ? (h + rows - 1) / rows : 1;
+    first[t + 1] = first[t] + (h + per[t] - 1) / per[t];
+  }
+}
+
+// Heads per thread: six or three (whole groups of loads in flight) where that leaves a wave of threads on 152 SMs,
+// so that the sines are shared.
+int heads_per_thread(int64_t thread_heads) {
+  const int64_t hp = thread_heads / (152 * 512);
+  return hp >= 6 ? 6 : hp >= 3 ? 3 : 1;
+}
+// Block columns for `groups` of tokens: a wave of two blocks an SM, each block taking its groups one after
+// another behind one set of tables (2, 4 and 8 waves: 43, 44, 47 against 41 us for 24 heads of 32768 tokens).
+int columns(int64_t groups, int rows) {
+  const int64_t wave = rows > 0 && rows < 152 * 2 ? 152 * 2 / rows : 1;
+  return static_cast<int>(groups < wave ? groups : wave);
+}
+
+template <typename T, bool HALF, bool APPEND, int LG>
+cudaError_t run(const HeadArgs& a, dim3 grid, cudaStream_t st) {
+  head_kernel<T, HALF, APPEND, LG><<<grid, kT, 0, st>>>(a);
   return cudaGetLastError();
+}
+template <typename T, bool HALF, bool APPEND>
+cudaError_t run(const HeadArgs& a, int LG, dim3 grid, cudaStream_t st) {
+  constexpr int S = sizeof(T) / 2;  // threads per token: d = 32, 64, 96 and 128, 256
+  return LG == 2 * S   ? run<T, HALF, APPEND, 2 * S>(a, grid, st)
+         : LG == 4 * S ? run<T, HALF, APPEND, 4 * S>(a, grid, st)
+         : LG == 8 * S ? run<T, HALF, APPEND, 8 * S>(a, grid, st)
+                       : run<T, HALF, APPEND, 16 * S>(a, grid, st);
+}
+template <typename T>
+cudaError_t run(HeadArgs a, bool half, bool append, cudaStream_t st) {
+  const int LG = group_threads(a.d, 16 / static_cast<int>(sizeof(T)));
+  const int64_t threads = a.B * a.N * LG;
+  int64_t heads[4];
+  for (int t = 0; t < 4; ++t) heads[t] = a.t[t].heads;
+  split_heads(4, heads, heads_per_thread(a.heads * threads), a.per, a.first);
+  const dim3 grid(static_cast<unsigned>(columns((threads + kT - 1) / kT, a.first[4])), static_cast<unsigned>(a.first[4]));
+  if (append) return half ? run<T, true, true>(a, LG, grid, st) : run<T, false, true>(a, LG, grid, st);
+  return half ? run<T, true, false>(a, LG, grid, st) : run<T, false, false>(a, LG, grid, st);
 }
 
 struct GradPlan {
-  int per, rows, cols;
+  int per[4], first[5], cols;
 };
 GradPlan grad_plan(int64_t B, int64_t N, int64_t d, int dtype, const int64_t* heads, int count) {
   const int W = dtype == ATTN_BF16 ? 8 : 4, step = kT / group_threads(static_cast<int>(d), W);
@@ -329,26 +480,30 @@ GradPlan grad_plan(int64_t B, int64_t N, int64_t d, int dtype, const int64_t* he
   int64_t all = 0;
   for (int t = 0; t < count; ++t) all += heads[t];
   GradPlan p;
-  const int64_t hp = all * groups * kT / (152 * 2048);
-  p.per = hp >= 8 ? 8 : hp >= 4 ? 4 : 1;
-  p.rows = 0;
-  for (int t = 0; t < count; ++t) p.rows += static_cast<int>((heads[t] + p.per - 1) / p.per);
-  const int64_t want = p.rows > 0 ? (152 * 8 + p.rows - 1) / p.rows : 1;
-  p.cols = static_cast<int>(groups < want ? groups : want);
+  split_heads(count, heads, heads_per_thread(all * groups * kT), p.per, p.first);
+  p.cols = columns(groups, p.first[4]);
   return p;
+}
+
+template <typename T, bool HALF>
+cudaError_t run_grad(const HeadGradArgs& a, int LG, dim3 grid, cudaStream_t st) {
+  constexpr int S = sizeof(T) / 2;
+  if (LG == 2 * S) grad_kernel<T, HALF, 2 * S><<<grid, kT, 0, st>>>(a);
+  else if (LG == 4 * S) grad_kernel<T, HALF, 4 * S><<<grid, kT, 0, st>>>(a);
+  else if (LG == 8 * S) grad_kernel<T, HALF, 8 * S><<<grid, kT, 0, st>>>(a);
+  else grad_kernel<T, HALF, 16 * S><<<grid, kT, 0, st>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t head_norm(const HeadArgs& a, int dtype, bool half, bool append, cudaStream_t st) {
-  if (append)
-    return dtype == ATTN_BF16 ? run<__nv_bfloat16, true>(a, half, st) : run<float, true>(a, half, st);
-  return dtype == ATTN_BF16 ? run<__nv_bfloat16, false>(a, half, st) : run<float, false>(a, half, st);
+  return dtype == ATTN_BF16 ? run<__nv_bfloat16>(a, half, append, st) : run<float>(a, half, append, st);
 }
 
 size_t head_norm_bwd_bytes(int64_t B, int64_t N, int64_t d, int dtype, const int64_t* heads, int count) {
   const GradPlan p = grad_plan(B, N, d, dtype, heads, count);
-  return static_cast<size_t>(p.rows) * p.cols * d * sizeof(float);
+  return static_cast<size_t>(p.first[4]) * p.cols * d * sizeof(float);
 }
 
 cudaError_t head_norm_bwd(const HeadGradArgs& args, int dtype, bool half, cudaStream_t st) {
@@ -357,17 +512,14 @@ cudaError_t head_norm_bwd(const HeadGradArgs& args, int dtype, bool half, cudaSt
   bool dw = false;
   for (int t = 0; t < a.count; ++t) heads[t] = a.t[t].heads, dw = dw || a.t[t].dw != nullptr;
   const GradPlan p = grad_plan(a.B, a.N, a.d, dtype, heads, a.count);
-  a.per = p.per, a.cols = p.cols, a.first[0] = 0;
-  for (int t = 0; t < a.count; ++t) a.first[t + 1] = a.first[t] + static_cast<int>((heads[t] + p.per - 1) / p.per);
-  const dim3 grid(static_cast<unsigned>(p.cols), static_cast<unsigned>(p.rows));
-  if (dtype == ATTN_BF16) {
-    if (half) grad_kernel<__nv_bfloat16, true><<<grid, kT, 0, st>>>(a);
-    else grad_kernel<__nv_bfloat16, false><<<grid, kT, 0, st>>>(a);
-  } else {
-    if (half) grad_kernel<float, true><<<grid, kT, 0, st>>>(a);
-    else grad_kernel<float, false><<<grid, kT, 0, st>>>(a);
-  }
-  const cudaError_t e = cudaGetLastError();
+  for (int t = 0; t < 4; ++t) a.per[t] = p.per[t];
+  for (int t = 0; t < 5; ++t) a.first[t] = p.first[t];
+  a.cols = p.cols;
+  const dim3 grid(static_cast<unsigned>(p.cols), static_cast<unsigned>(p.first[4]));
+  const int LG = group_threads(a.d, dtype == ATTN_BF16 ? 8 : 4);
+  cudaError_t e;
+  if (dtype == ATTN_BF16) e = half ? run_grad<__nv_bfloat16, true>(a, LG, grid, st) : run_grad<__nv_bfloat16, false>(a, LG, grid, st);
+  else e = half ? run_grad<float, true>(a, LG, grid, st) : run_grad<float, false>(a, LG, grid, st);
   if (e != cudaSuccess || !dw) return e;
   return launch_behind(weight_kernel, a.count, 1024, 0, st, a);
 }

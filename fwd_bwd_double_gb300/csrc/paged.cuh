@@ -35,43 +35,24 @@ struct Work {
   Cut cut;
   int causal, window;
 };
-// What the planning launch leaves in front of the workspace.
-struct Head {
-  int64_t total, stretch;
-};
-struct Start {  // the item in which a CTA's stretch begins (b < 0: none)
-  int64_t pos;  // of the item on the line
-  int b, tile, vh, pad;
-};
 struct Tail {  // the item that begins in a CTA's stretch and goes on behind it
   int b, tile, vh, parts;  // parts 0: none
 };
-// Workspace: Head, Start[ctas], Tail[ctas], the line position behind each of the B sequences, then two slots
-// per CTA of `rows` rows: o [rows][D], (max in powers of two, sum) [rows].  Slot 2p holds CTA p's part of
-// an item that began before, slot 2p + 1 of one that begins here and goes on.
+// Workspace: Tail[ctas], then two slots per CTA of `rows` rows: o [rows][D], (max in powers of two, sum) [rows].  Slot 2p
+// holds CTA p's part of an item that began before, slot 2p + 1 of one that begins here and goes on.
 struct Space {
-  Head* head;
-  Start* start;
   Tail* tail;
-  int64_t* ends;
   float* slots;
   int64_t slot;  // floats of a slot
   int rows, D;
-  static int64_t header(int ctas, int64_t B) {
-    return (static_cast<int64_t>(sizeof(Head)) + ctas * static_cast<int64_t>(sizeof(Start) + sizeof(Tail)) + B * 8 + 255) /
-           256 * 256;
+  static int64_t header(int ctas) { return (ctas * static_cast<int64_t>(sizeof(Tail)) + 255) / 256 * 256; }
+  static size_t bytes(int ctas, int rows, int D) {
+    return static_cast<size_t>(header(ctas)) + 2ull * ctas * rows * (D + 2) * sizeof(float);
   }
-  static size_t bytes(int ctas, int64_t B, int rows, int D) {
-    return static_cast<size_t>(header(ctas, B)) + 2ull * ctas * rows * (D + 2) * sizeof(float);
-  }
-  static Space at(void* ws, int ctas, int64_t B, int rows, int D) {
-    uint8_t* w = static_cast<uint8_t*>(ws);
+  static Space at(void* ws, int ctas, int rows, int D) {
     Space s;
-    s.head = reinterpret_cast<Head*>(w);
-    s.start = reinterpret_cast<Start*>(w + sizeof(Head));
-    s.tail = reinterpret_cast<Tail*>(w + sizeof(Head) + ctas * sizeof(Start));
-    s.ends = reinterpret_cast<int64_t*>(s.tail + ctas);
-    s.slots = reinterpret_cast<float*>(w + header(ctas, B));
+    s.tail = static_cast<Tail*>(ws);
+    s.slots = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + header(ctas));
     s.slot = static_cast<int64_t>(rows) * (D + 2);
     s.rows = rows, s.D = D;
     return s;
@@ -110,49 +91,73 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
   return v;
 }
 
-// The plan for one CTA, by one warp of its own (every lane gets it): for calls whose sequences have few tiles, where
-// it costs less than a launch.
-__device__ __forceinline__ void plan_here(const Work& w, int p, Head& head, Start& start) {
+// The stretch of one CTA and the item in which it begins (b < 0: none), by one warp of its own (every lane gets
+// them).  Each CTA plans for itself: a planning launch in front took 4 to 5 us of every call.
+struct Plan {
+  int64_t from, to, stretch;
+  int64_t pos;  // of the item on the line
+  int b, tile, vh;
+};
+__device__ __forceinline__ Plan plan(const Work& w, int p) {
   const int lane = threadIdx.x & 31, B = w.seqs.B, step = w.cut.step;
-  auto units = [&](int b) {
+  constexpr int kFew = 4;  // tiles of a sequence that its lane looks at alone; the others are the warp's
+  auto units = [&](int b0) {  // of sequence b0 + lane
+    Seq s{};
+    if (b0 + lane < B) s = seq_at(w.seqs, b0 + lane);
     int64_t v = 0;
-    if (b < B) {
-      const Seq s = seq_at(w.seqs, b);
-      for (int64_t t = 0; t * step < s.n; ++t) v += tile_units(w, s, static_cast<int>(t));
+    for (int t = 0; t < kFew && static_cast<int64_t>(t) * step < s.n; ++t) v += tile_units(w, s, t);
+    for (unsigned many = __ballot_sync(0xffffffffu, s.n > static_cast<int64_t>(kFew) * step); many != 0; many &= many - 1) {
+      const int from = __ffs(many) - 1;
+      const Seq q = seq_at(w.seqs, b0 + from);
+      int64_t u = 0;
+      for (int64_t t = kFew + lane; t * step < q.n; t += 32) u += tile_units(w, q, static_cast<int>(t));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+      if (lane == from) v += u;
     }
     return v * w.cut.nv;
   };
   int64_t total = 0;
-  const int64_t mine = units(lane);  // (the first 32 sequences are looked at once)
-  for (int b0 = 0; b0 < B; b0 += 32) total += b0 == 0 ? mine : units(b0 + lane);
+  const int64_t mine = units(0);  // (the first 32 sequences are looked at once)
+  for (int b0 = 0; b0 < B; b0 += 32) total += b0 == 0 ? mine : units(b0);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   const int64_t even = (total + w.cut.ctas - 1) / w.cut.ctas;
-  head = Head{total, even > w.cut.least ? even : w.cut.least};
-  start = Start{0, -1, 0, 0, 0};
-  const int64_t x = head.stretch * p;
-  if (x >= total) return;
+  Plan r{};
+  r.stretch = even > w.cut.least ? even : w.cut.least;
+  r.from = r.stretch * p, r.to = min(r.from + r.stretch, total);
+  r.b = -1;
+  if (r.from >= total) return r;
   int64_t at = 0;
-  for (int b0 = 0; b0 < B; b0 += 32) {
-    const int64_t v = b0 == 0 ? mine : units(b0 + lane), cum = at + warp_scan(v, lane);
-    const unsigned behind = __ballot_sync(0xffffffffu, cum > x);
+  for (int b0 = 0; b0 < B; b0 += 32) {  // the first sequence that ends behind `from`
+    const int64_t v = b0 == 0 ? mine : units(b0), cum = at + warp_scan(v, lane);
+    const unsigned behind = __ballot_sync(0xffffffffu, cum > r.from);
     if (behind == 0) {
       at = __shfl_sync(0xffffffffu, cum, 31);
       continue;
     }
     const int from = __ffs(behind) - 1;
-    int64_t base = __shfl_sync(0xffffffffu, cum - v, from);
-    const Seq s = seq_at(w.seqs, b0 + from);
-    for (int t = 0;; ++t) {
-      const int64_t u = tile_units(w, s, t);
-      if (base + u * w.cut.nv > x) {
-        const int64_t vh = (x - base) / u;
-        start = Start{base + vh * u, b0 + from, t, static_cast<int>(vh), 0};
-        return;
-      }
-      base += u * w.cut.nv;
-    }
+    at = __shfl_sync(0xffffffffu, cum - v, from);
+    r.b = b0 + from;
+    break;
   }
+  const Seq s = seq_at(w.seqs, r.b);
+  for (int64_t t0 = 0; t0 * step < s.n; t0 += 32) {  // ... and its tile that does
+    const int64_t t = t0 + lane, u = t * step < s.n ? tile_units(w, s, static_cast<int>(t)) : 0;
+    const int64_t cum = at + warp_scan(u * w.cut.nv, lane);
+    const unsigned behind = __ballot_sync(0xffffffffu, cum > r.from);
+    if (behind == 0) {
+      at = __shfl_sync(0xffffffffu, cum, 31);
+      continue;
+    }
+    const int k = __ffs(behind) - 1;
+    const int64_t unit = __shfl_sync(0xffffffffu, u, k), begin = __shfl_sync(0xffffffffu, cum, k) - unit * w.cut.nv;
+    r.tile = static_cast<int>(t0) + k;
+    r.vh = static_cast<int>((r.from - begin) / unit);
+    r.pos = begin + r.vh * unit;
+    break;
+  }
+  return r;
 }
 
 // The items of a CTA's stretch, one after another.
@@ -176,12 +181,10 @@ struct Walk {
     k1 = end >= to ? static_cast<int>(max(static_cast<int64_t>(0), (to - pos + weight - 1) / weight)) : n;
   }
   // false: nothing to do
-  __device__ __forceinline__ bool begin(const Work& w, const Space& sp, int p) { return begin(w, *sp.head, sp.start[p], p); }
-  __device__ __forceinline__ bool begin(const Work& w, const Head& h, const Start& st, int p) {
-    if (st.b < 0) return false;
-    stretch = h.stretch;
-    from = stretch * p, to = min(from + stretch, h.total);
-    pos = st.pos, b = st.b, tile = st.tile, vh = st.vh;
+  __device__ __forceinline__ bool begin(const Work& w, const Plan& r) {
+    if (r.b < 0) return false;
+    stretch = r.stretch, from = r.from, to = r.to;
+    pos = r.pos, b = r.b, tile = r.tile, vh = r.vh;
     s = seq_at(w.seqs, b);
     set_tile(w);
     set_range();

@@ -70,8 +70,8 @@ struct HeadArgs {
   const float* freq;            // null: nothing turns
   const int* axis;
   int d, axes, heads;           // heads: of all tensors together
-  int per_thread;               // heads per thread (set by the launcher)
   float eps;
+  int per[4], first[5];         // heads per thread and first block row of each tensor (set by the launcher)
   Seqs seqs;                    // of an append (else unused)
 };
 cudaError_t head_norm(const HeadArgs& a, int dtype, bool half, bool append, cudaStream_t st);
@@ -95,8 +95,8 @@ struct HeadGradArgs {
   int d, axes, count;
   float eps;
   float* ws;
-  // set by the launcher: heads per block row, the first block row of each tensor, block columns
-  int per, first[5], cols;
+  // set by the launcher: heads per block row and the first block row of each tensor, block columns
+  int per[4], first[5], cols;
 };
 size_t head_norm_bwd_bytes(int64_t B, int64_t N, int64_t d, int dtype, const int64_t* heads, int count);
 cudaError_t head_norm_bwd(const HeadGradArgs& a, int dtype, bool half, cudaStream_t st);

@@ -1,5 +1,5 @@
-// The planning launch of the attention over a paged cache (one block), and the launch that joins the
-// parts of items that several CTAs shared.
+// The launch that joins the parts of items that several CTAs shared, and the choice of a kernel for the
+// attention over a paged cache.
 #include <cuda_bf16.h>
 
 #include "paged.cuh"
@@ -8,77 +8,6 @@
 namespace fbd {
 namespace paged {
 namespace {
-
-constexpr int kT = 1024;
-
-constexpr int kNear = 2048;  // sequences whose ends are kept in shared memory
-
-__global__ void __launch_bounds__(kT) plan_kernel(const Work w, const Space sp) {
-  __shared__ int64_t carry, part[kT / 32], near[kNear];
-  ptx::grid_dependency_launch();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, B = w.seqs.B, step = w.cut.step;
-  int64_t* ends = B <= kNear ? near : sp.ends;
-  if (threadIdx.x == 0) carry = 0;
-  for (int b0 = 0; b0 < B; b0 += kT) {
-    const int b = b0 + threadIdx.x;
-    // A sequence's tiles: its thread's, the warp's together where they are many.
-    int64_t v = 0;
-    Seq s{};
-    if (b < B) s = seq_at(w.seqs, b);
-    for (int t = 0; t < 4 && static_cast<int64_t>(t) * step < s.n; ++t) v += tile_units(w, s, t);
-    for (unsigned many = __ballot_sync(0xffffffffu, s.n > 4ll * step); many != 0; many &= many - 1) {
-      const int from = __ffs(many) - 1;
-      const Seq q = seq_at(w.seqs, b0 + warp * 32 + from);
-      int64_t u = 0;
-      for (int64_t t = 4 + lane; t * step < q.n; t += 32) u += tile_units(w, q, static_cast<int>(t));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-      if (lane == from) v += u;
-    }
-    v = warp_scan(v * w.cut.nv, lane);
-    __syncthreads();  // `part` and `carry` of the round before
-    if (lane == 31) part[warp] = v;
-    __syncthreads();
-    if (warp == 0) part[lane] = warp_scan(part[lane], lane);
-    __syncthreads();
-    v += carry + (warp > 0 ? part[warp - 1] : 0);
-    if (b < B) ends[b] = v;
-    __syncthreads();
-    if (threadIdx.x == kT - 1) carry = v;
-  }
-  __syncthreads();
-  const int64_t total = carry;
-  const int64_t even = (total + w.cut.ctas - 1) / w.cut.ctas, stretch = even > w.cut.least ? even : w.cut.least;
-  if (threadIdx.x == 0) *sp.head = Head{total, stretch};
-  for (int p = warp; p < w.cut.ctas; p += kT / 32) {
-    const int64_t x = stretch * p;
-    if (lane == 0) sp.tail[p] = Tail{0, 0, 0, 0};
-    if (x >= total) {
-      if (lane == 0) sp.start[p] = Start{0, -1, 0, 0, 0};
-      continue;
-    }
-    int hi = B - 1;  // the first sequence that ends behind x
-    for (int lo = -1; hi - lo > 1;) {
-      const int mid = (lo + hi) >> 1;
-      if (ends[mid] > x) hi = mid; else lo = mid;
-    }
-    const Seq s = seq_at(w.seqs, hi);
-    int64_t at = hi > 0 ? ends[hi - 1] : 0;
-    for (int64_t t0 = 0; t0 * step < s.n; t0 += 32) {  // ... and its tile that does
-      const int64_t t = t0 + lane;
-      const int64_t u = t * step < s.n ? tile_units(w, s, static_cast<int>(t)) : 0, cum = at + warp_scan(u * w.cut.nv, lane);
-      const unsigned behind = __ballot_sync(0xffffffffu, cum > x);
-      if (behind != 0) {
-        if (lane == __ffs(behind) - 1) {
-          const int64_t b = cum - u * w.cut.nv, vh = (x - b) / u;
-          sp.start[p] = Start{b + vh * u, hi, static_cast<int>(t), static_cast<int>(vh), 0};
-        }
-        break;
-      }
-      at = __shfl_sync(0xffffffffu, cum, 31);
-    }
-  }
-}
 
 __device__ __forceinline__ void put(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float4 v) {
@@ -188,11 +117,6 @@ __global__ void __launch_bounds__(kJ) join_kernel(const Work w, const Space sp, 
 }
 
 }  // namespace
-
-cudaError_t plan(const Work& w, const Space& sp, cudaStream_t st) {
-  plan_kernel<<<1, kT, 0, st>>>(w, sp);
-  return cudaGetLastError();
-}
 
 cudaError_t join(const Work& w, const Space& sp, const Out& out, int dtype, int d, int tile_rows, int64_t few, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};

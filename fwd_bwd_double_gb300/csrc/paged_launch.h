@@ -1,11 +1,10 @@
-// Launches of the attention over a paged cache: the plan and the join around each of its kernels.
+// Launches of the attention over a paged cache: its kernels, and the join behind each.
 #pragma once
 #include "paged.cuh"
 
 namespace fbd {
 namespace paged {
 
-cudaError_t plan(const Work& w, const Space& sp, cudaStream_t st);
 // tile_rows: rows of a slot that a tile takes; few: the most new tokens of a sequence, as far as is known.
 cudaError_t join(const Work& w, const Space& sp, const Out& out, int dtype, int d, int tile_rows, int64_t few, cudaStream_t st);
 

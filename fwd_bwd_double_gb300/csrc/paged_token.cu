@@ -5,7 +5,7 @@
 // of four forms the scores of 16 keys, the four agree on the rows' maxima, each writes its
 // weights (bf16) to shared memory, and each multiplies all 64 with its quarter of V's columns: no sums are joined
 // at the end, where a batch of short contexts would spend its time.
-// CTAs take the stretches of paged.cuh; the loading warp plans its own (a launch less).
+// CTAs take the stretches of paged.cuh.
 #include <cuda_bf16.h>
 
 #include "handover.h"
@@ -93,11 +93,8 @@ __global__ void __launch_bounds__(kThreads, Lay<D>::per_sm)
 
   if (warp == 4) {
     // ------------------------------------------------------------ plan and loads
-    Head head;
-    Start start;
-    plan_here(w, p, head, start);
     Walk it;
-    bool more = it.begin(w, head, start, p) && *abort_flag == 0, go = true;
+    bool more = it.begin(w, plan(w, p)) && *abort_flag == 0, go = true;
     int E = 0, n = 0;
     const int per = MK / pg.box;
     const int c0 = pg.whole ? 0 : lane % SL, g0 = pg.whole ? lane : lane / SL;  // this lane's box
@@ -362,11 +359,11 @@ Work work_of(const PagedArgs& a) {
 
 }  // namespace
 
-size_t token_bytes(const PagedArgs& a) { return Space::bytes(work_of(a).cut.ctas, a.seqs.B, kRows, columns(a)); }
+size_t token_bytes(const PagedArgs& a) { return Space::bytes(work_of(a).cut.ctas, kRows, columns(a)); }
 
 cudaError_t token_paged(const PagedArgs& a, void* ws, cudaStream_t st) {
   const Work w = work_of(a);
-  const Space sp = Space::at(ws, w.cut.ctas, a.seqs.B, kRows, columns(a));
+  const Space sp = Space::at(ws, w.cut.ctas, kRows, columns(a));
   const Out out{a.O, a.lse, {a.os[0], a.os[1], a.os[2]}, {a.ls[0], a.ls[1]}};
   // d = 32 and 96: the columns past d are zeros (TMA fills them).
   return a.d <= 64 ? launch<64>(a, w, sp, out, st) : a.d <= 128 ? launch<128>(a, w, sp, out, st) : launch<256>(a, w, sp, out, st);

@@ -17,9 +17,16 @@ constexpr int kT = 256, BN = 64;
 template <int D, int R>
 struct Lay {
   static constexpr int PK = D + 4, PP = BN + 4;
-  static constexpr int oQ = 0, oK = oQ + R * D, oV = oK + BN * PK, oP = oV + BN * D, oRow = oP + R * PP;
-  static constexpr int bytes = 4 * oRow + BN * 8 * 2;
+  static constexpr int kStage = BN * (PK + D);      // K and V of a block
+  static constexpr int NB = D <= 128 ? 2 : 1;       // blocks: the next one's copies run behind this one's sums
+  static constexpr int oQ = 0, oStage = oQ + R * D, oP = oStage + NB * kStage;
+  static constexpr int bytes = 4 * (oP + R * PP);
 };
+
+// 16 bytes global -> shared, or 16 bytes of zeros (nothing is read) where !in.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ void put2(float* p, float x, float y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); }
@@ -32,13 +39,18 @@ __global__ void __launch_bounds__(kT)
   using L = Lay<D, R>;
   constexpr int RT = R / 16, C2 = D / 32;  // rows, pairs of columns of a thread
   extern __shared__ __align__(16) float sh[];
-  float *sQ = sh + L::oQ, *sK = sh + L::oK, *sV = sh + L::oV, *sP = sh + L::oP;
-  int64_t* sRow = reinterpret_cast<int64_t*>(sh + L::oRow);  // [2][BN]: offsets of the block's keys, values (-1: none)
+  float *sQ = sh + L::oQ, *sP = sh + L::oP;
+  __shared__ Plan planned;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, p = blockIdx.x, gt = w.cut.gt;
-  ptx::grid_dependency_wait();
   ptx::grid_dependency_launch();
+  if (threadIdx.x < 32) {
+    const Plan r = plan(w, p);
+    if (threadIdx.x == 0) planned = r;
+  }
+  __syncthreads();
+  Tail tail{0, 0, 0, 0};
   Walk it;
-  for (bool more = it.begin(w, sp, p); more; more = it.next(w)) {
+  for (bool more = it.begin(w, planned); more; more = it.next(w)) {
     const Seq& s = it.s;
     const int rows = (it.t1 - it.t0) * gt, kvh = it.vh / w.cut.per_kv;
     const int64_t h0 = static_cast<int64_t>(it.vh) * gt;
@@ -63,33 +75,54 @@ __global__ void __launch_bounds__(kT)
       for (int x = 0; x < C2; ++x) acc[i][x][0] = acc[i][x][1] = 0.f;
     }
     const int64_t at0 = static_cast<int64_t>(s.start) + it.t0, at1 = static_cast<int64_t>(s.start) + it.t1 - 1;
-    for (int k = it.k0; k < it.k1; ++k) {
+    // Block k's copies into its buffer; the 16-key runs of it without a page or behind the last key.
+    auto load = [&](int k) {
       const int64_t key0 = static_cast<int64_t>(it.j0 + k) * BN;
-      __syncthreads();  // the block before has been read
-      if (threadIdx.x < BN) {
-        const int64_t j = key0 + threadIdx.x;
-        int page = -1;
-        int e = 0;
-        if (j < s.len) {
-          e = static_cast<int>(j) / w.seqs.page;
-          page = page_at(w.seqs, it.b, e);
-        }
-        const int64_t slot = j - static_cast<int64_t>(e) * w.seqs.page;
-        sRow[threadIdx.x] = page < 0 ? -1 : page * ks0 + kvh * ks1 + slot * ks2;
-        sRow[BN + threadIdx.x] = page < 0 ? -1 : page * vs0 + kvh * vs1 + slot * vs2;
+      const uint32_t dst = ptx::smem_u32(sh + L::oStage + (L::NB == 2 ? k & 1 : 0) * L::kStage);
+      unsigned gone = 0;
+      int page[BN / 16], slot[BN / 16];
+#pragma unroll
+      for (int g = 0; g < BN / 16; ++g) {
+        const int64_t j = key0 + g * 16;
+        const int e = static_cast<int>(j) / w.seqs.page;
+        page[g] = j < s.len ? page_at(w.seqs, it.b, e) : -1, slot[g] = static_cast<int>(j) - e * w.seqs.page;
+        if (page[g] < 0) gone |= 1u << g;
+      }
+      constexpr int C = D / 4, kStep = kT / C;  // 16-byte pieces of a key; keys a step
+#pragma unroll
+      for (int r0 = 0; r0 < BN; r0 += kStep) {
+        const int r = r0 + threadIdx.x / C, cc = threadIdx.x % C * 4;
+        if (kT % C != 0 && (threadIdx.x / C >= kStep || r >= BN)) continue;
+        int pg = page[0], sl = slot[0];
+#pragma unroll
+        for (int g = 1; g < BN / 16; ++g)
+          if (r >> 4 == g) pg = page[g], sl = slot[g];
+        // keys that the sequence does not hold are not read: zeros there (a cache row not yet written may hold anything)
+        const bool in = pg >= 0 && key0 + r < s.len;
+        const int64_t at = in ? sl + (r & 15) : 0;
+        copy16(dst + (r * L::PK + cc) * 4, in ? K + pg * ks0 + kvh * ks1 + at * ks2 + cc : K, in);
+        copy16(dst + (BN * L::PK + r * D + cc) * 4, in ? V + pg * vs0 + kvh * vs1 + at * vs2 + cc : V, in);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      return gone;
+    };
+    unsigned gone = load(it.k0), then = 0;
+    for (int k = it.k0; k < it.k1; ++k, gone = then) {
+      const int64_t key0 = static_cast<int64_t>(it.j0 + k) * BN;
+      const float *sK = sh + L::oStage + (L::NB == 2 ? k & 1 : 0) * L::kStage, *sV = sK + BN * L::PK;
+      if (L::NB == 1 && k > it.k0) {
+        __syncthreads();  // the block before has been read
+        gone = load(k);
+      }
+      if (L::NB == 2 && k + 1 < it.k1) {
+        then = load(k + 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      } else {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
       }
       __syncthreads();
-      bool gap = false;
-      for (int u = threadIdx.x; u < BN * D / 4; u += kT) {
-        const int r = u / (D / 4), cc = u % (D / 4) * 4;
-        const int64_t ko = sRow[r], vo = sRow[BN + r];
-        gap = gap || ko < 0;
-        const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-        *reinterpret_cast<float4*>(sK + r * L::PK + cc) = ko < 0 ? z : load4(K + ko + cc);
-        *reinterpret_cast<float4*>(sV + r * D + cc) = vo < 0 ? z : load4(V + vo + cc);
-      }
       // some row does not see some key of the block
-      const bool part = __syncthreads_or(gap) || (w.causal && key0 + BN - 1 > at0) || (w.window > 0 && key0 <= at1 - w.window);
+      const bool part = gone != 0 || key0 + BN > s.len || (w.causal && key0 + BN - 1 > at0) || (w.window > 0 && key0 <= at1 - w.window);
       float sc[RT][4];
 #pragma unroll
       for (int i = 0; i < RT; ++i)
@@ -115,7 +148,7 @@ __global__ void __launch_bounds__(kT)
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const int64_t j = key0 + tx + 16 * x;
-            if (j < first[i] || j > last[i] || sRow[tx + 16 * x] < 0) sc[i][x] = -INFINITY;
+            if (j < first[i] || j > last[i] || (gone >> x & 1)) sc[i][x] = -INFINITY;  // (key tx + 16 x: run x)
           }
         }
         float t = fmaxf(fmaxf(sc[i][0], sc[i][1]), fmaxf(sc[i][2], sc[i][3]));
@@ -166,6 +199,7 @@ __global__ void __launch_bounds__(kT)
 #pragma unroll
         for (int x = 0; x < C2; ++x)
           acc[i][x][0] = fmaf(acc[i][x][0], alpha[i], o[i][x][0]), acc[i][x][1] = fmaf(acc[i][x][1], alpha[i], o[i][x][1]);
+      if (L::NB == 2) __syncthreads();  // (this block's buffer is the next but one's)
     }
     const bool whole = it.whole();
     const int slot = it.slot(p);
@@ -189,8 +223,9 @@ __global__ void __launch_bounds__(kT)
         out.lse[s.batch * out.ls[0] + h * out.ls[1] + pos] =
             l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.69314718055994531f;
     }
-    if (threadIdx.x == 0 && !whole && it.k0 == 0) sp.tail[p] = Tail{it.b, it.tile, it.vh, it.parts(p)};
+    if (!whole && it.k0 == 0) tail = Tail{it.b, it.tile, it.vh, it.parts(p)};
   }
+  if (threadIdx.x == 0) sp.tail[p] = tail;
 }
 
 template <int D, int R>
@@ -198,11 +233,10 @@ cudaError_t launch(const PagedArgs& a, const Work& w, const Space& sp, const Out
   auto kern = paged_kernel<D, R>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D, R>::bytes);
   if (e != cudaSuccess) return e;
-  if ((e = plan(w, sp, st)) != cudaSuccess) return e;
-  e = launch_behind(kern, w.cut.ctas, kT, Lay<D, R>::bytes, st, w, sp, out, static_cast<const float*>(a.Q), static_cast<const float*>(a.K),
+  kern<<<static_cast<unsigned>(w.cut.ctas), kT, Lay<D, R>::bytes, st>>>(w, sp, out, static_cast<const float*>(a.Q), static_cast<const float*>(a.K),
                     static_cast<const float*>(a.V), a.qs[0], a.qs[1], a.qs[2], a.ks[0], a.ks[1], a.ks[2], a.vs[0], a.vs[1],
                     a.vs[2], a.scale * kLog2e);
-  if (e != cudaSuccess) return e;
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return join(w, sp, out, a.dtype, D, R, a.max_new, st);
 }
 
@@ -222,8 +256,7 @@ Work work_of(const PagedArgs& a) {
   w.cut.nv = a.H / w.cut.gt, w.cut.per_kv = g / w.cut.gt;
   w.cut.tile = w.cut.step = R / w.cut.gt;
   w.cut.shift = 6, w.cut.over = 1, w.cut.least = 4;
-  const int smem = R == 16 ? 4 * (BN * 2 * a.d) : 4 * (BN * 2 * a.d + 64 * a.d);
-  w.cut.ctas = 152 * (smem <= 50000 ? 3 : smem <= 100000 ? 2 : 1);
+  w.cut.ctas = 152 * (a.d <= 32 ? 3 : a.d <= 64 ? 2 : 1);  // CTAs that fit an SM
   return w;
 }
 
@@ -231,12 +264,12 @@ Work work_of(const PagedArgs& a) {
 
 size_t simt_bytes(const PagedArgs& a) {
   const Work w = work_of(a);
-  return Space::bytes(w.cut.ctas, a.seqs.B, tile_rows(a), a.d);
+  return Space::bytes(w.cut.ctas, tile_rows(a), a.d);
 }
 
 cudaError_t simt_paged(const PagedArgs& a, void* ws, cudaStream_t st) {
   const Work w = work_of(a);
-  const Space sp = Space::at(ws, w.cut.ctas, a.seqs.B, tile_rows(a), a.d);
+  const Space sp = Space::at(ws, w.cut.ctas, tile_rows(a), a.d);
   const Out out{a.O, a.lse, {a.os[0], a.os[1], a.os[2]}, {a.ls[0], a.ls[1]}};
   return a.d == 32 ? rows<32>(a, w, sp, out, st) : a.d == 64 ? rows<64>(a, w, sp, out, st) : a.d == 96 ? rows<96>(a, w, sp, out, st)
          : a.d == 128 ? rows<128>(a, w, sp, out, st) : rows<256>(a, w, sp, out, st);

@@ -89,6 +89,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, p = blockIdx.x;
   const int gt = w.cut.gt, tq = w.cut.tile;
+  ptx::grid_dependency_launch();
   if (threadIdx.x == 8 * 32) {
     ptx::prefetch_tmap(&tmQ);
     ptx::prefetch_tmap(&tmK);
@@ -126,8 +127,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const ptx::BoundedWait wait{abort_flag, &g_err};
   const bool ok = *abort_flag == 0;
-  ptx::grid_dependency_wait();  // the plan
-  ptx::grid_dependency_launch();
   // Item n, once it is known (ring of 8: the loading warp is three items ahead at most, since it waits for the
   // products with Q of the one before, and those for the softmax of the one before that).
   auto item = [&](int n) -> const Item* {
@@ -142,7 +141,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 8) {
     // ------------------------------------------------------------ TMA producer
     Walk it;
-    bool more = it.begin(w, sp, p) && ok, go = true;
+    Tail tail{0, 0, 0, 0};
+    bool more = it.begin(w, plan(w, p)) && ok, go = true;
     int E = 0, n = 0, nq = 0, T0 = 0, T1 = 0;
     const int per = BN / pg.box;                                                // boxes of an entry along its keys
     const int c0 = pg.whole ? 0 : lane % SL, g0 = pg.whole ? lane : lane / SL;  // this lane's box
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         x.slot = it.whole() ? -1 : it.slot(p);
         x.b = it.b, x.batch = it.s.batch, x.row0 = it.s.row0, x.vh = it.vh, x.kvh = kvh;
         ptx::mbar_arrive(&known[n & 7]);
-        if (!it.whole() && it.k0 == 0) sp.tail[p] = Tail{it.b, it.tile, it.vh, it.parts(p)};
+        if (!it.whole() && it.k0 == 0) tail = Tail{it.b, it.tile, it.vh, it.parts(p)};
         ptx::mbar_expect_tx(q_full, tiles * SL * gt * tq * 128);
         for (int m = 0; m < tiles; ++m)
           for (int u = 0; u < SL; ++u)
@@ -214,6 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         items[n & 7].n = 0;
         ptx::mbar_arrive(&known[n & 7]);
       }
+      sp.tail[p] = tail;
       started[0] = nq, started[1] = E;
     }
   } else if (warp == 9 || warp == 10) {
@@ -536,10 +537,9 @@ cudaError_t launch(const PagedArgs& a, const Work& w, const Space& sp, const Out
   auto kern = paged_kernel<D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::bytes);
   if (e != cudaSuccess) return e;
-  if ((e = plan(w, sp, st)) != cudaSuccess) return e;
-  e = launch_behind(kern, w.cut.ctas, kThreads, Lay<D>::bytes, st, mq, mk, mv, w, sp, out,
+  kern<<<static_cast<unsigned>(w.cut.ctas), kThreads, Lay<D>::bytes, st>>>(mq, mk, mv, w, sp, out,
                     static_cast<const __nv_bfloat16*>(a.V), a.vs[0], a.vs[1], a.vs[2], a.d, pg, a.scale, a.scale * kLog2e);
-  if (e != cudaSuccess) return e;
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return join(w, sp, out, a.dtype, a.d, BM, a.max_new, st);
 }
 
@@ -556,11 +556,11 @@ Work work_of(const PagedArgs& a) {
 
 }  // namespace
 
-size_t tc_bytes(const PagedArgs& a) { return Space::bytes(152, a.seqs.B, 2 * BM, a.d <= 64 ? 64 : 128); }
+size_t tc_bytes(const PagedArgs& a) { return Space::bytes(152, 2 * BM, a.d <= 64 ? 64 : 128); }
 
 cudaError_t tc_paged(const PagedArgs& a, void* ws, cudaStream_t st) {
   const Work w = work_of(a);
-  const Space sp = Space::at(ws, w.cut.ctas, a.seqs.B, 2 * BM, a.d <= 64 ? 64 : 128);
+  const Space sp = Space::at(ws, w.cut.ctas, 2 * BM, a.d <= 64 ? 64 : 128);
   const Out out{a.O, a.lse, {a.os[0], a.os[1], a.os[2]}, {a.ls[0], a.ls[1]}};
   // d = 32 runs the kernel of 64 columns and d = 96 that of 128: TMA fills the columns past d with zeros.
   return a.d <= 64 ? launch<64>(a, w, sp, out, st) : launch<128>(a, w, sp, out, st);

@@ -54,6 +54,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, p = blockIdx.x;
   const int gt = w.cut.gt, tq = w.cut.tile;
+  ptx::grid_dependency_launch();
   if (threadIdx.x == 4 * 32) {
     ptx::prefetch_tmap(&tmQ);
     ptx::prefetch_tmap(&tmK);
@@ -90,8 +91,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const ptx::BoundedWait wait{abort_flag, &g_err};
   const bool ok = *abort_flag == 0;
-  ptx::grid_dependency_wait();  // the plan
-  ptx::grid_dependency_launch();
   // Item n, once it is known (tc_paged.cu).
   auto item = [&](int n) -> const Item* {
     wait(&known[n & 7], (n >> 3) & 1);
@@ -116,7 +115,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 4) {
     // ------------------------------------------------------------ TMA producer
     Walk it;
-    bool more = it.begin(w, sp, p) && ok, go = true;
+    Tail tail{0, 0, 0, 0};
+    bool more = it.begin(w, plan(w, p)) && ok, go = true;
     int E = 0, n = 0, nq = 0, T = 0;
     const int per = HN / pg.box;                                                // boxes of an entry along its keys
     const int c0 = pg.whole ? 0 : lane % SL, g0 = pg.whole ? lane : lane / SL;  // this lane's box
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         x.slot = it.whole() ? -1 : it.slot(p);
         x.b = it.b, x.batch = it.s.batch, x.row0 = it.s.row0, x.vh = it.vh, x.kvh = kvh;
         ptx::mbar_arrive(&known[n & 7]);
-        if (!it.whole() && it.k0 == 0) sp.tail[p] = Tail{it.b, it.tile, it.vh, it.parts(p)};
+        if (!it.whole() && it.k0 == 0) tail = Tail{it.b, it.tile, it.vh, it.parts(p)};
         ptx::mbar_expect_tx(q_full, SL * gt * tq * 128);
         for (int u = 0; u < SL; ++u)
           ptx::tma_load_5d(sm + u * BM * 128, &tmQ, q_full, u * 64, 0, it.s.row0 + it.t0, it.vh, it.s.batch);
@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         items[n & 7].n = 0;
         ptx::mbar_arrive(&known[n & 7]);
       }
+      sp.tail[p] = tail;
       started[0] = nq, started[1] = E;
     }
   } else if (warp == 5) {
@@ -457,21 +458,20 @@ Work work_of(const PagedArgs& a) {
 
 }  // namespace
 
-size_t tc_wide_bytes(const PagedArgs& a) { return Space::bytes(152, a.seqs.B, BM, D); }
+size_t tc_wide_bytes(const PagedArgs& a) { return Space::bytes(152, BM, D); }
 
 cudaError_t tc_paged_wide(const PagedArgs& a, void* ws, cudaStream_t st) {
   const Work w = work_of(a);
-  const Space sp = Space::at(ws, w.cut.ctas, a.seqs.B, BM, D);
+  const Space sp = Space::at(ws, w.cut.ctas, BM, D);
   const Out out{a.O, a.lse, {a.os[0], a.os[1], a.os[2]}, {a.ls[0], a.ls[1]}};
   alignas(64) CUtensorMap mq, mk, mv;
   Pages pg;
   if (!make_maps(a, w.cut, HN, SL, &mq, &mk, &mv, pg, BN)) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
   if (e != cudaSuccess) return e;
-  if ((e = plan(w, sp, st)) != cudaSuccess) return e;
-  e = launch_behind(wide_kernel, w.cut.ctas, kThreads, kBytes, st, mq, mk, mv, w, sp, out, static_cast<const __nv_bfloat16*>(a.V),
+  wide_kernel<<<static_cast<unsigned>(w.cut.ctas), kThreads, kBytes, st>>>(mq, mk, mv, w, sp, out, static_cast<const __nv_bfloat16*>(a.V),
                     a.vs[0], a.vs[1], a.vs[2], pg, a.scale, a.scale * kLog2e);
-  if (e != cudaSuccess) return e;
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return join(w, sp, out, a.dtype, D, BM, a.max_new, st);
 }
 
