@@ -17,7 +17,7 @@ namespace fbd {
 namespace paged {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kMaxCtas = 456;
+constexpr int kMaxCtas = 304;
 
 struct Cut {
   int gt;      // query heads handled together (divides the heads of a key/value head)

@@ -16,12 +16,20 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, float4 v) {
 
 constexpr int kJ = 256;
 
+// A row of an item: its token and head, and its place in a slot.
+struct Row {
+  int t, head, at;
+  __device__ __forceinline__ Row(const Cut& c, int row, int tile_rows) {
+    t = c.gt == 1 ? row : row / c.gt, head = row - t * c.gt;
+    const int tl = t < c.tile ? 0 : t / c.tile;
+    at = tl * tile_rows + (t - tl * c.tile) * c.gt + head;
+  }
+};
 template <typename T>
-__device__ __forceinline__ void put_row(const Work& w, const Out& out, const Seq& s, const Tail& q, int row, int t0, int col, int d,
-                                        float4 o, float m, float l) {
-  const int t = row / w.cut.gt, hh = row - t * w.cut.gt;
+__device__ __forceinline__ void put_row(const Work& w, const Out& out, const Seq& s, const Tail& q, const Row& row, int t0, int col,
+                                        int d, float4 o, float m, float l) {
   const float inv = l == 0.f ? 0.f : 1.f / l;  // (a row that sees no key: 0)
-  const int64_t h = static_cast<int64_t>(q.vh) * w.cut.gt + hh, pos = s.row0 + t0 + t;
+  const int64_t h = static_cast<int64_t>(q.vh) * w.cut.gt + row.head, pos = s.row0 + t0 + row.t;
   if (col < d)
     put(static_cast<T*>(out.O) + s.batch * out.os[0] + h * out.os[1] + pos * out.os[2] + col,
         make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
@@ -29,9 +37,11 @@ __device__ __forceinline__ void put_row(const Work& w, const Out& out, const Seq
     out.lse[s.batch * out.ls[0] + h * out.ls[1] + pos] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
+constexpr int kFewRows = 16;  // items of at most as many rows may have many parts
+
 // Block (p, y): every gridDim.y-th run of rows of the item that begins in CTA p's stretch and goes on behind it.  A
-// row's columns are d / 4 threads' (rounded up to a power of two).  Few parts: such groups take a row each;
-// many: a row at a time, its parts' weights formed once and the parts shared by the groups.
+// row's columns are d / 4 threads' (rounded up to a power of two); such groups take a row each, or, of an
+// item of few rows and many parts, the parts of one row after another, whose weights are formed once.
 template <typename T>
 __global__ void __launch_bounds__(kJ) join_kernel(const Work w, const Space sp, const Out out, int d, int tile_rows) {
   __shared__ float weight[kMaxCtas];
@@ -41,52 +51,43 @@ __global__ void __launch_bounds__(kJ) join_kernel(const Work w, const Space sp, 
   const Tail q = sp.tail[blockIdx.x];
   if (q.parts == 0) return;
   const Seq s = seq_at(w.seqs, q.b);
-  const int t0 = q.tile * w.cut.step, t1 = min(s.n, t0 + w.cut.step), gt = w.cut.gt;
-  const int rows = (t1 - t0) * gt, p = blockIdx.x, parts = q.parts;
+  const int t0 = q.tile * w.cut.step, t1 = min(s.n, t0 + w.cut.step);
+  const int rows = (t1 - t0) * w.cut.gt, p = blockIdx.x, parts = q.parts;
   int C = 8;
   while (C * 4 < d) C *= 2;
   const int groups = kJ / C, g = threadIdx.x / C, col = (threadIdx.x & (C - 1)) * 4;
-  auto in_slot = [&](int row) {
-    const int t = row / gt, tl = t / w.cut.tile;
-    return tl * tile_rows + (t - tl * w.cut.tile) * gt + row - t * gt;
-  };
   auto slot_of = [&](int k) { return k == 0 ? 2 * p + 1 : 2 * (p + k); };
-  if (parts <= 4) {
-    for (int row = blockIdx.y * groups + g; row < rows; row += gridDim.y * groups) {
-      const int at = in_slot(row);
-      float2 x[4];
-      float4 v[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        x[k] = make_float2(-INFINITY, 0.f), v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k >= parts) continue;
-        x[k] = *sp.ml(slot_of(k), at);
-        if (col < d) v[k] = *reinterpret_cast<const float4*>(sp.o(slot_of(k), at) + col);
-      }
-      const float m = fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x)), sub = m == -INFINITY ? 0.f : m;
-      float l = 0.f;
+  if (parts <= 4 || rows > kFewRows) {
+    for (int r = blockIdx.y * groups + g; r < rows; r += gridDim.y * groups) {
+      const Row row(w.cut, r, tile_rows);
+      float m = -INFINITY, l = 0.f;
+      for (int k = 0; k < parts; ++k) m = fmaxf(m, sp.ml(slot_of(k), row.at)->x);
+      const float sub = m == -INFINITY ? 0.f : m;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float f = ptx::ex2(x[k].x - sub);
-        l = fmaf(f, x[k].y, l);
-        o.x = fmaf(f, v[k].x, o.x), o.y = fmaf(f, v[k].y, o.y), o.z = fmaf(f, v[k].z, o.z), o.w = fmaf(f, v[k].w, o.w);
+#pragma unroll 2
+      for (int k = 0; k < parts; ++k) {
+        const float2 x = *sp.ml(slot_of(k), row.at);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (col < d) v = *reinterpret_cast<const float4*>(sp.o(slot_of(k), row.at) + col);
+        const float f = ptx::ex2(x.x - sub);
+        l = fmaf(f, x.y, l);
+        o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y), o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
       }
       put_row<T>(w, out, s, q, row, t0, col, d, o, m, l);
     }
     return;
   }
-  for (int row = blockIdx.y; row < rows; row += gridDim.y) {
-    const int at = in_slot(row);
+  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    const Row row(w.cut, r, tile_rows);
     __syncthreads();  // the row before has been read
     if (threadIdx.x < 32) {
       float m = -INFINITY, l = 0.f;
-      for (int k = threadIdx.x; k < parts; k += 32) m = fmaxf(m, sp.ml(slot_of(k), at)->x);
+      for (int k = threadIdx.x; k < parts; k += 32) m = fmaxf(m, sp.ml(slot_of(k), row.at)->x);
 #pragma unroll
       for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
       const float sub = m == -INFINITY ? 0.f : m;
       for (int k = threadIdx.x; k < parts; k += 32) {
-        const float2 x = *sp.ml(slot_of(k), at);
+        const float2 x = *sp.ml(slot_of(k), row.at);
         const float f = ptx::ex2(x.x - sub);
         weight[k] = f, l = fmaf(f, x.y, l);
       }
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(kJ) join_kernel(const Work w, const Space sp, 
     if (col < d) {
 #pragma unroll 8
       for (int k = g; k < parts; k += groups) {
-        const float4 v = *reinterpret_cast<const float4*>(sp.o(slot_of(k), at) + col);
+        const float4 v = *reinterpret_cast<const float4*>(sp.o(slot_of(k), row.at) + col);
         const float f = weight[k];
         o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y), o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
       }
@@ -120,9 +121,10 @@ __global__ void __launch_bounds__(kJ) join_kernel(const Work w, const Space sp, 
 
 cudaError_t join(const Work& w, const Space& sp, const Out& out, int dtype, int d, int tile_rows, int64_t few, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
-  // Blocks for up to eight rows of an item (a row each where the parts are many, eight or four rows each where few).
+  // A row a block where items have few (their parts may be many), else as many as a block's groups take at once.
   const int64_t rows = (few < w.cut.step ? few : w.cut.step) * w.cut.gt;
-  cfg.gridDim = dim3(static_cast<unsigned>(w.cut.ctas), static_cast<unsigned>(rows <= 8 ? rows : rows <= 32 ? 8 : 32));
+  const int groups = d <= 32 ? kJ / 8 : d <= 64 ? kJ / 16 : d <= 128 ? kJ / 32 : kJ / 64;
+  cfg.gridDim = dim3(static_cast<unsigned>(w.cut.ctas), static_cast<unsigned>(rows <= kFewRows ? rows : (rows + groups - 1) / groups));
   cfg.blockDim = dim3(kJ);
   cfg.stream = st;
   cudaLaunchAttribute attr{};

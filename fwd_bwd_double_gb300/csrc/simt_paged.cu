@@ -32,7 +32,7 @@ __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_ca
 __device__ __forceinline__ void put2(float* p, float x, float y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); }
 
 template <int D, int R>
-__global__ void __launch_bounds__(kT)
+__global__ void __launch_bounds__(kT, (D <= 64 ? 2 : 1))
     paged_kernel(const Work w, const Space sp, const Out out, const float* __restrict__ Q, const float* __restrict__ K,
                  const float* __restrict__ V, int64_t qs0, int64_t qs1, int64_t qs2, int64_t ks0, int64_t ks1, int64_t ks2,
                  int64_t vs0, int64_t vs1, int64_t vs2, float c) {
@@ -256,7 +256,7 @@ Work work_of(const PagedArgs& a) {
   w.cut.nv = a.H / w.cut.gt, w.cut.per_kv = g / w.cut.gt;
   w.cut.tile = w.cut.step = R / w.cut.gt;
   w.cut.shift = 6, w.cut.over = 1, w.cut.least = 4;
-  w.cut.ctas = 152 * (a.d <= 32 ? 3 : a.d <= 64 ? 2 : 1);  // CTAs that fit an SM
+  w.cut.ctas = 152 * (a.d <= 64 ? 2 : 1);  // CTAs that fit an SM
   return w;
 }
 
