@@ -148,8 +148,8 @@ __device__ __forceinline__ bool hide_values(uint8_t* V, int keys, int held, int 
 }
 
 // Tensor maps of Q (a tile's tokens and heads; mq may be null), K and V in entries of `keys` keys and `slabs` slabs of 64
-// columns (`rows`: keys of the operand that an entry is part of, where it is more).
-inline bool make_maps(const PagedArgs& a, const Cut& k, int keys, int slabs, void* mq, void* mk, void* mv, Pages& pg, int rows = 0) {
+// columns.
+inline bool make_maps(const PagedArgs& a, const Cut& k, int keys, int slabs, void* mq, void* mk, void* mv, Pages& pg) {
   const bool none = a.seqs.pages == 0;  // no key anywhere: a tensor that is never read
   const int64_t q_dims[5] = {a.d, k.gt, a.seqs.N, k.nv, a.seqs.cu != nullptr ? 1 : a.seqs.B};
   const int64_t q_str[4] = {a.qs[1], a.qs[2], a.qs[1] * k.gt, a.qs[0]};
@@ -177,7 +177,7 @@ inline bool make_maps(const PagedArgs& a, const Cut& k, int keys, int slabs, voi
     const int boxes[5] = {64, 8, a.d / 64, pg.box / 8, 1};
     made = make_tmap_view(mk, K, 5, dims, k_str, boxes) && make_tmap_view(mv, V, 5, dims, v_str, boxes);
   } else {
-    pg.slab = (rows > 0 ? rows : keys) * 128, pg.sbo = 1024;
+    pg.slab = keys * 128, pg.sbo = 1024;
     const int64_t dims[4] = {a.d, a.seqs.page, a.Hkv, pages};
     const int64_t k_str[3] = {a.ks[2], a.ks[1], a.ks[0]}, v_str[3] = {a.vs[2], a.vs[1], a.vs[0]};
     const int boxes[4] = {64, pg.box, 1, 1};

@@ -1,11 +1,12 @@
 // Attention of new tokens over a paged cache at d = 256, bf16, on the tensor cores (tc_paged.cu has the
-// method; d = 256 leaves TMEM room for one tile's O, 256 columns, and two S of 128).
+// method; d = 256 leaves TMEM room for one tile's O, 256 columns).
 //
-// One tile of 128 rows; S of the next block is formed while this one is exponentiated, in the other of
-// two S (P over the S it came from), so that the tensor cores wait for the softmax only where it is the
-// longer: 2048 cycles of products a block; S and P V are issued by a warp each.  K and V come in entries of 64 keys
-// (32 KB; Q takes 64 KB, so a ring of four: two operands of 128 keys).  O is rescaled, where the
-// maximum moved, once the product before has ended.
+// One tile of 128 rows over blocks of 64 keys; S of the next block is formed while this one is
+// exponentiated, in the other of two S (P over the S it came from), by a warp of its own, P V by another: 1024 cycles
+// of products a block.  What bounds it is the way of K and V into shared memory, 64 KB a block, so Q lies in
+// TMEM (128 columns, written by the softmax threads, a row each), and shared memory is a ring of six entries
+// of 64 keys.  With Q in shared memory and four such entries a block took 3600 cycles.  O is rescaled, where
+// the maximum moved, once the product before has ended.
 #include <cuda_bf16.h>
 
 #include "handover.h"
@@ -17,26 +18,24 @@ namespace {
 
 __device__ unsigned int g_err = 0;
 
-constexpr int D = 256, HN = 64;  // columns; keys of an entry, half a block
+constexpr int D = 256, KN = 64;  // columns; keys of a block and of an entry
 // Warps 0-3: softmax, 4: TMA, 5: S, 6: P V, 7: values that a row must not see.
 constexpr int kThreads = 256;
-constexpr int NS = 4, SL = D / 64;
-constexpr int kQ = BM * D * 2, kEntry = HN * D * 2, kOperand = 2 * kEntry;
-constexpr int oRing = kQ, oOut = oRing + NS * kEntry, oBar = oOut + 4 * kOut, oItem = oBar + 512, kBytes = oItem + 8 * 64;
+constexpr int NS = 6, SL = D / 64;
+constexpr int kEntry = KN * D * 2;
+constexpr int oOut = NS * kEntry, oBar = oOut + 4 * kOut, oItem = oBar + 512, kBytes = oItem + 8 * 64;
 static_assert(kBytes <= 232448, "shared memory");
-constexpr uint32_t cS = 0, cO = 2 * BN;  // S of an even (odd) block at cS (+ BN)
+constexpr uint32_t cS = 0, cQ = 2 * KN, cO = cQ + D / 2;  // S of an even (odd) block at cS (+ KN)
 
 __global__ void __launch_bounds__(kThreads, 1)
-    wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                const __grid_constant__ CUtensorMap tmV, const Work w, const Space sp, const Out out,
+    wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Work w, const Space sp,
+                const Out out, const __nv_bfloat16* __restrict__ Q, int64_t qs0, int64_t qs1, int64_t qs2,
                 const __nv_bfloat16* __restrict__ Vg, int64_t vs0, int64_t vs1, int64_t vs2, Pages pg, float scale, float c) {
   extern __shared__ __align__(1024) uint8_t sm[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + oBar);
-  uint64_t* q_full = bars;
-  uint64_t* q_empty = bars + 1;     // the item's last product with Q done
-  uint64_t* s_full = bars + 2;      // [2] S in TMEM
-  uint64_t* p_half = s_full + 2;    // [2] P of the first 64 keys in TMEM, O rescaled
-  uint64_t* p_ready = p_half + 2;   // [2] of all keys
+  uint64_t* q_full = bars;          // Q in TMEM
+  uint64_t* s_full = bars + 1;      // [2] S in TMEM
+  uint64_t* p_ready = s_full + 2;   // [2] P in TMEM, O rescaled
   uint64_t* pv_done = p_ready + 2;  // [2] the block's P V done
   uint64_t* o_full = pv_done + 2;
   uint64_t* o_empty = o_full + 1;   // O read by the epilogue
@@ -47,23 +46,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* known = v_ok + NS;      // [8] items
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(known + 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* started = abort_flag + 1;                                       // Q loads, ring entries (the TMA warp's)
-  volatile uint8_t* hidden = reinterpret_cast<volatile uint8_t*>(started + 2);  // [8][2] of blocks' halves: 16-key runs without a page
-  volatile int* spoilt = reinterpret_cast<volatile int*>(hidden + 16);          // [8] of items: n + 1 where values were made 0
+  volatile int* started = abort_flag + 1;                                       // ring entries (the TMA warp's)
+  volatile uint8_t* hidden = reinterpret_cast<volatile uint8_t*>(started + 1);  // [8] of blocks: 16-key runs without a page
+  volatile int* spoilt = reinterpret_cast<volatile int*>(hidden + 8);           // [8] of items: n + 1 where values were made 0
   Item* items = reinterpret_cast<Item*>(sm + oItem);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, p = blockIdx.x;
   const int gt = w.cut.gt, tq = w.cut.tile;
   ptx::grid_dependency_launch();
   if (threadIdx.x == 4 * 32) {
-    ptx::prefetch_tmap(&tmQ);
     ptx::prefetch_tmap(&tmK);
     ptx::prefetch_tmap(&tmV);
-    ptx::mbar_init(q_full, 1);
-    ptx::mbar_init(q_empty, 1);
+    ptx::mbar_init(q_full, 128);
     for (int m = 0; m < 2; ++m) {
       ptx::mbar_init(&s_full[m], 2);  // the products' end and the warp that issued them
-      ptx::mbar_init(&p_half[m], 128);
       ptx::mbar_init(&p_ready[m], 128);
       ptx::mbar_init(&pv_done[m], 1);
     }
@@ -76,7 +72,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&v_ok[s], 1);
     }
     for (int s = 0; s < 8; ++s) ptx::mbar_init(&known[s], 1), spoilt[s] = 0;
-    started[0] = started[1] = 0;
+    *started = 0;
     *abort_flag = (ptx::smem_u32(sm) & 1023u) ? 1 : 0;  // the swizzled tiles need 1024-byte alignment
     if (*abort_flag) atomicOr(&g_err, FBD_ERR_TIMEOUT);
     ptx::fence_mbar_init();
@@ -117,38 +113,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     Walk it;
     Tail tail{0, 0, 0, 0};
     bool more = it.begin(w, plan(w, p)) && ok, go = true;
-    int E = 0, n = 0, nq = 0, T = 0;
-    const int per = HN / pg.box;                                                // boxes of an entry along its keys
+    int E = 0, n = 0, T = 0;
+    const int per = KN / pg.box;                                                // boxes of an entry along its keys
     const int c0 = pg.whole ? 0 : lane % SL, g0 = pg.whole ? lane : lane / SL;  // this lane's box
-    struct Block {
-      Box half[2];
-    };
-    auto box = [&](int kb) {
-      return Block{{box_at(w, pg, it.s, it.b, kb * BN, g0, per), box_at(w, pg, it.s, it.b, kb * BN + HN, g0, per)}};
-    };
-    // The two entries of a block of K or V.
-    auto load = [&](const CUtensorMap* map, bool key, const Block& x, int kvh) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h, ++E) {
-        const int s = E % NS;
-        if (E >= NS) go = wait(&empty[s], ((E / NS) - 1) & 1) && go;
-        go = __all_sync(0xffffffffu, go);
-        if (!go) return;
-        if (lane == 0) {
-          if (key) hidden[(T & 7) * 2 + h] = static_cast<uint8_t>(x.half[h].hidden);
-          ptx::mbar_expect_tx(&full[s], kEntry);
-        }
-        __syncwarp();
-        load_box(sm + oRing + (s >> 1) * kOperand + h * 8 * pg.sbo, map, &full[s], pg, x.half[h], g0, per, c0, kvh);
+    // The next entry: block kb of K or V.
+    auto load = [&](const CUtensorMap* map, bool key, int kb, int kvh) {
+      const Box x = box_at(w, pg, it.s, it.b, kb * KN, g0, per);  // (looked up before the wait for room in the ring)
+      const int s = E % NS;
+      if (E >= NS) go = wait(&empty[s], ((E / NS) - 1) & 1) && go;
+      go = __all_sync(0xffffffffu, go);
+      if (!go) return;
+      if (lane == 0) {
+        if (key) hidden[T & 7] = static_cast<uint8_t>(x.hidden);
+        ptx::mbar_expect_tx(&full[s], kEntry);
       }
-      T += key;
+      __syncwarp();
+      load_box(sm + s * kEntry, map, &full[s], pg, x, g0, per, c0, kvh);
+      ++E, T += key;
     };
     for (; more && go; more = it.next(w), ++n) {
       const int kvh = it.vh / w.cut.per_kv, nb = it.k1 - it.k0, b0 = it.j0 + it.k0;
-      if (n > 0) go = wait(q_empty, (n - 1) & 1) && go;
-      go = __all_sync(0xffffffffu, go);
-      if (!go) break;
-      ++nq;
+      // (the ring of items is longer than the loads' lead, half the entries)
       if (lane == 0) {
         Item& x = items[n & 7];
         x.n = nb, x.b0 = b0, x.pair = 0, x.t0 = it.t0, x.t1 = it.t1, x.start = it.s.start, x.len = it.s.len;
@@ -159,21 +144,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         x.b = it.b, x.batch = it.s.batch, x.row0 = it.s.row0, x.vh = it.vh, x.kvh = kvh;
         ptx::mbar_arrive(&known[n & 7]);
         if (!it.whole() && it.k0 == 0) tail = Tail{it.b, it.tile, it.vh, it.parts(p)};
-        ptx::mbar_expect_tx(q_full, SL * gt * tq * 128);
-        for (int u = 0; u < SL; ++u)
-          ptx::tma_load_5d(sm + u * BM * 128, &tmQ, q_full, u * 64, 0, it.s.row0 + it.t0, it.vh, it.s.batch);
       }
-      // (a block's pages are looked up before the wait for room in the ring)
-      Block x = box(b0), y = x;
-      load(&tmK, true, x, kvh);
-      if (nb > 1) y = box(b0 + 1);
-      if (go && nb > 1) load(&tmK, true, y, kvh);
-      for (int j = 0; j < nb && go; ++j) {
-        Block z = y;
-        if (j + 2 < nb) z = box(b0 + j + 2);
-        load(&tmV, false, x, kvh);
-        if (go && j + 2 < nb) load(&tmK, true, z, kvh);
-        x = y, y = z;
+      // K_0 K_1 V_0 K_2 V_1 ...
+      for (int i = 0; i < nb + 2 && go; ++i) {
+        if (i >= 2) load(&tmV, false, b0 + i - 2, kvh);
+        if (go && i < nb) load(&tmK, true, b0 + i, kvh);
       }
     }
     if (lane == 0) {
@@ -182,73 +157,64 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_arrive(&known[n & 7]);
       }
       sp.tail[p] = tail;
-      started[0] = nq, started[1] = E;
+      *started = E;
     }
   } else if (warp == 5) {
-    // ------------------------------------------------------------- S = Q K^T
-    constexpr uint32_t idS = ptx::idesc_bf16(BM, BN, 0, 0);
-    const uint64_t dQ = tc::kmajor_desc(ptx::smem_u32(sm), BM, 0);
-    const uint64_t dK = ptx::sdesc_sw128(ptx::smem_u32(sm + oRing), 16, pg.sbo);
+    // ------------------------------------------------------------ S = Q K^T
+    constexpr uint32_t idS = ptx::idesc_bf16(BM, KN, 0, 0);
+    const uint64_t dK = ptx::sdesc_sw128(ptx::smem_u32(sm), 16, pg.sbo);
     int base = 0, n = 0, T = 0;
     for (const Item* it; (it = item(n)) != nullptr; ++n) {
       const Order o{base, it->n, false};
       wait(q_full, n & 1);
       for (int j = 0; j < o.n; ++j, ++T) {
-        const int e = 2 * o.K(j), s = e % NS;
+        const int e = o.K(j), s = e % NS;
         pass(e);
-        loaded(e), loaded(e + 1);
+        loaded(e);
         // the block before the last has been multiplied with V: its P's columns are free
         if (T >= 2) wait(&pv_done[T & 1], ((T >> 1) - 1) & 1);
         ptx::tc_fence_after();
-        const uint32_t so = static_cast<uint32_t>((s >> 1) * kOperand);
+        const uint32_t so = static_cast<uint32_t>(s * kEntry);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          ptx::mma_ss_e(tmem + cS + (T & 1) * BN, tc::desc_add(dQ, tc::kmajor_off(BM, k)),
-                        tc::desc_add(dK, so + (k >> 2) * pg.slab + (k & 3) * 32), idS, k > 0 ? 1u : 0u);
+          ptx::mma_ts_e(tmem + cS + (T & 1) * KN, tmem + cQ + k * 8, tc::desc_add(dK, so + (k >> 2) * pg.slab + (k & 3) * 32), idS,
+                        k > 0 ? 1u : 0u);
         ptx::mma_commit_e(&s_full[T & 1]);
         if (lane == 0) ptx::mbar_arrive(&s_full[T & 1]);
         ptx::mma_commit_e(&empty[s]);
-        ptx::mma_commit_e(&empty[s + 1]);
       }
-      ptx::mma_commit_e(q_empty);
       base += 2 * o.n;
-      pass(2 * base);
+      pass(base);
     }
   } else if (warp == 6) {
-    // ------------------------------------------------------------- O += P V
+    // ------------------------------------------------------------ O += P V
     constexpr uint32_t idO = ptx::idesc_bf16(BM, D, 0, 1);
-    const uint64_t dV = ptx::sdesc_sw128(ptx::smem_u32(sm + oRing), pg.slab, pg.sbo);
+    const uint64_t dV = ptx::sdesc_sw128(ptx::smem_u32(sm), pg.slab, pg.sbo);
     int base = 0, n = 0, T = 0, masked = 0;
     for (const Item* it; (it = item(n)) != nullptr; ++n) {
       const Order o{base, it->n, false};
       for (int j = 0; j < o.n; ++j, ++T) {
-        const int b = T & 1, phase = (T >> 1) & 1, e = 2 * o.V(j);
+        const int b = T & 1, e = o.V(j), s = e % NS;
         pass(e);
-        if (it->hides(it->b0 + j)) {
+        loaded(e);
+        if (it->hides(it->b0 + j, KN)) {
           wait(&v_ok[masked % NS], (masked / NS) & 1);
           ++masked;
         }
-        wait(&p_half[b], phase);
+        wait(&p_ready[b], (T >> 1) & 1);
         if (j == 0 && n > 0) wait(o_empty, (n - 1) & 1);
+        ptx::tc_fence_after();
+        const uint32_t so = static_cast<uint32_t>(s * kEntry);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int s = (e + h) % NS;
-          loaded(e + h);
-          if (h == 1) wait(&p_ready[b], phase);
-          ptx::tc_fence_after();
-          const uint32_t so = static_cast<uint32_t>((s >> 1) * kOperand);
-#pragma unroll
-          for (int k = h * 4; k < h * 4 + 4; ++k)
-            ptx::mma_ts_e(tmem + cO, tmem + cS + b * BN + k * 8, tc::desc_add(dV, so + k * 2 * pg.sbo), idO,
-                          (j > 0 || k > 0) ? 1u : 0u);
-          ptx::mma_commit_e(&empty[s]);
-        }
+        for (int k = 0; k < KN / 16; ++k)
+          ptx::mma_ts_e(tmem + cO, tmem + cS + b * KN + k * 8, tc::desc_add(dV, so + k * 2 * pg.sbo), idO, (j > 0 || k > 0) ? 1u : 0u);
+        ptx::mma_commit_e(&empty[s]);
         ptx::mma_commit_e(&pv_done[b]);
       }
       ptx::mma_commit_e(o_full);
       if (lane == 0) ptx::mbar_arrive(o_full);
       base += 2 * o.n;
-      pass(2 * base);
+      pass(base);
     }
   } else if (warp == 7) {
     // ------------------------- values that some row does not see: made 0 where they are not finite
@@ -256,12 +222,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (const Item* it; (it = item(n)) != nullptr; ++n) {
       const Order o{base, it->n, false};
       for (int j = 0; j < o.n; ++j) {
-        const int e = 2 * o.V(j), key0 = (it->b0 + j) * BN;
+        const int e = o.V(j), key0 = (it->b0 + j) * KN;
         pass(e);
-        if (!it->hides(it->b0 + j)) continue;
+        if (!it->hides(it->b0 + j, KN)) continue;
         wait(&full[e % NS], (e / NS) & 1);
-        wait(&full[(e + 1) % NS], ((e + 1) / NS) & 1);
-        const bool some = hide_values(sm + oRing + (e % NS >> 1) * kOperand, BN, min(max(it->len - key0, 0), BN), SL, pg);
+        const bool some = hide_values(sm + e % NS * kEntry, KN, min(max(it->len - key0, 0), KN), SL, pg);
         if (some) spoilt[n & 7] = n + 1;
         ptx::fence_proxy_async_smem();
         __syncwarp();
@@ -269,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++masked;
       }
       base += 2 * o.n;
-      pass(2 * base);
+      pass(base);
     }
   } else {
     // --------------------------- softmax: thread r owns row r
@@ -279,9 +244,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t c2 = tc::pk2f(c, c);
     const int rt = r / gt, rh = r - rt * gt;  // this row's token of the tile, and its head
     uint8_t* stage = sm + oOut + warp * kOut;
+    // This row's queries of an item to TMEM (the products with the last item's have ended: their last S has been seen).
+    auto bring_q = [&](const Item* it) {
+      const bool live = rt < tq && it->t0 + rt < it->t1;
+      const __nv_bfloat16* q =
+          Q + it->batch * qs0 + (static_cast<int64_t>(it->vh) * gt + rh) * qs1 + static_cast<int64_t>(it->row0 + it->t0 + rt) * qs2;
+#pragma unroll 1
+      for (int x0 = 0; x0 < D / 2; x0 += 32) {
+        uint32_t v[32];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const uint4 y = live ? *reinterpret_cast<const uint4*>(q + 2 * x0 + u * 8) : make_uint4(0, 0, 0, 0);
+          v[4 * u] = y.x, v[4 * u + 1] = y.y, v[4 * u + 2] = y.z, v[4 * u + 3] = y.w;
+        }
+        ptx::tmem_st32(tmem + cQ + lane_off + x0, v);
+      }
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(q_full);
+    };
     int T = 0;
-    const Item* it;
-    for (int n = 0; (it = item(n)) != nullptr; ++n) {
+    const Item* it = item(0);
+    if (it != nullptr) bring_q(it);
+    for (int n = 0; it != nullptr; ++n) {
       const int nb = it->n;
       // the keys that this row sees: its token's position less the window, up to that position or the last key
       int last, first;
@@ -292,46 +277,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         first = static_cast<int>(min(max(f, static_cast<int64_t>(0)), static_cast<int64_t>(0x7fffffff)));
       }
       const int last0 = __shfl_sync(0xffffffffu, last, 0), first31 = __shfl_sync(0xffffffffu, first, 31);
-      int key0 = it->b0 * BN;
+      int key0 = it->b0 * KN;
       float mref = -INFINITY, l = 0.f;
-      for (int j = 0; j < nb; ++j, ++T, key0 += BN) {
+      for (int j = 0; j < nb; ++j, ++T, key0 += KN) {
         const int b = T & 1;
-        const uint32_t tS = tmem + cS + b * BN + lane_off;
+        const uint32_t tS = tmem + cS + b * KN + lane_off;
         wait(&s_full[b], (T >> 1) & 1);
         ptx::tc_fence_after();
-        uint32_t v[4][32];
+        uint32_t v[2][32];
 #pragma unroll
-        for (int ch = 0; ch < 4; ++ch) ptx::tmem_ld32(tS + ch * 32, v[ch]);
-        const uint32_t hid = hidden[(T & 7) * 2] | static_cast<uint32_t>(hidden[(T & 7) * 2 + 1]) << 4;
+        for (int ch = 0; ch < 2; ++ch) ptx::tmem_ld32(tS + ch * 32, v[ch]);
+        const uint32_t hid = hidden[T & 7];
         ptx::tmem_wait_ld();
-        if (key0 + BN - 1 > last0 || key0 < first31 || hid != 0) {
+        if (key0 + KN - 1 > last0 || key0 < first31 || hid != 0) {
 #pragma unroll
-          for (int ch = 0; ch < 4; ++ch)
-            if (key0 + ch * 32 + 31 > last0 || key0 + ch * 32 < first31 || hid != 0) {
-              uint32_t see = tc::bits_between(first - key0 - ch * 32, last - key0 - ch * 32);
-              if (hid & (1u << (2 * ch))) see &= 0xffff0000u;
-              if (hid & (2u << (2 * ch))) see &= 0x0000ffffu;
+          for (int ch = 0; ch < 2; ++ch) {
+            uint32_t see = tc::bits_between(first - key0 - ch * 32, last - key0 - ch * 32);
+            if (hid & (1u << (2 * ch))) see &= 0xffff0000u;
+            if (hid & (2u << (2 * ch))) see &= 0x0000ffffu;
 #pragma unroll
-              for (int t = 0; t < 32; ++t)
-                if (!(see & (1u << t))) v[ch][t] = __float_as_uint(-INFINITY);
-            }
+            for (int t = 0; t < 32; ++t)
+              if (!(see & (1u << t))) v[ch][t] = __float_as_uint(-INFINITY);
+          }
         }
         float mx[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) mx[u] = -INFINITY;
+        for (int u = 0; u < 8; ++u) mx[u] = fmaxf(tc::f(v[0][u]), tc::f(v[1][u]));
 #pragma unroll
-        for (int ch = 0; ch < 4; ++ch)
+        for (int t = 8; t < 32; t += 8)
 #pragma unroll
-          for (int t = 0; t < 32; t += 16)
-#pragma unroll
-            for (int u = 0; u < 8; ++u) mx[u] = fmaxf(mx[u], fmaxf(tc::f(v[ch][t + u]), tc::f(v[ch][t + 8 + u])));
+          for (int u = 0; u < 8; ++u) mx[u] = fmaxf(mx[u], fmaxf(tc::f(v[0][t + u]), tc::f(v[1][t + u])));
 #pragma unroll
         for (int u = 1; u < 8; ++u) mx[0] = fmaxf(mx[0], mx[u]);
         // (always at the first visible key: mref = -inf)
         const bool moved = ptx::ex2((mx[0] - mref) * c) > fminf(fmaxf(kShare * l, 1.f), kSlack);
         const float mnew = moved ? mx[0] : mref;
         const float alpha = moved ? ptx::ex2((mref - mnew) * c) : 1.f;
-        const bool rescale = j > 0 && __any_sync(0xffffffffu, moved);
         l *= alpha;
         mref = mnew;
         // a row that has seen no key yet subtracts 0, not -inf: every term is 2^-inf = 0
@@ -339,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t nm2 = tc::pk2f(nm, nm);
         uint64_t rs[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
+        for (int ch = 0; ch < 2; ++ch) {
           uint32_t pk[16];
 #pragma unroll
           for (int t = 0; t < 32; t += 2) {
@@ -349,17 +330,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             pk[t >> 1] = ptx::pack_bf16(p0, p1);
           }
           ptx::tmem_st16(tS + ch * 16, pk);
-          if (ch == 1 && !rescale) {
-            ptx::tmem_wait_st();
-            ptx::tc_fence_before();
-            ptx::mbar_arrive(&p_half[b]);
-          }
         }
-        if (j > 0) {
+        // (waited for only here: S of the block before came behind the product two before that, so the phase is not
+        // mistaken for an older one)
+        if (j > 0 && __any_sync(0xffffffffu, moved)) {
           wait(&pv_done[b ^ 1], ((T - 1) >> 1) & 1);
           ptx::tc_fence_after();
-        }
-        if (rescale) {
           const uint64_t a2 = tc::pk2f(alpha, alpha);
 #pragma unroll 1
           for (int x0 = 0; x0 < D; x0 += 32) {
@@ -377,11 +353,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
-        if (rescale) ptx::mbar_arrive(&p_half[b]);
         ptx::mbar_arrive(&p_ready[b]);
         const float2 x = tc::unpk2(tc::add2(tc::add2(rs[0], rs[1]), tc::add2(rs[2], rs[3])));
         l += x.x + x.y;
       }
+      // The next item's queries, so that its first S are formed under this one's epilogue.
+      const Item* then = item(n + 1);
+      if (then != nullptr) bring_q(then);
       // ------------------------------------------------------------------ epilogue
       wait(o_full, n & 1);
       ptx::tc_fence_after();
@@ -414,12 +392,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       if (live) {
-        if (spoilt[n & 7] == n + 1) add_spoilt(w, *it, first, last, Vg + it->kvh * vs1, vs0, vs2, D, dst, part);
+        if (spoilt[n & 7] == n + 1) add_spoilt(w, *it, first, last, Vg + it->kvh * vs1, vs0, vs2, D, dst, part, KN);
         if (part != nullptr)
           *sp.ml(slot, r) = make_float2(mref == -INFINITY ? mref : mref * c, l);
         else if (out.lse != nullptr)
           out.lse[it->batch * out.ls[0] + h * out.ls[1] + pos] = l == 0.f ? -INFINITY : fmaf(mref, scale, logf(l));
       }
+      it = then;
     }
   }
 
@@ -428,11 +407,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // A wait has given up: loads and products may still be on their way into this CTA's shared memory and
   // TMEM, which others get when it ends.
   if (*abort_flag != 0) {
-    if (threadIdx.x == 4 * 32) {
-      const int nq = started[0], E = started[1];
-      if (nq > 0) ptx::settle(q_full, (nq - 1) & 1);
-      for (int s = 0; s < NS && s < E; ++s) ptx::settle(&full[s], handover::last_phase(E, NS, s));
-    }
+    if (threadIdx.x == 4 * 32)
+      for (int s = 0; s < NS && s < *started; ++s) ptx::settle(&full[s], handover::last_phase(*started, NS, s));
     if (warp == 5 || warp == 6) {
       ptx::mma_commit_e(settled);
       ptx::settle(settled, 0);
@@ -452,7 +428,7 @@ Work work_of(const PagedArgs& a) {
   w.cut.gt = heads_together(g, BM, a.max_new);
   w.cut.nv = a.H / w.cut.gt, w.cut.per_kv = g / w.cut.gt;
   w.cut.tile = w.cut.step = BM / w.cut.gt;
-  w.cut.shift = 7, w.cut.over = 1, w.cut.least = 4, w.cut.ctas = 152;
+  w.cut.shift = 6, w.cut.over = 2, w.cut.least = 8, w.cut.ctas = 152;
   return w;
 }
 
@@ -464,13 +440,14 @@ cudaError_t tc_paged_wide(const PagedArgs& a, void* ws, cudaStream_t st) {
   const Work w = work_of(a);
   const Space sp = Space::at(ws, w.cut.ctas, BM, D);
   const Out out{a.O, a.lse, {a.os[0], a.os[1], a.os[2]}, {a.ls[0], a.ls[1]}};
-  alignas(64) CUtensorMap mq, mk, mv;
+  alignas(64) CUtensorMap mk, mv;
   Pages pg;
-  if (!make_maps(a, w.cut, HN, SL, &mq, &mk, &mv, pg, BN)) return cudaErrorInvalidValue;
+  if (!make_maps(a, w.cut, KN, SL, nullptr, &mk, &mv, pg)) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
   if (e != cudaSuccess) return e;
-  wide_kernel<<<static_cast<unsigned>(w.cut.ctas), kThreads, kBytes, st>>>(mq, mk, mv, w, sp, out, static_cast<const __nv_bfloat16*>(a.V),
-                    a.vs[0], a.vs[1], a.vs[2], pg, a.scale, a.scale * kLog2e);
+  wide_kernel<<<static_cast<unsigned>(w.cut.ctas), kThreads, kBytes, st>>>(
+      mk, mv, w, sp, out, static_cast<const __nv_bfloat16*>(a.Q), a.qs[0], a.qs[1], a.qs[2], static_cast<const __nv_bfloat16*>(a.V),
+      a.vs[0], a.vs[1], a.vs[2], pg, a.scale, a.scale * kLog2e);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return join(w, sp, out, a.dtype, D, BM, a.max_new, st);
 }
