@@ -335,7 +335,9 @@ __global__ void __launch_bounds__(kT, 2) grad_kernel(const HeadGradArgs a) {
       widen2(now.xl, x, T{}), widen2(now.xh, x + W / 2, T{});
       widen2(now.yl, y, T{}), widen2(now.yh, y + W / 2, T{});
       now = next;
-      if (h + 2 < heads) fetch(tok, h + 2, next); else fetch(then, min(h + 2 - heads, heads - 1), next);
+      if (h + 2 < heads) fetch(tok, h + 2, next);
+      else if (heads > 1) fetch(then, h + 2 - heads, next);
+      else fetch(token_at(base + 2 * stride), 0, next);
       if (HALF) {  // the turn back
 #pragma unroll
         for (int k = 0; k < W / 2; ++k) {

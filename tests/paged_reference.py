@@ -135,8 +135,11 @@ class Batch:
         return see & (j > p - window) if window else see
 
 
-def attention(x: Batch, causal=True, window=0, scale=None):
-    """Per sequence: (O, bound), (lse, bound) [H, n, d] and [H, n] of its new tokens."""
+def attention(x: Batch, causal=True, window=0, scale=None, sums=False):
+    """Per sequence: (O, bound), (lse, bound) [H, n, d] and [H, n] of its new tokens.  sums: the bounds include what the
+    scores' own sums may be off by: a chain of d fp32 additions is within d 2^-24 of s sum |q_i k_i|, each
+    weight by that power of e, and their sum too (FP32 alone holds for sums of either sign, whose partial ones stay
+    small)."""
     u, h = (2.0 ** -8 if x.dtype == torch.bfloat16 else 0.0), half_step(x.dtype)
     s = scale or 1.0 / math.sqrt(x.d)
     g = x.H // x.Hkv
@@ -154,6 +157,10 @@ def attention(x: Batch, causal=True, window=0, scale=None):
         L = torch.logsumexp(S, -1) if S.shape[-1] else torch.full(q.shape[:2], -math.inf, device="cuda", dtype=torch.float64)
         A = torch.where(see, torch.exp(S - torch.where(some, L, torch.zeros_like(L))[..., None]), torch.zeros_like(S))
         O = A @ V
-        tO = (u + FP32) * (A @ V.abs()) + h * O.abs()
-        out.append(((O, tO), (L, FP32 * (1 + L.abs()))))
+        e = torch.zeros_like(L)[..., None]
+        if sums:
+            mag = (s * q.abs() @ K.abs().transpose(-1, -2)).masked_fill(~see, 0.0)
+            e = x.d * 2.0 ** -24 * mag.amax(-1, keepdim=True)
+        tO = (u + FP32 + 2 * e) * (A @ V.abs()) + h * O.abs()
+        out.append(((O, tO), (L, FP32 * (1 + L.abs()) + e[..., 0])))
     return out

@@ -235,7 +235,7 @@ def test_append_outside_the_table_or_the_cache():
 
 
 # -------------------------------------------------------------------------------- attention
-def attend(x, causal=True, window=0, scale=0.0, max_new=None, check=True, **kw):
+def attend(x, causal=True, window=0, scale=0.0, max_new=None, check=True, sums=False, **kw):
     import fwd_bwd_double_gb300 as fbd
     import paged_reference as R
     torch = _t()
@@ -247,7 +247,7 @@ def attend(x, causal=True, window=0, scale=0.0, max_new=None, check=True, **kw):
     if not check:
         return O, lse
     inside = torch.zeros(x.rows, dtype=torch.bool, device="cuda")
-    for b, (o, L) in enumerate(R.attention(x, causal, window, scale or None)):
+    for b, (o, L) in enumerate(R.attention(x, causal, window, scale or None, sums)):
         r, rows = x.place(b)
         inside[r, rows] = True
         within(O[r, :, rows], o, f"O of sequence {b}")
