@@ -6,9 +6,10 @@
 // that a warp holds whole groups; at d = 96 a quarter of them idle) takes a token: a thread holds
 // 16 bytes of each half of the head (neighbouring pairs: 32 bytes in a row), so that both
 // coordinates of its pairs are its own and the sum of squares is a few shuffles.  The sines of its
-// pairs, times the weights, serve all its heads; arithmetic goes two floats an instruction.  The first heads'
-// loads are issued before the tables and the token's place are looked up, each next ones' before
-// these are worked on.  Squares, sums and r are fp32; each output is rounded once.
+// pairs, times the weights, serve all its heads; arithmetic goes two floats an instruction.  Each thread brings its
+// own 16-byte pieces by asynchronous copies to a ring in shared memory that only it reads (no barrier), the first
+// ones before the tables and the token's place are looked up, and the next token's behind this one's: held in
+// registers, half as many bytes were on their way.  Squares, sums and r are fp32; each output is rounded once.
 #include <cuda_bf16.h>
 
 #include "angle.cuh"
@@ -116,8 +117,18 @@ __device__ __forceinline__ void weights(const float* w, int c0, int c1, float (&
   for (int u = 0; u < W; ++u) w0[u] = __ldg(w + c0 + u), w1[u] = __ldg(w + c1 + u);  // (aligned to 4 bytes only)
 }
 
-constexpr int kHU = 3;      // heads whose loads are in flight together
-constexpr int kNear = 512;  // sequences of an append that are looked up in shared memory
+constexpr int kNear = 512;    // sequences of an append that are looked up in shared memory
+constexpr int kAhead = 6;     // heads on their way (the gradient: four of x and of dy)
+constexpr int kAheadGrad = 4;
+
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 template <typename T, bool HALF, bool APPEND, int LG>
 __global__ void __launch_bounds__(kT, 2) head_kernel(const HeadArgs a) {
@@ -150,21 +161,33 @@ __global__ void __launch_bounds__(kT, 2) head_kernel(const HeadArgs a) {
     k.x = static_cast<const T*>(z.x) + k.b * z.xs[0] + hb * z.xs[1] + k.n * z.xs[2];
     return k;
   };
-  struct Heads {
-    uint4 lo[kHU], hi[kHU];
-  };
-  auto fetch = [&](const T* x, int h, Heads& v) {  // (behind the last head: the last one)
-#pragma unroll
-    for (int k = 0; k < kHU; ++k) {
-      const T* at = x + min(h + k, heads - 1) * z.xs[1];
-      v.lo[k] = *reinterpret_cast<const uint4*>(at + c0);
-      v.hi[k] = *reinterpret_cast<const uint4*>(at + c1);
-    }
-  };
-  Heads now, next;
+  // This thread's ring: head i of its sequence of (token, head) in place i % kAhead.
+  extern __shared__ __align__(16) uint4 ring[];
+  uint4* own_ring = ring + threadIdx.x;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * step;
+  struct {
+    int64_t base;
+    const T* x;
+    int h, place;
+  } ahead;
+  ahead.base = first, ahead.h = 0, ahead.place = 0;
   Token tok = token_at(first);
-  fetch(tok.x, 0, now);
+  ahead.x = tok.x;
+  auto fetch = [&] {
+    if (ahead.base < tokens) {
+      copy16(own_ring + ahead.place * 2 * kT, ahead.x + c0);
+      copy16(own_ring + (ahead.place * 2 + 1) * kT, ahead.x + c1);
+      ahead.place = ahead.place + 1 == kAhead ? 0 : ahead.place + 1;
+      ahead.x += z.xs[1];
+      if (++ahead.h == heads) {
+        ahead.h = 0, ahead.base += stride;
+        ahead.x = token_at(ahead.base).x;
+      }
+    }
+    copy_commit();
+  };
+#pragma unroll 1
+  for (int i = 0; i < kAhead - 1; ++i) fetch();
   // Behind those loads: the tables.
   const bool turn = z.turn;
   if (turn) angle_tables(a.freq, a.axis, pairs, a.axes, sT, sAx);
@@ -210,6 +233,7 @@ __global__ void __launch_bounds__(kT, 2) head_kernel(const HeadArgs a) {
     return x;
   };
   Place place = place_at(tok, first);
+  int at_ring = 0;
   for (int64_t base = first; base < tokens; base += stride) {
     const bool live = place.live;
     const int at = place.at, slot = place.slot, page = place.page < q.pages ? place.page : -1;
@@ -234,38 +258,35 @@ __global__ void __launch_bounds__(kT, 2) head_kernel(const HeadArgs a) {
     const bool put = live && !(APPEND && z.paged && page < 0);
     T* y = static_cast<T*>(z.y) + hb * z.ys[1] +
            (APPEND && z.paged ? page * z.ys[0] + slot * z.ys[2] : tok.b * z.ys[0] + tok.n * z.ys[2]);
-    const T* x = tok.x;
     tok = token_at(base + stride);
     if (APPEND) place = place_at(tok, base + stride);  // (its page is not waited for here)
     else place.live = mine && base + stride + threadIdx.x / LG < tokens;
-    for (int h = 0; h < heads; h += kHU) {
-      fetch(h + kHU < heads ? x : tok.x, h + kHU < heads ? h + kHU : 0, next);
+    for (int h = 0; h < heads; ++h, y += z.ys[1]) {
+      copy_wait<kAhead - 2>();
+      const uint4 lo = own_ring[at_ring * 2 * kT], hi = own_ring[(at_ring * 2 + 1) * kT];
+      at_ring = at_ring + 1 == kAhead ? 0 : at_ring + 1;
+      fetch();
+      if (z.norm || turn) {
+        uint64_t v[W], o[W];
+        widen2(lo, v, T{}), widen2(hi, v + W / 2, T{});
+        m.apply(v, o);
+        if (z.norm) {
+          const float ss = sum_squares(v);
+          const float r = rsqrtf(fmaf(group_sum<LG>(mine ? ss : 0.f), inv, a.eps));
 #pragma unroll
-      for (int k = 0; k < kHU; ++k) {
-        if (h + k >= heads) break;
-        T* to = y + (h + k) * z.ys[1];
-        if (z.norm || turn) {
-          uint64_t v[W], o[W];
-          widen2(now.lo[k], v, T{}), widen2(now.hi[k], v + W / 2, T{});
-          m.apply(v, o);
-          if (z.norm) {
-            const float ss = sum_squares(v);
-            const float r = rsqrtf(fmaf(group_sum<LG>(mine ? ss : 0.f), inv, a.eps));
-#pragma unroll
-            for (int u = 0; u < W; ++u) o[u] = tc::mul2(o[u], both(r));
-          }
-          if (put) {
-            put2(to + c0, o);
-            put2(to + c1, o + W / 2);
-          }
-        } else if (put) {
-          *reinterpret_cast<uint4*>(to + c0) = now.lo[k];
-          *reinterpret_cast<uint4*>(to + c1) = now.hi[k];
+          for (int u = 0; u < W; ++u) o[u] = tc::mul2(o[u], both(r));
         }
+        if (put) {
+          put2(y + c0, o);
+          put2(y + c1, o + W / 2);
+        }
+      } else if (put) {
+        *reinterpret_cast<uint4*>(y + c0) = lo;
+        *reinterpret_cast<uint4*>(y + c1) = hi;
       }
-      now = next;
     }
   }
+  copy_wait<0>();
 }
 
 template <typename T, bool HALF, int LG>
@@ -299,20 +320,34 @@ __global__ void __launch_bounds__(kT, 2) grad_kernel(const HeadGradArgs a) {
     k.dy = static_cast<const T*>(z.dy) + k.b * z.dys[0] + hb * z.dys[1] + k.n * z.dys[2];
     return k;
   };
-  // A head of x and dy at a time, the loads of the next but one, of the next token too, before it is worked on.
-  struct Head {
-    uint4 xl, xh, yl, yh;
-  };
-  auto fetch = [&](const Token& k, int h, Head& v) {
-    const T *x = k.x + h * z.xs[1], *dy = k.dy + h * z.dys[1];
-    v.xl = *reinterpret_cast<const uint4*>(x + c0), v.xh = *reinterpret_cast<const uint4*>(x + c1);
-    v.yl = *reinterpret_cast<const uint4*>(dy + c0), v.yh = *reinterpret_cast<const uint4*>(dy + c1);
-  };
+  extern __shared__ __align__(16) uint4 ring[];  // (as in head_kernel: x's two pieces and dy's)
+  uint4* own_ring = ring + threadIdx.x;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * step, stride = static_cast<int64_t>(gridDim.x) * step;
-  Token tok = token_at(first), then = token_at(first + stride);
-  Head now, next;
-  fetch(tok, 0, now);
-  if (heads > 1) fetch(tok, 1, next); else fetch(then, 0, next);
+  Token tok = token_at(first);
+  struct {
+    int64_t base;
+    const T *x, *dy;
+    int h, place;
+  } ahead;
+  ahead.base = first, ahead.h = 0, ahead.place = 0, ahead.x = tok.x, ahead.dy = tok.dy;
+  auto fetch = [&] {
+    if (ahead.base < tokens) {
+      uint4* to = own_ring + ahead.place * 4 * kT;
+      copy16(to, ahead.x + c0), copy16(to + kT, ahead.x + c1);
+      copy16(to + 2 * kT, ahead.dy + c0), copy16(to + 3 * kT, ahead.dy + c1);
+      ahead.place = (ahead.place + 1) % kAheadGrad;
+      ahead.x += z.xs[1], ahead.dy += z.dys[1];
+      if (++ahead.h == heads) {
+        ahead.h = 0, ahead.base += stride;
+        const Token k = token_at(ahead.base);
+        ahead.x = k.x, ahead.dy = k.dy;
+      }
+    }
+    copy_commit();
+  };
+#pragma unroll 1
+  for (int i = 0; i < kAheadGrad - 1; ++i) fetch();
+  int at_ring = 0;
   if (turn) angle_tables(a.freq, a.axis, pairs, a.axes, sT, sAx);
   for (int i = threadIdx.x; i < a.d; i += kT) sW[i] = z.w != nullptr ? z.w[i] : 1.f;
   uint64_t g[W];
@@ -332,12 +367,14 @@ __global__ void __launch_bounds__(kT, 2) grad_kernel(const HeadGradArgs a) {
     T* dx = static_cast<T*>(z.dx) + tok.b * z.dxs[0] + hb * z.dxs[1] + tok.n * z.dxs[2];
     for (int h = 0; h < heads; ++h, dx += z.dxs[1]) {
       uint64_t x[W], y[W], f[W];
-      widen2(now.xl, x, T{}), widen2(now.xh, x + W / 2, T{});
-      widen2(now.yl, y, T{}), widen2(now.yh, y + W / 2, T{});
-      now = next;
-      if (h + 2 < heads) fetch(tok, h + 2, next);
-      else if (heads > 1) fetch(then, h + 2 - heads, next);
-      else fetch(token_at(base + 2 * stride), 0, next);
+      copy_wait<kAheadGrad - 2>();
+      {
+        const uint4* from = own_ring + at_ring * 4 * kT;
+        widen2(from[0], x, T{}), widen2(from[kT], x + W / 2, T{});
+        widen2(from[2 * kT], y, T{}), widen2(from[3 * kT], y + W / 2, T{});
+      }
+      at_ring = (at_ring + 1) % kAheadGrad;
+      fetch();
       if (HALF) {  // the turn back
 #pragma unroll
         for (int k = 0; k < W / 2; ++k) {
@@ -375,9 +412,9 @@ __global__ void __launch_bounds__(kT, 2) grad_kernel(const HeadGradArgs a) {
         put2(dx + c1, y + W / 2);
       }
     }
-    tok = then;
-    then = token_at(base + 2 * stride);
+    tok = token_at(base + stride);
   }
+  copy_wait<0>();
   if (z.dw == nullptr) return;
   // This block's share of dw: over the groups of a warp, then over the warps.
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -425,32 +462,40 @@ __global__ void __launch_bounds__(1024) weight_kernel(const HeadGradArgs a) {
   }
 }
 
-// Heads of a block row: up to `most`, a tensor's rows alike; the block rows before each tensor.
-void split_heads(int count, const int64_t* heads, int most, int* per, int* first) {
-  first[0] = 0;
-  for (int t = 0; t < 4; ++t) {
-    const int h = t < count ? static_cast<int>(heads[t]) : 0, rows = (h + most - 1) / most;
-    per[t] = rows > 0 ? (h + rows - 1) / rows : 1;
-    first[t + 1] = first[t] + (h + per[t] - 1) / per[t];
+// How a call's heads and tokens are dealt to blocks: block rows of up to `per` heads of a tensor, and block columns, each
+// of which takes groups of tokens one after another behind one set of tables, two blocks an SM.  The most heads
+// a row that end soonest: a group costs its heads and its sines (about two and a half heads' time).  For 24 heads
+// of 32768 tokens 41 us; columns for 2, 4 and 8 waves instead 43, 44, 47.
+struct Split {
+  int per[4], first[5], cols;
+};
+Split split(int64_t groups, const int64_t* heads, int count) {
+  Split best{};
+  double least = 0;
+  for (int most = 1; most <= 12; ++most) {
+    Split s{};
+    int widest = 0;
+    for (int t = 0; t < 4; ++t) {
+      const int h = t < count ? static_cast<int>(heads[t]) : 0, rows = (h + most - 1) / most;
+      s.per[t] = rows > 0 ? (h + rows - 1) / rows : 1;
+      s.first[t + 1] = s.first[t] + (h + s.per[t] - 1) / s.per[t];
+      if (h > 0 && s.per[t] > widest) widest = s.per[t];
+    }
+    const int64_t rows = s.first[4], fit = 152 * 2, wave = rows > 0 && rows < fit ? fit / rows : 1;
+    s.cols = static_cast<int>(groups < wave ? groups : wave);
+    const int64_t blocks = rows * s.cols, each = s.cols > 0 ? (groups + s.cols - 1) / s.cols : 0;
+    const double cost = static_cast<double>((blocks + fit - 1) / fit) * each * (widest + 2.5);
+    if (most == 1 || cost <= least) best = s, least = cost;
   }
-}
-
-// Heads per thread: six or three (whole groups of loads in flight) where that leaves a wave of threads on 152 SMs,
-// so that the sines are shared.
-int heads_per_thread(int64_t thread_heads) {
-  const int64_t hp = thread_heads / (152 * 512);
-  return hp >= 6 ? 6 : hp >= 3 ? 3 : 1;
-}
-// Block columns for `groups` of tokens: a wave of two blocks an SM, each block taking its groups one after
-// another behind one set of tables (2, 4 and 8 waves: 43, 44, 47 against 41 us for 24 heads of 32768 tokens).
-int columns(int64_t groups, int rows) {
-  const int64_t wave = rows > 0 && rows < 152 * 2 ? 152 * 2 / rows : 1;
-  return static_cast<int>(groups < wave ? groups : wave);
+  return best;
 }
 
 template <typename T, bool HALF, bool APPEND, int LG>
 cudaError_t run(const HeadArgs& a, dim3 grid, cudaStream_t st) {
-  head_kernel<T, HALF, APPEND, LG><<<grid, kT, 0, st>>>(a);
+  constexpr int smem = kAhead * 2 * kT * 16;
+  const cudaError_t e = cudaFuncSetAttribute(head_kernel<T, HALF, APPEND, LG>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  head_kernel<T, HALF, APPEND, LG><<<grid, kT, smem, st>>>(a);
   return cudaGetLastError();
 }
 template <typename T, bool HALF, bool APPEND>
@@ -464,37 +509,37 @@ cudaError_t run(const HeadArgs& a, int LG, dim3 grid, cudaStream_t st) {
 template <typename T>
 cudaError_t run(HeadArgs a, bool half, bool append, cudaStream_t st) {
   const int LG = group_threads(a.d, 16 / static_cast<int>(sizeof(T)));
-  const int64_t threads = a.B * a.N * LG;
+  const int step = kT / LG;
   int64_t heads[4];
   for (int t = 0; t < 4; ++t) heads[t] = a.t[t].heads;
-  split_heads(4, heads, heads_per_thread(a.heads * threads), a.per, a.first);
-  const dim3 grid(static_cast<unsigned>(columns((threads + kT - 1) / kT, a.first[4])), static_cast<unsigned>(a.first[4]));
+  const Split p = split((a.B * a.N + step - 1) / step, heads, 4);
+  for (int t = 0; t < 4; ++t) a.per[t] = p.per[t];
+  for (int t = 0; t < 5; ++t) a.first[t] = p.first[t];
+  const dim3 grid(static_cast<unsigned>(p.cols), static_cast<unsigned>(p.first[4]));
   if (append) return half ? run<T, true, true>(a, LG, grid, st) : run<T, false, true>(a, LG, grid, st);
   return half ? run<T, true, false>(a, LG, grid, st) : run<T, false, false>(a, LG, grid, st);
 }
 
-struct GradPlan {
-  int per[4], first[5], cols;
-};
-GradPlan grad_plan(int64_t B, int64_t N, int64_t d, int dtype, const int64_t* heads, int count) {
-  const int W = dtype == ATTN_BF16 ? 8 : 4, step = kT / group_threads(static_cast<int>(d), W);
-  const int64_t groups = (B * N + step - 1) / step;  // block columns that have work
-  int64_t all = 0;
-  for (int t = 0; t < count; ++t) all += heads[t];
-  GradPlan p;
-  split_heads(count, heads, heads_per_thread(all * groups * kT), p.per, p.first);
-  p.cols = columns(groups, p.first[4]);
-  return p;
+Split grad_split(int64_t B, int64_t N, int64_t d, int dtype, const int64_t* heads, int count) {
+  const int step = kT / group_threads(static_cast<int>(d), dtype == ATTN_BF16 ? 8 : 4);
+  return split((B * N + step - 1) / step, heads, count);
 }
 
+template <typename T, bool HALF, int LG>
+cudaError_t run_grad(const HeadGradArgs& a, dim3 grid, cudaStream_t st) {
+  constexpr int smem = kAheadGrad * 4 * kT * 16;
+  const cudaError_t e = cudaFuncSetAttribute(grad_kernel<T, HALF, LG>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  grad_kernel<T, HALF, LG><<<grid, kT, smem, st>>>(a);
+  return cudaGetLastError();
+}
 template <typename T, bool HALF>
 cudaError_t run_grad(const HeadGradArgs& a, int LG, dim3 grid, cudaStream_t st) {
   constexpr int S = sizeof(T) / 2;
-  if (LG == 2 * S) grad_kernel<T, HALF, 2 * S><<<grid, kT, 0, st>>>(a);
-  else if (LG == 4 * S) grad_kernel<T, HALF, 4 * S><<<grid, kT, 0, st>>>(a);
-  else if (LG == 8 * S) grad_kernel<T, HALF, 8 * S><<<grid, kT, 0, st>>>(a);
-  else grad_kernel<T, HALF, 16 * S><<<grid, kT, 0, st>>>(a);
-  return cudaGetLastError();
+  return LG == 2 * S   ? run_grad<T, HALF, 2 * S>(a, grid, st)
+         : LG == 4 * S ? run_grad<T, HALF, 4 * S>(a, grid, st)
+         : LG == 8 * S ? run_grad<T, HALF, 8 * S>(a, grid, st)
+                       : run_grad<T, HALF, 16 * S>(a, grid, st);
 }
 
 }  // namespace
@@ -504,7 +549,7 @@ cudaError_t head_norm(const HeadArgs& a, int dtype, bool half, bool append, cuda
 }
 
 size_t head_norm_bwd_bytes(int64_t B, int64_t N, int64_t d, int dtype, const int64_t* heads, int count) {
-  const GradPlan p = grad_plan(B, N, d, dtype, heads, count);
+  const Split p = grad_split(B, N, d, dtype, heads, count);
   return static_cast<size_t>(p.first[4]) * p.cols * d * sizeof(float);
 }
 
@@ -513,7 +558,7 @@ cudaError_t head_norm_bwd(const HeadGradArgs& args, int dtype, bool half, cudaSt
   int64_t heads[4] = {0, 0, 0, 0};
   bool dw = false;
   for (int t = 0; t < a.count; ++t) heads[t] = a.t[t].heads, dw = dw || a.t[t].dw != nullptr;
-  const GradPlan p = grad_plan(a.B, a.N, a.d, dtype, heads, a.count);
+  const Split p = grad_split(a.B, a.N, a.d, dtype, heads, a.count);
   for (int t = 0; t < 4; ++t) a.per[t] = p.per[t];
   for (int t = 0; t < 5; ++t) a.first[t] = p.first[t];
   a.cols = p.cols;
