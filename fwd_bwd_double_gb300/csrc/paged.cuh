@@ -1,8 +1,9 @@
 // How the attention over a paged cache is cut into work, shared by its kernels.
 //
 // An item is a run of new tokens of one sequence with `gt` query heads of a key/value head: the rows
-// (token, head) of a tile.  Its cost is its key blocks (two units each where it fills two tiles) and a
-// constant.  All items stand on a line, sequence by sequence, tile by tile, the heads of a tile side
+// (token, head) of a tile.  Its cost is its key blocks and a constant, for an item of two tiles as for one of one: the
+// block is fetched once for both, and a lone tile's two halves of a CTA take turns at its blocks.  (Two units a block
+// for two tiles: 182 us for the ragged window of 8 sequences, 163 at best with a larger constant; one unit: 142.)  All items stand on a line, sequence by sequence, tile by tile, the heads of a tile side
 // by side, and each CTA takes an equal stretch of it, cut between key blocks: ragged batches spread
 // evenly, and a long context with few rows is shared by all SMs.  An item that lies in several
 // stretches leaves its parts (o unnormalised, maximum, sum) in the workspace, at most two a CTA, and
@@ -24,10 +25,10 @@ struct Cut {
   int nv;      // groups of gt query heads
   int per_kv;  // ... of a key/value head
   int tile;    // tokens of a tile
-  int step;    // tokens of an item (tile, or 2 tile: then an item of more than `tile` tokens costs double)
+  int step;    // tokens of an item (tile, or 2 tile: then an item of more than `tile` tokens fills two)
   int shift;   // a block holds 1 << shift keys
-  int over;    // cost of an item beside its blocks
-  int least;   // units of a stretch, at the least
+  int over;    // cost of an item beside its blocks, in blocks
+  int least;   // blocks of a stretch, at the least
   int ctas;
 };
 struct Work {
@@ -80,7 +81,7 @@ __device__ __forceinline__ Blocks blocks_of(const Work& w, const Seq& s, int t0,
 __device__ __forceinline__ int64_t tile_units(const Work& w, const Seq& s, int tile) {
   const int t0 = tile * w.cut.step, t1 = min(s.n, t0 + w.cut.step);
   const Blocks k = blocks_of(w, s, t0, t1);
-  return static_cast<int64_t>(t1 - t0 > w.cut.tile ? 2 : 1) * k.n + w.cut.over;
+  return static_cast<int64_t>(k.n) + w.cut.over;
 }
 __device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
 #pragma unroll
@@ -165,7 +166,8 @@ struct Walk {
   int64_t pos, from, to, stretch;  // this item on the line; the stretch
   int b, tile, vh;
   Seq s;
-  int t0, t1, j0, n, weight;
+  int t0, t1, j0, n;
+  bool pair;              // it fills two tiles
   int k0, k1;             // this CTA's blocks of the item: k0 .. k1 - 1
   int64_t end;            // the item's last block on the line
 
@@ -173,12 +175,12 @@ struct Walk {
     t0 = tile * w.cut.step, t1 = min(s.n, t0 + w.cut.step);
     const Blocks k = blocks_of(w, s, t0, t1);
     j0 = k.j0, n = k.n;
-    weight = t1 - t0 > w.cut.tile ? 2 : 1;
+    pair = t1 - t0 > w.cut.tile;
   }
   __device__ __forceinline__ void set_range() {
-    end = pos + static_cast<int64_t>(weight) * (n - 1);
-    k0 = from > pos ? static_cast<int>(min(static_cast<int64_t>(n), (from - pos + weight - 1) / weight)) : 0;
-    k1 = end >= to ? static_cast<int>(max(static_cast<int64_t>(0), (to - pos + weight - 1) / weight)) : n;
+    end = pos + n - 1;
+    k0 = from > pos ? static_cast<int>(min(static_cast<int64_t>(n), from - pos)) : 0;
+    k1 = end >= to ? static_cast<int>(max(static_cast<int64_t>(0), to - pos)) : n;
   }
   // false: nothing to do
   __device__ __forceinline__ bool begin(const Work& w, const Plan& r) {
@@ -193,7 +195,7 @@ struct Walk {
   // the next item with blocks in the stretch
   __device__ __forceinline__ bool next(const Work& w) {
     do {
-      pos += static_cast<int64_t>(weight) * n + w.cut.over;
+      pos += static_cast<int64_t>(n) + w.cut.over;
       if (pos >= to) return false;
       if (++vh == w.cut.nv) {
         vh = 0;

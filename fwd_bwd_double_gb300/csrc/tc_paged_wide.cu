@@ -428,7 +428,9 @@ Work work_of(const PagedArgs& a) {
   w.cut.gt = heads_together(g, BM, a.max_new);
   w.cut.nv = a.H / w.cut.gt, w.cut.per_kv = g / w.cut.gt;
   w.cut.tile = w.cut.step = BM / w.cut.gt;
-  w.cut.shift = 6, w.cut.over = 2, w.cut.least = 8, w.cut.ctas = 152;
+  // An item's start and epilogue cost about eight blocks of 64 keys: 89.7 us for 2 x 1000 tokens over 4500 keys with 2,
+  // 88.2 with 8, 89.5 with 16.
+  w.cut.shift = 6, w.cut.over = 8, w.cut.least = 8, w.cut.ctas = 152;
   return w;
 }
 
