@@ -141,8 +141,8 @@ attn_status_t check_paged_desc(const attn_desc_t* desc, Paged& p) {
   if (s != ATTN_OK) return s;
   if (desc->seg_lo != nullptr) return fail(ATTN_ERR_UNSUPPORTED, "no document mask over a cache%s");
   const int64_t lim = int64_t(1) << 31;
-  if (desc->B < 0 || desc->N < 0 || desc->B >= lim / 64 || desc->N >= lim || desc->H > 65535)
-    return fail(ATTN_ERR_INVALID_ARG, "0 <= B < 2^25, 0 <= N < 2^31, H <= 65535%s");
+  if (desc->B < 0 || desc->N < 0 || desc->B >= lim / 64 || desc->N > lim - 4096 || desc->H > 65535)  // (a tile's end behind the last token is an int too)
+    return fail(ATTN_ERR_INVALID_ARG, "0 <= B < 2^25, 0 <= N <= 2^31 - 4096, H <= 65535%s");
   p.B = desc->B, p.H = desc->H, p.Hkv = desc->H / q.group, p.N = desc->N, p.d = desc->d;
   p.dtype = desc->dtype, p.e = desc->dtype == ATTN_F32 ? 4 : 2;
   p.causal = desc->causal, p.window = desc->window, p.scale = q.scale;
@@ -209,7 +209,7 @@ attn_status_t attn_qk_norm(const attn_rope_desc_t* desc, const attn_norm_tensor_
   if (all * B * N == 0) return ATTN_OK;
   Ranges ranges;
   HeadArgs a{};
-  a.B = B, a.N = N, a.d = static_cast<int>(d), a.axes = desc->axes, a.heads = static_cast<int>(all), a.eps = eps;
+  a.B = B, a.N = N, a.d = static_cast<int>(d), a.axes = desc->axes, a.eps = eps;
   a.pos_batch = desc->pos_batch_stride, a.pos_axis = desc->pos_batch_stride == 0 ? N : B * N;
   a.pos = pos, a.freq = freq, a.axis = axis;
   if (freq != nullptr || pos != nullptr || axis != nullptr)
@@ -332,8 +332,7 @@ attn_status_t attn_cache_append(const attn_desc_t* desc, const attn_new_tokens_t
     if ((s = check_view(x, p.d, p.e, true, q.xs, ranges, same_view(x, y))) != ATTN_OK) return s;
     if ((s = check_view(y, p.d, p.e, false, q.ys, ranges)) != ATTN_OK) return s;
   }
-  a.heads = k.heads + v.heads + q.heads;
-  if (a.heads > 65535) return fail(ATTN_ERR_INVALID_ARG, "0 to 65535 heads in all%s");
+  if (k.heads + v.heads + q.heads > 65535) return fail(ATTN_ERR_INVALID_ARG, "0 to 65535 heads in all%s");
   if (t->normed) {
     if (t->k_weight != nullptr && (s = check_words("k_weight", t->k_weight)) != ATTN_OK) return s;
     if (t->q_weight != nullptr && (s = check_words("q_weight", t->q_weight)) != ATTN_OK) return s;

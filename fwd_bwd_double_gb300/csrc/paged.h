@@ -69,7 +69,7 @@ struct HeadArgs {
   const int* pos;               // null: the tokens' positions in their sequences
   const float* freq;            // null: nothing turns
   const int* axis;
-  int d, axes, heads;           // heads: of all tensors together
+  int d, axes;
   float eps;
   int per[4], first[5];         // heads per thread and first block row of each tensor (set by the launcher)
   Seqs seqs;                    // of an append (else unused)

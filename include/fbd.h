@@ -458,7 +458,7 @@ attn_status_t attn_qk_norm_bwd(const attn_rope_desc_t* desc, const attn_norm_gra
  *   page_size: a multiple of 16, up to 2^20 (else ATTN_ERR_UNSUPPORTED); width * page_size <= 2^31 - 4096.
  *   A table entry outside 0 .. pages - 1 is no page: nothing is written there, and the keys that
  *   would lie there are hidden from every token (as pages given up behind a window may be).
- * The sequences of a call: desc->B of them, lens [B] int32 (device) the keys each holds, its new
+ * The sequences of a call: desc->B of them (below 2^25, of at most 2^31 - 4096 tokens), lens [B] int32 (device) the keys each holds, its new
  * tokens' among them; new token t of the n of a sequence stands at position lens[b] - n + t.
  *   cu [B + 1] int32 (device), non-decreasing: packed tokens; the tensors are [1, heads, N, d] and sequence
  *   b has the rows cu[b] .. cu[b + 1] - 1 (rows of no sequence are left as they were);
@@ -481,7 +481,7 @@ typedef struct {
  *   freq, axis: the rotary's tables (both NULL: nothing turns); pos NULL: the tokens' positions in their
  *   sequences (axes = 1), else [axes, B, N] (pos_batch_stride = N) or [axes, N] (0; packed tokens).
  *   A token whose position is outside the table or has no page is not written (its query is).  Two tokens
- *   with the same slot: either may stay.  The cache may not overlap the new tokens. */
+ *   with the same slot: each element is one's or the other's.  The cache may not overlap the new tokens. */
 typedef struct {
   const void* K;
   const void* V;

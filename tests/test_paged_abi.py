@@ -259,3 +259,13 @@ def test_window_and_hint_past_32_bits():
     for window, hint in ((1 << 40, 1 << 40), ((1 << 32) + 5, 7)):
         with pytest.raises(FbdError, match="one CUDA device"):  # past every other check
             fbd.attn_paged(Q, (K, K.clone(), table), lens, cu, window=window, max_new=hint)
+
+
+def test_tokens_at_the_end_of_the_index_range():
+    """Token counts whose last tile would end behind 2^31 are refused; the most that are taken pass the descriptor."""
+    for n, code in (((1 << 31) - 1, INVALID), ((1 << 31) - 4095, INVALID), ((1 << 31) - 4096, WS)):
+        d = desc(B=1, H=1, N=n, group=1)
+        assert paged(d=d, nbytes=0, qs=(0, 0, D), os=(0, 0, D), Q=1 << 50, O=1 << 51, lse=0) == code
+        assert (lib.attn_paged_workspace_bytes(ctypes.byref(d), 0) > 0) == (code == WS)
+        if code == INVALID:
+            assert append(dsc=d) == code
