@@ -10,6 +10,10 @@
 // own 16-byte pieces by asynchronous copies to a ring in shared memory that only it reads (no barrier), the first
 // ones before the tables and the token's place are looked up, and the next token's behind this one's: held in
 // registers, half as many bytes were on their way.  Squares, sums and r are fp32; each output is rounded once.
+//
+// 24 heads of 64 over 32768 tokens in bf16 (201 MB): 39 us, 5.1 TB/s; the gradient (302 MB) 56 us, 5.4 TB/s (with the
+// next pieces in registers 41 and 79 us); 19.8 thousand prompt tokens of 16 + 4 + 4 heads of 128 into pages (243 MB)
+// 57 us, 4.3 TB/s.  Half of the issue slots are the sums, turns and conversions.
 #include <cuda_bf16.h>
 
 #include "angle.cuh"
@@ -465,7 +469,7 @@ __global__ void __launch_bounds__(1024) weight_kernel(const HeadGradArgs a) {
 // How a call's heads and tokens are dealt to blocks: block rows of up to `per` heads of a tensor, and block columns, each
 // of which takes groups of tokens one after another behind one set of tables, two blocks an SM.  The most heads
 // a row that end soonest: a group costs its heads and its sines (about two and a half heads' time).  For 24 heads
-// of 32768 tokens 41 us; columns for 2, 4 and 8 waves instead 43, 44, 47.
+// of 32768 tokens one wave took 41 us when columns for 2, 4 and 8 waves took 43, 44, 47 (39 since the ring).
 struct Split {
   int per[4], first[5], cols;
 };
