@@ -375,3 +375,20 @@ def test_norm_gradient_of_many_tokens(dtype):
         within(dw, want[1], "dw")
         again = fbd.attn_qk_norm_bwd(x, dy, w, pos, freq, axis)
         assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+
+
+# --------------------------------------------------------------------------- a few rows
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [32, 64, 96, 128, 256])
+@pytest.mark.parametrize("n,heads", [(1, (3, 1)), (4, (2, 2)), (2, (6, 2)), (8, (1, 1)), (3, (5, 1)), (4, (8, 2)), (16, (2, 2)), (1, (16, 1))])
+def test_few_rows_over_long_contexts(n, heads, d, dtype):
+    """Up to 4, 8 and 16 rows (tokens and grouped heads) over contexts of many blocks, of a few keys and of none, with
+    pages given up, windows that begin inside a block, and every key visible."""
+    new, lens = [n, 1, n, n, 0], [2500, 1, 517, n + 63, 40]
+    x = batch(new, lens, 48, heads, d, dtype, behind=3)
+    attend(x)
+    attend(x, causal=False)
+    x.table[0, 3:20] = -1
+    x.table[2, 1] = x.K.shape[0]
+    attend(x)
+    attend(x, window=300)
