@@ -6,13 +6,16 @@
 //
 // R = 64 (paged_kernel): a row belongs to 16 threads of a half-warp, four rows to a thread, so that scores, maxima and
 // probabilities pass between them by shuffles and a row of shared memory.  Bound by the reads of shared memory beside the
-// multiply-adds (24 wavefronts for 64 of a warp; two floats an instruction made it slower, 652 -> 830 us): 4 x 1000 tokens
-// over 3000 keys, 8 heads of 64 in pairs (20 GFLOP) 615 us, 33 TFLOP/s.
+// multiply-adds (32 cycles of reads for 16 of products; two floats an instruction made it slower, 652 -> 830 us): 4 x 1000
+// tokens over 3000 keys, 8 heads of 64 in pairs (20 GFLOP) 604 us, 34 TFLOP/s; at d = 256 2.3 ms (2.6 with the test for
+// hidden keys in every block's products).
 // R = 4, 8, 16 (few_kernel): one or a few tokens, bound by reading the cache.  A warp takes an eighth of a block's keys
 // for all rows, so that K and V are read from shared memory once, not by every warp, and keeps maxima, sums and
 // outputs of its own, which meet at the end of the item.  32 tokens over 100 to 4000 keys, 16 heads in groups of 4: at
 // d = 128 (269 MB) 83 us, 3.2 TB/s, at d = 64 51 us (with rows dealt to half-warps as above 248 and 116), bound by
 // the instructions a key (half of the issue slots) and the waits of their chains.
+#include <type_traits>
+
 #include "paged_launch.h"
 
 namespace fbd {
@@ -224,24 +227,27 @@ __global__ void __launch_bounds__(kT, (D <= 64 ? 2 : 1))
       for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int x = 0; x < C2; ++x) o[i][x][0] = o[i][x][1] = 0.f;
-      for (int j = 0; j < BN; j += 4) {
-        float4 e[RT];
+      auto products = [&](auto some) {  // some: keys may be hidden
+        for (int j = 0; j < BN; j += 4) {
+          float4 e[RT];
 #pragma unroll
-        for (int i = 0; i < RT; ++i) e[i] = *reinterpret_cast<const float4*>(sP + (ty * RT + i) * L::PP + j);
+          for (int i = 0; i < RT; ++i) e[i] = *reinterpret_cast<const float4*>(sP + (ty * RT + i) * L::PP + j);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          float2 v[C2];
+          for (int u = 0; u < 4; ++u) {
+            float2 v[C2];
 #pragma unroll
-          for (int x = 0; x < C2; ++x) v[x] = *reinterpret_cast<const float2*>(sV + (j + u) * D + tx * 2 + 32 * x);
+            for (int x = 0; x < C2; ++x) v[x] = *reinterpret_cast<const float2*>(sV + (j + u) * D + tx * 2 + 32 * x);
 #pragma unroll
-          for (int i = 0; i < RT; ++i) {
-            const float f = u == 0 ? e[i].x : u == 1 ? e[i].y : u == 2 ? e[i].z : e[i].w;
-            if (part && f == 0.f) continue;  // (hidden: 0 times an infinity would be NaN)
+            for (int i = 0; i < RT; ++i) {
+              const float f = u == 0 ? e[i].x : u == 1 ? e[i].y : u == 2 ? e[i].z : e[i].w;
+              if (some.value && f == 0.f) continue;  // (hidden: 0 times an infinity would be NaN)
 #pragma unroll
-            for (int x = 0; x < C2; ++x) o[i][x][0] = fmaf(f, v[x].x, o[i][x][0]), o[i][x][1] = fmaf(f, v[x].y, o[i][x][1]);
+              for (int x = 0; x < C2; ++x) o[i][x][0] = fmaf(f, v[x].x, o[i][x][0]), o[i][x][1] = fmaf(f, v[x].y, o[i][x][1]);
+            }
           }
         }
-      }
+      };
+      if (part) products(std::true_type{}); else products(std::false_type{});
 #pragma unroll
       for (int i = 0; i < RT; ++i)
 #pragma unroll
@@ -421,22 +427,25 @@ __global__ void __launch_bounds__(kT, few_per_sm(D, R))
       for (int j = 0; j < KW; ++j)
 #pragma unroll
         for (int x = 0; x < NX; ++x) take<VW>(sV + (warp * KW + j) * D + (x * 32 + lane) * VW, v[j] + x * VW);
+      auto products = [&](auto some) {
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        float e[KW], o[NC];
+        for (int i = 0; i < R; ++i) {
+          float e[KW], o[NC];
 #pragma unroll
-        for (int j = 0; j < KW; j += 4) take<4>(sP + i * KW + j, e + j);
+          for (int j = 0; j < KW; j += 4) take<4>(sP + i * KW + j, e + j);
 #pragma unroll
-        for (int x = 0; x < NC; ++x) o[x] = 0.f;
+          for (int x = 0; x < NC; ++x) o[x] = 0.f;
 #pragma unroll
-        for (int j = 0; j < KW; ++j) {
-          if (cut && e[j] == 0.f) continue;  // (hidden: 0 times an infinity would be NaN)
+          for (int j = 0; j < KW; ++j) {
+            if (some.value && e[j] == 0.f) continue;  // (hidden: 0 times an infinity would be NaN)
 #pragma unroll
-          for (int x = 0; x < NC; ++x) o[x] = fmaf(e[j], v[j][x], o[x]);
+            for (int x = 0; x < NC; ++x) o[x] = fmaf(e[j], v[j][x], o[x]);
+          }
+#pragma unroll
+          for (int x = 0; x < NC; ++x) acc[i][x] = fmaf(acc[i][x], alpha[i], o[x]);
         }
-#pragma unroll
-        for (int x = 0; x < NC; ++x) acc[i][x] = fmaf(acc[i][x], alpha[i], o[x]);
-      }
+      };
+      if (cut) products(std::true_type{}); else products(std::false_type{});
     }
     // The warps' outputs meet.
     __syncthreads();
