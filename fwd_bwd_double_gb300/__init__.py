@@ -235,7 +235,9 @@ def _launch(fn, tensors, *args):
     """fn(*args, stream) on the device the tensors are on: one CUDA device, made current for the call, and its current
     stream.  Empty tensors launch nothing, so they may be anywhere."""
     cuda = _torch().cuda
-    devices = {t.get_device() for t in tensors if t is not None and t.numel()}
+    devices = {t.get_device() for t in tensors if t is not None}
+    if len(devices) > 1 or -1 in devices:
+        devices = {t.get_device() for t in tensors if t is not None and t.numel()}
     if len(devices) > 1 or -1 in devices:
         raise FbdError(1, f"tensors must be on one CUDA device (got {sorted({str(t.device) for t in tensors if t is not None})})")
     if not devices:
@@ -410,10 +412,9 @@ def _view(name, x, shape, dtype, strides):
         raise FbdError(1, f"{name} is None")
     if x.shape != shape or x.dtype != dtype:
         raise FbdError(1, f"{name} must be {dtype} {tuple(shape)} (got {x.dtype} {tuple(x.shape)})")
-    s = x.stride()
-    if s[3] != 1 and x.numel():
+    strides[0], strides[1], strides[2], last = x.stride()
+    if last != 1 and x.numel():
         raise FbdError(1, f"the last dimension of {name} must be contiguous")
-    strides[:] = s[:3]
     return x.data_ptr()
 
 
@@ -437,8 +438,9 @@ def _norm_desc(xs, pos, freq, axis, paired):
     """Descriptor of a call on normed heads, the shape [B, heads, N, d] of its first tensor, and its tables."""
     if not 1 <= len(xs) <= ATTN_ROPE_MAX_TENSORS:
         raise FbdError(1, f"1 to {ATTN_ROPE_MAX_TENSORS} tensors, got {len(xs)}")
-    if any(x is None or x.dim() != 4 for x in xs):
-        raise FbdError(1, "tensors must be [B, heads, N, d]")
+    for x in xs:
+        if x is None or x.dim() != 4:
+            raise FbdError(1, "tensors must be [B, heads, N, d]")
     if paired not in ("half", "neighbour"):
         raise FbdError(1, f"paired must be 'half' or 'neighbour' (got {paired!r})")
     B, _, N, d = xs[0].shape
@@ -452,7 +454,7 @@ def _listed(ts, n, what):
     """A tensor, None or a list of n of them as a list."""
     if ts is None:
         return [None] * n
-    ts = [ts] if _torch().is_tensor(ts) else list(ts)
+    ts = list(ts) if isinstance(ts, (list, tuple)) or not _torch().is_tensor(ts) else [ts]
     if len(ts) != n:
         raise FbdError(1, f"{n} tensors and {len(ts)} {what}")
     return ts
