@@ -617,7 +617,7 @@ def attn_paged(Q, cache, lens, cu=None, O=None, lse=None, workspace=None, scale:
     qs, os_ = _Strides(), _Strides()
     Q_at, O_at = _view("Q", Q, Q.shape, dtype, qs), _view("O", O, Q.shape, dtype, os_)
     lse_at = _want("lse", lse, (batch, H, N), torch.float32)
-    window = max(-1, min(window, (1 << 31) - 1))  # (the field has 32 bits; a cache's capacity or more is no window)
+    window = max(-1, min(window, (1 << 31) - 1))  # (the field has 32 bits; positions are below 2^31 - 1, so that much is no window)
     desc = AttnDesc(B, H, N, d, scale, causal, _dtype_code(Q), H // Hkv if Hkv else 1, window, None, None)
     max_new = N if cu is None else min(max_new, N)
     workspace = _workspace(lib.attn_paged_workspace_bytes(ctypes.byref(desc), max_new), Q, workspace)

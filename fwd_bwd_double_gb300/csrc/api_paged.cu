@@ -179,7 +179,6 @@ attn_status_t check_cache(const attn_cache_t* c, Paged& p, const int32_t* cu, co
                 static_cast<int>(c->page_size),
                 static_cast<int>(c->pages),
                 static_cast<int>(c->width * c->page_size)};
-  if (p.window >= p.seqs.cap) p.window = 0;  // (as wide as the cache: none)
   return ATTN_OK;
 }
 
