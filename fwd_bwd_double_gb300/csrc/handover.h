@@ -53,5 +53,12 @@ FBD_HD int agree(int x, const All& all) {
 // what a CTA that gave up waits for before it ends.
 FBD_HD int last_phase(int fills, int stages, int s) { return ((fills - 1 - s) / stages) & 1; }
 
+// Buffers handed from one role to another in turn, each with a barrier of its own that completes a phase a
+// hand-over.  A parity tells two neighbouring phases apart, so a giver that may be `n` hand-overs ahead of a taker
+// that has not yet looked needs n barriers, as it needs n buffers: on one barrier the second hand-over would
+// look like none.  The buffer (and barrier) of hand-over k of n, and the parity of its wait.
+FBD_HD int buffer_of(int k, int n) { return k % n; }
+FBD_HD int parity_of(int k, int n) { return (k / n) & 1; }
+
 }  // namespace handover
 }  // namespace fbd

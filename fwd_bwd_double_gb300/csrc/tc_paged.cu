@@ -50,7 +50,7 @@ struct Lay {
   static constexpr int NS = D == 64 ? 8 : 4;
   static constexpr int oRing = 2 * kTile;
   static constexpr int oOut = oRing + NS * kTile;
-  static constexpr int oStat = oOut + 8 * kOut;  // [2][128] (max, sum) of the second half of an item's blocks
+  static constexpr int oStat = oOut + 8 * kOut;  // [2][128] (max, sum) of the second half of an item's blocks, of two items
   static constexpr int oBar = oStat + 2 * BM * 8;
   static constexpr int oItem = oBar + 512;
   static constexpr int bytes = oItem + 8 * 64;
@@ -75,8 +75,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* p_ready = p_half + 2;    // [2] of all keys
   uint64_t* o_full = p_ready + 2;
   uint64_t* o_empty = o_full + 1;    // O_0, O_1 read by the epilogue
-  uint64_t* x_full = o_empty + 1;    // tile 1's maxima and sums are there for tile 0
-  uint64_t* settled = x_full + 1;    // after a wait that gave up: the products in flight done
+  uint64_t* x_full = o_empty + 1;    // [2] tile 1's maxima and sums are there for tile 0, in each buffer of stat
+  uint64_t* settled = x_full + 2;    // after a wait that gave up: the products in flight done
   uint64_t* full = settled + 1;      // [NS]
   uint64_t* empty = full + NS;       // [NS]
   uint64_t* v_ok = empty + NS;       // [NS] values that some row does not see are finite
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* spoilt = reinterpret_cast<volatile int*>(hidden + 16);    // [8] of items: n + 1 where values were made 0
   float2* stat = reinterpret_cast<float2*>(sm + L::oStat);
   Item* items = reinterpret_cast<Item*>(sm + L::oItem);
-  static_assert(sizeof(Item) == 64 && (12 + 3 * NS + 10) * 8 + 4 * 4 + 16 + 32 <= 512, "the barriers' region");
+  static_assert(sizeof(Item) == 64 && (13 + 3 * NS + 10) * 8 + 4 * 4 + 16 + 32 <= 512, "the barriers' region");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, p = blockIdx.x;
   const int gt = w.cut.gt, tq = w.cut.tile;
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     ptx::mbar_init(o_full, 4);
     ptx::mbar_init(o_empty, 256);
-    ptx::mbar_init(x_full, 128);
+    for (int s = 0; s < 2; ++s) ptx::mbar_init(&x_full[s], 128);
     ptx::mbar_init(settled, 2);
     for (int s = 0; s < NS; ++s) {
       ptx::mbar_init(&full[s], 1);
@@ -444,13 +444,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // ------------------------------------------------------------------ epilogue
       float a0 = 1.f, a1 = 0.f;  // weights of this tile's sums and of the other's
-      if (!pair && it->n > 1) {  // (tile 1 of the item after next waits for this one's epilogue: two buffers)
-        float2* mine = stat + (shared & 1) * BM + r;
+      // Tile 1 hands over for the next such item before tile 0 has looked at this one where it has one block there, whose
+      // S needs nothing of tile 0's; for the one after that it needs this item's epilogue, tile 0's o_empty: two buffers, each
+      // with its barrier.
+      if (!pair && it->n > 1) {
+        const int buf = handover::buffer_of(shared, 2);
+        float2* mine = stat + buf * BM + r;
         if (m == 1) {
           *mine = make_float2(mref, l);
-          ptx::mbar_arrive(x_full);
+          ptx::mbar_arrive(&x_full[buf]);
         } else {
-          wait(x_full, shared & 1);
+          wait(&x_full[buf], handover::parity_of(shared, 2));
           const float2 z = *mine;
           const float top = fmaxf(mref, z.x), sub = top == -INFINITY ? 0.f : top * c;
           a0 = mref == -INFINITY ? 0.f : ptx::ex2(fmaf(mref, c, -sub)), a1 = z.x == -INFINITY ? 0.f : ptx::ex2(fmaf(z.x, c, -sub));

@@ -1,8 +1,8 @@
-"""Calls at the limits of what the paged cache takes: lengths past the table under masks.  References and
+"""Calls at the limits of what the paged cache takes: lengths past the table under masks, many small items.  References and
 bounds: tests/paged_reference.py."""
 import pytest
 
-from test_gpu_paged import _lib, _t, attend, dt  # noqa: F401
+from test_gpu_paged import _lib, _t, attend, batch, dt  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +56,17 @@ def test_windows_near_the_largest_length(dtype):
         x.lens[0] = top
         for window in (0, 100, top - 60, top - 1, top):
             attend(x, window=window)
+
+
+# --------------------------------------------------------------------- items of few key blocks
+@pytest.mark.parametrize("d,heads", [(64, (4, 4)), (128, (8, 2)), (96, (3, 1))])
+def test_many_items_of_two_and_three_blocks(d, heads):
+    """Items of one tile over one, two and three blocks of 128 keys, tens of them a CTA one after another: the second half
+    of each is joined to the first while the next ones are under way."""
+    import random
+    rng = random.Random(7)
+    new = [rng.randint(17, 40) for _ in range(900)]
+    lens = [n + rng.choice([0, 60, 130, 200, 230, 300, 340]) for n in new]
+    x = batch(new, lens, 32, heads, d, "bf16")
+    attend(x)
+    attend(x, window=90)
