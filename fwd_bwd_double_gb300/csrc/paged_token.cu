@@ -90,13 +90,15 @@ __global__ void __launch_bounds__(kThreads, Lay<D>::per_sm)
     if (*abort_flag) atomicOr(&g_err, FBD_ERR_TIMEOUT);
     ptx::fence_mbar_init();
   }
+  Plan planned{};
+  if (warp == 4) planned = plan(w, p);
   __syncthreads();
   const ptx::BoundedWait wait{abort_flag, &g_err};
 
   if (warp == 4) {
     // ------------------------------------------------------------ plan and loads
     Walk it;
-    bool more = it.begin(w, plan(w, p)) && *abort_flag == 0, go = true;
+    bool more = it.begin(w, planned) && *abort_flag == 0, go = true;
     int E = 0, n = 0;
     const int per = MK / pg.box;
     const int c0 = pg.whole ? 0 : lane % SL, g0 = pg.whole ? lane : lane / SL;  // this lane's box

@@ -125,6 +125,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tmem_alloc(tmem_slot, 512);
     ptx::tmem_relinquish();
   }
+  Plan planned{};
+  if (warp == 8) planned = plan(w, p);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -146,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ TMA producer
     Walk it;
     Tail tail{0, 0, 0, 0};
-    bool more = it.begin(w, plan(w, p)) && ok, go = true;
+    bool more = it.begin(w, planned) && ok, go = true;
     int E = 0, n = 0, nq = 0, T0 = 0, T1 = 0;
     const int per = BN / pg.box;                                                // boxes of an entry along its keys
     const int c0 = pg.whole ? 0 : lane % SL, g0 = pg.whole ? lane : lane / SL;  // this lane's box

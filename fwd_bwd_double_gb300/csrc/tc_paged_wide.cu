@@ -82,6 +82,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tmem_alloc(tmem_slot, 512);
     ptx::tmem_relinquish();
   }
+  Plan planned{};
+  if (warp == 4) planned = plan(w, p);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -113,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ TMA producer
     Walk it;
     Tail tail{0, 0, 0, 0};
-    bool more = it.begin(w, plan(w, p)) && ok, go = true;
+    bool more = it.begin(w, planned) && ok, go = true;
     int E = 0, n = 0, T = 0;
     const int per = KN / pg.box;                                                // boxes of an entry along its keys
     const int c0 = pg.whole ? 0 : lane % SL, g0 = pg.whole ? lane : lane / SL;  // this lane's box

@@ -1,8 +1,8 @@
-"""Calls at the limits of what the paged cache takes: lengths past the table under masks, many small items.  References and
-bounds: tests/paged_reference.py."""
+"""Calls at the limits of what the paged cache takes: lengths past the table under masks, many small items,
+sequences by the million.  References and bounds: tests/paged_reference.py."""
 import pytest
 
-from test_gpu_paged import _lib, _t, attend, batch, dt  # noqa: F401
+from test_gpu_paged import _lib, _t, attend, batch, dt, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -70,3 +70,47 @@ def test_many_items_of_two_and_three_blocks(d, heads):
     x = batch(new, lens, 32, heads, d, "bf16")
     attend(x)
     attend(x, window=90)
+
+
+# ------------------------------------------------------------------------ very many sequences
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("n", [1, 30])
+def test_a_few_tokens_among_the_most_sequences(n, d, dtype):
+    """New tokens of a few sequences among 2^25 - 1, the most that a call takes: the first and the last one follow one another
+    in a CTA's stretch, and what lies between is passed within the waits' bounds."""
+    import fwd_bwd_double_gb300 as fbd
+    import paged_reference as R
+    torch = _t()
+    B = (1 << 25) - 1
+    for where in ([0, B - 1], [0, 1, B // 2, B - 2, B - 1]):
+        x = batch([n] * len(where), [n + 20 * k for k in range(len(where))], 64, (1, 1), d, dtype, width=2)
+        at = torch.tensor(where, device="cuda")
+        new = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+        new[at + 1] = n
+        cu = new.cumsum(0, dtype=torch.int32)
+        lens = torch.full((B,), 9, dtype=torch.int32, device="cuda")
+        table = torch.full((B, 2), -1, dtype=torch.int32, device="cuda")
+        lens[at], table[at] = x.lens, x.table
+        O, lse = torch.full_like(x.Q, 7.0), torch.full(x.Q.shape[:3], 7.0, device="cuda")
+        fbd.attn_paged(x.Q, (x.K, x.V, table), lens, cu, O=O, lse=lse, max_new=n)
+        fbd.attn_device_status()
+        for b, (o, L) in enumerate(R.attention(x)):
+            r, rows = x.place(b)
+            within(O[r, :, rows], o, f"O of sequence {where[b]}")
+            within(lse[r, :, rows], L, f"lse of sequence {where[b]}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_runs_of_empty_sequences(dtype):
+    """Empty sequences in runs of every length around the 32 and 128 that are passed at once, in front and behind too."""
+    for runs in ([0, 1, 30, 31, 32, 33, 95, 96, 97], [127, 128, 129, 255, 256, 257, 500], [31, 127, 0, 0, 160]):
+        new = []
+        for k, r in enumerate(runs):
+            new += [0] * r + [1 + k % 3]
+        new += [0] * runs[-1]
+        lens = [v + (7 * i) % 40 if v else i % 50 for i, v in enumerate(new)]
+        x = batch(new, lens, 16, (1, 1), 64, dtype)
+        attend(x)
+        attend(x, max_new=0)
+        attend(batch(new, lens, 16, (1, 1), 256, dtype), max_new=0)
