@@ -598,8 +598,9 @@ def attn_paged(Q, cache, lens, cu=None, O=None, lse=None, workspace=None, scale:
     ones).  cu [B + 1] int32: packed tokens, Q [1, H, N, d], sequence b has the rows cu[b] .. cu[b + 1] - 1.  Q, K, V and O
     are views of any strides with d contiguous; O is given its memory token by token ([B, N, H, d]) when it is not given,
     as a layer's output projection takes it.  lse float32 [B, H, N].  max_new: the most new tokens of a sequence, where the
-    host knows it (1 when each has one: chooses the kernel, nothing else).  A token that sees no key gives O = 0, lse =
-    -inf; rows of no sequence stay as they were."""
+    host knows it (1 when each has one): it chooses the kernel and may change roundings, nothing else, and a workspace given
+    is sized with the same one (N without cu).  A token that sees no key gives O = 0, lse = -inf; rows of no sequence stay
+    as they were."""
     torch = _torch()
     if Q is None or Q.dim() != 4:
         raise FbdError(1, "Q must be [B, H, N, d]")

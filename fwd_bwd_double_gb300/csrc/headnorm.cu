@@ -11,9 +11,11 @@
 // ones before the tables and the token's place are looked up, and the next token's behind this one's: held in
 // registers, half as many bytes were on their way.  Squares, sums and r are fp32; each output is rounded once.
 //
-// 24 heads of 64 over 32768 tokens in bf16 (201 MB): 39 us, 5.1 TB/s; the gradient (302 MB) 56 us, 5.4 TB/s (with the
-// next pieces in registers 41 and 79 us); 19.8 thousand prompt tokens of 16 + 4 + 4 heads of 128 into pages (243 MB)
-// 57 us, 4.3 TB/s.  Half of the issue slots are the sums, turns and conversions.
+// 24 heads of 64 over 32768 tokens in bf16 (201 MB): 39 us, 5.2 TB/s; the gradient (302 MB) 55 us, 5.5 TB/s (with the
+// next pieces in registers 41 and 78 us); 19.8 thousand prompt tokens of 16 + 4 + 4 heads of 128 into pages (243 MB)
+// 57 us, 4.3 TB/s (with registers 55).  float32: 71 us, 5.7 TB/s; 101 us, 6.0 TB/s; 90 us, 5.4 TB/s.  Half of the issue slots are
+// the sums, turns and conversions; that does not bound it, the cut does (split): the 24 heads' blocks take three or four
+// groups of tokens where 3.4 would be even, and the SMs are active for 78 % of the time.
 #include <cuda_bf16.h>
 
 #include "angle.cuh"

@@ -23,7 +23,7 @@
 //
 // 8192 tokens over 32192 keys, 16 heads of 128 in groups of 4: 1.27 ms, 1.49 PFLOP/s (77 % of what a plain product
 // reaches), bound by the chain S -> softmax -> P V of each tile.  12 sequences of up to 1500 tokens behind up to 9000 keys,
-// window 2000, 12 heads of 96 (run as 128): 141 us, 0.52 PFLOP/s, bound by the items' starts and epilogues and by
+// window 2000, 12 heads of 96 (run as 128): 142 us, 0.52 PFLOP/s, bound by the items' starts and epilogues and by
 // blocks that are partly masked.
 // CTAs take the stretches of paged.cuh.  The reference maximum M_m moves as in the differential forward
 // (tc_diff_fwd.cu): when the new largest P would be above a quarter of the row's sum so far, or above 2^8.

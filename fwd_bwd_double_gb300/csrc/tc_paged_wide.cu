@@ -6,7 +6,7 @@
 // of products a block.  What bounds it is the way of K and V into shared memory, 64 KB a block, so Q lies in
 // TMEM (128 columns, written by the softmax threads, a row each), and shared memory is a ring of six entries
 // of 64 keys.  With Q in shared memory and four such entries a block took 3600 cycles: 126 us for 2 x 1000 tokens over
-// 4500 keys, 8 heads in pairs, 86 us so (0.86 PFLOP/s).  O is rescaled, where
+// 4500 keys, 8 heads in pairs, 84 us so (0.87 PFLOP/s).  O is rescaled, where
 // the maximum moved, once the product before has ended.
 #include <cuda_bf16.h>
 

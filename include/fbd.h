@@ -506,14 +506,19 @@ attn_status_t attn_cache_append(const attn_desc_t* desc, const attn_new_tokens_t
  * next token) over the keys the cache holds, their own among them:
  *   O = softmax(s Q K^T + mask) V,  lse the natural log-sum-exp [.., H, N] float32 (NULL: not written).
  *   desc: B, H, N, d, scale, dtype, group, causal = 1: a token at position p sees the keys j <= p, with
- *   window W > 0 only j > p - W; causal = 0: every key.  No document bounds (ATTN_ERR_UNSUPPORTED).
+ *   window W > 0 only j > p - W (also where p lies behind the table); causal = 0: every key.  No document
+ *   bounds (ATTN_ERR_UNSUPPORTED).
  *   Q, O: [.., H, N, d] views with strides of (batch, head, position), positive.
  *   A token that sees no key gives O = 0 and lse = -inf.  A key that a token does not see has no part
  *   in its result, whatever the cache holds there.
+ *   bf16: each weight is rounded to bf16 for its product with V (off by at most 2^-8 of itself); sums and lse
+ *   are fp32 and take the weights unrounded.  float32: fp32 throughout.
  *   max_new: the most new tokens that a sequence has, as far as the host knows (0: not known; N where
  *   cu is NULL).  It chooses the kernel and may change roundings, nothing else.
- *   workspace: >= attn_paged_workspace_bytes(desc, max_new) bytes, 16-byte aligned, contents ignored on
- *   entry.  Calls that may run at the same time need one each. */
+ *   workspace: >= attn_paged_workspace_bytes(desc, max_new) bytes for the same max_new (N where cu is NULL),
+ *   16-byte aligned, contents ignored on entry: up to 41 MB, whatever the sizes.  Calls that may run at the
+ *   same time need one each.
+ *   The sequences are looked at on the device, 21 us a thousand of them. */
 size_t attn_paged_workspace_bytes(const attn_desc_t* desc, int64_t max_new);
 attn_status_t attn_paged(const attn_desc_t* desc, const void* Q, const int64_t* q_stride, const attn_cache_t* cache,
                          const int32_t* cu, const int32_t* lens, int64_t max_new, void* O, const int64_t* o_stride,
